@@ -203,12 +203,14 @@ m2_status m2_check(m2_handle* h);
 
 /*
  * The same for the standalone entry points (fp8_linear, fp8_linear_bf16,
- * bf16_linear, fp8_linear_noalloc), which have no handle: they share one
+ * bf16_linear, fp8_linear_noalloc, m2_lora_add, m2_state_reorder), which have
+ * no handle: they share one
  * library-owned error word per device (a file-scope device variable, looked
  * up once per device on the first such call, which should therefore come
  * before any stream capture).  Synchronises the current device, reads and
  * clears its word.  M2_ETIMEOUT: a bounded wait of one of those calls ran
- * out and its y is incomplete.
+ * out and its y is incomplete; M2_EINVAL: a row of m2_lora_add named an
+ * adapter that is not there, or m2_state_reorder left a request as it was.
  */
 m2_status m2_check_standalone(void);
 
@@ -431,6 +433,109 @@ m2_status m2_rmsnorm_residual(uint16_t* h, const uint16_t* add, const uint16_t* 
  */
 m2_status m2_rmsnorm_residual_quant(uint16_t* h, const uint16_t* add, const uint16_t* w, float eps, float s_q,
                                     uint16_t* normed, uint8_t* q, int T, int n, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Many requests on one block: low-rank adapters per row, beam selection, and
+ * the reordering of the paged states after it.  (The pages have no
+ * counterpart to these entry points.)
+ * ------------------------------------------------------------------------ */
+
+/* Workspace bytes m2_lora_add needs. */
+m2_status m2_lora_add_workspace_size(int M, int N, int K, int rank, int n_adapters, size_t* bytes);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection: row m names
+ * adapter a = row_adapter[m], and
+ *   out[m, n] = bf16( y[m, n] + scale[a] * sum_j b[a, n, j] * (sum_k a_w[a, j, k] * x[m, k]) )
+ * with y the projection's bf16 rows.  Sums, products and the rank-wide
+ * intermediate are held to f32 or better than 2^-16 of it; out is rounded
+ * once (nearest even).  A row with row_adapter[m] = -1 takes no adapter:
+ * out[m] = y[m], bit for bit.  An id outside [-1, n_adapters) is treated as
+ * -1 and m2_check_standalone() reports M2_EINVAL.
+ *   y            bf16 [M, N] device
+ *   x            bf16 [M, K] device, the projection's input
+ *   a_w          bf16 [n_adapters, rank, K] device
+ *   b            bf16 [n_adapters, N, rank] device
+ *   scale        f32 [n_adapters] device or NULL (1 for every adapter)
+ *   row_adapter  int32 [M] device
+ *   out          bf16 [M, N] device: y itself (in place) or a buffer that
+ *                overlaps neither y nor x
+ *   workspace    device, >= m2_lora_add_workspace_size bytes, 256-byte aligned
+ *                (may be NULL when that is 0)
+ * rank: a multiple of 8 in [8, 128] (adapters of lower rank are padded with
+ * zero rows of a_w and columns of b); K: a multiple of 16; N >= 1; M from 0
+ * to 2^24; n_adapters in [1, 4096].  x, a_w and b 16-byte aligned, y and out
+ * 2-byte.  Errors: M2_EINVAL, M2_ESHAPE, M2_ENOMEM, M2_EDEVICE, M2_ECUDA.
+ */
+m2_status m2_lora_add(const uint16_t* y, const uint16_t* x, const uint16_t* a_w, const uint16_t* b, const float* scale,
+                      int n_adapters, int rank, const int32_t* row_adapter, uint16_t* out, int M, int N, int K,
+                      void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes m2_beam_select needs. */
+m2_status m2_beam_select_workspace_size(int batch, int beams, int vocab, int k, size_t* bytes);
+
+/*
+ * Beam selection: for each of `batch` requests, the k best of beams x vocab
+ * continuations by
+ *   value(b, v) = scores[b] + logits[b, v] - log sum_u exp(logits[b, u]),
+ * greatest first, equal values by the lower b * vocab + v.  The logits are
+ * read once; values are compared in 64 bits and returned rounded to f32.
+ *   logits      bf16 or f32 (dtype) device, row i * beams + b of request i's
+ *               beam b starting row_stride elements after the one before
+ *               (>= vocab: a padded vocabulary is read in place); any
+ *               alignment of the element type
+ *   scores      f32 [batch, beams] device: the beams' summed log
+ *               probabilities.  A beam whose score is not finite has no
+ *               continuations (and its logits are not read).
+ *   done        uint8 [batch, beams] device or NULL: a finished beam (nonzero)
+ *               has one continuation, token `eos` with its score unchanged
+ *   eos         the end token; with done or out_done it must be in
+ *               [0, vocab), else it is not used
+ *   tokens      int32 [batch, k] device
+ *   parents     int32 [batch, k] device: the beam each continues (0 <= b < beams)
+ *   out_scores  f32 [batch, k] device
+ *   out_done    uint8 [batch, k] device or NULL: 1 where the parent was
+ *               finished or the token is eos, else 0
+ * A logit of -inf is masked (no continuation); a NaN is treated as masked.  A
+ * row of +inf logits shares the probability equally among them.  Where a
+ * request has fewer than k continuations, the rest is token -1, parent -1,
+ * score -inf, done 0.
+ * out_scores may be scores, and out_done done, when k == beams; otherwise no
+ * output may overlap an input.  beams in [1, 32], k in [1, 64], vocab in
+ * [1, 2^24], batch * beams in [0, 4096].
+ * Errors: M2_EINVAL, M2_ESHAPE, M2_ENOMEM, M2_EDEVICE, M2_ECUDA.
+ */
+m2_status m2_beam_select(const void* logits, int dtype, size_t row_stride, int batch, int beams, int vocab,
+                         const float* scores, const uint8_t* done, int eos, int k, int32_t* tokens, int32_t* parents,
+                         float* out_scores, uint8_t* out_done, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The paged states after a selection: row (i, j) goes on from beam
+ * p = parents[i, j] of its request, whose state is in slot slot_idx[i, p] of
+ * every layer's pools.  Slots are renamed where that is enough, so only the
+ * rows that have to exist twice are copied: within a request, the first row
+ * naming a beam takes that beam's slot; each further one takes, in order of
+ * slot_idx, a slot whose beam no row names, and the parent's conv window and
+ * state are copied to it in all layers.  Rows with parent -1 (none) get the
+ * slots left over, nothing copied, or -1.  So new_slot_idx[i] is a permutation
+ * of slot_idx[i], and pass it to m2_decode next.
+ *   conv_pools    host array of `layers` device pointers, bf16 [n_slots, 6144, 3]
+ *   ssm_pools     host array of `layers` device pointers, [n_slots, 64, 64, 128]
+ *                 f32 or bf16 (ssm_dtype)
+ *   slot_idx      int32 [batch, beams] device; -1: the row has no slot
+ *   parents       int32 [batch, beams] device, in [-1, beams)
+ *   new_slot_idx  int32 [batch, beams] device; overlaps neither input
+ * A request keeps its slots, copies nothing and is reported by
+ * m2_check_standalone() as M2_EINVAL if a slot is outside [-1, n_slots) or
+ * named by an earlier row of the call, if a parent is outside [-1, beams) or
+ * has no slot, or if its rows with a parent outnumber its slots.
+ * layers in [1, 64], beams in [1, 32], batch * beams in [0, 4096]; pools
+ * 16-byte aligned.  Errors: M2_EINVAL, M2_ESHAPE, M2_EDEVICE, M2_ECUDA.
+ */
+#define M2_REORDER_MAX_LAYERS 64
+m2_status m2_state_reorder(uint16_t* const* conv_pools, void* const* ssm_pools, int layers, int ssm_dtype, int n_slots,
+                           const int32_t* slot_idx, const int32_t* parents, int32_t* new_slot_idx, int batch, int beams,
+                           void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import typing
 
 import torch
 
@@ -36,7 +37,8 @@ EXPORTED = ["m2_last_error", "m2_create", "m2_destroy", "m2_get_stats", "m2_set_
             "m2_rmsnorm_residual", "m2_profile_enable", "m2_profile_read", "fp8_linear_noalloc",
             "m2_prefill_q", "m2_decode_q", "m2_rmsnorm_residual_quant", "m2_mixed_workspace_size", "m2_mixed",
             "fp8_dequant", "bf16_linear_workspace_size", "bf16_linear", "m2_check_standalone",
-            "m2_selftest_timeout"]
+            "m2_selftest_timeout", "m2_lora_add_workspace_size", "m2_lora_add", "m2_beam_select_workspace_size",
+            "m2_beam_select", "m2_state_reorder"]
 
 STAGES = ["quant_in", "in_proj", "conv", "conv_state", "ssd_cumsum", "ssd_chunk_state", "ssd_state_pass",
           "ssd_chunk_scan", "norm_quant", "out_proj", "decode_fused", "dec_quant_in", "dec_in_proj",
@@ -105,6 +107,11 @@ _sigs = {
     "bf16_linear": ([_vp, _vp, _f, _vp, _i, _i, _i, _vp, _sz, _vp], _i),
     "m2_check_standalone": ([], _i),
     "m2_selftest_timeout": ([_vp, ctypes.c_uint, _vp], _i),
+    "m2_lora_add_workspace_size": ([_i, _i, _i, _i, _i, ctypes.POINTER(_sz)], _i),
+    "m2_lora_add": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _i, _vp, _sz, _vp], _i),
+    "m2_beam_select_workspace_size": ([_i, _i, _i, _i, ctypes.POINTER(_sz)], _i),
+    "m2_beam_select": ([_vp, _i, _sz, _i, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "m2_state_reorder": ([_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _vp], _i),
 }
 for _name, (_args, _ret) in _sigs.items():
     _fn = getattr(_lib, _name)
@@ -471,6 +478,194 @@ def m2_rmsnorm_residual_quant(h: torch.Tensor, add: torch.Tensor | None, w: torc
     _check(_lib.m2_rmsnorm_residual_quant(_ptr(h), _ptr(add), _ptr(w), eps, s_q, _ptr(normed), _ptr(q), T, n,
                                           _stream(stream)))
     return q
+
+
+class _OnDevice:
+    """Scope of one call on tensors of one device: that device is current, the
+    call's stream is current for what the call allocates (so the allocator
+    frees it in that stream's order), and .stream is its handle."""
+
+    __slots__ = ("_dev", "_on", "stream")
+
+    def __init__(self, ref: torch.Tensor, stream, *others):
+        if not ref.is_cuda:
+            raise ValueError("the tensors of the call must be CUDA tensors")
+        dev = ref.device
+        for t in others:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensors of one call are on {dev} and {t.device}")
+        if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        self._dev = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        self._on = stream
+
+    def __enter__(self):
+        if self._dev is not None:
+            self._dev.__enter__()
+        if self._on is None:
+            self.stream = torch.cuda.current_stream().cuda_stream
+        else:
+            s = self._on if isinstance(self._on, torch.cuda.Stream) else torch.cuda.ExternalStream(int(self._on))
+            self.stream = s.cuda_stream
+            self._on = torch.cuda.stream(s)
+            self._on.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._on is not None:
+            self._on.__exit__(*exc)
+        if self._dev is not None:
+            self._dev.__exit__(*exc)
+
+
+def _scratch(workspace, need: int, device):
+    """The caller's workspace, or one of `need` bytes (None for 0)."""
+    if workspace is None:
+        return (None, 0) if need == 0 else (torch.empty(need, dtype=torch.uint8, device=device), need)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def m2_lora_add_workspace_size(M: int, N: int, K: int, rank: int, n_adapters: int) -> int:
+    n = _sz()
+    _check(_lib.m2_lora_add_workspace_size(M, N, K, rank, n_adapters, ctypes.byref(n)))
+    return n.value
+
+
+def m2_lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, row_adapter: torch.Tensor,
+                scale: torch.Tensor | None = None, out: torch.Tensor | None = None, workspace=None,
+                stream=None) -> torch.Tensor:
+    """Low-rank adapters of many requests beside a shared projection:
+    out[m] = bf16(y[m] + scale[i] * b[i] @ (a[i] @ x[m])) with i = row_adapter[m];
+    rows with i = -1 are y.  y bf16 [M, N], x bf16 [M, K], a bf16
+    [n_adapters, rank, K], b bf16 [n_adapters, N, rank], row_adapter int32 [M],
+    scale f32 [n_adapters].  out may be y (in place)."""
+    M, K = x.shape
+    n_adapters, rank, _ = a.shape
+    N = b.shape[1]
+    _need(x, "x", torch.bfloat16)
+    _need(y, "y", torch.bfloat16, (M, N))
+    _need(a, "a", torch.bfloat16, (n_adapters, rank, K))
+    _need(b, "b", torch.bfloat16, (n_adapters, N, rank))
+    _need(row_adapter, "row_adapter", torch.int32, (M,))
+    if scale is not None:
+        _need(scale, "scale", torch.float32, (n_adapters,))
+    if out is not None:
+        _need(out, "out", torch.bfloat16, (M, N))
+    with _OnDevice(x, stream, y, a, b, row_adapter, scale, out, workspace) as on:
+        if out is None:
+            out = torch.empty_like(y)
+        ws, nbytes = _scratch(workspace, m2_lora_add_workspace_size(M, N, K, rank, n_adapters), x.device)
+        _check(_lib.m2_lora_add(y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(scale), n_adapters, rank,
+                                row_adapter.data_ptr(), out.data_ptr(), M, N, K, _ptr(ws), nbytes, on.stream))
+    return out
+
+
+class BeamStep(typing.NamedTuple):
+    """What m2_beam_select returns: [batch, k] each; done is None without an
+    end token."""
+    tokens: torch.Tensor     # int32; -1 where a request has no further continuation
+    parents: torch.Tensor    # int32: the beam each continues, or -1
+    scores: torch.Tensor     # f32, best first; -inf where there is none
+    done: torch.Tensor | None
+
+
+def m2_beam_select_workspace_size(batch: int, beams: int, vocab: int, k: int) -> int:
+    n = _sz()
+    _check(_lib.m2_beam_select_workspace_size(batch, beams, vocab, k, ctypes.byref(n)))
+    return n.value
+
+
+def m2_beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None, eos_token: int | None = None,
+                   done: torch.Tensor | None = None, out: BeamStep | None = None, workspace=None,
+                   stream=None) -> BeamStep:
+    """The k (default: beams) best continuations of each request by scores +
+    log_softmax(logits), ties to the lower beam * vocab + token.  logits bf16
+    or f32 [batch * beams, vocab], rows contiguous and at a constant stride (a
+    slice of a padded vocabulary); scores f32 [batch, beams]; done bool
+    [batch, beams]: finished beams, which go on as eos_token with their score
+    unchanged.  out: a BeamStep of tensors to write."""
+    batch, beams = scores.shape
+    rows, vocab = logits.shape
+    if k is None:
+        k = beams
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    if rows != batch * beams:
+        raise ValueError(f"logits must have batch * beams = {batch * beams} rows, got {rows}")
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("logits rows must be contiguous")
+    row_stride = logits.stride(0) if rows > 1 else max(vocab, logits.stride(0))
+    if row_stride < vocab:
+        raise ValueError(f"logits rows overlap (stride {row_stride} for {vocab} tokens)")
+    _need(scores, "scores", torch.float32)
+    if done is not None:
+        if eos_token is None:
+            raise ValueError("done needs eos_token")
+        _need(done, "done", torch.bool, (batch, beams))
+    if out is not None:
+        _need(out.tokens, "out.tokens", torch.int32, (batch, k))
+        _need(out.parents, "out.parents", torch.int32, (batch, k))
+        _need(out.scores, "out.scores", torch.float32, (batch, k))
+        if out.done is not None:
+            if eos_token is None:
+                raise ValueError("out.done needs eos_token")
+            _need(out.done, "out.done", torch.bool, (batch, k))
+        elif eos_token is not None:
+            raise ValueError("out.done is missing (eos_token is given)")
+    with _OnDevice(logits, stream, scores, done, workspace, *(out or ())) as on:
+        dev = logits.device
+        if out is None:
+            ints = torch.empty((2, batch, k), dtype=torch.int32, device=dev)
+            out = BeamStep(ints[0], ints[1], torch.empty((batch, k), dtype=torch.float32, device=dev),
+                           None if eos_token is None else torch.empty((batch, k), dtype=torch.bool, device=dev))
+        ws, nbytes = _scratch(workspace, m2_beam_select_workspace_size(batch, beams, vocab, k), dev)
+        _check(_lib.m2_beam_select(logits.data_ptr(), M2_DTYPE_BF16 if logits.dtype == torch.bfloat16 else M2_DTYPE_F32,
+                                   row_stride, batch, beams, vocab, scores.data_ptr(), _ptr(done),
+                                   -1 if eos_token is None else eos_token, k, out.tokens.data_ptr(),
+                                   out.parents.data_ptr(), out.scores.data_ptr(), _ptr(out.done), _ptr(ws), nbytes,
+                                   on.stream))
+    return out
+
+
+def m2_state_reorder(conv_pools, ssm_pools, slot_idx: torch.Tensor, parents: torch.Tensor,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The paged states after a beam selection, in every layer's pools by one
+    call: row (i, j) of slot_idx goes on from beam parents[i, j].  Slots are
+    renamed where that is enough and copied where a beam has several children;
+    returns the new slots (int32 [batch, beams]).  conv_pools, ssm_pools: one
+    tensor per layer (or a single tensor for one layer), bf16
+    [n_slots, 6144, 3] and f32 or bf16 [n_slots, 64, 64, 128]; slot_idx and
+    parents int32 [batch, beams], -1 for none."""
+    if isinstance(conv_pools, torch.Tensor):
+        conv_pools = [conv_pools]
+    if isinstance(ssm_pools, torch.Tensor):
+        ssm_pools = [ssm_pools]
+    layers = len(conv_pools)
+    if layers != len(ssm_pools) or not layers:
+        raise ValueError(f"{layers} conv pools and {len(ssm_pools)} ssm pools")
+    batch, beams = slot_idx.shape
+    n_slots, dtype = ssm_pools[0].shape[0], ssm_pools[0].dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"ssm pools must be float32 or bfloat16, got {dtype}")
+    conv_shape, ssm_shape = (n_slots, CONV_DIM, CONV_WIDTH - 1), (n_slots, NHEADS, HEADDIM, D_STATE)
+    for c, s in zip(conv_pools, ssm_pools):
+        _need(c, "conv pool", torch.bfloat16, conv_shape)
+        _need(s, "ssm pool", dtype, ssm_shape)
+    _need(slot_idx, "slot_idx", torch.int32)
+    _need(parents, "parents", torch.int32, (batch, beams))
+    if out is not None:
+        _need(out, "out", torch.int32, (batch, beams))
+    with _OnDevice(slot_idx, stream, parents, out, *conv_pools, *ssm_pools) as on:
+        if out is None:
+            out = torch.empty_like(slot_idx)
+        conv = (_vp * layers)(*[t.data_ptr() for t in conv_pools])
+        ssm = (_vp * layers)(*[t.data_ptr() for t in ssm_pools])
+        _check(_lib.m2_state_reorder(conv, ssm, layers, M2_DTYPE_BF16 if dtype == torch.bfloat16 else M2_DTYPE_F32,
+                                     n_slots, slot_idx.data_ptr(), parents.data_ptr(), out.data_ptr(), batch, beams,
+                                     on.stream))
+    return out
 
 
 class Mamba2Stack:

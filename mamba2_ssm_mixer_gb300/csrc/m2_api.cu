@@ -309,6 +309,9 @@ static m2_status error_word_status(int v, const char* who) {
   if (v & kErrSlot) return fail(M2_EINVAL, "%s: a decode row named a slot outside [0, n_slots)", who);
   if (v & kErrDupSlot)
     return fail(M2_EINVAL, "%s: two decode rows named the same slot (the later rows were skipped)", who);
+  if (v & kErrAdapter) return fail(M2_EINVAL, "%s: a row named an adapter outside [-1, n_adapters)", who);
+  if (v & kErrBeam)
+    return fail(M2_EINVAL, "%s: a row's parent names no beam with a slot, or a request has more rows than slots", who);
   return M2_OK;
 }
 
@@ -1064,3 +1067,152 @@ extern "C" m2_status m2_check_standalone(void) {
   return error_word_status(v, "m2_check_standalone");
 }
 
+
+// ---------------------------------------------------------------- many requests: adapters, beams
+
+// Whether [p, p + pn) and [q, q + qn) share a byte.
+static bool overlap(const void* p, size_t pn, const void* q, size_t qn) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return pn && qn && p && q && a < b + qn && b < a + pn;
+}
+
+static m2_status check_lora_shape(int M, int N, int K, int rank, int n_adapters, const char* who) {
+  if (M < 0 || M > (1 << 24) || N < 1 || K < 16 || K % 16)
+    return fail(M2_ESHAPE, "%s: M %d, N %d, K %d (M up to 2^24, N >= 1, K a multiple of 16)", who, M, N, K);
+  if (rank < 8 || rank > kLoraMaxRank || rank % 8)
+    return fail(M2_ESHAPE, "%s: rank %d must be a multiple of 8 in [8, %d]", who, rank, kLoraMaxRank);
+  if (n_adapters < 1 || n_adapters > kLoraMaxAdapters)
+    return fail(M2_ESHAPE, "%s: n_adapters %d not in [1, %d]", who, n_adapters, kLoraMaxAdapters);
+  return M2_OK;
+}
+
+extern "C" m2_status m2_lora_add_workspace_size(int M, int N, int K, int rank, int n_adapters, size_t* bytes) {
+  if (!bytes) return fail(M2_EINVAL, "m2_lora_add_workspace_size: null argument");
+  m2_status s = check_lora_shape(M, N, K, rank, n_adapters, "m2_lora_add_workspace_size");
+  if (s) return s;
+  *bytes = lora_workspace_bytes(M, N, K, rank, n_adapters);
+  return M2_OK;
+}
+
+extern "C" m2_status m2_lora_add(const uint16_t* y, const uint16_t* x, const uint16_t* a_w, const uint16_t* b,
+                                 const float* scale, int n_adapters, int rank, const int32_t* row_adapter,
+                                 uint16_t* out, int M, int N, int K, void* workspace, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  m2_status s = check_lora_shape(M, N, K, rank, n_adapters, "m2_lora_add");
+  if (s) return s;
+  if (M && (!y || !x || !a_w || !b || !row_adapter || !out)) return fail(M2_EINVAL, "m2_lora_add: null pointer");
+  if ((uintptr_t)x % 16 || (uintptr_t)a_w % 16 || (uintptr_t)b % 16)
+    return fail(M2_EINVAL, "m2_lora_add: x, a_w and b must be 16-byte aligned");
+  if ((uintptr_t)y % 2 || (uintptr_t)out % 2 || (uintptr_t)scale % 4 || (uintptr_t)row_adapter % 4)
+    return fail(M2_EINVAL, "m2_lora_add: a pointer is not aligned to its element");
+  const size_t yb = (size_t)M * N * 2;
+  if ((out != y && overlap(out, yb, y, yb)) || overlap(out, yb, x, (size_t)M * K * 2))
+    return fail(M2_EINVAL, "m2_lora_add: out must be y or overlap neither y nor x");
+  const size_t need = lora_workspace_bytes(M, N, K, rank, n_adapters);
+  if (ws_bytes < need || (need && !workspace))
+    return fail(M2_ENOMEM, "m2_lora_add: workspace %zu bytes < %zu needed", ws_bytes, need);
+  if (need && (uintptr_t)workspace % 256) return fail(M2_EINVAL, "m2_lora_add: workspace must be 256-byte aligned");
+  if ((s = check_device())) return s;
+  int* err = nullptr;
+  if ((s = standalone_error_word(&err))) return s;
+  int nl = 0;
+  const LoraWeights w{n_adapters, rank, a_w, b, scale};
+  M2_CUDA(launch_lora_add(y, x, w, row_adapter, out, M, N, K, workspace, err, static_cast<cudaStream_t>(stream), &nl));
+  return M2_OK;
+}
+
+static m2_status check_beam_shape(int batch, int beams, int vocab, int k, const char* who) {
+  if (beams < 1 || beams > kBeamMaxBeams) return fail(M2_ESHAPE, "%s: beams %d not in [1, %d]", who, beams, kBeamMaxBeams);
+  if (batch < 0 || (long long)batch * beams > 4096)
+    return fail(M2_ESHAPE, "%s: batch %d x beams %d not in [0, 4096]", who, batch, beams);
+  if (vocab < 1 || vocab > (1 << 24)) return fail(M2_ESHAPE, "%s: vocab %d not in [1, 2^24]", who, vocab);
+  if (k < 1 || k > kBeamMaxK) return fail(M2_ESHAPE, "%s: k %d not in [1, %d]", who, k, kBeamMaxK);
+  return M2_OK;
+}
+
+extern "C" m2_status m2_beam_select_workspace_size(int batch, int beams, int vocab, int k, size_t* bytes) {
+  if (!bytes) return fail(M2_EINVAL, "m2_beam_select_workspace_size: null argument");
+  m2_status s = check_beam_shape(batch, beams, vocab, k, "m2_beam_select_workspace_size");
+  if (s) return s;
+  *bytes = beam_workspace_bytes(batch, beams, vocab, k);
+  return M2_OK;
+}
+
+extern "C" m2_status m2_beam_select(const void* logits, int dtype, size_t row_stride, int batch, int beams, int vocab,
+                                    const float* scores, const uint8_t* done, int eos, int k, int32_t* tokens,
+                                    int32_t* parents, float* out_scores, uint8_t* out_done, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+  g_err.clear();
+  m2_status s = check_beam_shape(batch, beams, vocab, k, "m2_beam_select");
+  if (s) return s;
+  if (dtype != M2_DTYPE_F32 && dtype != M2_DTYPE_BF16)
+    return fail(M2_EINVAL, "m2_beam_select: dtype must be M2_DTYPE_F32 or M2_DTYPE_BF16");
+  const size_t rows = (size_t)batch * beams, outs = (size_t)batch * k, es = dtype == M2_DTYPE_BF16 ? 2 : 4;
+  if (rows && (!logits || !scores || !tokens || !parents || !out_scores))
+    return fail(M2_EINVAL, "m2_beam_select: null pointer");
+  if (row_stride < (size_t)vocab || row_stride > ((size_t)1 << 40))
+    return fail(M2_ESHAPE, "m2_beam_select: row_stride %zu is below vocab %d or above 2^40", row_stride, vocab);
+  if ((done || out_done) && (eos < 0 || eos >= vocab))
+    return fail(M2_EINVAL, "m2_beam_select: done flags need eos in [0, vocab), got %d", eos);
+  if ((uintptr_t)logits % es || (uintptr_t)scores % 4 || (uintptr_t)tokens % 4 || (uintptr_t)parents % 4 ||
+      (uintptr_t)out_scores % 4)
+    return fail(M2_EINVAL, "m2_beam_select: a pointer is not aligned to its element");
+  if (rows) {
+    const size_t lb = ((rows - 1) * row_stride + vocab) * es;
+    const void* o[4] = {tokens, parents, out_scores, out_done};
+    const size_t ob[4] = {outs * 4, outs * 4, outs * 4, outs};
+    const void* in[3] = {logits, scores, done};
+    const size_t ib[3] = {lb, rows * 4, rows};
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 3; ++j) {
+        const bool same = k == beams && ((i == 2 && j == 1) || (i == 3 && j == 2)) && o[i] == in[j];
+        if (!same && overlap(o[i], ob[i], in[j], ib[j]))
+          return fail(M2_EINVAL, "m2_beam_select: an output overlaps an input");
+      }
+    for (int i = 0; i < 4; ++i)
+      for (int j = i + 1; j < 4; ++j)
+        if (overlap(o[i], ob[i], o[j], ob[j])) return fail(M2_EINVAL, "m2_beam_select: two outputs overlap");
+  }
+  const size_t need = beam_workspace_bytes(batch, beams, vocab, k);
+  if (ws_bytes < need || (need && !workspace))
+    return fail(M2_ENOMEM, "m2_beam_select: workspace %zu bytes < %zu needed", ws_bytes, need);
+  if ((uintptr_t)workspace % 256) return fail(M2_EINVAL, "m2_beam_select: workspace must be 256-byte aligned");
+  if ((s = check_device())) return s;
+  if (!rows) return M2_OK;
+  M2_CUDA(launch_beam_select(logits, dtype == M2_DTYPE_BF16, row_stride, batch, beams, vocab, scores, done, eos, k,
+                             tokens, parents, out_scores, out_done, workspace, static_cast<cudaStream_t>(stream)));
+  return M2_OK;
+}
+
+extern "C" m2_status m2_state_reorder(uint16_t* const* conv_pools, void* const* ssm_pools, int layers, int ssm_dtype,
+                                      int n_slots, const int32_t* slot_idx, const int32_t* parents,
+                                      int32_t* new_slot_idx, int batch, int beams, void* stream) {
+  g_err.clear();
+  if (layers < 1 || layers > kReorderMaxLayers)
+    return fail(M2_ESHAPE, "m2_state_reorder: layers %d not in [1, %d]", layers, kReorderMaxLayers);
+  if (ssm_dtype != M2_DTYPE_F32 && ssm_dtype != M2_DTYPE_BF16)
+    return fail(M2_EINVAL, "m2_state_reorder: ssm_dtype must be M2_DTYPE_F32 or M2_DTYPE_BF16");
+  if (beams < 1 || beams > kBeamMaxBeams)
+    return fail(M2_ESHAPE, "m2_state_reorder: beams %d not in [1, %d]", beams, kBeamMaxBeams);
+  if (batch < 0 || (long long)batch * beams > kReorderMaxRows)
+    return fail(M2_ESHAPE, "m2_state_reorder: batch %d x beams %d not in [0, %d]", batch, beams, kReorderMaxRows);
+  if (n_slots < 1) return fail(M2_EINVAL, "m2_state_reorder: n_slots %d < 1", n_slots);
+  if (!conv_pools || !ssm_pools) return fail(M2_EINVAL, "m2_state_reorder: null pointer");
+  for (int l = 0; l < layers; ++l)
+    if (!conv_pools[l] || !ssm_pools[l] || (uintptr_t)conv_pools[l] % 16 || (uintptr_t)ssm_pools[l] % 16)
+      return fail(M2_EINVAL, "m2_state_reorder: layer %d's pools must be set and 16-byte aligned", l);
+  const size_t rb = (size_t)batch * beams * 4;
+  if (rb && (!slot_idx || !parents || !new_slot_idx)) return fail(M2_EINVAL, "m2_state_reorder: null pointer");
+  if ((uintptr_t)slot_idx % 4 || (uintptr_t)parents % 4 || (uintptr_t)new_slot_idx % 4)
+    return fail(M2_EINVAL, "m2_state_reorder: a pointer is not aligned to its element");
+  if (overlap(new_slot_idx, rb, slot_idx, rb) || overlap(new_slot_idx, rb, parents, rb))
+    return fail(M2_EINVAL, "m2_state_reorder: new_slot_idx overlaps an input");
+  m2_status s = check_device();
+  if (s) return s;
+  if (!rb) return M2_OK;
+  int* err = nullptr;
+  if ((s = standalone_error_word(&err))) return s;
+  M2_CUDA(launch_state_reorder(conv_pools, ssm_pools, layers, ssm_dtype == M2_DTYPE_BF16, n_slots, slot_idx, parents,
+                               new_slot_idx, batch, beams, err, static_cast<cudaStream_t>(stream)));
+  return M2_OK;
+}

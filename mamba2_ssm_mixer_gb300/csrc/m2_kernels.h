@@ -90,4 +90,44 @@ cudaError_t launch_decode_stream(const uint16_t* zx, const BlockParams& bp, uint
                                  const DecodeTaps& taps, cudaStream_t st, int* launches,
                                  const void* l2_prefetch = nullptr, size_t l2_prefetch_bytes = 0);
 
+// lora.cu: low-rank adapters of many requests beside a shared projection,
+// out[m] = bf16(y[m] + s_a B_a (A_a x[m])) with a = ids[m]; rows with a = -1
+// are y (copied when out != y).  A row naming an adapter outside
+// [-1, n_adapters) is treated as -1 and flagged in *err.
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxAdapters = 4096;
+struct LoraWeights {
+  int n_adapters, rank;
+  const uint16_t* a;      // bf16 [n_adapters, rank, K]
+  const uint16_t* b;      // bf16 [n_adapters, N, rank]
+  const float* scale;     // f32 [n_adapters] or null (1)
+};
+size_t lora_workspace_bytes(int M, int N, int K, int rank, int n_adapters);
+cudaError_t launch_lora_add(const uint16_t* y, const uint16_t* x, const LoraWeights& w, const int32_t* ids, uint16_t* out,
+                            int M, int N, int K, void* ws, int* err, cudaStream_t st, int* launches);
+// Adapter of every row of a packed call: rows [0, Bt) from dec_ids, then the
+// tokens of each sequence.
+struct SeqAdapters {
+  int id[kMaxSeq];
+};
+cudaError_t launch_lora_row_ids(const int32_t* dec_ids, int Bt, const SeqInfo& si, const SeqAdapters& sa, int32_t* ids,
+                                cudaStream_t st);
+
+// beam.cu: the k best of beams x vocabulary of each request by
+// score + log_softmax(logits), ties to the lower beam * vocab + token.
+constexpr int kBeamMaxBeams = 32;
+constexpr int kBeamMaxK = 64;
+size_t beam_workspace_bytes(int batch, int beams, int vocab, int k);
+cudaError_t launch_beam_select(const void* logits, bool bf16, size_t stride, int batch, int beams, int vocab,
+                               const float* scores, const uint8_t* done, int eos, int k, int32_t* tokens,
+                               int32_t* parents, float* out_scores, uint8_t* out_done, void* ws, cudaStream_t st);
+
+// reorder.cu: the paged states after a beam selection (slots renamed, the
+// rows of a beam's further children copied, in every layer's pools).
+constexpr int kReorderMaxLayers = 64;
+constexpr int kReorderMaxRows = 4096;
+cudaError_t launch_state_reorder(uint16_t* const* conv_pools, void* const* ssm_pools, int layers, bool bf16_state,
+                                 int n_slots, const int32_t* slot_idx, const int32_t* parents, int32_t* new_slot,
+                                 int batch, int beams, int* err, cudaStream_t st);
+
 }  // namespace m2
