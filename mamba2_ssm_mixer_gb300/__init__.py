@@ -9,6 +9,7 @@ library has not been built (``__graft_entry__.build()`` or
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import typing
 
@@ -480,42 +481,33 @@ def m2_rmsnorm_residual_quant(h: torch.Tensor, add: torch.Tensor | None, w: torc
     return q
 
 
-class _OnDevice:
-    """Scope of one call on tensors of one device: that device is current, the
-    call's stream is current for what the call allocates (so the allocator
-    frees it in that stream's order), and .stream is its handle."""
+# The current stream's handle by device index, without building a Stream object
+# (a call of a few microseconds would spend a third of itself on that).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("_dev", "_on", "stream")
 
-    def __init__(self, ref: torch.Tensor, stream, *others):
-        if not ref.is_cuda:
-            raise ValueError("the tensors of the call must be CUDA tensors")
-        dev = ref.device
-        for t in others:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors of one call are on {dev} and {t.device}")
-        if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+def _on_device(ref: torch.Tensor, stream, others, call):
+    """call(stream handle) with ref's device current and the call's stream
+    current for what it allocates, so that the allocator frees that in the
+    stream's order.  All tensors of the call have to be on ref's device."""
+    dev = ref.device
+    if dev.type != "cuda":
+        raise ValueError("the tensors of the call must be CUDA tensors")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors of one call are on {dev} and {t.device}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(_raw_stream(dev.index))
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(_raw_stream(dev.index))
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        elif stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        self._dev = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        self._on = stream
-
-    def __enter__(self):
-        if self._dev is not None:
-            self._dev.__enter__()
-        if self._on is None:
-            self.stream = torch.cuda.current_stream().cuda_stream
-        else:
-            s = self._on if isinstance(self._on, torch.cuda.Stream) else torch.cuda.ExternalStream(int(self._on))
-            self.stream = s.cuda_stream
-            self._on = torch.cuda.stream(s)
-            self._on.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._on is not None:
-            self._on.__exit__(*exc)
-        if self._dev is not None:
-            self._dev.__exit__(*exc)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _scratch(workspace, need: int, device):
@@ -527,6 +519,7 @@ def _scratch(workspace, need: int, device):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+@functools.lru_cache(maxsize=1024)
 def m2_lora_add_workspace_size(M: int, N: int, K: int, rank: int, n_adapters: int) -> int:
     n = _sz()
     _check(_lib.m2_lora_add_workspace_size(M, N, K, rank, n_adapters, ctypes.byref(n)))
@@ -553,13 +546,15 @@ def m2_lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
         _need(scale, "scale", torch.float32, (n_adapters,))
     if out is not None:
         _need(out, "out", torch.bfloat16, (M, N))
-    with _OnDevice(x, stream, y, a, b, row_adapter, scale, out, workspace) as on:
-        if out is None:
-            out = torch.empty_like(y)
+
+    def call(handle):
+        o = torch.empty_like(y) if out is None else out
         ws, nbytes = _scratch(workspace, m2_lora_add_workspace_size(M, N, K, rank, n_adapters), x.device)
         _check(_lib.m2_lora_add(y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(scale), n_adapters, rank,
-                                row_adapter.data_ptr(), out.data_ptr(), M, N, K, _ptr(ws), nbytes, on.stream))
-    return out
+                                row_adapter.data_ptr(), o.data_ptr(), M, N, K, _ptr(ws), nbytes, handle))
+        return o
+
+    return _on_device(x, stream, (y, a, b, row_adapter, scale, out, workspace), call)
 
 
 class BeamStep(typing.NamedTuple):
@@ -571,6 +566,7 @@ class BeamStep(typing.NamedTuple):
     done: torch.Tensor | None
 
 
+@functools.lru_cache(maxsize=1024)
 def m2_beam_select_workspace_size(batch: int, beams: int, vocab: int, k: int) -> int:
     n = _sz()
     _check(_lib.m2_beam_select_workspace_size(batch, beams, vocab, k, ctypes.byref(n)))
@@ -614,19 +610,21 @@ def m2_beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = N
             _need(out.done, "out.done", torch.bool, (batch, k))
         elif eos_token is not None:
             raise ValueError("out.done is missing (eos_token is given)")
-    with _OnDevice(logits, stream, scores, done, workspace, *(out or ())) as on:
-        dev = logits.device
-        if out is None:
-            ints = torch.empty((2, batch, k), dtype=torch.int32, device=dev)
-            out = BeamStep(ints[0], ints[1], torch.empty((batch, k), dtype=torch.float32, device=dev),
-                           None if eos_token is None else torch.empty((batch, k), dtype=torch.bool, device=dev))
+
+    def call(handle):
+        dev, shape = logits.device, (batch, k)
+        o = out if out is not None else BeamStep(
+            torch.empty(shape, dtype=torch.int32, device=dev), torch.empty(shape, dtype=torch.int32, device=dev),
+            torch.empty(shape, dtype=torch.float32, device=dev),
+            None if eos_token is None else torch.empty(shape, dtype=torch.bool, device=dev))
         ws, nbytes = _scratch(workspace, m2_beam_select_workspace_size(batch, beams, vocab, k), dev)
         _check(_lib.m2_beam_select(logits.data_ptr(), M2_DTYPE_BF16 if logits.dtype == torch.bfloat16 else M2_DTYPE_F32,
                                    row_stride, batch, beams, vocab, scores.data_ptr(), _ptr(done),
-                                   -1 if eos_token is None else eos_token, k, out.tokens.data_ptr(),
-                                   out.parents.data_ptr(), out.scores.data_ptr(), _ptr(out.done), _ptr(ws), nbytes,
-                                   on.stream))
-    return out
+                                   -1 if eos_token is None else eos_token, k, o.tokens.data_ptr(),
+                                   o.parents.data_ptr(), o.scores.data_ptr(), _ptr(o.done), _ptr(ws), nbytes, handle))
+        return o
+
+    return _on_device(logits, stream, (scores, done, workspace, *(out or ())), call)
 
 
 def m2_state_reorder(conv_pools, ssm_pools, slot_idx: torch.Tensor, parents: torch.Tensor,
@@ -657,15 +655,17 @@ def m2_state_reorder(conv_pools, ssm_pools, slot_idx: torch.Tensor, parents: tor
     _need(parents, "parents", torch.int32, (batch, beams))
     if out is not None:
         _need(out, "out", torch.int32, (batch, beams))
-    with _OnDevice(slot_idx, stream, parents, out, *conv_pools, *ssm_pools) as on:
-        if out is None:
-            out = torch.empty_like(slot_idx)
+
+    def call(handle):
+        o = torch.empty_like(slot_idx) if out is None else out
         conv = (_vp * layers)(*[t.data_ptr() for t in conv_pools])
         ssm = (_vp * layers)(*[t.data_ptr() for t in ssm_pools])
         _check(_lib.m2_state_reorder(conv, ssm, layers, M2_DTYPE_BF16 if dtype == torch.bfloat16 else M2_DTYPE_F32,
-                                     n_slots, slot_idx.data_ptr(), parents.data_ptr(), out.data_ptr(), batch, beams,
-                                     on.stream))
-    return out
+                                     n_slots, slot_idx.data_ptr(), parents.data_ptr(), o.data_ptr(), batch, beams,
+                                     handle))
+        return o
+
+    return _on_device(slot_idx, stream, (parents, out, *conv_pools, *ssm_pools), call)
 
 
 class Mamba2Stack:

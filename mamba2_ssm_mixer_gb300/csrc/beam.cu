@@ -2,9 +2,9 @@
 //   value(b, v) = score_b + x_bv - lse_b,   lse_b = log sum_u exp(x_bu)
 // in one pass over the logits x.
 //
-// k_beam_rows: a CTA takes one chunk of one row, held in registers: each warp's
-// maximum and sum of exponentials (online softmax, joined later), and the
-// chunk's k best tokens.  The k best need no sort: if every one of the 8 warps
+// k_beam_rows: a CTA takes one chunk of one row, held packed in registers: each
+// warp's maximum and sum of exponentials (online softmax, joined later), and
+// the chunk's k best tokens.  The k best need no sort: if every one of the 8 warps
 // has ceil(k / 8) threads whose own maximum is at least tau, then at least k
 // elements of the chunk are >= tau, so only those are looked at further (for
 // unordered logits a small multiple of k).  tau is the least, over the warps,
@@ -29,6 +29,7 @@ namespace {
 constexpr int kBeThreads = 256;
 constexpr int kBeWarps = kBeThreads / 32;
 constexpr int kCap = 1024;   // survivors ranked by counting
+constexpr int kCapV = 512;   // vectors with survivors among their elements
 
 struct ChunkSum {
   float m, s;   // maximum and sum of exp(x - m) of one chunk
@@ -57,18 +58,75 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// f32 pairs in one 64-bit register: one instruction for two lanes' worth.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Logits in 16-byte vectors, kept packed in registers.  Maxima ignore NaN.
 template <typename T>
-struct Elem;   // logits: vector width and widening; + 0 makes -0 a +0 (equal logits)
+struct Elem;
 template <>
 struct Elem<uint16_t> {
   static constexpr int kVec = 8;
+  static constexpr uint32_t kNegInf = 0xFF80FF80u;
   __device__ static float load(const uint16_t* p) { return bfbits2f(*p); }
+  __device__ static float at(const uint4& q, int e) {
+    const uint32_t w = e < 2 ? q.x : e < 4 ? q.y : e < 6 ? q.z : q.w;
+    return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ static float max(const uint4& q) {
+    const uint32_t m = max2(max2(q.x, q.y), max2(q.z, q.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  __device__ static void put(uint4* q, int e, uint16_t v) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(q) + e / 2;
+    *w = e & 1 ? (*w & 0xFFFFu) | ((uint32_t)v << 16) : (*w & 0xFFFF0000u) | v;
+  }
 };
 template <>
 struct Elem<float> {
   static constexpr int kVec = 4;
+  static constexpr uint32_t kNegInf = 0xFF800000u;
   __device__ static float load(const float* p) { return *p; }
+  __device__ static float at(const uint4& q, int e) {
+    return __uint_as_float(e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w);
+  }
+  __device__ static float max(const uint4& q) {
+    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
+  __device__ static void put(uint4* q, int e, float v) { reinterpret_cast<float*>(q)[e] = v; }
 };
+
+// Keeps the vectors packed: without it the compiler holds every unpacked
+// element from the sum to the selection.
+template <int VPT>
+__device__ __forceinline__ void repack(uint4 (&q)[VPT]) {
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) asm volatile("" : "+r"(q[j].x), "+r"(q[j].y), "+r"(q[j].z), "+r"(q[j].w));
+}
 
 // 16 bytes from p, whose address may sit `off` bytes past a 16-byte boundary
 // (off uniform over the row): two aligned loads and byte shifts.  Both loads
@@ -101,154 +159,224 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 }  // namespace
 
 // VPT 16-byte vectors per thread; element e of vector j of thread t is token
-// chunk * 256 VPT kVec + (256 j + t) kVec + e.
-template <typename T, int VPT>
+// split * chunk + (256 j + t) kVec + e.  kAligned: every row starts on a
+// 16-byte boundary.  Keys go to [request][rank][split][beam], the order in
+// which the merge's warps each meet every beam and every rank.
+template <typename T, int VPT, bool kAligned>
 __global__ void __launch_bounds__(kBeThreads) k_beam_rows(const T* __restrict__ logits, size_t stride, int vocab,
                                                           const float* __restrict__ scores,
-                                                          const uint8_t* __restrict__ done, int k, int splits,
-                                                          uint64_t* __restrict__ keys, ChunkSum* __restrict__ sums) {
-  constexpr int V = Elem<T>::kVec, kEl = V * VPT;
+                                                          const uint8_t* __restrict__ done, int k, int beams,
+                                                          int chunk, uint64_t* __restrict__ keys,
+                                                          ChunkSum* __restrict__ sums) {
+  using E = Elem<T>;
+  constexpr int V = E::kVec;
   __shared__ uint64_t cand[kCap];
+  __shared__ uint4 vecs[kCapV];
+  __shared__ int vec_at[kCapV];
   __shared__ float wm[kBeWarps], ws[kBeWarps];
-  __shared__ uint32_t wtau[kBeWarps];
-  __shared__ int n_cand;
+  __shared__ __align__(16) uint32_t wtau[kBeWarps];
+  __shared__ int n_vec, n_cand;
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x / splits, split = blockIdx.x % splits;
-  if (!isfinite(scores[row]) || (done && done[row])) return;   // no candidates here (the merge reads nothing either)
+  const int row = blockIdx.y, split = blockIdx.x, splits = gridDim.x;
+  const float score = scores[row];
+  const bool ended = done && done[row];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* base = logits + (size_t)row * stride;
-  const uint32_t off = (uint32_t)((uintptr_t)base & 15u);
-  const int first = split * (kBeThreads * kEl);
-  if (tid == 0) n_cand = 0;
+  const uint32_t off = kAligned ? 0u : (uint32_t)((uintptr_t)base & 15u);
+  const int first = split * chunk, end = min(vocab, first + chunk);
+  if (tid == 0) n_vec = n_cand = 0;
+  if (!isfinite(score) || ended) return;   // no candidates here (the merge reads nothing either)
 
-  float x[kEl];
-  float mx = -INFINITY;
+  uint4 q[VPT];
+  float vm[VPT], mx = -INFINITY;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int at = first + (j * kBeThreads + tid) * V;
-    if (at + V <= vocab) {
-      const uint4 q = load16(base + at, off);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (V == 8) {
-          x[j * V + 2 * e] = __uint_as_float(w[e] << 16);
-          x[j * V + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        } else {
-          x[j * V + e] = __uint_as_float(w[e]);
-        }
-      }
+    if (at + V <= end) {
+      q[j] = load16(base + at, off);
     } else {
+      q[j] = make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
 #pragma unroll
-      for (int e = 0; e < V; ++e) x[j * V + e] = at + e < vocab ? Elem<T>::load(base + at + e) : -INFINITY;
+      for (int e = 0; e < V; ++e)
+        if (at + e < end) E::put(&q[j], e, base[at + e]);
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) mx = fmaxf(mx, x[j * V + e]);   // a NaN never is the maximum
   }
-  const uint32_t om = ord32(mx + 0.f);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) vm[j] = E::max(q[j]), mx = fmaxf(mx, vm[j]);
+  const uint32_t om = ord32(mx + 0.f);   // + 0: -0 and +0 are equal logits
   const uint32_t owm = __reduce_max_sync(0xffffffffu, om);
   const float m = unord32(owm);
-  float s = 0.f;
+  // sum of exp(x - m) = 2^r sum 2^(c x - cm), cm = c m rounded, r its rounding
+  // error: one multiply-add per element, and the error of c scales x - m only
   constexpr float kLog2e = 1.4426950408889634f;
+  const float cm = m * kLog2e;
+  uint64_t acc = pair(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < kEl; ++i) s += exp2_fast((x[i] - m) * kLog2e);
-  if (isnan(s)) {   // a NaN (no candidate), a row of -inf, or +inf (takes all the probability)
+  for (int j = 0; j < VPT; ++j) {
+    const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      uint64_t x;
+      if constexpr (V == 8)
+        x = pair(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+      else
+        x = pair(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+      const float2 t = unpair(fma_pair(x, pair(kLog2e, kLog2e), pair(-cm, -cm)));
+      acc = add_pair(acc, pair(exp2_fast(t.x), exp2_fast(t.y)));
+    }
+  }
+  const float2 acc2 = unpair(acc);
+  float s = acc2.x + acc2.y;
+  const float r = fmaf(m, kLog2e, -cm);
+  s = fmaf(s, -0.6931471805599453f * r, s);
+  repack(q);
+  if (isnan(s)) {   // a NaN (no candidate), a warp of -inf, +inf (takes all the probability), c x past the f32 range
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kEl; ++i)
-      if (x[i] > -INFINITY) s += x[i] == m ? 1.f : exp2_fast((x[i] - m) * kLog2e);
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll 1
+      for (int e = 0; e < V; ++e) {
+        const float x = E::at(q[j], e);
+        if (x > -INFINITY) s += x == m ? 1.f : exp2_fast((x - m) * kLog2e);
+      }
   }
+  repack(q);
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   // the warp's ceil(k / 8)-th largest thread maximum
   uint32_t tau = owm, left = om;
-  for (int r = (k + kBeWarps - 1) / kBeWarps; r > 1; --r) {
+  for (int i = (k + kBeWarps - 1) / kBeWarps; i > 1; --i) {
     const uint32_t who = __ballot_sync(0xffffffffu, left == tau);
     if (lane == __ffs(who) - 1) left = 0;
     tau = __reduce_max_sync(0xffffffffu, left);
   }
   if (lane == 0) wm[warp] = m, ws[warp] = s, wtau[warp] = tau;
   __syncthreads();
-  uint32_t t = wtau[0];
+  const uint4 t0 = reinterpret_cast<const uint4*>(wtau)[0], t1 = reinterpret_cast<const uint4*>(wtau)[1];
+  static_assert(kBeWarps == 8, "one threshold per warp, in two vectors");
+  uint32_t t = min(min(min(t0.x, t0.y), min(t0.z, t0.w)), min(min(t1.x, t1.y), min(t1.z, t1.w)));
+  if (warp == 0) {
+    const float wmi = wm[lane & 7];
+    float M = wmi;
 #pragma unroll
-  for (int i = 1; i < kBeWarps; ++i) t = min(t, wtau[i]);
-  if (tid == 0) {
-    float M = wm[0];
+    for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float wsi = ws[lane & 7];
+    float S = wsi > 0.f ? wsi * (wmi == M ? 1.f : expf(wmi - M)) : 0.f;
 #pragma unroll
-    for (int i = 1; i < kBeWarps; ++i) M = fmaxf(M, wm[i]);
-    double S = 0.;
-    for (int i = 0; i < kBeWarps; ++i)
-      if (ws[i] > 0.f) S += (double)ws[i] * (wm[i] == M ? 1. : (double)expf(wm[i] - M));
-    sums[blockIdx.x] = ChunkSum{M, (float)S};
+    for (int o = 1; o < 8; o <<= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+    if (lane == 0) sums[row * splits + split] = ChunkSum{M, S};
   }
-  // survivors: >= tau and above -inf
-  const float low = unord32(max(t, kOrdNegInf));
-  if (mx >= low && mx > -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < kEl; ++i)
-      if (x[i] >= low && x[i] > -INFINITY) {
-        const int at = atomicAdd(&n_cand, 1);
-        const uint32_t token = (uint32_t)(first + ((i / V) * kBeThreads + tid) * V + i % V);
-        if (at < kCap) cand[at] = ((uint64_t)ord32(x[i] + 0.f) << 32) | (0xffffffffu - token);
-      }
+  if (t <= kOrdNegInf) {   // a warp has too few unmasked tokens: the k-th largest of all thread maxima
+    uint64_t* mine = cand;
+    mine[tid] = ((uint64_t)om << 32) | (uint32_t)(kBeThreads - tid);
+    __syncthreads();
+    int above = 0;
+    for (int i = 0; i < kBeThreads; ++i) above += mine[i] > mine[tid];
+    __syncthreads();
+    if (above == k - 1) wtau[0] = om;
+    __syncthreads();
+    t = wtau[0];
   }
+  // survivors: >= tau and above -inf.  First the few vectors that hold some,
+  // then their elements, one a thread (in place, each warp would step through
+  // all elements of its vectors for one lane's sake).
+  const float low = unord32(max(t, kOrdNegInf + 1u));
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+    if (vm[j] >= low) {
+      const int at = atomicAdd(&n_vec, 1);
+      if (at < kCapV) vecs[at] = q[j], vec_at[at] = first + (j * kBeThreads + tid) * V;
+    }
   __syncthreads();
-  const int n = n_cand;
-  uint64_t* out = keys + (size_t)blockIdx.x * k;
+  const int nv = n_vec;
+  if (nv <= kCapV)
+    for (int i = tid; i < nv * V; i += kBeThreads) {
+      const float x = E::load(reinterpret_cast<const T*>(vecs) + i);
+      if (x >= low) {
+        const int at = atomicAdd(&n_cand, 1);
+        const uint32_t token = (uint32_t)(vec_at[i / V] + i % V);
+        if (at < kCap) cand[at] = ((uint64_t)ord32(x + 0.f) << 32) | (0xffffffffu - token);
+      }
+    }
+  __syncthreads();
+  const int n = nv <= kCapV ? n_cand : kCap + 1;
+  const int request = row / beams;
+  uint64_t* out = keys + (size_t)request * beams * splits * k + split * beams + (row - request * beams);
+  const int next = splits * beams;   // from one rank to the next
   if (n <= kCap) {
     for (int i = tid; i < n; i += kBeThreads) {
       const uint64_t mine = cand[i];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < n; ++j) rank += cand[j] > mine;
-      if (rank < k) out[rank] = mine;
+      if (rank < k) out[(size_t)rank * next] = mine;
     }
-    for (int i = n + tid; i < k; i += kBeThreads) out[i] = 0;
+    for (int i = n + tid; i < k; i += kBeThreads) out[(size_t)i * next] = 0;
   } else {   // many equal values: the greatest key below the last one, k times
     uint64_t last = ~0ull;
-    for (int r = 0; r < k; ++r) {
+    for (int i = 0; i < k; ++i) {
+      repack(q);
       uint64_t best = 0;
 #pragma unroll
-      for (int i = 0; i < kEl; ++i)
-        if (x[i] > -INFINITY) {
-          const uint32_t token = (uint32_t)(first + ((i / V) * kBeThreads + tid) * V + i % V);
-          const uint64_t key = ((uint64_t)ord32(x[i] + 0.f) << 32) | (0xffffffffu - token);
-          if (key < last && key > best) best = key;
+      for (int j = 0; j < VPT; ++j)
+#pragma unroll 1
+        for (int e = 0; e < V; ++e) {
+          const float x = E::at(q[j], e);
+          if (x > -INFINITY) {
+            const uint32_t token = (uint32_t)(first + (j * kBeThreads + tid) * V + e);
+            const uint64_t key = ((uint64_t)ord32(x + 0.f) << 32) | (0xffffffffu - token);
+            if (key < last && key > best) best = key;
+          }
         }
       best = warp_max64(best);
       __syncthreads();
       if (lane == 0) cand[warp] = best;
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kBeWarps; ++i) best = cand[i] > best ? cand[i] : best;
-      if (tid == 0) out[r] = best;
+      for (int w = 0; w < kBeWarps; ++w) best = cand[w] > best ? cand[w] : best;
+      if (tid == 0) out[(size_t)i * next] = best;
       last = best;
     }
   }
 }
 
-// One request.  offs[b] = score_b - lse_b; a finished beam has one candidate.
+// One request.  The chunks' keys are first bounded in f32: value(b, v) lies
+// within 2^-22 (|score_b - lse_b| + |x|) of its f32 sum (f64 runs at a small
+// fraction of the f32 rate); tau is taken over the lower bounds, and only the
+// few whose upper bound reaches it are valued in 64 bits and ranked.
+constexpr int kKeep = 4;   // keys a thread holds in registers between the two looks at them
 __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict__ keys,
                                                      const ChunkSum* __restrict__ sums, const float* scores,
-                                                     const uint8_t* done, int beams, int vocab, int eos, int k,
-                                                     int splits, int32_t* __restrict__ tokens,
+                                                     const uint8_t* done, int beams, int eos, int k, int splits, int32_t* __restrict__ tokens,
                                                      int32_t* __restrict__ parents, float* out_scores,
                                                      uint8_t* out_done) {
   __shared__ double score[kBeamMaxBeams], lse[kBeamMaxBeams];
+  __shared__ float offs[kBeamMaxBeams];     // f32 of score - lse
   __shared__ float top[kBeamMaxBeams];      // the row's maximum (+inf: lse holds the log of their count)
   __shared__ int kind[kBeamMaxBeams];       // 0: no candidates, 1: live, 2: finished
-  __shared__ uint64_t wtau[32], cval[kCap], cflat[kCap];
+  __shared__ uint32_t wtau[32];
+  __shared__ uint64_t cval[kCap], cflat[kCap];
   __shared__ int n_cand;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int row0 = blockIdx.x * beams;
+  const int per = splits * k, total = beams * per;
+  const uint64_t* mykeys = keys + (size_t)row0 * per;
+  // (rows without candidates have no keys: what is read there is not used)
+  uint64_t held[kKeep];
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int c = tid + i * blockDim.x;
+    held[i] = c < total ? mykeys[c] : 0;
+  }
   if (tid == 0) n_cand = 0;
   for (int b = warp; b < beams; b += nw) {
     const float sc = scores[row0 + b];
     const bool fin = done && done[row0 + b];
     if (!isfinite(sc) || fin) {
-      if (lane == 0) kind[b] = isfinite(sc) ? 2 : 0, score[b] = (double)sc;
+      if (lane == 0) kind[b] = isfinite(sc) ? 2 : 0, score[b] = (double)sc, offs[b] = sc;
       continue;
     }
     const ChunkSum* cs = sums + (size_t)(row0 + b) * splits;
@@ -256,65 +384,91 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
     for (int i = lane; i < splits; i += 32) m = fmaxf(m, cs[i].m);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    double s = 0.;
+    float s = 0.f;
     for (int i = lane; i < splits; i += 32) {
       const ChunkSum c = cs[i];
-      if (c.s > 0.f) s += c.m == m ? (double)c.s : (double)c.s * exp((double)c.m - (double)m);
+      if (c.s > 0.f) s += c.m == m ? c.s : c.s * expf(c.m - m);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) {
-      kind[b] = s > 0. ? 1 : 0;
+      // log s = e log 2 + log f, f near 1: the f32 log's error stays below 2^-25
+      int e;
+      float f = frexpf(s, &e);
+      if (f < 0.70710678f) f *= 2.f, --e;
+      const double l = (double)e * 0.693147180559945309 + (double)logf(f) + (isinf(m) ? 0. : (double)m);
+      kind[b] = s > 0.f ? 1 : 0;
       top[b] = m;
       score[b] = (double)sc;
-      lse[b] = isinf(m) ? log(s) : (double)m + log(s);
+      lse[b] = l;
+      offs[b] = (float)((double)sc - l);
     }
   }
   __syncthreads();
 
-  const int per = splits * k, total = beams * per;
-  // candidate i: its ordered 64-bit value (0: none) and beam * vocab + token
-  auto candidate = [&](int i, uint64_t* flat) -> uint64_t {
-    const int b = i / per, j = i - b * per;
+  // candidate c with key `key`: lower and upper bound of its value as ordered
+  // f32 (0: no candidate)
+  auto bounds = [&](int c, uint64_t key, uint32_t* hi) -> uint32_t {
+    const int b = c % beams;
+    *hi = 0;
     if (kind[b] == 0) return 0;
-    if (kind[b] == 2) {
-      *flat = (uint64_t)b * vocab + eos;
-      return j == 0 ? ord64(score[b]) : 0;
-    }
-    const uint64_t key = keys[(size_t)(row0 + b) * per + j];
+    if (kind[b] == 2) return c < beams ? *hi = ord32(offs[b] + 0.f) : 0;
     if (key == 0) return 0;
-    const float x = unord32((uint32_t)(key >> 32));
-    *flat = (uint64_t)b * vocab + (0xffffffffu - (uint32_t)key);
-    if (isinf(top[b])) return x == top[b] ? ord64(score[b] - lse[b]) : 0;
-    return ord64(score[b] + ((double)x - lse[b]));
+    float x = unord32((uint32_t)(key >> 32));
+    if (isinf(top[b])) {
+      if (x != top[b]) return 0;
+      x = 0.f;
+    }
+    const float v = x + offs[b], err = 0x1p-22f * (fabsf(x) + fabsf(offs[b]));
+    *hi = ord32(v + err + 0.f);
+    return ord32(v - err + 0.f);
   };
-  uint64_t mine = 0, f = 0;
-  for (int i = tid; i < total; i += blockDim.x) {
-    const uint64_t v = candidate(i, &f);
-    mine = v > mine ? v : mine;
+  // its 64-bit value and place (beam, token), which orders like beam * vocab + token
+  auto value = [&](int c, uint64_t key, uint64_t* flat) -> uint64_t {
+    const int b = c % beams;
+    if (kind[b] == 2) {
+      *flat = ((uint64_t)b << 32) | (uint32_t)eos;
+      return ord64(score[b] + 0.);
+    }
+    *flat = ((uint64_t)b << 32) | (0xffffffffu - (uint32_t)key);
+    const double x = isinf(top[b]) ? 0. : (double)unord32((uint32_t)(key >> 32));
+    return ord64(score[b] + (x - lse[b]) + 0.);
+  };
+  uint32_t mine = 0, hi;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int c = tid + i * blockDim.x;
+    if (c < total) mine = max(mine, bounds(c, held[i], &hi));
   }
-  uint64_t tau = warp_max64(mine);
-  for (int r = (k + nw - 1) / nw; r > 1; --r) {
+  for (int c = tid + kKeep * blockDim.x; c < total; c += blockDim.x) mine = max(mine, bounds(c, mykeys[c], &hi));
+  uint32_t tau = __reduce_max_sync(0xffffffffu, mine);
+  for (int i = (k + nw - 1) / nw; i > 1; --i) {
     const uint32_t who = __ballot_sync(0xffffffffu, mine == tau);
     if (lane == __ffs(who) - 1) mine = 0;
-    tau = warp_max64(mine);
+    tau = __reduce_max_sync(0xffffffffu, mine);
   }
   if (lane == 0) wtau[warp] = tau;
   __syncthreads();
-  for (int i = 0; i < nw; ++i) tau = wtau[i] < tau ? wtau[i] : tau;
+  tau = __reduce_min_sync(0xffffffffu, lane < nw ? wtau[lane] : 0xffffffffu);
   if (tau == 0) tau = 1;
-  for (int i = tid; i < total; i += blockDim.x) {
-    const uint64_t v = candidate(i, &f);
-    if (v >= tau) {
-      const int at = atomicAdd(&n_cand, 1);
-      if (at < kCap) cval[at] = v, cflat[at] = f;
-    }
+  auto keep = [&](int c, uint64_t key) {
+    bounds(c, key, &hi);
+    if (hi < tau) return;
+    const int at = atomicAdd(&n_cand, 1);
+    uint64_t f;
+    if (at < kCap) cval[at] = value(c, key, &f), cflat[at] = f;
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int c = tid + i * blockDim.x;
+    if (c < total) keep(c, held[i]);
   }
+  for (int c = tid + kKeep * blockDim.x; c < total; c += blockDim.x) keep(c, mykeys[c]);
   __syncthreads();
   const int n = n_cand;
   const size_t o0 = (size_t)blockIdx.x * k;
   auto put = [&](int rank, uint64_t v, uint64_t flat) {
-    const int b = (int)(flat / vocab), token = (int)(flat % vocab);
+    const int b = (int)(flat >> 32), token = (int)(uint32_t)flat;
     tokens[o0 + rank] = token;
     parents[o0 + rank] = b;
     out_scores[o0 + rank] = (float)unord64(v);
@@ -336,11 +490,15 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
     for (int i = n + tid; i < k; i += blockDim.x) none(i);
   } else {   // many equal values: the best after the last one, k times
     uint64_t lv = ~0ull, lf = 0;
-    for (int r = 0; r < k; ++r) {
+    for (int i = 0; i < k; ++i) {
       uint64_t bv = 0, bf = ~0ull;
-      for (int i = tid; i < total; i += blockDim.x) {
-        const uint64_t v = candidate(i, &f);
-        if (v == 0 || v > lv || (v == lv && f <= lf)) continue;
+      for (int c = tid; c < total; c += blockDim.x) {
+        const uint64_t key = mykeys[c];
+        bounds(c, key, &hi);
+        if (hi < tau) continue;
+        uint64_t f;
+        const uint64_t v = value(c, key, &f);
+        if (v > lv || (v == lv && f <= lf)) continue;
         if (v > bv || (v == bv && f < bf)) bv = v, bf = f;
       }
 #pragma unroll
@@ -351,11 +509,11 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
       __syncthreads();
       if (lane == 0) cval[warp] = bv, cflat[warp] = bf;
       __syncthreads();
-      for (int i = 0; i < nw; ++i)
-        if (cval[i] > bv || (cval[i] == bv && cflat[i] < bf)) bv = cval[i], bf = cflat[i];
+      for (int w = 0; w < nw; ++w)
+        if (cval[w] > bv || (cval[w] == bv && cflat[w] < bf)) bv = cval[w], bf = cflat[w];
       if (tid == 0) {
-        if (bv) put(r, bv, bf);
-        else none(r);
+        if (bv) put(i, bv, bf);
+        else none(i);
       }
       lv = bv, lf = bf;
     }
@@ -364,18 +522,35 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
 
 namespace {
 
-// Tokens per chunk (a CTA's work): 8192, or fewer where that leaves SMs idle.
-int beam_chunk(int rows, int vocab, int sms) {
-  int chunk = 8192;
-  while (chunk > 2048 && (long long)rows * ((vocab + chunk - 1) / chunk) < 2ll * sms) chunk /= 2;
-  return chunk;
+// 16-byte vectors per thread and chunk: 8 (32 KB), or fewer where that leaves
+// SMs idle.
+int beam_vectors(int rows, int vocab, int vec, int sms) {
+  int vpt = 8;
+  while (vpt > 1 && (long long)rows * ((vocab + kBeThreads * vec * vpt - 1) / (kBeThreads * vec * vpt)) < 2ll * sms)
+    vpt /= 2;
+  return vpt;
 }
 
-template <typename T, int VPT>
+template <typename T, int VPT, bool kAligned>
 cudaError_t launch_rows(const void* logits, size_t stride, int rows, int vocab, const float* scores, const uint8_t* done,
-                        int k, int splits, uint64_t* keys, ChunkSum* sums, cudaStream_t st) {
-  return launch_pdl(k_beam_rows<T, VPT>, dim3((unsigned)(rows * splits)), dim3(kBeThreads), 0, st,
-                    static_cast<const T*>(logits), stride, vocab, scores, done, k, splits, keys, sums);
+                        int k, int beams, int splits, uint64_t* keys, ChunkSum* sums, cudaStream_t st) {
+  const int vec = Elem<T>::kVec, chunk = ((vocab + splits - 1) / splits + vec - 1) / vec * vec;   // even parts
+  return launch_pdl(k_beam_rows<T, VPT, kAligned>, dim3((unsigned)splits, (unsigned)rows), dim3(kBeThreads), 0, st,
+                    static_cast<const T*>(logits), stride, vocab, scores, done, k, beams, chunk, keys, sums);
+}
+
+template <typename T>
+cudaError_t launch_rows(int vpt, bool aligned, const void* logits, size_t stride, int rows, int vocab,
+                        const float* scores, const uint8_t* done, int k, int beams, int splits, uint64_t* keys,
+                        ChunkSum* sums, cudaStream_t st) {
+#define M2_BEAM_ROWS(VPT)                                                                                           \
+  return aligned ? launch_rows<T, VPT, true>(logits, stride, rows, vocab, scores, done, k, beams, splits, keys, sums, st)   \
+                 : launch_rows<T, VPT, false>(logits, stride, rows, vocab, scores, done, k, beams, splits, keys, sums, st)
+  if (vpt == 8) M2_BEAM_ROWS(8);
+  if (vpt == 4) M2_BEAM_ROWS(4);
+  if (vpt == 2) M2_BEAM_ROWS(2);
+  M2_BEAM_ROWS(1);
+#undef M2_BEAM_ROWS
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -383,28 +558,25 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 }  // namespace
 
 size_t beam_workspace_bytes(int batch, int beams, int vocab, int k) {
-  const size_t parts = (size_t)batch * beams * ((vocab + 2047) / 2048);   // the most chunks any device's rule makes
+  constexpr int kLeast = kBeThreads * Elem<float>::kVec;   // the smallest chunk: the most parts
+  const size_t parts = (size_t)batch * beams * ((vocab + kLeast - 1) / kLeast);
   return align256(parts * k * sizeof(uint64_t)) + align256(parts * sizeof(ChunkSum));
 }
 
 cudaError_t launch_beam_select(const void* logits, bool bf16, size_t stride, int batch, int beams, int vocab,
                                const float* scores, const uint8_t* done, int eos, int k, int32_t* tokens,
                                int32_t* parents, float* out_scores, uint8_t* out_done, void* ws, cudaStream_t st) {
-  const int rows = batch * beams, chunk = beam_chunk(rows, vocab, device_sm_count());
-  const int splits = (vocab + chunk - 1) / chunk;
+  const int rows = batch * beams, vec = bf16 ? 8 : 4, vpt = beam_vectors(rows, vocab, vec, device_sm_count());
+  const int chunk = kBeThreads * vec * vpt, splits = (vocab + chunk - 1) / chunk;
+  const bool aligned = (uintptr_t)logits % 16 == 0 && (rows == 1 || stride % vec == 0);
   uint64_t* keys = static_cast<uint64_t*>(ws);
   ChunkSum* sums = reinterpret_cast<ChunkSum*>(static_cast<char*>(ws) + align256((size_t)rows * splits * k * sizeof(uint64_t)));
-  cudaError_t e;
-#define M2_BEAM_ROWS(T, VPT) launch_rows<T, VPT>(logits, stride, rows, vocab, scores, done, k, splits, keys, sums, st)
-  if (bf16)
-    e = chunk == 8192 ? M2_BEAM_ROWS(uint16_t, 4) : chunk == 4096 ? M2_BEAM_ROWS(uint16_t, 2) : M2_BEAM_ROWS(uint16_t, 1);
-  else
-    e = chunk == 8192 ? M2_BEAM_ROWS(float, 8) : chunk == 4096 ? M2_BEAM_ROWS(float, 4) : M2_BEAM_ROWS(float, 2);
-#undef M2_BEAM_ROWS
+  cudaError_t e = bf16 ? launch_rows<uint16_t>(vpt, aligned, logits, stride, rows, vocab, scores, done, k, beams, splits, keys, sums, st)
+                       : launch_rows<float>(vpt, aligned, logits, stride, rows, vocab, scores, done, k, beams, splits, keys, sums, st);
   if (e != cudaSuccess) return e;
-  const int threads = beams * splits * k > 2048 ? 1024 : 256;
-  return launch_pdl(k_beam_merge, dim3((unsigned)batch), dim3(threads), 0, st, keys, sums, scores, done, beams, vocab,
-                    eos, k, splits, tokens, parents, out_scores, out_done);
+  const int threads = beams * splits * k > 1024 ? 1024 : 256;
+  return launch_pdl(k_beam_merge, dim3((unsigned)batch), dim3(threads), 0, st, keys, sums, scores, done, beams, eos, k,
+                    splits, tokens, parents, out_scores, out_done);
 }
 
 }  // namespace m2
