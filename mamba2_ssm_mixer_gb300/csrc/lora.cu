@@ -1,96 +1,820 @@
 // Low-rank adapters of many requests beside a shared projection: row m of a
 // batch names adapter a = row_adapter[m] (or none, -1) and
-//   out[m] = bf16( y[m] + s_a B_a (A_a x[m]) ),     A_a [rank, K], B_a [N, rank]
-// with y the shared projection's bf16 rows.  A_a x and the sum over the rank
-// are held in f32; out is rounded once.
+//   out[m] = bf16( y[m] + s_a B_a t ),   t = A_a x[m],   A_a [rank, K], B_a [N, rank]
+// with y the shared projection's bf16 rows.  At these ranks the products are
+// small change (2 rank (K + N) operations per row); what bounds the call is
+// reading y and writing out once, or, in a decode batch, reading each named
+// adapter once.  Two forms:
+//  - up to kFewRows rows: one kernel, one 8-CTA cluster per (up to kUnit rows
+//    of one adapter, slice of N).  Which rows share an adapter is found by
+//    each cluster itself from the batch's ids (a ballot), so there is no
+//    sorting launch and no workspace, and a shared adapter is read once per
+//    kUnit rows.  Each CTA forms rank / 8 of t's entries over all of K, hands
+//    them to the cluster through distributed shared memory, and adds its part
+//    of N.  All in f32.
+//  - more rows: k_lora_group sorts the rows by adapter into tiles of 64,
+//    k_lora_down forms t on the tensor cores (K split over CTAs, the parts
+//    added in order), k_lora_up streams y through registers in 16-byte pieces
+//    and adds B t from tensor-core fragments.
+// mma.sync is enough: the tensor work is a few per cent of the stream's time.
+// t is summed in f32 and enters the second product as two bf16 parts (its
+// rounding and the remainder, 2^-17 of it in all), so no accuracy is lost to
+// the 16-bit operands.
+#include <algorithm>
+#include <type_traits>
+
 #include "launch_util.h"
 #include "m2_kernels.h"
+#include "tc_ptx.cuh"
 
 namespace m2 {
 
+using tc::smem_u32;
+
 namespace {
+
 constexpr int kLoThreads = 256;
+constexpr int kLoWarps = kLoThreads / 32;
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// a, b as two bf16 pairs: their rounding and the remainder.  An infinite or
+// NaN value has no remainder; its rounding carries it.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t* hi, uint32_t* lo) {
+  *hi = pack_bf16x2(a, b);
+  const float ra = a - lo_f(*hi), rb = b - hi_f(*hi);
+  *lo = pack_bf16x2(isfinite(ra) ? ra : 0.f, isfinite(rb) ? rb : 0.f);
 }
 
-// t[m][j] = A_a[j] . x[m]: one warp per (row, rank index).
+__device__ __forceinline__ uint32_t lo_cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void lo_cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void lo_cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// Another CTA's copy of this CTA's shared float.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [ra];\n\t}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Up to kFewRows rows.  Grid (8 x slices of N, M), clusters of 4 along x; the
+// cluster of row m goes on if m is the first of a run of 8 among the rows of
+// its adapter.  Both products put the adapter's matrix on the 16-wide side of
+// m16n8k16 and the rows (up to 8) on the other, and take their operands
+// straight from global memory: the order of the summed index inside an MMA is
+// free, so each lane loads whole 8- or 16-byte pieces.  A x: K in 32-wide
+// blocks over the cluster's 32 warps, the parts summed in shared memory, then
+// over the CTAs' shared memories.  B t: 16 columns per warp and step, the
+// first steps' B and y on their way before t is known.
+// A decode batch is bound by reading each adapter once and by latency: 64 rows
+// with 64 adapters of rank 16 (2688 -> 10304) in 10.0 us, floor 4.4; one row
+// 3.7 us.  Clusters of 8 and of 2 took 13.2 and 11.3; a form on FMA units, with
+// ten times the instructions for unpacking, 16.8; the kernels below, with their
+// sorting launch, 30.
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kFewRows = 256;
+constexpr int kFewCluster = 4;
+constexpr int kUnit = 8;   // rows that share the reads of an adapter
+}  // namespace
+
+// NT: rank / 16 rounded up to a power of two.  kPair: y and out move two
+// columns at a time (N even, 4-byte aligned).
+template <int NT, bool kPair>
+__global__ void __launch_bounds__(kLoThreads) k_lora_few(const uint16_t* y, const uint16_t* __restrict__ x,
+                                                         const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
+                                                         const float* __restrict__ scale,
+                                                         const int32_t* __restrict__ ids, int n_adapters, int rank,
+                                                         uint16_t* out, int M, int N, int K, int* err) {
+  constexpr int kAheadF = NT == 1 ? 8 : NT == 2 ? 4 : NT == 4 ? 2 : 1;   // steps of B and y under way
+  __shared__ uint32_t same_w[kFewRows / 32];
+  __shared__ int rows_s[kUnit];
+  __shared__ __align__(16) float red[kLoWarps][NT * 128];
+  __shared__ float part[NT * 128];
+  __shared__ __align__(16) float t_s[kUnit][NT * 16 + 4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int crank = (int)lo_cluster_rank();
+  const int m = blockIdx.y;
+  const int cols16 = (N + 15) / 16;
+  const int n_lo = 16 * (int)((long long)cols16 * blockIdx.x / gridDim.x);
+  const int n_hi = min(N, 16 * (int)((long long)cols16 * (blockIdx.x + 1) / gridDim.x));
+  pdl_wait();
+  pdl_trigger();
+  const int id = ids[m];
+  const int other = tid < M ? ids[tid] : -1;
+  if (id < 0 || id >= n_adapters) {   // the same for the whole cluster
+    if (id != -1 && blockIdx.x == 0 && tid == 0) atomicOr(err, kErrAdapter);
+    if (out != y)
+      for (int n = n_lo + tid; n < n_hi; n += kLoThreads) out[(size_t)m * N + n] = y[(size_t)m * N + n];
+    return;
+  }
+  const bool mine = tid < M && other == id;
+  const uint32_t word = __ballot_sync(0xffffffffu, mine);
+  if (lane == 0) same_w[warp] = word;
+  if (tid < kUnit) rows_s[tid] = -1;
+  __syncthreads();
+  int before = 0, place = __popc(word & ((1u << lane) - 1u));   // rows of this adapter before m, before tid
+#pragma unroll
+  for (int w = 0; w < kFewRows / 32; ++w) {
+    const uint32_t v = same_w[w];
+    before += w < m / 32 ? __popc(v) : w == m / 32 ? __popc(v & ((1u << (m % 32)) - 1u)) : 0;
+    place += w < warp ? __popc(v) : 0;
+  }
+  if (before % kUnit) return;   // an earlier row's cluster takes this row along
+  if (mine && place >= before && place < before + kUnit) rows_s[place - before] = tid;
+  __syncthreads();
+  const int xrow = rows_s[g], row0 = rows_s[2 * q], row1 = rows_s[2 * q + 1];
+
+  // the first steps of B and y: step i of this warp holds columns n, n + 1
+  const uint16_t* bp = b + (size_t)id * N * rank + 4 * q;
+  uint2 bv[kAheadF][NT][2];
+  uint32_t yv[kAheadF][2];
+  auto fetch = [&](int u, int n) {
+#pragma unroll
+    for (int s = 0; s < NT; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        bv[u][s][h] = n + h < n_hi && 16 * s + 4 * q < rank
+                          ? __ldg(reinterpret_cast<const uint2*>(bp + (size_t)(n + h) * rank + 16 * s))
+                          : make_uint2(0u, 0u);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = r ? row1 : row0;
+      yv[u][r] = 0;
+      if (row >= 0) {
+        const uint16_t* yp = y + (size_t)row * N + n;
+        if constexpr (kPair) {
+          if (n < n_hi) yv[u][r] = *reinterpret_cast<const uint32_t*>(yp);
+        } else {
+          if (n < n_hi) yv[u][r] = yp[0];
+          if (n + 1 < n_hi) yv[u][r] |= (uint32_t)yp[1] << 16;
+        }
+      }
+    }
+  };
+  const int n_first = n_lo + warp * 16 + 2 * g;
+#pragma unroll
+  for (int u = 0; u < kAheadF; ++u) fetch(u, n_first + u * (16 * kLoWarps));
+
+  // t = A x: 32-wide K blocks over the cluster's warps
+  float acc[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  const uint16_t* ap = a + ((size_t)id * rank + g) * K + 8 * q;
+  const uint16_t* xp = x + (size_t)(xrow < 0 ? 0 : xrow) * K + 8 * q;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+  for (int kb = crank * kLoWarps + warp; kb * 32 < K; kb += kFewCluster * kLoWarps) {
+    const bool in = kb * 32 + 8 * q < K;
+    const uint4 xv = in && xrow >= 0 ? __ldg(reinterpret_cast<const uint4*>(xp + kb * 32)) : zero;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint16_t* p = ap + (size_t)i * 16 * K + kb * 32;
+      const uint4 a0 = in && 16 * i < rank ? __ldg(reinterpret_cast<const uint4*>(p)) : zero;
+      const uint4 a1 = in && 16 * i + 8 < rank ? __ldg(reinterpret_cast<const uint4*>(p + (size_t)8 * K)) : zero;
+      mma16816(acc[i], {a0.x, a1.x, a0.y, a1.y}, xv.x, xv.y);
+      mma16816(acc[i], {a0.z, a1.z, a0.w, a1.w}, xv.z, xv.w);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+    *reinterpret_cast<float4*>(&red[warp][i * 128 + lane * 4]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  __syncthreads();
+  for (int i = tid; i < NT * 128; i += kLoThreads) {
+    float t = red[0][i];
+#pragma unroll
+    for (int w = 1; w < kLoWarps; ++w) t += red[w][i];
+    part[i] = t;
+  }
+  const float sc = scale ? scale[id] : 1.f;
+  lo_cluster_arrive();
+  lo_cluster_wait();
+  for (int i = tid; i < NT * 128; i += kLoThreads) {
+    float v[kFewCluster];
+#pragma unroll
+    for (int r = 0; r < kFewCluster; ++r) v[r] = ld_cluster_f32(smem_u32(&part[i]), (uint32_t)r);
+    float t = v[0];
+#pragma unroll
+    for (int r = 1; r < kFewCluster; ++r) t += v[r];
+    const int l = (i >> 2) & 31, e = i & 3;   // fragment entry: rank index l / 4 (+ 8), row 2 (l % 4) (+ 1)
+    t_s[2 * (l & 3) + (e & 1)][(i >> 7) * 16 + (l >> 2) + 8 * (e >> 1)] = t * sc;
+  }
+  lo_cluster_arrive();   // (waited for at the end: no CTA leaves while its part is read)
+  __syncthreads();
+
+  // t of row g in two bf16 parts, in the order of B's pieces
+  uint32_t th[NT][2], tl[NT][2];
+#pragma unroll
+  for (int s = 0; s < NT; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(&t_s[g][16 * s + 4 * q]);
+    split_bf16x2(v.x, v.y, &th[s][0], &tl[s][0]);
+    split_bf16x2(v.z, v.w, &th[s][1], &tl[s][1]);
+  }
+  for (int n0 = n_first; n0 - 2 * g < n_hi; n0 += kAheadF * (16 * kLoWarps)) {
+#pragma unroll
+    for (int u = 0; u < kAheadF; ++u) {
+      const int n = n0 + u * (16 * kLoWarps);
+      float d[4] = {0.f, 0.f, 0.f, 0.f};   // (n, row0), (n, row1), (n + 1, row0), (n + 1, row1)
+#pragma unroll
+      for (int s = 0; s < NT; ++s) {
+        const uint32_t(&bf)[4] = {bv[u][s][0].x, bv[u][s][1].x, bv[u][s][0].y, bv[u][s][1].y};
+        mma16816(d, bf, tl[s][0], tl[s][1]);
+        mma16816(d, bf, th[s][0], th[s][1]);
+      }
+      const uint32_t y0 = yv[u][0], y1 = yv[u][1];
+      fetch(u, n + kAheadF * (16 * kLoWarps));
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = r ? row1 : row0;
+        if (row < 0 || n >= n_hi) continue;
+        const uint32_t w = r ? y1 : y0, o = pack_bf16x2(lo_f(w) + d[r], hi_f(w) + d[2 + r]);
+        uint16_t* op = out + (size_t)row * N + n;
+        if constexpr (kPair) {
+          *reinterpret_cast<uint32_t*>(op) = o;
+        } else {
+          op[0] = (uint16_t)o;
+          if (n + 1 < n_hi) op[1] = (uint16_t)(o >> 16);
+        }
+      }
+    }
+  }
+  lo_cluster_wait();
+}
+
+// ---------------------------------------------------------------------------
+// More rows: grouping by adapter.  One CTA counts the rows of each adapter
+// (bucket n_adapters: rows without one) and deals them out to tiles of up to
+// 64 rows of one bucket: tile i holds rows row_of[64 i] .. of info[i].adapter.
+// The order of rows inside a bucket varies with the atomics' order; each
+// row's result does not depend on it.
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kTile = 64;
+constexpr int kGroupThreads = 1024;
+constexpr int kRun = 8;   // consecutive rows per thread
+
+struct TileInfo {
+  int adapter, rows;   // adapter -1: rows without one
+};
+}  // namespace
+
+__global__ void __launch_bounds__(kGroupThreads) k_lora_group(const int32_t* __restrict__ ids, int n_adapters, int M,
+                                                              int32_t* __restrict__ row_of, TileInfo* __restrict__ info,
+                                                              int* __restrict__ n_tiles, int* err) {
+  extern __shared__ int lg_smem[];
+  int* cnt = lg_smem;                       // rows of each bucket
+  int* tstart = cnt + n_adapters + 1;       // its first tile
+  int* cur = tstart + n_adapters + 1;       // rows placed so far
+  __shared__ int wsum[32];
+  __shared__ int carry;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool bad = false;
+  const bool vec = ((uintptr_t)ids & 15u) == 0;
+  // A thread takes kRun consecutive rows, a warp kRun * 32: rows in runs of one
+  // adapter (the tokens of a sequence) are dealt with kRun at a time.
+  int first[kRun];   // the buckets of the first rows, kept for the placing (-1: no row)
+  auto load = [&](int r0, int (&v)[kRun]) {
+    static_assert(kRun == 8, "two 16-byte loads");
+    if (r0 + kRun <= M && vec) {
+      const int4 p = *reinterpret_cast<const int4*>(ids + r0), w = *reinterpret_cast<const int4*>(ids + r0 + 4);
+      v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = w.x, v[5] = w.y, v[6] = w.z, v[7] = w.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) v[i] = r0 + i < M ? ids[r0 + i] : -2;
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const bool in = r0 + i < M, named = v[i] >= 0 && v[i] < n_adapters;
+      bad |= in && !named && v[i] != -1;
+      v[i] = !in ? -1 : named ? v[i] : n_adapters;
+    }
+  };
+  auto one_run = [&](const int (&v)[kRun]) {
+    bool same = true;
+#pragma unroll
+    for (int i = 1; i < kRun; ++i) same &= v[i] == v[0];
+    return __all_sync(0xffffffffu, same);
+  };
+  load(tid * kRun, first);
+  for (int i = tid; i <= n_adapters; i += kGroupThreads) cnt[i] = cur[i] = 0;
+  if (tid == 0) carry = 0;
+  __syncthreads();
+  auto count = [&](int bkt, int weight) {
+    const uint32_t same = __match_any_sync(0xffffffffu, bkt);
+    if (bkt >= 0 && __ffs(same) - 1 == lane) atomicAdd(&cnt[bkt], weight * __popc(same));
+  };
+  for (int r0 = tid * kRun; r0 - lane * kRun < M; r0 += kGroupThreads * kRun) {
+    int v[kRun];
+    if (r0 == tid * kRun) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) v[i] = first[i];
+    } else {
+      load(r0, v);
+    }
+    if (one_run(v)) {
+      count(v[0], kRun);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) count(v[i], 1);
+    }
+  }
+  if (bad) atomicOr(err, kErrAdapter);
+  __syncthreads();
+  for (int i0 = 0; i0 <= n_adapters; i0 += kGroupThreads) {   // exclusive sum of the buckets' tiles
+    const int i = i0 + tid;
+    const int v = i <= n_adapters ? (cnt[i] + kTile - 1) / kTile : 0;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += t;
+    }
+    if (lane == 31) wsum[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+      int w = wsum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += t;
+      }
+      wsum[lane] = w;
+    }
+    __syncthreads();
+    if (i <= n_adapters) tstart[i] = carry + (warp ? wsum[warp - 1] : 0) + s - v;
+    __syncthreads();
+    if (tid == 0) carry += wsum[31];
+    __syncthreads();
+  }
+  if (tid == 0) *n_tiles = carry;
+  auto place = [&](int bkt, int r, auto weight) {
+    constexpr int kW = decltype(weight)::value;
+    const uint32_t same = __match_any_sync(0xffffffffu, bkt);
+    const int lead = __ffs(same) - 1;
+    int at = 0;
+    if (bkt >= 0 && lead == lane) at = atomicAdd(&cur[bkt], kW * __popc(same));
+    at = __shfl_sync(0xffffffffu, at, lead) + kW * __popc(same & ((1u << lane) - 1u));
+    if (bkt < 0) return;
+    if (kW == 8 && at % 8 == 0) {   // the run lies in one tile
+      const int tile = tstart[bkt] + at / kTile;
+      int4* to = reinterpret_cast<int4*>(row_of + (size_t)tile * kTile + at % kTile);
+      to[0] = make_int4(r, r + 1, r + 2, r + 3), to[1] = make_int4(r + 4, r + 5, r + 6, r + 7);
+      if (at % kTile == 0) info[tile] = TileInfo{bkt == n_adapters ? -1 : bkt, min(kTile, cnt[bkt] - at)};
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kW; ++i, ++at) {
+        const int tile = tstart[bkt] + at / kTile;
+        row_of[(size_t)tile * kTile + at % kTile] = r + i;
+        if (at % kTile == 0) info[tile] = TileInfo{bkt == n_adapters ? -1 : bkt, min(kTile, cnt[bkt] - at)};
+      }
+    }
+  };
+  for (int r0 = tid * kRun; r0 - lane * kRun < M; r0 += kGroupThreads * kRun) {
+    int v[kRun];
+    if (r0 == tid * kRun) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) v[i] = first[i];
+    } else {
+      load(r0, v);
+    }
+    if (one_run(v)) {
+      place(v[0], r0, std::integral_constant<int, kRun>());
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kRun; ++i) {
+        int bkt = v[0];
+#pragma unroll
+        for (int j = 1; j < kRun; ++j) bkt = i == j ? v[j] : bkt;
+        place(bkt, r0 + i, std::integral_constant<int, 1>());
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// t of a tile: 64 rows x K by the adapter's A^T, K split over `splits` CTAs.
+// Four 16-row warps x two halves of each 64-wide K block; operands by cp.async
+// into 128-byte-swizzled stages.  The parts are stored in f32 in the order of
+// k_lora_up's operand fragments, part[split][tile][16-row group][16-wide
+// step][half][lane], and added there in order.  (Adding them here through a
+// cluster's shared memory, or loading fragments straight from global memory
+// without stages, took 14.5 and 17.5 us where this takes 11.6: 8192 x 2688,
+// rank 16.)
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kDownStages = 4;
+constexpr int kDownK = 64;
+
+// 16-byte piece `c` (0..7) of 128-byte row r of a swizzled tile.
+__device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+}  // namespace
+
+// NK: 16-wide steps of the rank (rank / 16 rounded up to a power of two).
+template <int NK>
 __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a,
-                                                          const int32_t* __restrict__ ids, int n_adapters, int rank,
-                                                          int M, int K, float* __restrict__ t, int* err) {
+                                                          const int32_t* __restrict__ row_of,
+                                                          const TileInfo* __restrict__ info,
+                                                          const int* __restrict__ n_tiles, int rank, int K, int splits,
+                                                          int max_tiles, float4* __restrict__ parts) {
+  extern __shared__ __align__(128) uint8_t ld_smem[];
+  constexpr int kItems = 4 * NK * 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int at = blockIdx.x / splits, split = blockIdx.x - at * splits;
+  const int piece = tid & 7, r0 = tid >> 3;                  // this thread's pieces: rows r0 + 32 i
   pdl_wait();
   pdl_trigger();
-  const size_t w = ((size_t)blockIdx.x * kLoThreads + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w >= (size_t)M * rank) return;
-  const int m = (int)(w / rank), j = (int)(w % rank);
-  const int id = ids[m];
-  if (id < -1 || id >= n_adapters) {
-    if (lane == 0 && j == 0) atomicOr(err, kErrAdapter);
-    return;
-  }
-  if (id < 0) return;
-  const uint4* xp = reinterpret_cast<const uint4*>(x + (size_t)m * K);
-  const uint4* ap = reinterpret_cast<const uint4*>(a + ((size_t)id * rank + j) * K);
-  float acc = 0.f;
-  for (int v = lane; v < K / 8; v += 32) {
-    const uint4 xv = xp[v], av = ap[v];
-    const uint32_t xb[4] = {xv.x, xv.y, xv.z, xv.w}, ab[4] = {av.x, av.y, av.z, av.w};
+  const int have = *n_tiles;
+  const TileInfo tile = info[at];
+  int src[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      acc = fmaf(__uint_as_float(xb[e] << 16), __uint_as_float(ab[e] << 16), acc);
-      acc = fmaf(__uint_as_float(xb[e] & 0xFFFF0000u), __uint_as_float(ab[e] & 0xFFFF0000u), acc);
+  for (int i = 0; i < 2; ++i) src[i] = row_of[(size_t)at * kTile + r0 + 32 * i];
+  if (at >= have || tile.adapter < 0) return;   // (what was read past the last tile is not used)
+  const int arows = (rank + 15) & ~15;                       // rows of an A stage (the last 8 may be unused)
+  const uint32_t stage = (uint32_t)(kTile + arows) * 128;
+  const uint32_t s0 = smem_u32(ld_smem);
+  const int kblocks = (K + kDownK - 1) / kDownK;
+  const int kb0 = kblocks * split / splits, nk = kblocks * (split + 1) / splits - kb0;
+  const uint16_t* xr[2];
+  bool xin[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    xin[i] = r0 + 32 * i < tile.rows;
+    xr[i] = x + (size_t)(xin[i] ? src[i] : 0) * K + piece * 8;
+  }
+  const uint16_t* ar = a + (size_t)tile.adapter * rank * K + piece * 8;
+  auto load = [&](int kb, int s) {
+    const int k = (kb0 + kb) * kDownK;
+    const bool kin = k + piece * 8 < K;
+    const uint32_t base = s0 + s * stage;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool in = kin && xin[i];
+      cp16(base + swz(r0 + 32 * i, piece), in ? xr[i] + k : x, in);
+    }
+    for (int r = r0; r < rank; r += 32) cp16(base + kTile * 128 + swz(r, piece), kin ? ar + (size_t)r * K + k : a, kin);
+  };
+#pragma unroll
+  for (int s = 0; s < kDownStages - 1; ++s) {
+    if (s < nk) load(s, s);
+    cp_commit();
+  }
+  const int mg = warp & 3, kh = warp >> 2;
+  float acc[2 * NK][4];
+#pragma unroll
+  for (int i = 0; i < 2 * NK; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  const int am = mg * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, ac = lane >> 4;     // x fragment: row, piece
+  const int bm = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;               // A fragment: rank row, piece
+  for (int kb = 0; kb < nk; ++kb) {
+    cp_wait<kDownStages - 2>();
+    __syncthreads();
+    const int s = kb % kDownStages;
+    if (kb + kDownStages - 1 < nk) load(kb + kDownStages - 1, (kb + kDownStages - 1) % kDownStages);
+    cp_commit();
+    if (mg * 16 >= tile.rows) continue;   // no rows for this warp
+    const uint32_t xs = s0 + s * stage, as = xs + kTile * 128;
+#pragma unroll
+    for (int k16 = 0; k16 < 2; ++k16) {
+      const int c = kh * 4 + k16 * 2;
+      uint32_t af[4];
+      ldsm4(af, xs + swz(am, c + ac));
+#pragma unroll
+      for (int p = 0; p < NK; ++p)
+        if (p * 16 < rank) {
+          uint32_t bf[4];
+          ldsm4(bf, as + swz(p * 16 + bm, c + bc));
+          mma16816(acc[2 * p], af, bf[0], bf[1]);
+          if (p * 16 + 8 < rank) mma16816(acc[2 * p + 1], af, bf[2], bf[3]);
+        }
     }
   }
+  cp_wait<0>();
+  __syncthreads();
+  float4* half = reinterpret_cast<float4*>(ld_smem);   // [8-wide half of the step][16-row group][step][lane]
+  if (kh == 1) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  if (lane == 0) t[w] = acc;
+    for (int i = 0; i < 2 * NK; ++i)
+      half[(i & 1) * kItems + (mg * NK + i / 2) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  }
+  __syncthreads();
+  if (kh == 0) {
+    float4* o = parts + ((size_t)split * max_tiles + at) * kItems * 2 + (size_t)mg * NK * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < 2 * NK; ++i) {
+      const float4 w = half[(i & 1) * kItems + (mg * NK + i / 2) * 32 + lane];
+      o[i * 32] = make_float4(acc[i][0] + w.x, acc[i][1] + w.y, acc[i][2] + w.z, acc[i][3] + w.w);
+    }
+  }
 }
 
-// out[m][n] = bf16(y[m][n] + s_a sum_j t[m][j] B_a[n][j]): one thread per element.
-__global__ void __launch_bounds__(kLoThreads) k_lora_up(const uint16_t* y, const float* __restrict__ t,
-                                                        const uint16_t* __restrict__ b, const float* __restrict__ scale,
-                                                        const int32_t* __restrict__ ids, int n_adapters, int rank, int N,
+// ---------------------------------------------------------------------------
+// out of a tile and kUpCols columns: y + B t.  Column n of a 32-column group
+// sits at MMA j = (n % 8) / 2, column 2 (n / 8) + n % 2, so that a thread's
+// accumulators of the four MMAs are 8 consecutive columns: y and out move in
+// 16-byte pieces, 64 bytes of a row per four lanes.  Many small CTAs: the
+// stream runs at the copy rate when its tail is short (a pure copy in this
+// pattern: 41 CTAs per tile 6580 GB/s, 3 to 6 of them 5200 to 5600), so what a
+// CTA needs before its first load of y is two dependent reads deep.
+// ---------------------------------------------------------------------------
+namespace {
+template <int NK>
+struct Up {
+  static constexpr int kCols = NK <= 4 ? 256 : 128;
+};
+}  // namespace
+
+template <int NK, bool kVec>
+__global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : 1) k_lora_up(const uint16_t* y, const float4* __restrict__ parts, int splits, int max_tiles,
+                                                        const uint16_t* __restrict__ b,
+                                                        const float* __restrict__ scale,
+                                                        const int32_t* __restrict__ row_of,
+                                                        const TileInfo* __restrict__ info,
+                                                        const int* __restrict__ n_tiles, int rank, int N, int chunks,
                                                         uint16_t* out) {
+  extern __shared__ __align__(128) uint8_t lu_smem[];
+  constexpr int kCols = Up<NK>::kCols, kGroups = kCols / 64;   // 32-column groups per warp
+  const int at = blockIdx.x / chunks, c0 = (blockIdx.x - at * chunks) * kCols, c_hi = min(N, c0 + kCols);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3, mg = warp & 3;
   pdl_wait();
   pdl_trigger();
-  const int m = blockIdx.x, n = blockIdx.y * kLoThreads + threadIdx.x;
-  if (n >= N) return;
-  const int id = ids[m];
-  const size_t at = (size_t)m * N + n;
-  if (id < 0 || id >= n_adapters) {
-    if (out != y) out[at] = y[at];
+  const int have = *n_tiles;
+  const TileInfo tile = info[at];
+  int row[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) row[h] = row_of[(size_t)at * kTile + mg * 16 + g + 8 * h];
+  if (at >= have) return;   // (what was read past the last tile is not used)
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (mg * 16 + g + 8 * h >= tile.rows) row[h] = -1;
+  if (tile.adapter < 0) {
+    if (out == y) return;
+    for (int r = warp; r < tile.rows; r += kLoWarps) {
+      const size_t o = (size_t)row_of[(size_t)at * kTile + r] * N;
+      if constexpr (kVec) {
+        for (int c = c0 + lane * 8; c < c_hi; c += 256)
+          *reinterpret_cast<uint4*>(out + o + c) = *reinterpret_cast<const uint4*>(y + o + c);
+      } else {
+        for (int c = c0 + lane; c < c_hi; c += 32) out[o + c] = y[o + c];
+      }
+    }
     return;
   }
-  const uint4* bp = reinterpret_cast<const uint4*>(b + ((size_t)id * N + n) * rank);
-  const float* tp = t + (size_t)m * rank;
-  float acc = 0.f;
-  for (int v = 0; v < rank / 8; ++v) {
-    const uint4 bv = bp[v];
-    const uint32_t bb[4] = {bv.x, bv.y, bv.z, bv.w};
+  // y of this thread's groups (into its own slots of shared memory: all of it
+  // is asked for at once and holds no registers), then B's rows of the CTA's
+  // columns in MMA order
+  const int cw = c0 + (warp >> 2) * (kCols / 2);
+  uint4* ys = reinterpret_cast<uint4*>(lu_smem) + tid;   // [group][half][thread]
+  if constexpr (kVec) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      acc = fmaf(tp[8 * v + 2 * e], __uint_as_float(bb[e] << 16), acc);
-      acc = fmaf(tp[8 * v + 2 * e + 1], __uint_as_float(bb[e] & 0xFFFF0000u), acc);
+    for (int u = 0; u < kGroups; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = cw + u * 32 + q * 8;
+        if (row[h] >= 0 && n < c_hi) cp16(smem_u32(ys + (u * 2 + h) * kLoThreads), y + (size_t)row[h] * N + n, true);
+      }
+  }
+  const int pitch = rank * 2 + 16, rv = rank / 8;
+  uint8_t* bsm = lu_smem + (kVec ? kGroups * 2 * kLoThreads * 16 : 0);
+  const uint32_t s0 = smem_u32(bsm);
+  {
+    const uint16_t* bt = b + ((size_t)tile.adapter * N + c0) * rank;
+    for (int i = tid; i < kCols * rv; i += kLoThreads) {
+      const int n = i / rv, v = i - n * rv;
+      const int pos = (n & ~31) | ((n >> 1) & 3) << 3 | ((n >> 3) & 3) << 1 | (n & 1);
+      const bool in = c0 + n < c_hi;
+      cp16(s0 + (uint32_t)(pos * pitch + v * 16), in ? bt + (size_t)i * 8 : b, in);
+    }
+    cp_commit();
+    if (rank & 8)   // the last 16-wide step reads 8 entries past the rank: zeros
+      for (int n = tid; n < kCols; n += kLoThreads)
+        *reinterpret_cast<uint4*>(bsm + n * pitch + rank * 2) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  // t of the warp's 16 rows: the K parts in order, scaled, in two bf16 parts
+  uint32_t th[NK][4], tl[NK][4];
+  {
+    const float sc = scale ? scale[tile.adapter] : 1.f;
+    const float4* tp = parts + ((size_t)at * 4 + mg) * NK * 64 + lane;
+    const size_t next = (size_t)max_tiles * 4 * NK * 64;
+#pragma unroll
+    for (int s = 0; s < NK; ++s) {
+      float4 v[2] = {__ldg(tp + s * 64), __ldg(tp + s * 64 + 32)};
+      for (int sp = 1; sp < splits; ++sp)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 w = __ldg(tp + sp * next + s * 64 + h * 32);
+          v[h].x += w.x, v[h].y += w.y, v[h].z += w.z, v[h].w += w.w;
+        }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        split_bf16x2(v[h].x * sc, v[h].y * sc, &th[s][2 * h], &tl[s][2 * h]);
+        split_bf16x2(v[h].z * sc, v[h].w * sc, &th[s][2 * h + 1], &tl[s][2 * h + 1]);
+      }
     }
   }
-  out[at] = f2bfbits(fmaf(scale ? scale[id] : 1.f, acc, bfbits2f(y[at])));
+  cp_wait<0>();
+  __syncthreads();
+  if (mg * 16 >= tile.rows) return;   // no rows for this warp
+  const uint32_t bs = s0 + (uint32_t)((warp >> 2) * (kCols / 2) + (lane & 7) + (lane >> 4) * 8) * pitch +
+                      (uint32_t)((lane >> 3) & 1) * 16;
+#pragma unroll
+  for (int u = 0; u < kGroups; ++u) {
+    const int n = cw + u * 32 + q * 8;
+    float acc[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+    for (int s = 0; s < NK; ++s)
+      if (s * 16 < rank) {
+#pragma unroll
+        for (int jp = 0; jp < 2; ++jp) {
+          uint32_t bf[4];
+          ldsm4(bf, bs + (uint32_t)(u * 32 + jp * 16) * pitch + s * 32);
+          mma16816(acc[2 * jp], tl[s], bf[0], bf[1]);
+          mma16816(acc[2 * jp + 1], tl[s], bf[2], bf[3]);
+          mma16816(acc[2 * jp], th[s], bf[0], bf[1]);
+          mma16816(acc[2 * jp + 1], th[s], bf[2], bf[3]);
+        }
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (row[h] < 0) continue;
+      const size_t o = (size_t)row[h] * N + n;
+      if constexpr (kVec) {
+        if (n >= c_hi) continue;
+        const uint4 yv = ys[(u * 2 + h) * kLoThreads];
+        *reinterpret_cast<uint4*>(out + o) =
+            make_uint4(pack_bf16x2(lo_f(yv.x) + acc[0][2 * h], hi_f(yv.x) + acc[0][2 * h + 1]),
+                       pack_bf16x2(lo_f(yv.y) + acc[1][2 * h], hi_f(yv.y) + acc[1][2 * h + 1]),
+                       pack_bf16x2(lo_f(yv.z) + acc[2][2 * h], hi_f(yv.z) + acc[2][2 * h + 1]),
+                       pack_bf16x2(lo_f(yv.w) + acc[3][2 * h], hi_f(yv.w) + acc[3][2 * h + 1]));
+      } else {
+        uint16_t yv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) yv[j] = n + j < c_hi ? y[o + j] : (uint16_t)0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (n + j < c_hi) out[o + j] = f2bfbits(bfbits2f(yv[j]) + acc[j / 2][2 * h + (j & 1)]);
+      }
+    }
+  }
 }
+
+namespace {
+
+size_t lo_align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// No more tiles than the full ones and one partial per bucket.
+int lora_max_tiles(int M, int n_adapters) { return M / kTile + (n_adapters < M ? n_adapters + 1 : M); }
+
+int lora_steps(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+
+struct LoraWs {
+  int32_t* row_of;
+  TileInfo* info;
+  int* n_tiles;
+  float4* parts;
+  size_t total;
+};
+
+// CTAs sharing a tile's K: two per SM for the fewest tiles the rows can make.
+int lora_splits(int M, int K) {
+  const int tiles = (M + kTile - 1) / kTile, kblocks = (K + kDownK - 1) / kDownK;
+  const int s = (2 * device_sm_count() + tiles - 1) / tiles;
+  return std::min({s, 8, kblocks});
+}
+
+LoraWs carve_lora(void* base, int M, int K, int rank, int n_adapters) {
+  char* p = static_cast<char*>(base);
+  const size_t tiles = (size_t)lora_max_tiles(M, n_adapters);
+  LoraWs w;
+  size_t off = 0;
+  w.row_of = reinterpret_cast<int32_t*>(p + off), off += lo_align256(tiles * kTile * 4);
+  w.info = reinterpret_cast<TileInfo*>(p + off), off += lo_align256(tiles * sizeof(TileInfo));
+  w.n_tiles = reinterpret_cast<int*>(p + off), off += 256;
+  w.parts = reinterpret_cast<float4*>(p + off);
+  off += tiles * lora_splits(M, K) * lora_steps(rank) * 4 * 64 * sizeof(float4);
+  w.total = off;
+  return w;
+}
+
+template <int NT, bool kPair>
+cudaError_t launch_few(const uint16_t* y, const uint16_t* x, const LoraWeights& w, const int32_t* ids, uint16_t* out,
+                       int M, int N, int K, int* err, cudaStream_t st) {
+  // slices of N: enough clusters for every SM, but no less than a step of each warp
+  const int sms = device_sm_count(), least = kFewCluster * kLoWarps * 16;
+  int slices = (sms + kFewCluster * M - 1) / (kFewCluster * M);
+  const int most = (N + least - 1) / least;
+  if (slices > most) slices = most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(kFewCluster * slices), (unsigned)M);
+  cfg.blockDim = dim3(kLoThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kFewCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_lora_few<NT, kPair>, y, x, w.a, w.b, w.scale, ids, w.n_adapters, w.rank, out, M, N, K,
+                            err);
+}
+
+template <int NK>
+cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights& w, uint16_t* out, int M, int N, int K,
+                        const LoraWs& ws, int max_tiles, cudaStream_t st) {
+  const int splits = lora_splits(M, K);
+  const size_t dsm = (size_t)kDownStages * (kTile + ((w.rank + 15) & ~15)) * 128;
+  static_assert(kDownStages * (kTile + 8) * 128 >= 2 * 4 * 32 * 16, "a K half's part fits where the stages were");
+  cudaError_t e = ensure_smem_optin((const void*)k_lora_down<NK>, kDownStages * (kTile + 16 * NK) * 128);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k_lora_down<NK>, dim3((unsigned)splits * (unsigned)max_tiles), dim3(kLoThreads), dsm, st, x, w.a,
+                 ws.row_of, ws.info, ws.n_tiles, w.rank, K, splits, max_tiles, ws.parts);
+  if (e != cudaSuccess) return e;
+  constexpr int kCols = Up<NK>::kCols;
+  const int chunks = (N + kCols - 1) / kCols;
+  if ((long long)chunks * max_tiles > 0x7fffffffll) return cudaErrorInvalidValue;
+  const bool vec = N % 8 == 0 && (uintptr_t)y % 16 == 0 && (uintptr_t)out % 16 == 0;
+  const size_t usm = (size_t)kCols * (w.rank * 2 + 16) + (vec ? (size_t)kCols / 32 * kLoThreads * 16 : 0);
+  const dim3 grid((unsigned)(chunks * max_tiles));
+  const auto kernel = vec ? k_lora_up<NK, true> : k_lora_up<NK, false>;
+  if ((e = ensure_smem_optin((const void*)kernel, kCols * (32 * NK + 16) + kCols / 32 * kLoThreads * 16)) != cudaSuccess)
+    return e;
+  return launch_pdl(kernel, grid, dim3(kLoThreads), usm, st, y, ws.parts, splits, max_tiles, w.b, w.scale, ws.row_of, ws.info, ws.n_tiles, w.rank, N,
+                    chunks, out);
+}
+
+}  // namespace
 
 size_t lora_workspace_bytes(int M, int N, int K, int rank, int n_adapters) {
-  (void)N, (void)K, (void)n_adapters;
-  return (size_t)M * rank * 4;
+  (void)N;
+  return M <= kFewRows ? 0 : carve_lora(nullptr, M, K, rank, n_adapters).total;
 }
 
 cudaError_t launch_lora_add(const uint16_t* y, const uint16_t* x, const LoraWeights& w, const int32_t* ids, uint16_t* out,
                             int M, int N, int K, void* ws, int* err, cudaStream_t st, int* launches) {
   if (M == 0) return cudaSuccess;
-  float* t = static_cast<float*>(ws);
-  const unsigned blocks = (unsigned)(((size_t)M * w.rank * 32 + kLoThreads - 1) / kLoThreads);
-  cudaError_t e = launch_pdl(k_lora_down, dim3(blocks), dim3(kLoThreads), 0, st, x, w.a, ids, w.n_adapters, w.rank, M, K,
-                             t, err);
+  if (M <= kFewRows) {
+    *launches = 1;
+    const bool pair = N % 2 == 0 && (uintptr_t)y % 4 == 0 && (uintptr_t)out % 4 == 0;
+#define M2_LORA_FEW(NT)                                                            \
+  return pair ? launch_few<NT, true>(y, x, w, ids, out, M, N, K, err, st)           \
+              : launch_few<NT, false>(y, x, w, ids, out, M, N, K, err, st)
+    if (w.rank <= 16) M2_LORA_FEW(1);
+    if (w.rank <= 32) M2_LORA_FEW(2);
+    if (w.rank <= 64) M2_LORA_FEW(4);
+    M2_LORA_FEW(8);
+#undef M2_LORA_FEW
+  }
+  *launches = 3;
+  const LoraWs lw = carve_lora(ws, M, K, w.rank, w.n_adapters);
+  const size_t gsm = (size_t)3 * (w.n_adapters + 1) * 4;
+  cudaError_t e = ensure_smem_optin((const void*)k_lora_group, 3 * (kLoraMaxAdapters + 1) * 4);
   if (e != cudaSuccess) return e;
-  *launches = 2;
-  return launch_pdl(k_lora_up, dim3(M, (N + kLoThreads - 1) / kLoThreads), dim3(kLoThreads), 0, st, y, t, w.b, w.scale,
-                    ids, w.n_adapters, w.rank, N, out);
+  e = launch_pdl(k_lora_group, dim3(1), dim3(kGroupThreads), gsm, st, ids, w.n_adapters, M, lw.row_of, lw.info,
+                 lw.n_tiles, err);
+  if (e != cudaSuccess) return e;
+  const int max_tiles = lora_max_tiles(M, w.n_adapters);
+  if (w.rank <= 16) return launch_many<1>(y, x, w, out, M, N, K, lw, max_tiles, st);
+  if (w.rank <= 32) return launch_many<2>(y, x, w, out, M, N, K, lw, max_tiles, st);
+  if (w.rank <= 64) return launch_many<4>(y, x, w, out, M, N, K, lw, max_tiles, st);
+  return launch_many<8>(y, x, w, out, M, N, K, lw, max_tiles, st);
 }
 
 // Adapter of every row of a packed call: the decode rows' own, then each
