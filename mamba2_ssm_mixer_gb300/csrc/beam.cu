@@ -135,16 +135,7 @@ __device__ __forceinline__ uint4 load16(const void* p, uint32_t off) {
   const uint4* q = reinterpret_cast<const uint4*>((const char*)p - off);
   const uint4 a = __ldg(q);
   if (off == 0) return a;
-  const uint4 b = __ldg(q + 1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  const uint32_t words = off >> 2, sh = (off & 3) * 8;
-  uint32_t r[5];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) {
-    r[i] = words == 0 ? w[i] : words == 1 ? w[i + 1] : words == 2 ? w[i + 2] : w[i + 3];
-  }
-  return make_uint4(__funnelshift_r(r[0], r[1], sh), __funnelshift_r(r[1], r[2], sh),
-                    __funnelshift_r(r[2], r[3], sh), __funnelshift_r(r[3], r[4], sh));
+  return bytes16_at(a, __ldg(q + 1), off);
 }
 
 __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {

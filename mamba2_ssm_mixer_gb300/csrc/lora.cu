@@ -92,7 +92,7 @@ __device__ __forceinline__ void cp_wait() {
 // ---------------------------------------------------------------------------
 // Up to kFewRows rows.  Grid (8 x slices of N, M), clusters of 4 along x; the
 // cluster of row m goes on if m is the first of a run of 8 among the rows of
-// its adapter.  Both products put the adapter's matrix on the 16-wide side of
+// its adapter in its window of 256 rows (a ballot in every warp, no barrier).  Both products put the adapter's matrix on the 16-wide side of
 // m16n8k16 and the rows (up to 8) on the other, and take their operands
 // straight from global memory: the order of the summed index inside an MMA is
 // free, so each lane loads whole 8- or 16-byte pieces.  A x: K in 32-wide
@@ -106,7 +106,8 @@ __device__ __forceinline__ void cp_wait() {
 // sorting launch, 30.
 // ---------------------------------------------------------------------------
 namespace {
-constexpr int kFewRows = 256;
+constexpr int kFewRows = 256, kFewMost = 512;   // see few_rows
+constexpr int kWindow = 256;
 constexpr int kFewCluster = 4;
 constexpr int kUnit = 8;   // rows that share the reads of an adapter
 }  // namespace
@@ -120,7 +121,6 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_few(const uint16_t* y, cons
                                                          const int32_t* __restrict__ ids, int n_adapters, int rank,
                                                          uint16_t* out, int M, int N, int K, int* err) {
   constexpr int kAheadF = NT == 1 ? 8 : NT == 2 ? 4 : NT == 4 ? 2 : 1;   // steps of B and y under way
-  __shared__ uint32_t same_w[kFewRows / 32];
   __shared__ int rows_s[kUnit];
   __shared__ __align__(16) float red[kLoWarps][NT * 128];
   __shared__ float part[NT * 128];
@@ -133,28 +133,36 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_few(const uint16_t* y, cons
   const int n_hi = min(N, 16 * (int)((long long)cols16 * (blockIdx.x + 1) / gridDim.x));
   pdl_wait();
   pdl_trigger();
-  const int id = ids[m];
-  const int other = tid < M ? ids[tid] : -1;
+  const int id = ids[m], w0 = m - m % kWindow;
+  int other[kWindow / 32];
+#pragma unroll
+  for (int i = 0; i < kWindow / 32; ++i) other[i] = w0 + 32 * i + lane < M ? ids[w0 + 32 * i + lane] : -1;
   if (id < 0 || id >= n_adapters) {   // the same for the whole cluster
     if (id != -1 && blockIdx.x == 0 && tid == 0) atomicOr(err, kErrAdapter);
     if (out != y)
       for (int n = n_lo + tid; n < n_hi; n += kLoThreads) out[(size_t)m * N + n] = y[(size_t)m * N + n];
     return;
   }
-  const bool mine = tid < M && other == id;
-  const uint32_t word = __ballot_sync(0xffffffffu, mine);
-  if (lane == 0) same_w[warp] = word;
-  if (tid < kUnit) rows_s[tid] = -1;
-  __syncthreads();
-  int before = 0, place = __popc(word & ((1u << lane) - 1u));   // rows of this adapter before m, before tid
+  uint32_t same[kWindow / 32];
+  int before = 0;   // rows of this adapter in the window before m
 #pragma unroll
-  for (int w = 0; w < kFewRows / 32; ++w) {
-    const uint32_t v = same_w[w];
-    before += w < m / 32 ? __popc(v) : w == m / 32 ? __popc(v & ((1u << (m % 32)) - 1u)) : 0;
-    place += w < warp ? __popc(v) : 0;
+  for (int i = 0; i < kWindow / 32; ++i) {
+    same[i] = __ballot_sync(0xffffffffu, other[i] == id);
+    const int k = m - w0 - 32 * i;
+    before += __popc(same[i] & (k >= 32 ? 0xffffffffu : k > 0 ? (1u << k) - 1u : 0u));
   }
   if (before % kUnit) return;   // an earlier row's cluster takes this row along
-  if (mine && place >= before && place < before + kUnit) rows_s[place - before] = tid;
+  if (warp == 0) {   // the unit's rows: places `before` .. of the adapter's
+    if (lane < kUnit) rows_s[lane] = -1;
+    __syncwarp();
+    int base = 0;
+#pragma unroll
+    for (int i = 0; i < kWindow / 32; ++i) {
+      const int place = base + __popc(same[i] & ((1u << lane) - 1u)) - before;
+      if (((same[i] >> lane) & 1u) && place >= 0 && place < kUnit) rows_s[place] = w0 + 32 * i + lane;
+      base += __popc(same[i]);
+    }
+  }
   __syncthreads();
   const int xrow = rows_s[g], row0 = rows_s[2 * q], row1 = rows_s[2 * q + 1];
 
@@ -162,27 +170,28 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_few(const uint16_t* y, cons
   const uint16_t* bp = b + (size_t)id * N * rank + 4 * q;
   uint2 bv[kAheadF][NT][2];
   uint32_t yv[kAheadF][2];
+  // (loads are unconditional, from a valid place instead where there is none:
+  // a condition around them costs the overlap)
+  const size_t ybase0 = (size_t)(row0 < 0 ? m : row0) * N, ybase1 = (size_t)(row1 < 0 ? m : row1) * N;
   auto fetch = [&](int u, int n) {
 #pragma unroll
-    for (int s = 0; s < NT; ++s)
+    for (int h = 0; h < 2; ++h) {
+      const uint16_t* bn = bp + (size_t)(n + h < n_hi ? n + h : n_lo) * rank;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        bv[u][s][h] = n + h < n_hi && 16 * s + 4 * q < rank
-                          ? __ldg(reinterpret_cast<const uint2*>(bp + (size_t)(n + h) * rank + 16 * s))
-                          : make_uint2(0u, 0u);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = r ? row1 : row0;
-      yv[u][r] = 0;
-      if (row >= 0) {
-        const uint16_t* yp = y + (size_t)row * N + n;
-        if constexpr (kPair) {
-          if (n < n_hi) yv[u][r] = *reinterpret_cast<const uint32_t*>(yp);
-        } else {
-          if (n < n_hi) yv[u][r] = yp[0];
-          if (n + 1 < n_hi) yv[u][r] |= (uint32_t)yp[1] << 16;
-        }
+      for (int s = 0; s < NT; ++s) {
+        const bool in = 16 * s + 4 * q < rank;
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(bn + (in ? 16 * s : -4 * q)));
+        bv[u][s][h] = in ? v : make_uint2(0u, 0u);
       }
+    }
+    const int nc = n < n_hi ? n : n_lo;
+    if constexpr (kPair) {
+      yv[u][0] = *reinterpret_cast<const uint32_t*>(y + ybase0 + nc);
+      yv[u][1] = *reinterpret_cast<const uint32_t*>(y + ybase1 + nc);
+    } else {
+      const int nd = nc + 1 < n_hi ? nc + 1 : nc;
+      yv[u][0] = (uint32_t)y[ybase0 + nc] | ((uint32_t)y[ybase0 + nd] << 16);
+      yv[u][1] = (uint32_t)y[ybase1 + nc] | ((uint32_t)y[ybase1 + nd] << 16);
     }
   };
   const int n_first = n_lo + warp * 16 + 2 * g;
@@ -193,20 +202,35 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_few(const uint16_t* y, cons
   float acc[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  const uint16_t* ap = a + ((size_t)id * rank + g) * K + 8 * q;
-  const uint16_t* xp = x + (size_t)(xrow < 0 ? 0 : xrow) * K + 8 * q;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
-  for (int kb = crank * kLoWarps + warp; kb * 32 < K; kb += kFewCluster * kLoWarps) {
-    const bool in = kb * 32 + 8 * q < K;
-    const uint4 xv = in && xrow >= 0 ? __ldg(reinterpret_cast<const uint4*>(xp + kb * 32)) : zero;
+  const uint16_t* ap = a + ((size_t)id * rank + g) * K;
+  const uint16_t* xp = x + (size_t)(xrow < 0 ? m : xrow) * K;
+  constexpr int kStep = kFewCluster * kLoWarps, kBlocks = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+  for (int kb = crank * kLoWarps + warp; kb * 32 < K; kb += kBlocks * kStep) {
+    uint4 xv[kBlocks], av[kBlocks][2 * NT];
+    bool in[kBlocks];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const uint16_t* p = ap + (size_t)i * 16 * K + kb * 32;
-      const uint4 a0 = in && 16 * i < rank ? __ldg(reinterpret_cast<const uint4*>(p)) : zero;
-      const uint4 a1 = in && 16 * i + 8 < rank ? __ldg(reinterpret_cast<const uint4*>(p + (size_t)8 * K)) : zero;
-      mma16816(acc[i], {a0.x, a1.x, a0.y, a1.y}, xv.x, xv.y);
-      mma16816(acc[i], {a0.z, a1.z, a0.w, a1.w}, xv.z, xv.w);
+    for (int u = 0; u < kBlocks; ++u) {
+      const int k = (kb + u * kStep) * 32 + 8 * q;
+      in[u] = k < K;
+      const int o = in[u] ? k : 0;
+      xv[u] = __ldg(reinterpret_cast<const uint4*>(xp + o));
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i)
+        av[u][i] = __ldg(reinterpret_cast<const uint4*>(ap + (size_t)(8 * i < rank ? 8 * i : 0) * K + o));
+    }
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      if (!in[u]) {   // past K: zeros on both sides
+        xv[u] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) av[u][i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint4 a0 = av[u][2 * i], a1 = av[u][2 * i + 1];
+        mma16816(acc[i], {a0.x, a1.x, a0.y, a1.y}, xv[u].x, xv[u].y);
+        mma16816(acc[i], {a0.z, a1.z, a0.w, a1.w}, xv[u].z, xv[u].w);
+      }
     }
   }
 #pragma unroll
@@ -230,7 +254,8 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_few(const uint16_t* y, cons
 #pragma unroll
     for (int r = 1; r < kFewCluster; ++r) t += v[r];
     const int l = (i >> 2) & 31, e = i & 3;   // fragment entry: rank index l / 4 (+ 8), row 2 (l % 4) (+ 1)
-    t_s[2 * (l & 3) + (e & 1)][(i >> 7) * 16 + (l >> 2) + 8 * (e >> 1)] = t * sc;
+    const int j = (i >> 7) * 16 + (l >> 2) + 8 * (e >> 1);
+    t_s[2 * (l & 3) + (e & 1)][j] = j < rank ? t * sc : 0.f;
   }
   lo_cluster_arrive();   // (waited for at the end: no CTA leaves while its part is read)
   __syncthreads();
@@ -427,14 +452,15 @@ __global__ void __launch_bounds__(kGroupThreads) k_lora_group(const int32_t* __r
 }
 
 // ---------------------------------------------------------------------------
-// t of a tile: 64 rows x K by the adapter's A^T, K split over `splits` CTAs.
-// Four 16-row warps x two halves of each 64-wide K block; operands by cp.async
-// into 128-byte-swizzled stages.  The parts are stored in f32 in the order of
-// k_lora_up's operand fragments, part[split][tile][16-row group][16-wide
-// step][half][lane], and added there in order.  (Adding them here through a
-// cluster's shared memory, or loading fragments straight from global memory
-// without stages, took 14.5 and 17.5 us where this takes 11.6: 8192 x 2688,
-// rank 16.)
+// t of a tile: 64 rows x K by the adapter's A^T; a cluster of `splits` CTAs
+// shares a tile, each a part of K.  Four 16-row warps x two halves of each
+// 64-wide K block; operands by cp.async into 128-byte-swizzled stages.  The
+// parts are added in order (halves, then CTAs, through distributed shared
+// memory), scaled, and stored as the two bf16 parts of k_lora_up's operand
+// fragments: frag[tile][16-row group][16-wide step][part][lane].  (Loading
+// fragments straight from global memory, without stages, was a third slower;
+// handing f32 parts on to k_lora_up to add saves 3 us here and costs it more
+// from rank 32 on.)
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kDownStages = 4;
@@ -442,15 +468,28 @@ constexpr int kDownK = 64;
 
 // 16-byte piece `c` (0..7) of 128-byte row r of a swizzled tile.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [ra];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
 }  // namespace
 
 // NK: 16-wide steps of the rank (rank / 16 rounded up to a power of two).
 template <int NK>
 __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a,
+                                                          const float* __restrict__ scale,
                                                           const int32_t* __restrict__ row_of,
                                                           const TileInfo* __restrict__ info,
                                                           const int* __restrict__ n_tiles, int rank, int K, int splits,
-                                                          int max_tiles, float4* __restrict__ parts) {
+                                                          uint4* __restrict__ frag) {
   extern __shared__ __align__(128) uint8_t ld_smem[];
   constexpr int kItems = 4 * NK * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -524,20 +563,39 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
   }
   cp_wait<0>();
   __syncthreads();
-  float4* half = reinterpret_cast<float4*>(ld_smem);   // [8-wide half of the step][16-row group][step][lane]
-  if (kh == 1) {
+  float4* part = reinterpret_cast<float4*>(ld_smem);   // [K half][8-wide half of the step][16-row group][step][lane]
 #pragma unroll
-    for (int i = 0; i < 2 * NK; ++i)
-      half[(i & 1) * kItems + (mg * NK + i / 2) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  for (int i = 0; i < 2 * NK; ++i)
+    part[(kh * 2 + (i & 1)) * kItems + (mg * NK + i / 2) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  const float sc = scale ? scale[tile.adapter] : 1.f;
+  if (splits > 1) {
+    lo_cluster_arrive();
+    lo_cluster_wait();
+  } else {
+    __syncthreads();
   }
-  __syncthreads();
-  if (kh == 0) {
-    float4* o = parts + ((size_t)split * max_tiles + at) * kItems * 2 + (size_t)mg * NK * 64 + lane;
+  uint4* out = frag + (size_t)at * kItems * 2;
+  for (int i = split * kLoThreads + tid; i < kItems; i += splits * kLoThreads) {
+    float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int c = 0; c < splits; ++c)
 #pragma unroll
-    for (int i = 0; i < 2 * NK; ++i) {
-      const float4 w = half[(i & 1) * kItems + (mg * NK + i / 2) * 32 + lane];
-      o[i * 32] = make_float4(acc[i][0] + w.x, acc[i][1] + w.y, acc[i][2] + w.z, acc[i][3] + w.w);
-    }
+      for (int e = 0; e < 4; ++e) {
+        const float4 w = splits > 1 ? ld_cluster_f32x4(smem_u32(part + e * kItems + i), (uint32_t)c) : part[e * kItems + i];
+        float4& t = v[e & 1];
+        t.x += w.x, t.y += w.y, t.z += w.z, t.w += w.w;
+      }
+    uint4 hi, lo;   // rows g, g + 8 of entries 2 q, + 1; the same of 8 + 2 q, + 1
+    split_bf16x2(v[0].x * sc, v[0].y * sc, &hi.x, &lo.x);
+    split_bf16x2(v[0].z * sc, v[0].w * sc, &hi.y, &lo.y);
+    split_bf16x2(v[1].x * sc, v[1].y * sc, &hi.z, &lo.z);
+    split_bf16x2(v[1].z * sc, v[1].w * sc, &hi.w, &lo.w);
+    uint4* o = out + (size_t)(i >> 5) * 64 + (i & 31);
+    o[0] = hi;
+    o[32] = lo;
+  }
+  if (splits > 1) {   // no CTA leaves while its part is read
+    lo_cluster_arrive();
+    lo_cluster_wait();
   }
 }
 
@@ -554,17 +612,15 @@ namespace {
 template <int NK>
 struct Up {
   static constexpr int kCols = NK <= 4 ? 256 : 128;
+  static constexpr int kRowBytes = kCols * 2 + 64;   // of an unaligned row in shared memory (pieces, and no bank conflicts)
 };
 }  // namespace
 
 template <int NK, bool kVec>
-__global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : 1) k_lora_up(const uint16_t* y, const float4* __restrict__ parts, int splits, int max_tiles,
-                                                        const uint16_t* __restrict__ b,
-                                                        const float* __restrict__ scale,
-                                                        const int32_t* __restrict__ row_of,
-                                                        const TileInfo* __restrict__ info,
-                                                        const int* __restrict__ n_tiles, int rank, int N, int chunks,
-                                                        uint16_t* out) {
+__global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_lora_up(
+    const uint16_t* y, const uint4* __restrict__ frag, const uint16_t* __restrict__ b,
+    const int32_t* __restrict__ row_of, const TileInfo* __restrict__ info, const int* __restrict__ n_tiles, int rank,
+    int N, int chunks, uint16_t* out) {
   extern __shared__ __align__(128) uint8_t lu_smem[];
   constexpr int kCols = Up<NK>::kCols, kGroups = kCols / 64;   // 32-column groups per warp
   const int at = blockIdx.x / chunks, c0 = (blockIdx.x - at * chunks) * kCols, c_hi = min(N, c0 + kCols);
@@ -577,6 +633,9 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : 1) k_lora_up(const u
   int row[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) row[h] = row_of[(size_t)at * kTile + mg * 16 + g + 8 * h];
+  // (unaligned: the warp moves rows warp + 8 i of the tile, known to lane i)
+  int moved = 0;
+  if constexpr (!kVec) moved = row_of[(size_t)at * kTile + warp + kLoWarps * (lane & 7)];
   if (at >= have) return;   // (what was read past the last tile is not used)
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -594,9 +653,10 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : 1) k_lora_up(const u
     }
     return;
   }
-  // y of this thread's groups (into its own slots of shared memory: all of it
-  // is asked for at once and holds no registers), then B's rows of the CTA's
-  // columns in MMA order
+  // y, asked for at once and held by no registers.  Aligned: each thread's
+  // pieces into slots of its own.  Otherwise each row's aligned 16-byte pieces
+  // (all of which hold bytes of the row's columns) into a row of shared memory,
+  // shifted there by the warp that fetched them, and back on the way out.
   const int cw = c0 + (warp >> 2) * (kCols / 2);
   uint4* ys = reinterpret_cast<uint4*>(lu_smem) + tid;   // [group][half][thread]
   if constexpr (kVec) {
@@ -607,9 +667,19 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : 1) k_lora_up(const u
         const int n = cw + u * 32 + q * 8;
         if (row[h] >= 0 && n < c_hi) cp16(smem_u32(ys + (u * 2 + h) * kLoThreads), y + (size_t)row[h] * N + n, true);
       }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTile / kLoWarps; ++i) {
+      const int r = warp + kLoWarps * i;
+      if (r >= tile.rows) break;
+      const uintptr_t p = (uintptr_t)(y + (size_t)__shfl_sync(0xffffffffu, moved, i) * N + c0), first = p & ~(uintptr_t)15;
+      const int pieces = (int)((p + (size_t)(c_hi - c0) * 2 - first + 15) / 16);
+      for (int j = lane; j < pieces; j += 32)
+        cp16(smem_u32(lu_smem + r * Up<NK>::kRowBytes + j * 16), (const void*)(first + j * 16), true);
+    }
   }
   const int pitch = rank * 2 + 16, rv = rank / 8;
-  uint8_t* bsm = lu_smem + (kVec ? kGroups * 2 * kLoThreads * 16 : 0);
+  uint8_t* bsm = lu_smem + (kVec ? kGroups * 2 * kLoThreads * 16 : kTile * Up<NK>::kRowBytes);
   const uint32_t s0 = smem_u32(bsm);
   {
     const uint16_t* bt = b + ((size_t)tile.adapter * N + c0) * rank;
@@ -624,31 +694,27 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : 1) k_lora_up(const u
       for (int n = tid; n < kCols; n += kLoThreads)
         *reinterpret_cast<uint4*>(bsm + n * pitch + rank * 2) = make_uint4(0u, 0u, 0u, 0u);
   }
-  // t of the warp's 16 rows: the K parts in order, scaled, in two bf16 parts
-  uint32_t th[NK][4], tl[NK][4];
-  {
-    const float sc = scale ? scale[tile.adapter] : 1.f;
-    const float4* tp = parts + ((size_t)at * 4 + mg) * NK * 64 + lane;
-    const size_t next = (size_t)max_tiles * 4 * NK * 64;
+  uint4 th[NK], tl[NK];   // t of the warp's 16 rows
+  const uint4* fp = frag + ((size_t)at * 4 + mg) * NK * 64 + lane;
 #pragma unroll
-    for (int s = 0; s < NK; ++s) {
-      float4 v[2] = {__ldg(tp + s * 64), __ldg(tp + s * 64 + 32)};
-      for (int sp = 1; sp < splits; ++sp)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 w = __ldg(tp + sp * next + s * 64 + h * 32);
-          v[h].x += w.x, v[h].y += w.y, v[h].z += w.z, v[h].w += w.w;
-        }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        split_bf16x2(v[h].x * sc, v[h].y * sc, &th[s][2 * h], &tl[s][2 * h]);
-        split_bf16x2(v[h].z * sc, v[h].w * sc, &th[s][2 * h + 1], &tl[s][2 * h + 1]);
-      }
-    }
-  }
+  for (int s = 0; s < NK; ++s) th[s] = __ldg(fp + s * 64), tl[s] = __ldg(fp + s * 64 + 32);
   cp_wait<0>();
+  if constexpr (!kVec) {
+    __syncwarp();   // (the row's pieces came through all lanes)
+    uint4 v[kTile / kLoWarps];
+#pragma unroll
+    for (int i = 0; i < kTile / kLoWarps; ++i) {
+      const uint32_t mis = (uint32_t)((uintptr_t)(y + (size_t)__shfl_sync(0xffffffffu, moved, i) * N + c0) & 15u);
+      const uint4* rp = reinterpret_cast<const uint4*>(lu_smem + (warp + kLoWarps * i) * Up<NK>::kRowBytes);
+      if (lane < kCols / 8) v[i] = bytes16_at(rp[lane], rp[lane + 1], mis);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kTile / kLoWarps; ++i)
+      if (lane < kCols / 8) reinterpret_cast<uint4*>(lu_smem + (warp + kLoWarps * i) * Up<NK>::kRowBytes)[lane] = v[i];
+  }
   __syncthreads();
-  if (mg * 16 >= tile.rows) return;   // no rows for this warp
+  if (kVec && mg * 16 >= tile.rows) return;   // no rows for this warp
   const uint32_t bs = s0 + (uint32_t)((warp >> 2) * (kCols / 2) + (lane & 7) + (lane >> 4) * 8) * pitch +
                       (uint32_t)((lane >> 3) & 1) * 16;
 #pragma unroll
@@ -662,12 +728,13 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : 1) k_lora_up(const u
       if (s * 16 < rank) {
 #pragma unroll
         for (int jp = 0; jp < 2; ++jp) {
+          const uint32_t lo[4] = {tl[s].x, tl[s].y, tl[s].z, tl[s].w}, hi[4] = {th[s].x, th[s].y, th[s].z, th[s].w};
           uint32_t bf[4];
           ldsm4(bf, bs + (uint32_t)(u * 32 + jp * 16) * pitch + s * 32);
-          mma16816(acc[2 * jp], tl[s], bf[0], bf[1]);
-          mma16816(acc[2 * jp + 1], tl[s], bf[2], bf[3]);
-          mma16816(acc[2 * jp], th[s], bf[0], bf[1]);
-          mma16816(acc[2 * jp + 1], th[s], bf[2], bf[3]);
+          mma16816(acc[2 * jp], lo, bf[0], bf[1]);
+          mma16816(acc[2 * jp + 1], lo, bf[2], bf[3]);
+          mma16816(acc[2 * jp], hi, bf[0], bf[1]);
+          mma16816(acc[2 * jp + 1], hi, bf[2], bf[3]);
         }
       }
 #pragma unroll
@@ -683,13 +750,34 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : 1) k_lora_up(const u
                        pack_bf16x2(lo_f(yv.z) + acc[2][2 * h], hi_f(yv.z) + acc[2][2 * h + 1]),
                        pack_bf16x2(lo_f(yv.w) + acc[3][2 * h], hi_f(yv.w) + acc[3][2 * h + 1]));
       } else {
-        uint16_t yv[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) yv[j] = n + j < c_hi ? y[o + j] : (uint16_t)0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (n + j < c_hi) out[o + j] = f2bfbits(bfbits2f(yv[j]) + acc[j / 2][2 * h + (j & 1)]);
+        // (columns past the last are computed in place too, and not stored)
+        uint4* rp = reinterpret_cast<uint4*>(lu_smem + (mg * 16 + g + 8 * h) * Up<NK>::kRowBytes) + (n - c0) / 8;
+        const uint4 yv = *rp;
+        *rp = make_uint4(pack_bf16x2(lo_f(yv.x) + acc[0][2 * h], hi_f(yv.x) + acc[0][2 * h + 1]),
+                         pack_bf16x2(lo_f(yv.y) + acc[1][2 * h], hi_f(yv.y) + acc[1][2 * h + 1]),
+                         pack_bf16x2(lo_f(yv.z) + acc[2][2 * h], hi_f(yv.z) + acc[2][2 * h + 1]),
+                         pack_bf16x2(lo_f(yv.w) + acc[3][2 * h], hi_f(yv.w) + acc[3][2 * h + 1]));
       }
+    }
+  }
+  if constexpr (!kVec) {   // rows out, by out's aligned pieces; the ends by element
+    __syncthreads();
+    const int bytes = (c_hi - c0) * 2;
+#pragma unroll
+    for (int i = 0; i < kTile / kLoWarps; ++i) {
+      const int r = warp + kLoWarps * i;
+      if (r >= tile.rows) break;
+      uint8_t* o = reinterpret_cast<uint8_t*>(out + (size_t)__shfl_sync(0xffffffffu, moved, i) * N + c0);
+      const int mis = (int)((uintptr_t)o & 15u);
+      const uint4* rp = reinterpret_cast<const uint4*>(lu_smem + r * Up<NK>::kRowBytes);
+      // whole pieces: j = 1 .. (or 0, aligned) up to the last that ends inside
+      const int whole = (mis + bytes) / 16;
+      for (int j = lane + (mis ? 1 : 0); j < whole; j += 32)
+        *reinterpret_cast<uint4*>(o - mis + j * 16) = mis ? bytes16_at(rp[j - 1], rp[j], 16 - mis) : rp[j];
+      // the ends: lanes 0..7 the first piece's elements, 8..15 the last one's
+      const int e = lane < 8 ? 2 * lane : whole * 16 - mis + 2 * (lane - 8);
+      if (lane < 16 && e >= 0 && e < bytes && (lane < 8 ? mis && e < 16 - mis : whole > 0 || !mis))
+        *reinterpret_cast<uint16_t*>(o + e) = *reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(rp) + e);
     }
   }
 }
@@ -707,18 +795,21 @@ struct LoraWs {
   int32_t* row_of;
   TileInfo* info;
   int* n_tiles;
-  float4* parts;
+  uint4* frag;
   size_t total;
 };
 
 // CTAs sharing a tile's K: two per SM for the fewest tiles the rows can make.
 int lora_splits(int M, int K) {
   const int tiles = (M + kTile - 1) / kTile, kblocks = (K + kDownK - 1) / kDownK;
-  const int s = (2 * device_sm_count() + tiles - 1) / tiles;
-  return std::min({s, 8, kblocks});
+  #ifndef V_DT
+#define V_DT 2
+#endif
+  const int s = (V_DT * device_sm_count() + tiles - 1) / tiles;
+  return std::max(1, std::min({s, 8, kblocks / 4}));   // (four blocks each at least: the stages)
 }
 
-LoraWs carve_lora(void* base, int M, int K, int rank, int n_adapters) {
+LoraWs carve_lora(void* base, int M, int rank, int n_adapters) {
   char* p = static_cast<char*>(base);
   const size_t tiles = (size_t)lora_max_tiles(M, n_adapters);
   LoraWs w;
@@ -726,8 +817,7 @@ LoraWs carve_lora(void* base, int M, int K, int rank, int n_adapters) {
   w.row_of = reinterpret_cast<int32_t*>(p + off), off += lo_align256(tiles * kTile * 4);
   w.info = reinterpret_cast<TileInfo*>(p + off), off += lo_align256(tiles * sizeof(TileInfo));
   w.n_tiles = reinterpret_cast<int*>(p + off), off += 256;
-  w.parts = reinterpret_cast<float4*>(p + off);
-  off += tiles * lora_splits(M, K) * lora_steps(rank) * 4 * 64 * sizeof(float4);
+  w.frag = reinterpret_cast<uint4*>(p + off), off += tiles * lora_steps(rank) * 4 * 64 * sizeof(uint4);
   w.total = off;
   return w;
 }
@@ -761,36 +851,59 @@ cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights&
                         const LoraWs& ws, int max_tiles, cudaStream_t st) {
   const int splits = lora_splits(M, K);
   const size_t dsm = (size_t)kDownStages * (kTile + ((w.rank + 15) & ~15)) * 128;
-  static_assert(kDownStages * (kTile + 8) * 128 >= 2 * 4 * 32 * 16, "a K half's part fits where the stages were");
+  static_assert(kDownStages * (kTile + 8) * 128 >= 4 * 4 * 32 * 16, "the parts fit where the stages were");
   cudaError_t e = ensure_smem_optin((const void*)k_lora_down<NK>, kDownStages * (kTile + 16 * NK) * 128);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k_lora_down<NK>, dim3((unsigned)splits * (unsigned)max_tiles), dim3(kLoThreads), dsm, st, x, w.a,
-                 ws.row_of, ws.info, ws.n_tiles, w.rank, K, splits, max_tiles, ws.parts);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)splits * (unsigned)max_tiles);
+  cfg.blockDim = dim3(kLoThreads);
+  cfg.dynamicSmemBytes = dsm;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, k_lora_down<NK>, x, w.a, w.scale, (const int32_t*)ws.row_of, (const TileInfo*)ws.info,
+                         (const int*)ws.n_tiles, w.rank, K, splits, ws.frag);
   if (e != cudaSuccess) return e;
   constexpr int kCols = Up<NK>::kCols;
   const int chunks = (N + kCols - 1) / kCols;
   if ((long long)chunks * max_tiles > 0x7fffffffll) return cudaErrorInvalidValue;
   const bool vec = N % 8 == 0 && (uintptr_t)y % 16 == 0 && (uintptr_t)out % 16 == 0;
-  const size_t usm = (size_t)kCols * (w.rank * 2 + 16) + (vec ? (size_t)kCols / 32 * kLoThreads * 16 : 0);
+  constexpr int kRows = kTile * Up<NK>::kRowBytes;   // (more than the aligned form's kCols / 32 slots per thread)
+  static_assert(kRows >= kCols / 32 * kLoThreads * 16, "");
+  const size_t usm = (size_t)kCols * (w.rank * 2 + 16) + (vec ? kCols / 32 * kLoThreads * 16 : kRows);
   const dim3 grid((unsigned)(chunks * max_tiles));
   const auto kernel = vec ? k_lora_up<NK, true> : k_lora_up<NK, false>;
-  if ((e = ensure_smem_optin((const void*)kernel, kCols * (32 * NK + 16) + kCols / 32 * kLoThreads * 16)) != cudaSuccess)
+  if ((e = ensure_smem_optin((const void*)kernel, kCols * (32 * NK + 16) + kRows)) != cudaSuccess)
     return e;
-  return launch_pdl(kernel, grid, dim3(kLoThreads), usm, st, y, ws.parts, splits, max_tiles, w.b, w.scale, ws.row_of, ws.info, ws.n_tiles, w.rank, N,
+  return launch_pdl(kernel, grid, dim3(kLoThreads), usm, st, y, ws.frag, w.b, ws.row_of, ws.info, ws.n_tiles, w.rank, N,
                     chunks, out);
 }
 
 }  // namespace
 
+// Which form: units of an adapter's rows up to kFewRows rows; beyond, up to
+// kFewMost, while the adapters are so many that a 64-row tile would be nearly
+// empty.  Measured (us, units / tiles), 2688 -> 10304: rank 16, 1 adapter:
+// 64 rows 9 / 13, 256 rows 13 / 13; 64 adapters: 64 rows 11 / 30, 256 rows
+// 18 / 31, 384 rows 25 / 31; 256 adapters: 512 rows 64 / 87; 4096 -> 2688, rank
+// 64, 64 adapters: 256 rows 29 / 48, 384 rows 45 / 40.
+static bool few_rows(int M, int n_adapters) { return M <= kFewRows || (M <= kFewMost && M < 4 * n_adapters); }
+
 size_t lora_workspace_bytes(int M, int N, int K, int rank, int n_adapters) {
-  (void)N;
-  return M <= kFewRows ? 0 : carve_lora(nullptr, M, K, rank, n_adapters).total;
+  (void)N, (void)K;
+  return few_rows(M, n_adapters) ? 0 : carve_lora(nullptr, M, rank, n_adapters).total;
 }
 
 cudaError_t launch_lora_add(const uint16_t* y, const uint16_t* x, const LoraWeights& w, const int32_t* ids, uint16_t* out,
                             int M, int N, int K, void* ws, int* err, cudaStream_t st, int* launches) {
   if (M == 0) return cudaSuccess;
-  if (M <= kFewRows) {
+  if (few_rows(M, w.n_adapters)) {
     *launches = 1;
     const bool pair = N % 2 == 0 && (uintptr_t)y % 4 == 0 && (uintptr_t)out % 4 == 0;
 #define M2_LORA_FEW(NT)                                                            \
@@ -803,7 +916,7 @@ cudaError_t launch_lora_add(const uint16_t* y, const uint16_t* x, const LoraWeig
 #undef M2_LORA_FEW
   }
   *launches = 3;
-  const LoraWs lw = carve_lora(ws, M, K, w.rank, w.n_adapters);
+  const LoraWs lw = carve_lora(ws, M, w.rank, w.n_adapters);
   const size_t gsm = (size_t)3 * (w.n_adapters + 1) * 4;
   cudaError_t e = ensure_smem_optin((const void*)k_lora_group, 3 * (kLoraMaxAdapters + 1) * 4);
   if (e != cudaSuccess) return e;

@@ -48,6 +48,19 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
   return d;
 }
+// The 16 bytes that start `off` (0..15, even, the same for the whole warp)
+// bytes into the 32 of a, b.
+__device__ __forceinline__ uint4 bytes16_at(const uint4& a, const uint4& b, uint32_t off) {
+  const uint32_t sh = (off & 3) * 8;
+  auto from = [sh](uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t w4) {
+    return make_uint4(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh), __funnelshift_r(w2, w3, sh),
+                      __funnelshift_r(w3, w4, sh));
+  };
+  if (off < 4) return from(a.x, a.y, a.z, a.w, b.x);
+  if (off < 8) return from(a.y, a.z, a.w, b.x, b.y);
+  if (off < 12) return from(a.z, a.w, b.x, b.y, b.z);
+  return from(a.w, b.x, b.y, b.z, b.w);
+}
 // Round to bf16 and back (storage rounding between ops).
 __device__ __forceinline__ float round_bf16(float v) { return bfbits2f(f2bfbits(v)); }
 

@@ -72,7 +72,9 @@ def _run(x, y, a, b, scale, ids, out=None, **kw):
     (1, 10304, 2688, 16, 4), (1, 1, 16, 8, 1), (2, 2688, 4096, 8, 3), (3, 77, 48, 24, 2), (7, 203, 160, 40, 5),
     (37, 2688, 4096, 64, 9), (64, 10304, 2688, 16, 64), (65, 130, 2688, 128, 3), (128, 2688, 4096, 128, 17),
     (130, 64, 64, 8, 200), (255, 1000, 272, 32, 12), (257, 1001, 528, 56, 7), (300, 10304, 2688, 16, 3),
-    (513, 2688, 4096, 32, 2), (1000, 264, 2688, 104, 40), (2049, 136, 112, 16, 1), (5000, 33, 32, 8, 4096)])
+    (513, 2688, 4096, 32, 2), (1000, 264, 2688, 104, 40), (2049, 136, 112, 16, 1), (5000, 33, 32, 8, 4096),
+    (400, 1003, 272, 16, 120), (512, 520, 160, 72, 300), (900, 777, 1024, 24, 11), (300, 515, 96, 128, 2),
+    (700, 4099, 64, 64, 3)])
 def test_matches_the_formula(M, N, K, rank, na):
     args = _inputs(M, N, K, rank, na, M * 7 + N)
     x, y, a, b, scale, ids = args
@@ -149,7 +151,18 @@ def test_an_unknown_adapter_is_reported_and_taken_as_none(M):
 
 
 def test_unaligned_rows_of_y():
-    """y and out at an odd element offset of their buffers."""
+    """y and out at an odd element offset of their buffers, in place and with
+    an out of another alignment."""
+    for M in (5, 300):
+        x, y, a, b, scale, ids = _inputs(M, 264, 64, 16, 3, M + 9)
+        src, dst = (torch.zeros(M * 264 + 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        yd, od = src[3:3 + M * 264].view(M, 264), dst[1:1 + M * 264].view(M, 264)
+        yd.copy_(bf16_dev(y))
+        m2.m2_lora_add(yd, bf16_dev(x), bf16_dev(a), bf16_dev(b), torch.from_numpy(ids).cuda(), scale=f32_dev(scale),
+                       out=od)
+        val, err = _ref(x, y, a, b, scale, ids)
+        _check(to_np(od), val, err, y, ids)
+        assert not dst[:1].any() and not dst[1 + M * 264:].any() and torch.equal(yd, bf16_dev(y))
     for M in (5, 300):
         x, y, a, b, scale, ids = _inputs(M, 264, 64, 16, 3, M)
         buf = torch.zeros(M * 264 + 1, dtype=torch.bfloat16, device="cuda")
