@@ -140,6 +140,7 @@ enum {
   M2_STAGE_DEC_QUANT_IN = 11,  /* the same three stages inside m2_decode   */
   M2_STAGE_DEC_IN_PROJ = 12,
   M2_STAGE_DEC_OUT_PROJ = 13,
+  M2_STAGE_LORA = 14,          /* low-rank adapters beside a projection    */
   M2_NSTAGES = 16
 };
 
@@ -470,6 +471,52 @@ m2_status m2_lora_add_workspace_size(int M, int N, int K, int rank, int n_adapte
 m2_status m2_lora_add(const uint16_t* y, const uint16_t* x, const uint16_t* a_w, const uint16_t* b, const float* scale,
                       int n_adapters, int rank, const int32_t* row_adapter, uint16_t* out, int M, int N, int K,
                       void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Adapters of a block: low-rank additions to in_proj (in_a [n_adapters, rank,
+ * 2688], in_b [n_adapters, 10304, rank]), to out_proj (out_a [n_adapters,
+ * rank, 4096], out_b [n_adapters, 2688, rank]) or to both; a projection
+ * without adapters has both of its pointers NULL.  bf16, device, 16-byte
+ * aligned, caller-owned; scale f32 [n_adapters] device or NULL (1).  Limits as
+ * m2_lora_add.
+ */
+typedef struct m2_lora {
+  int n_adapters;
+  int rank;
+  const uint16_t* in_a;
+  const uint16_t* in_b;
+  const uint16_t* out_a;
+  const uint16_t* out_b;
+  const float* scale;
+} m2_lora;
+
+/*
+ * m2_prefill, m2_decode and m2_mixed with an adapter per request: after each
+ * projection of the call, its bf16 rows take m2_lora_add of the request's
+ * adapter (in_proj's on the block's bf16 input, out_proj's on the bf16 gated
+ * norm output), so a call whose requests name no adapter (-1) gives
+ * the plain call's bits.  Both arms of the block are served (m2_mixed: W8A8).
+ *   seq_adapter  int32 [nseq] host, each in [-1, n_adapters)
+ *   row_adapter  int32 [Bt] device; an id outside [-1, n_adapters) is treated
+ *                as -1 and m2_check() reports M2_EINVAL
+ * The workspace sizes come from the *_lora_workspace_size calls; everything
+ * else, and the errors, as in the plain calls.
+ */
+m2_status m2_prefill_lora_workspace_size(const m2_handle* h, const int32_t* seqlens_host, int nseq, const m2_lora* lora,
+                                         size_t* bytes);
+m2_status m2_prefill_lora(m2_handle* h, const uint16_t* hidden, const int32_t* seqlens_host, int nseq,
+                          const uint8_t* has_initial, uint16_t* conv_state, void* ssm_state, const m2_lora* lora,
+                          const int32_t* seq_adapter, uint16_t* out, void* workspace, size_t ws_bytes, void* stream);
+m2_status m2_decode_lora_workspace_size(const m2_handle* h, int Bt, const m2_lora* lora, size_t* bytes);
+m2_status m2_decode_lora(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_pool, void* ssm_pool, int n_slots,
+                         const int32_t* slot_idx, const m2_lora* lora, const int32_t* row_adapter, uint16_t* out,
+                         void* workspace, size_t ws_bytes, void* stream);
+m2_status m2_mixed_lora_workspace_size(const m2_handle* h, int Bt, const int32_t* seqlens_host, int nseq,
+                                       const m2_lora* lora, size_t* bytes);
+m2_status m2_mixed_lora(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_pool, void* ssm_pool, int n_slots,
+                        const int32_t* slot_idx, const int32_t* row_adapter, const int32_t* seqlens_host, int nseq,
+                        const uint8_t* has_initial, uint16_t* conv_state, void* ssm_state, const m2_lora* lora,
+                        const int32_t* seq_adapter, uint16_t* out, void* workspace, size_t ws_bytes, void* stream);
 
 /* Workspace bytes m2_beam_select needs. */
 m2_status m2_beam_select_workspace_size(int batch, int beams, int vocab, int k, size_t* bytes);

@@ -39,11 +39,12 @@ EXPORTED = ["m2_last_error", "m2_create", "m2_destroy", "m2_get_stats", "m2_set_
             "m2_prefill_q", "m2_decode_q", "m2_rmsnorm_residual_quant", "m2_mixed_workspace_size", "m2_mixed",
             "fp8_dequant", "bf16_linear_workspace_size", "bf16_linear", "m2_check_standalone",
             "m2_selftest_timeout", "m2_lora_add_workspace_size", "m2_lora_add", "m2_beam_select_workspace_size",
-            "m2_beam_select", "m2_state_reorder"]
+            "m2_beam_select", "m2_state_reorder", "m2_prefill_lora_workspace_size", "m2_prefill_lora",
+            "m2_decode_lora_workspace_size", "m2_decode_lora", "m2_mixed_lora_workspace_size", "m2_mixed_lora"]
 
 STAGES = ["quant_in", "in_proj", "conv", "conv_state", "ssd_cumsum", "ssd_chunk_state", "ssd_state_pass",
           "ssd_chunk_scan", "norm_quant", "out_proj", "decode_fused", "dec_quant_in", "dec_in_proj",
-          "dec_out_proj"]
+          "dec_out_proj", "lora"]
 NSTAGES = 16
 
 
@@ -76,6 +77,12 @@ class m2_stats(ctypes.Structure):
 
 class m2_taps(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "zx", "u", "dt", "y", "o", "q2")]
+
+
+class m2_lora(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int), ("rank", ctypes.c_int), ("in_a", ctypes.c_void_p),
+                ("in_b", ctypes.c_void_p), ("out_a", ctypes.c_void_p), ("out_b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
 
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -112,6 +119,13 @@ _sigs = {
     "m2_lora_add": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _i, _vp, _sz, _vp], _i),
     "m2_beam_select_workspace_size": ([_i, _i, _i, _i, ctypes.POINTER(_sz)], _i),
     "m2_beam_select": ([_vp, _i, _sz, _i, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "m2_prefill_lora_workspace_size": ([_vp, _vp, _i, ctypes.POINTER(m2_lora), ctypes.POINTER(_sz)], _i),
+    "m2_prefill_lora": ([_vp, _vp, _vp, _i, _vp, _vp, _vp, ctypes.POINTER(m2_lora), _vp, _vp, _vp, _sz, _vp], _i),
+    "m2_decode_lora_workspace_size": ([_vp, _i, ctypes.POINTER(m2_lora), ctypes.POINTER(_sz)], _i),
+    "m2_decode_lora": ([_vp, _vp, _i, _vp, _vp, _i, _vp, ctypes.POINTER(m2_lora), _vp, _vp, _vp, _sz, _vp], _i),
+    "m2_mixed_lora_workspace_size": ([_vp, _i, _vp, _i, ctypes.POINTER(m2_lora), ctypes.POINTER(_sz)], _i),
+    "m2_mixed_lora": ([_vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, ctypes.POINTER(m2_lora), _vp, _vp,
+                       _vp, _sz, _vp], _i),
     "m2_state_reorder": ([_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _vp], _i),
 }
 for _name, (_args, _ret) in _sigs.items():
@@ -167,6 +181,37 @@ def make_config(s_x: float, s_y: float, eps: float = 1e-5, chunk_size: int = 256
                      eps, s_x, s_y, arm)
 
 
+class LoraAdapters:
+    """Low-rank adapters of one block, kept on its device: for in_proj
+    in_a [n, rank, 2688] and in_b [n, 10304, rank], for out_proj out_a
+    [n, rank, 4096] and out_b [n, 2688, rank] (either pair may be None), bf16;
+    scale f32 [n] or None (1).  rank: a multiple of 8 up to 128."""
+
+    def __init__(self, in_a=None, in_b=None, out_a=None, out_b=None, scale=None):
+        if (in_a is None) != (in_b is None) or (out_a is None) != (out_b is None) or (in_a is None and out_a is None):
+            raise ValueError("a projection's adapters need both a and b, and one projection at least")
+        first = in_a if in_a is not None else out_a
+        if first.dim() != 3:
+            raise ValueError(f"a must be [n_adapters, rank, K], got {tuple(first.shape)}")
+        self.n_adapters, self.rank = first.shape[:2]
+        n, r = self.n_adapters, self.rank
+        for t, name, shape in ((in_a, "in_a", (n, r, HIDDEN)), (in_b, "in_b", (n, ZX_WIDTH, r)),
+                               (out_a, "out_a", (n, r, D_INNER)), (out_b, "out_b", (n, HIDDEN, r))):
+            if t is not None:
+                _need(t, name, torch.bfloat16, shape)
+        if scale is not None:
+            _need(scale, "scale", torch.float32, (n,))
+        self._keep = (in_a, in_b, out_a, out_b, scale)
+        self.device = first.device
+        if any(t is not None and t.device != self.device for t in self._keep):
+            raise ValueError("the adapters' tensors must be on one device")
+        self._c = m2_lora(n, r, *[_ptr(t) for t in self._keep])
+
+    @property
+    def ref(self):
+        return ctypes.byref(self._c)
+
+
 class Mamba2Mixer:
     """One mixer block.  ``weights`` maps names to CPU or CUDA tensors:
     in_proj uint8 [10304, 2688], s_w1, out_proj uint8 [2688, 4096], s_w2,
@@ -190,6 +235,7 @@ class Mamba2Mixer:
             h = ctypes.c_void_p()
             _check(_lib.m2_create(ctypes.byref(cfg), ctypes.byref(w), ctypes.byref(h)))
         self._h = h
+        self._index = self.device.index if self.device.index is not None else torch.cuda.current_device()
         self._taps = None
         self.s_x = float(weights["s_x"])   # the input quant scale (for pre-quantised inputs)
         self.arm = arm
@@ -256,6 +302,114 @@ class Mamba2Mixer:
         n = ctypes.c_size_t()
         _check(_lib.m2_decode_workspace_size(self._h, batch, ctypes.byref(n)))
         return n.value
+
+    def prefill_lora_workspace_size(self, seqlens, adapters: LoraAdapters) -> int:
+        arr = (ctypes.c_int32 * len(seqlens))(*seqlens)
+        n = ctypes.c_size_t()
+        _check(_lib.m2_prefill_lora_workspace_size(self._h, arr, len(seqlens), adapters.ref, ctypes.byref(n)))
+        return n.value
+
+    def decode_lora_workspace_size(self, batch: int, adapters: LoraAdapters) -> int:
+        n = ctypes.c_size_t()
+        _check(_lib.m2_decode_lora_workspace_size(self._h, batch, adapters.ref, ctypes.byref(n)))
+        return n.value
+
+    def mixed_lora_workspace_size(self, batch: int, seqlens, adapters: LoraAdapters) -> int:
+        arr = (ctypes.c_int32 * max(len(seqlens), 1))(*seqlens)
+        n = ctypes.c_size_t()
+        _check(_lib.m2_mixed_lora_workspace_size(self._h, batch, arr, len(seqlens), adapters.ref, ctypes.byref(n)))
+        return n.value
+
+    def _here(self, hidden, stream, others, call):
+        if hidden.device.index != self._index:
+            raise ValueError(f"hidden is on {hidden.device}, the block on cuda:{self._index}")
+        return _on_device(hidden, stream, others, call)
+
+    def prefill_lora(self, hidden, seqlens, conv_state, ssm_state, adapters: LoraAdapters, seq_adapter,
+                     has_initial=None, out=None, workspace=None, stream=None):
+        """prefill (bf16 hidden) with an adapter per sequence: seq_adapter is a
+        list of adapter numbers, -1 for none (m2_prefill_lora)."""
+        seqlens, T = list(seqlens), sum(seqlens)
+        _need(hidden, "hidden", torch.bfloat16, (T, HIDDEN))
+        _need(conv_state, "conv_state", torch.bfloat16, (len(seqlens), CONV_DIM, CONV_WIDTH - 1))
+        _need(ssm_state, "ssm_state", self.state_dtype, (len(seqlens), NHEADS, HEADDIM, D_STATE))
+        if len(seq_adapter) != len(seqlens):
+            raise ValueError(f"{len(seq_adapter)} adapter numbers for {len(seqlens)} sequences")
+        if out is not None:
+            _need(out, "out", torch.bfloat16, (T, HIDDEN))
+        arr = (ctypes.c_int32 * len(seqlens))(*seqlens)
+        ids = (ctypes.c_int32 * len(seqlens))(*[int(v) for v in seq_adapter])
+        hi = None if has_initial is None else (ctypes.c_uint8 * len(seqlens))(*[int(bool(v)) for v in has_initial])
+
+        def call(handle):
+            o = torch.empty((T, HIDDEN), dtype=torch.bfloat16, device=hidden.device) if out is None else out
+            ws, nbytes = _scratch(workspace, self.prefill_lora_workspace_size(seqlens, adapters), hidden.device)
+            _check(_lib.m2_prefill_lora(self._h, _ptr(hidden), arr, len(seqlens), hi, _ptr(conv_state), _ptr(ssm_state),
+                                        adapters.ref, ids, _ptr(o), _ptr(ws), nbytes, handle))
+            return o
+
+        return self._here(hidden, stream, (conv_state, ssm_state, out, workspace, adapters), call)
+
+    def decode_lora(self, hidden, conv_pool, ssm_pool, slot_idx, adapters: LoraAdapters, row_adapter, out=None,
+                    workspace=None, stream=None):
+        """decode (bf16 hidden) with an adapter per row: row_adapter int32 [Bt]
+        on the device, -1 for none (m2_decode_lora)."""
+        Bt, n_slots = hidden.shape[0], conv_pool.shape[0]
+        _need(hidden, "hidden", torch.bfloat16, (Bt, HIDDEN))
+        _need(conv_pool, "conv_pool", torch.bfloat16, (n_slots, CONV_DIM, CONV_WIDTH - 1))
+        _need(ssm_pool, "ssm_pool", self.state_dtype, (n_slots, NHEADS, HEADDIM, D_STATE))
+        _need(slot_idx, "slot_idx", torch.int32, (Bt,))
+        _need(row_adapter, "row_adapter", torch.int32, (Bt,))
+        if out is not None:
+            _need(out, "out", torch.bfloat16, (Bt, HIDDEN))
+
+        def call(handle):
+            o = torch.empty((Bt, HIDDEN), dtype=torch.bfloat16, device=hidden.device) if out is None else out
+            ws, nbytes = _scratch(workspace, self.decode_lora_workspace_size(Bt, adapters), hidden.device)
+            _check(_lib.m2_decode_lora(self._h, _ptr(hidden), Bt, _ptr(conv_pool), _ptr(ssm_pool), n_slots,
+                                       _ptr(slot_idx), adapters.ref, _ptr(row_adapter), _ptr(o), _ptr(ws), nbytes,
+                                       handle))
+            return o
+
+        return self._here(hidden, stream, (conv_pool, ssm_pool, slot_idx, row_adapter, out, workspace, adapters), call)
+
+    def mixed_lora(self, hidden, batch, conv_pool, ssm_pool, slot_idx, row_adapter, seqlens, conv_state, ssm_state,
+                   adapters: LoraAdapters, seq_adapter, has_initial=None, out=None, workspace=None, stream=None):
+        """mixed with an adapter per decode row (row_adapter, on the device)
+        and per prefill sequence (seq_adapter, a list) (m2_mixed_lora)."""
+        seqlens = list(seqlens)
+        R = batch + sum(seqlens)
+        _need(hidden, "hidden", torch.bfloat16, (R, HIDDEN))
+        n_slots = 0
+        if batch:
+            n_slots = conv_pool.shape[0]
+            _need(conv_pool, "conv_pool", torch.bfloat16, (n_slots, CONV_DIM, CONV_WIDTH - 1))
+            _need(ssm_pool, "ssm_pool", self.state_dtype, (n_slots, NHEADS, HEADDIM, D_STATE))
+            _need(slot_idx, "slot_idx", torch.int32, (batch,))
+            _need(row_adapter, "row_adapter", torch.int32, (batch,))
+        if seqlens:
+            _need(conv_state, "conv_state", torch.bfloat16, (len(seqlens), CONV_DIM, CONV_WIDTH - 1))
+            _need(ssm_state, "ssm_state", self.state_dtype, (len(seqlens), NHEADS, HEADDIM, D_STATE))
+        ids = list(seq_adapter or [])
+        if len(ids) != len(seqlens):
+            raise ValueError(f"{len(ids)} adapter numbers for {len(seqlens)} sequences")
+        if out is not None:
+            _need(out, "out", torch.bfloat16, (R, HIDDEN))
+        arr = (ctypes.c_int32 * max(len(seqlens), 1))(*seqlens)
+        sid = (ctypes.c_int32 * max(len(seqlens), 1))(*[int(v) for v in ids])
+        hi = None if has_initial is None else (ctypes.c_uint8 * len(seqlens))(*[int(bool(v)) for v in has_initial])
+        dec = (conv_pool, ssm_pool, slot_idx, row_adapter) if batch else (None,) * 4
+        pre = (conv_state, ssm_state) if seqlens else (None,) * 2
+
+        def call(handle):
+            o = torch.empty((R, HIDDEN), dtype=torch.bfloat16, device=hidden.device) if out is None else out
+            ws, nbytes = _scratch(workspace, self.mixed_lora_workspace_size(batch, seqlens, adapters), hidden.device)
+            _check(_lib.m2_mixed_lora(self._h, _ptr(hidden), batch, _ptr(dec[0]), _ptr(dec[1]), n_slots, _ptr(dec[2]),
+                                      _ptr(dec[3]), arr, len(seqlens), hi, _ptr(pre[0]), _ptr(pre[1]), adapters.ref,
+                                      sid, _ptr(o), _ptr(ws), nbytes, handle))
+            return o
+
+        return self._here(hidden, stream, (*dec, *pre, out, workspace, adapters), call)
 
     def prefill(self, hidden, seqlens, conv_state, ssm_state, has_initial=None, out=None, workspace=None,
                 stream=None):
@@ -680,15 +834,16 @@ class Mamba2Stack:
         assert len(blocks) == len(norm_ws) and blocks
         self.blocks, self.norm_ws, self.eps, self.fused = blocks, norm_ws, eps, fused
 
-    def _run(self, hidden, call, stream):
+    def _run(self, hidden, call, stream, fused=None):
+        fused = self.fused if fused is None else fused
         h = hidden.clone()
         out = torch.empty_like(h)
-        if self.fused:
+        if fused:
             x = torch.empty(h.shape, dtype=torch.uint8, device=h.device)
         else:
             x = torch.empty_like(h)
         for l, blk in enumerate(self.blocks):
-            if self.fused:
+            if fused:
                 m2_rmsnorm_residual_quant(h, out if l else None, self.norm_ws[l], self.eps, blk.s_x, q=x,
                                           stream=stream)
             else:
@@ -696,6 +851,54 @@ class Mamba2Stack:
             call(l, blk, x, out)
         m2_rmsnorm_residual(h, out, None, self.eps, stream=stream, norm=False)
         return h
+
+    # With adapters the blocks take their bf16 inputs (an adapter reads them),
+    # whether or not the stack is fused: the codes they quantise themselves are
+    # the ones the fused step would hand them.
+
+    def _adapters(self, adapters):
+        if len(adapters) != len(self.blocks):
+            raise ValueError(f"{len(adapters)} adapter sets for {len(self.blocks)} blocks")
+        return adapters
+
+    def decode_lora(self, hidden, conv_pools, ssm_pools, slot_idx, adapters, row_adapter, workspace=None, stream=None):
+        """decode with an adapter per row; adapters: one LoraAdapters per layer."""
+        ad = self._adapters(adapters)
+
+        def go(_):   # (the call's stream is current)
+            ws = workspace if workspace is not None else torch.empty(
+                max(b.decode_lora_workspace_size(hidden.shape[0], a) for b, a in zip(self.blocks, ad)),
+                dtype=torch.uint8, device=hidden.device)
+            return self._run(hidden, lambda l, blk, x, out: blk.decode_lora(x, conv_pools[l], ssm_pools[l], slot_idx,
+                                                                            ad[l], row_adapter, out=out, workspace=ws),
+                             None, fused=False)
+
+        return _on_device(hidden, stream, (slot_idx, row_adapter), go)
+
+    def prefill_lora(self, hidden, seqlens, conv_states, ssm_states, adapters, seq_adapter, has_initial=None,
+                     workspace=None, stream=None):
+        """prefill with an adapter per sequence; adapters: one LoraAdapters per layer."""
+        ad = self._adapters(adapters)
+
+        def go(_):
+            ws = workspace if workspace is not None else torch.empty(
+                max(b.prefill_lora_workspace_size(seqlens, a) for b, a in zip(self.blocks, ad)), dtype=torch.uint8,
+                device=hidden.device)
+            return self._run(hidden, lambda l, blk, x, out: blk.prefill_lora(x, seqlens, conv_states[l], ssm_states[l],
+                                                                             ad[l], seq_adapter,
+                                                                             has_initial=has_initial, out=out,
+                                                                             workspace=ws), None, fused=False)
+
+        return _on_device(hidden, stream, (), go)
+
+    def beam_step(self, logits, scores, conv_pools, ssm_pools, slot_idx, eos_token=None, done=None, stream=None):
+        """One step of a beam search over the stack's paged rows: selects each
+        request's best continuations (m2_beam_select, as many as beams) and
+        moves every layer's states to them (m2_state_reorder).  logits
+        [batch * beams, vocab] of the rows in slot_idx [batch, beams]; returns
+        (BeamStep, the slots for the next decode)."""
+        step = m2_beam_select(logits, scores, eos_token=eos_token, done=done, stream=stream)
+        return step, m2_state_reorder(conv_pools, ssm_pools, slot_idx, step.parents, stream=stream)
 
     def decode(self, hidden, conv_pools, ssm_pools, slot_idx, workspace=None, stream=None):
         ws = workspace if workspace is not None else torch.empty(

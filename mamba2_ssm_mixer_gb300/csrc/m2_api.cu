@@ -423,12 +423,77 @@ static m2_status copy_tap(void* dst, const void* src, size_t bytes, cudaStream_t
   return M2_OK;
 }
 
+// The adapters of one call: their weights, and where the ids of its rows, the
+// bf16 out_proj input (W8A8 keeps none otherwise) and the kernels' scratch lie
+// behind the plain call's workspace.
+struct LoraCall {
+  const m2_lora* w;
+  const int32_t* dec_ids;   // [Bt] device, decode rows
+  SeqAdapters seq;          // prefill sequences
+};
+
+struct LoraCallWs {
+  int32_t* ids;
+  uint16_t* o;
+  void* scratch;
+  size_t total;
+};
+
+static LoraCallWs carve_lora_call(void* base, size_t plain, int Bt, int T, const m2_lora* l, bool w8a16) {
+  Carve c{static_cast<char*>(base), plain};
+  LoraCallWs w;
+  const int rows = Bt + T;
+  w.ids = T > 0 ? c.take<int32_t>((size_t)rows) : nullptr;   // (a decode call uses the caller's ids)
+  w.o = l->out_a && !w8a16 ? c.take<uint16_t>((size_t)rows * kI) : nullptr;
+  const size_t s1 = l->in_a ? lora_workspace_bytes(rows, kZ, kH, l->rank, l->n_adapters) : 0;
+  const size_t s2 = l->out_a ? lora_workspace_bytes(rows, kH, kI, l->rank, l->n_adapters) : 0;
+  w.scratch = c.take<char>(s1 > s2 ? s1 : s2);
+  w.total = c.off;
+  return w;
+}
+
+static m2_status check_lora_shape(int M, int N, int K, int rank, int n_adapters, const char* who);
+
+static m2_status check_lora(const m2_lora* l, const char* who) {
+  if (!l) return fail(M2_EINVAL, "%s: lora is null", who);
+  m2_status s = check_lora_shape(0, kZ, kH, l->rank, l->n_adapters, who);
+  if (s) return s;
+  if (!l->in_a != !l->in_b || !l->out_a != !l->out_b || (!l->in_a && !l->out_a))
+    return fail(M2_EINVAL, "%s: a projection's adapters need both a and b, and one projection at least", who);
+  if ((uintptr_t)l->in_a % 16 || (uintptr_t)l->in_b % 16 || (uintptr_t)l->out_a % 16 || (uintptr_t)l->out_b % 16 ||
+      (uintptr_t)l->scale % 4)
+    return fail(M2_EINVAL, "%s: adapters must be 16-byte and scale 4-byte aligned", who);
+  return M2_OK;
+}
+
+static m2_status seq_adapters(const m2_lora* l, const int32_t* ids, int nseq, SeqAdapters* out, const char* who) {
+  if (!ids) return fail(M2_EINVAL, "%s: seq_adapter is null", who);
+  for (int i = 0; i < nseq; ++i) {
+    if (ids[i] < -1 || ids[i] >= l->n_adapters)
+      return fail(M2_EINVAL, "%s: seq_adapter[%d] = %d not in [-1, %d)", who, i, ids[i], l->n_adapters);
+    out->id[i] = ids[i];
+  }
+  return M2_OK;
+}
+
+// zx += s B (A hidden), and out += s B (A o).
+static cudaError_t lora_in(m2_handle* h, const LoraCall& lc, const uint16_t* hidden, const int32_t* ids, uint16_t* zx,
+                           int rows, void* scratch, cudaStream_t st, int* nl) {
+  const LoraWeights w{lc.w->n_adapters, lc.w->rank, lc.w->in_a, lc.w->in_b, lc.w->scale};
+  return launch_lora_add(zx, hidden, w, ids, zx, rows, kZ, kH, scratch, h->err, st, nl);
+}
+static cudaError_t lora_out(m2_handle* h, const LoraCall& lc, const uint16_t* o, const int32_t* ids, uint16_t* out,
+                            int rows, void* scratch, cudaStream_t st, int* nl) {
+  const LoraWeights w{lc.w->n_adapters, lc.w->rank, lc.w->out_a, lc.w->out_b, lc.w->scale};
+  return launch_lora_add(out, o, w, ids, out, rows, kH, kI, scratch, h->err, st, nl);
+}
+
 // The block's prefill from bf16 hidden (quantised here) or from hidden_q,
 // already quantised with the handle's s_x (exactly one of the two given).
 static m2_status prefill_impl(m2_handle* h, const uint16_t* hidden, const uint8_t* hidden_q,
                               const int32_t* seqlens_host, int nseq, const uint8_t* has_initial,
                               uint16_t* conv_state, void* ssm_state, uint16_t* out, void* workspace,
-                              size_t ws_bytes, void* stream) {
+                              size_t ws_bytes, void* stream, const LoraCall* lc = nullptr) {
   g_err.clear();
   if (!h || (!hidden && !hidden_q) || !conv_state || !ssm_state || !out || !workspace)
     return fail(M2_EINVAL, "m2_prefill: null argument");
@@ -445,6 +510,12 @@ static m2_status prefill_impl(m2_handle* h, const uint16_t* hidden, const uint8_
   PrefillWs w = carve_prefill(workspace, T, local.total_chunks, w8a16);
   if (ws_bytes < w.total)
     return fail(M2_ENOMEM, "m2_prefill: workspace %zu bytes < %zu needed", ws_bytes, w.total);
+  LoraCallWs lw{};
+  if (lc) {
+    lw = carve_lora_call(workspace, w.total, 0, T, lc->w, w8a16);
+    if (ws_bytes < lw.total)
+      return fail(M2_ENOMEM, "m2_prefill_lora: workspace %zu bytes < %zu needed", ws_bytes, lw.total);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const BlockParams bp = h->params();
   const float sc1 = h->cfg.s_x * h->s_w1, sc2 = h->cfg.s_y * h->s_w2;
@@ -459,6 +530,11 @@ static m2_status prefill_impl(m2_handle* h, const uint16_t* hidden, const uint8_
       M2_STAGE(h, st, M2_STAGE_QUANT_IN, 1, launch_quant_e4m3(hidden, (size_t)T * kH, h->cfg.s_x, w.q, st));
     M2_STAGE(h, st, M2_STAGE_IN_PROJ, nl,
              gemm_fp8(q, h->in_proj, w.zx, T, kZ, kH, sc1, w.gemm_ws, w.gemm_ws_bytes, h->err, st, &nl, true));
+  }
+  if (lc) {
+    M2_STAGE(h, st, M2_STAGE_LORA, 1, launch_lora_row_ids(nullptr, 0, local, lc->seq, lw.ids, st));
+    if (lc->w->in_a)
+      M2_STAGE(h, st, M2_STAGE_LORA, nl, lora_in(h, *lc, hidden, lw.ids, w.zx, T, lw.scratch, st, &nl));
   }
   const bool recur = max_seqlen(local) <= kRecMaxT;
   const bool bf16_state = h->cfg.ssm_dtype == M2_DTYPE_BF16;
@@ -497,15 +573,19 @@ static m2_status prefill_impl(m2_handle* h, const uint16_t* hidden, const uint8_
              gemm_bf16(w.o, h->out_proj_bf16, out, T, kH, kI, 1.0f, w.gemm_ws, w.gemm_ws_bytes, h->err, st, &nl, true));
   } else {
     M2_STAGE(h, st, M2_STAGE_NORM_QUANT, 1,
-             launch_gated_norm_quant(w.y, w.zx, bp, T, w.q2, h->taps_on ? h->taps.o : nullptr, st));
+             launch_gated_norm_quant(w.y, w.zx, bp, T, w.q2, lw.o ? lw.o : h->taps_on ? h->taps.o : nullptr, st));
     M2_STAGE(h, st, M2_STAGE_OUT_PROJ, nl,
              gemm_fp8(w.q2, h->out_proj, out, T, kH, kI, sc2, w.gemm_ws, w.gemm_ws_bytes, h->err, st, &nl, true));
   }
+  if (lc && lc->w->out_a)
+    M2_STAGE(h, st, M2_STAGE_LORA, nl,
+             lora_out(h, *lc, w8a16 ? w.o : lw.o, lw.ids, out, T, lw.scratch, st, &nl));
   if (h->taps_on) {
     if (w8a16) {
       if ((s = copy_tap(h->taps.o, w.o, (size_t)T * kI * 2, st))) return s;
     } else {
       if ((s = copy_tap(h->taps.q, q, (size_t)T * kH, st))) return s;
+      if (lw.o && (s = copy_tap(h->taps.o, lw.o, (size_t)T * kI * 2, st))) return s;
     }
     if ((s = copy_tap(h->taps.zx, w.zx, (size_t)T * kZ * 2, st))) return s;
     if ((s = copy_tap(h->taps.u, w.u, (size_t)T * kConv * 2, st))) return s;
@@ -532,6 +612,33 @@ m2_status m2_prefill_q(m2_handle* h, const uint8_t* hidden_q, const int32_t* seq
   if (!hidden_q) return fail(M2_EINVAL, "m2_prefill_q: null argument");
   return prefill_impl(h, nullptr, hidden_q, seqlens_host, nseq, has_initial, conv_state, ssm_state, out, workspace,
                       ws_bytes, stream);
+}
+
+m2_status m2_prefill_lora_workspace_size(const m2_handle* h, const int32_t* seqlens_host, int nseq, const m2_lora* lora,
+                                         size_t* bytes) {
+  if (!h || !bytes) return fail(M2_EINVAL, "m2_prefill_lora_workspace_size: null argument");
+  m2_status s = check_lora(lora, "m2_prefill_lora_workspace_size");
+  if (s) return s;
+  SeqInfo si;
+  if ((s = build_seqinfo(seqlens_host, nseq, nullptr, &si))) return s;
+  const size_t plain = carve_prefill(nullptr, si.total_tokens, si.total_chunks, h->w8a16()).total;
+  *bytes = carve_lora_call(nullptr, plain, 0, si.total_tokens, lora, h->w8a16()).total;
+  return M2_OK;
+}
+
+m2_status m2_prefill_lora(m2_handle* h, const uint16_t* hidden, const int32_t* seqlens_host, int nseq,
+                          const uint8_t* has_initial, uint16_t* conv_state, void* ssm_state, const m2_lora* lora,
+                          const int32_t* seq_adapter, uint16_t* out, void* workspace, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  if (!hidden) return fail(M2_EINVAL, "m2_prefill_lora: null argument");
+  if (nseq < 1 || nseq > kMaxSeq) return fail(M2_ESHAPE, "m2_prefill_lora: nseq %d not in [1, %d]", nseq, kMaxSeq);
+  m2_status s = check_lora(lora, "m2_prefill_lora");
+  if (s) return s;
+  LoraCall lc{};
+  lc.w = lora;
+  if ((s = seq_adapters(lora, seq_adapter, nseq, &lc.seq, "m2_prefill_lora"))) return s;
+  return prefill_impl(h, hidden, nullptr, seqlens_host, nseq, has_initial, conv_state, ssm_state, out, workspace,
+                      ws_bytes, stream, &lc);
 }
 
 // ---------------------------------------------------------------- decode
@@ -570,7 +677,8 @@ m2_status m2_decode_workspace_size(const m2_handle* h, int Bt, size_t* bytes) {
 
 static m2_status decode_impl(m2_handle* h, const uint16_t* hidden, const uint8_t* hidden_q, int Bt,
                              uint16_t* conv_pool, void* ssm_pool, int n_slots, const int32_t* slot_idx,
-                             uint16_t* out, void* workspace, size_t ws_bytes, void* stream) {
+                             uint16_t* out, void* workspace, size_t ws_bytes, void* stream,
+                             const LoraCall* lc = nullptr) {
   g_err.clear();
   if (!h || (!hidden && !hidden_q) || !conv_pool || !ssm_pool || !slot_idx || !out || !workspace)
     return fail(M2_EINVAL, "m2_decode: null argument");
@@ -584,6 +692,12 @@ static m2_status decode_impl(m2_handle* h, const uint16_t* hidden, const uint8_t
   const bool w8a16 = h->w8a16();
   DecodeWs w = carve_decode(workspace, Bt, w8a16);
   if (ws_bytes < w.total) return fail(M2_ENOMEM, "m2_decode: workspace %zu bytes < %zu needed", ws_bytes, w.total);
+  LoraCallWs lw{};
+  if (lc) {
+    lw = carve_lora_call(workspace, w.total, Bt, 0, lc->w, w8a16);
+    if (ws_bytes < lw.total)
+      return fail(M2_ENOMEM, "m2_decode_lora: workspace %zu bytes < %zu needed", ws_bytes, lw.total);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const BlockParams bp = h->params();
   const float sc1 = h->cfg.s_x * h->s_w1, sc2 = h->cfg.s_y * h->s_w2;
@@ -596,6 +710,10 @@ static m2_status decode_impl(m2_handle* h, const uint16_t* hidden, const uint8_t
   }
   int nl = 0;
   const uint8_t* q = hidden_q ? hidden_q : w.q;
+  // out_proj's adapters read the bf16 normed rows, which the state kernel
+  // does not write for padding rows: zeros, cleared ahead of the kernels so
+  // as not to part them
+  if (lw.o) M2_CUDA(cudaMemsetAsync(lw.o, 0, (size_t)Bt * kI * 2, st));
   if (w8a16) {
     M2_STAGE(h, st, M2_STAGE_DEC_IN_PROJ, nl,
              gemm_bf16(hidden, h->in_proj_bf16, w.zx, Bt, kZ, kH, 1.0f, w.gemm_ws, w.gemm_ws_bytes, h->err, st, &nl, true));
@@ -608,7 +726,10 @@ static m2_status decode_impl(m2_handle* h, const uint16_t* hidden, const uint8_t
       M2_STAGE(h, st, M2_STAGE_DEC_QUANT_IN, 1, launch_quant_e4m3(hidden, (size_t)Bt * kH, h->cfg.s_x, w.q, st));
     M2_STAGE(h, st, M2_STAGE_DEC_IN_PROJ, nl,
              gemm_fp8(q, h->in_proj, w.zx, Bt, kZ, kH, sc1, w.gemm_ws, w.gemm_ws_bytes, h->err, st, &nl, true));
+    if (lw.o) dt.o = lw.o;
   }
+  if (lc && lc->w->in_a)
+    M2_STAGE(h, st, M2_STAGE_LORA, nl, lora_in(h, *lc, hidden, lc->dec_ids, w.zx, Bt, lw.scratch, st, &nl));
   // the state kernel also brings out_proj's weights into L2 for the next kernel
   const void* w2 = w8a16 ? (const void*)h->out_proj_bf16 : (const void*)h->out_proj;
   const size_t w2_bytes = (size_t)kH * kI * (w8a16 ? 2 : 1);
@@ -622,12 +743,16 @@ static m2_status decode_impl(m2_handle* h, const uint16_t* hidden, const uint8_t
     M2_STAGE(h, st, M2_STAGE_DEC_OUT_PROJ, nl,
              gemm_fp8(w.q2, h->out_proj, out, Bt, kH, kI, sc2, w.gemm_ws, w.gemm_ws_bytes, h->err, st, &nl, true));
   }
+  if (lc && lc->w->out_a)
+    M2_STAGE(h, st, M2_STAGE_LORA, nl,
+             lora_out(h, *lc, w8a16 ? w.o : lw.o, lc->dec_ids, out, Bt, lw.scratch, st, &nl));
   if (h->taps_on) {
     m2_status s;
     if (w8a16) {
       if ((s = copy_tap(h->taps.o, w.o, (size_t)Bt * kI * 2, st))) return s;
     } else {
       if ((s = copy_tap(h->taps.q, q, (size_t)Bt * kH, st))) return s;
+      if (lw.o && (s = copy_tap(h->taps.o, lw.o, (size_t)Bt * kI * 2, st))) return s;
     }
     if ((s = copy_tap(h->taps.zx, w.zx, (size_t)Bt * kZ * 2, st))) return s;
     if ((s = copy_tap(h->taps.q2, w.q2, (size_t)Bt * kI, st))) return s;
@@ -652,6 +777,30 @@ m2_status m2_decode_q(m2_handle* h, const uint8_t* hidden_q, int Bt, uint16_t* c
   if (!hidden_q) return fail(M2_EINVAL, "m2_decode_q: null argument");
   return decode_impl(h, nullptr, hidden_q, Bt, conv_pool, ssm_pool, n_slots, slot_idx, out, workspace, ws_bytes,
                      stream);
+}
+
+m2_status m2_decode_lora_workspace_size(const m2_handle* h, int Bt, const m2_lora* lora, size_t* bytes) {
+  if (!h || !bytes) return fail(M2_EINVAL, "m2_decode_lora_workspace_size: null argument");
+  m2_status s = check_lora(lora, "m2_decode_lora_workspace_size");
+  if (s) return s;
+  if (Bt < 1 || Bt > 4096) return fail(M2_ESHAPE, "m2_decode_lora: Bt %d not in [1, 4096]", Bt);
+  *bytes = carve_lora_call(nullptr, carve_decode(nullptr, Bt, h->w8a16()).total, Bt, 0, lora, h->w8a16()).total;
+  return M2_OK;
+}
+
+m2_status m2_decode_lora(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_pool, void* ssm_pool, int n_slots,
+                         const int32_t* slot_idx, const m2_lora* lora, const int32_t* row_adapter, uint16_t* out,
+                         void* workspace, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  if (!hidden || !row_adapter) return fail(M2_EINVAL, "m2_decode_lora: null argument");
+  if ((uintptr_t)row_adapter % 4) return fail(M2_EINVAL, "m2_decode_lora: row_adapter must be 4-byte aligned");
+  m2_status s = check_lora(lora, "m2_decode_lora");
+  if (s) return s;
+  LoraCall lc{};
+  lc.w = lora;
+  lc.dec_ids = row_adapter;
+  return decode_impl(h, hidden, nullptr, Bt, conv_pool, ssm_pool, n_slots, slot_idx, out, workspace, ws_bytes, stream,
+                     &lc);
 }
 
 // ---------------------------------------------------------------- mixed batch
@@ -708,10 +857,10 @@ m2_status m2_mixed_workspace_size(const m2_handle* h, int Bt, const int32_t* seq
   return M2_OK;
 }
 
-m2_status m2_mixed(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_pool, void* ssm_pool, int n_slots,
-                   const int32_t* slot_idx, const int32_t* seqlens_host, int nseq, const uint8_t* has_initial,
-                   uint16_t* conv_state, void* ssm_state, uint16_t* out, void* workspace, size_t ws_bytes,
-                   void* stream) {
+static m2_status mixed_impl(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_pool, void* ssm_pool,
+                            int n_slots, const int32_t* slot_idx, const int32_t* seqlens_host, int nseq,
+                            const uint8_t* has_initial, uint16_t* conv_state, void* ssm_state, uint16_t* out,
+                            void* workspace, size_t ws_bytes, void* stream, const LoraCall* lc = nullptr) {
   g_err.clear();
   if (!h || !hidden || !out || !workspace) return fail(M2_EINVAL, "m2_mixed: null argument");
   if (h->w8a16()) return fail(M2_EINVAL, "m2_mixed: not offered for the W8A16 arm (use m2_prefill and m2_decode)");
@@ -734,6 +883,14 @@ m2_status m2_mixed(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_
   if (R < 1) return fail(M2_ESHAPE, "m2_mixed: empty batch");
   MixedWs w = carve_mixed(workspace, Bt, T, local.total_chunks);
   if (ws_bytes < w.total) return fail(M2_ENOMEM, "m2_mixed: workspace %zu bytes < %zu needed", ws_bytes, w.total);
+  LoraCallWs lw{};
+  const int32_t* ids = nullptr;
+  if (lc) {
+    lw = carve_lora_call(workspace, w.total, Bt, T, lc->w, false);
+    if (ws_bytes < lw.total)
+      return fail(M2_ENOMEM, "m2_mixed_lora: workspace %zu bytes < %zu needed", ws_bytes, lw.total);
+    ids = lw.ids ? lw.ids : lc->dec_ids;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const BlockParams bp = h->params();
   const float sc1 = h->cfg.s_x * h->s_w1, sc2 = h->cfg.s_y * h->s_w2;
@@ -742,9 +899,15 @@ m2_status m2_mixed(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_
   uint16_t* zx_pf = w.zx + (size_t)Bt * kZ;
   uint8_t* q2_pf = w.q2 + (size_t)Bt * kI;
   int nl = 0;
+  // (the state kernel leaves padding rows of o alone)
+  if (lw.o && Bt > 0) M2_CUDA(cudaMemsetAsync(lw.o, 0, (size_t)Bt * kI * 2, st));
   M2_STAGE(h, st, M2_STAGE_QUANT_IN, 1, launch_quant_e4m3(hidden, (size_t)R * kH, h->cfg.s_x, w.q, st));
   M2_STAGE(h, st, M2_STAGE_IN_PROJ, nl,
            gemm_fp8(w.q, h->in_proj, w.zx, R, kZ, kH, sc1, w.gemm_ws, w.gemm_ws_bytes, h->err, st, &nl, true));
+  if (lc) {
+    if (lw.ids) M2_STAGE(h, st, M2_STAGE_LORA, 1, launch_lora_row_ids(lc->dec_ids, Bt, local, lc->seq, lw.ids, st));
+    if (lc->w->in_a) M2_STAGE(h, st, M2_STAGE_LORA, nl, lora_in(h, *lc, hidden, ids, w.zx, R, lw.scratch, st, &nl));
+  }
   // A second stream runs the prefill cumsum beside the conv (it reads only
   // the in_proj output), and the decode rows' state kernel beside the chunk
   // scan: that kernel is HBM-bound and the scan latency-bound, while next to
@@ -764,6 +927,7 @@ m2_status m2_mixed(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_
   auto decode_on_side = [&]() -> cudaError_t {
     DecodeTaps dt{};
     if (h->taps_on) dt.o = h->taps.o, dt.y = h->taps.y;
+    if (lw.o) dt.o = lw.o;
     int dl = 0;
     cudaError_t e = launch_decode_stream(w.zx, bp, conv_pool, ssm_pool, bf16_state, n_slots, slot_idx, Bt, w.q2,
                                          h->err, dt, h->side, &dl);
@@ -808,6 +972,7 @@ m2_status m2_mixed(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_
                launch_ssd_chunk_scan_tc(w.pf.u, w.pf.cumdt, w.pf.sin_img, bp, local, w.pf.y, h->err, st));
     }
     uint16_t* o_tap = (h->taps_on && h->taps.o) ? h->taps.o + (size_t)Bt * kI : nullptr;
+    if (lw.o) o_tap = lw.o + (size_t)Bt * kI;
     M2_STAGE(h, st, M2_STAGE_NORM_QUANT, 1, launch_gated_norm_quant(w.pf.y, zx_pf, bp, T, q2_pf, o_tap, st));
   }
   if (fork_decode) {
@@ -815,6 +980,7 @@ m2_status m2_mixed(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_
   } else if (Bt > 0) {
     DecodeTaps dt{};
     if (h->taps_on) dt.o = h->taps.o, dt.y = h->taps.y;
+    if (lw.o) dt.o = lw.o;
     int dl = 0;
     M2_STAGE(h, st, M2_STAGE_DECODE_FUSED, dl,
              launch_decode_stream(w.zx, bp, conv_pool, ssm_pool, bf16_state, n_slots, slot_idx, Bt, w.q2, h->err,
@@ -822,9 +988,12 @@ m2_status m2_mixed(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_
   }
   M2_STAGE(h, st, M2_STAGE_OUT_PROJ, nl,
            gemm_fp8(w.q2, h->out_proj, out, R, kH, kI, sc2, w.gemm_ws, w.gemm_ws_bytes, h->err, st, &nl, true));
+  if (lc && lc->w->out_a)
+    M2_STAGE(h, st, M2_STAGE_LORA, nl, lora_out(h, *lc, lw.o, ids, out, R, lw.scratch, st, &nl));
   if (h->taps_on) {   // the row-aligned intermediates, in batch order
     m2_status s;
     if ((s = copy_tap(h->taps.q, w.q, (size_t)R * kH, st))) return s;
+    if (lw.o && (s = copy_tap(h->taps.o, lw.o, (size_t)R * kI * 2, st))) return s;
     if ((s = copy_tap(h->taps.zx, w.zx, (size_t)R * kZ * 2, st))) return s;
     if ((s = copy_tap(h->taps.q2, w.q2, (size_t)R * kI, st))) return s;
     if (h->taps.y && T > 0 && (s = copy_tap(h->taps.y + (size_t)Bt * kI, w.pf.y, (size_t)T * kI * 2, st))) return s;
@@ -840,6 +1009,44 @@ m2_status m2_mixed(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_
     h->stats.state_update_rows += (uint64_t)Bt;
   }
   return M2_OK;
+}
+
+m2_status m2_mixed(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_pool, void* ssm_pool, int n_slots,
+                   const int32_t* slot_idx, const int32_t* seqlens_host, int nseq, const uint8_t* has_initial,
+                   uint16_t* conv_state, void* ssm_state, uint16_t* out, void* workspace, size_t ws_bytes,
+                   void* stream) {
+  return mixed_impl(h, hidden, Bt, conv_pool, ssm_pool, n_slots, slot_idx, seqlens_host, nseq, has_initial, conv_state,
+                    ssm_state, out, workspace, ws_bytes, stream);
+}
+
+m2_status m2_mixed_lora_workspace_size(const m2_handle* h, int Bt, const int32_t* seqlens_host, int nseq,
+                                       const m2_lora* lora, size_t* bytes) {
+  m2_status s = m2_mixed_workspace_size(h, Bt, seqlens_host, nseq, bytes);
+  if (s) return s;
+  if ((s = check_lora(lora, "m2_mixed_lora_workspace_size"))) return s;
+  SeqInfo si;
+  memset(&si, 0, sizeof si);
+  if (nseq > 0 && (s = build_seqinfo(seqlens_host, nseq, nullptr, &si))) return s;
+  *bytes = carve_lora_call(nullptr, *bytes, Bt, si.total_tokens, lora, false).total;
+  return M2_OK;
+}
+
+m2_status m2_mixed_lora(m2_handle* h, const uint16_t* hidden, int Bt, uint16_t* conv_pool, void* ssm_pool, int n_slots,
+                        const int32_t* slot_idx, const int32_t* row_adapter, const int32_t* seqlens_host, int nseq,
+                        const uint8_t* has_initial, uint16_t* conv_state, void* ssm_state, const m2_lora* lora,
+                        const int32_t* seq_adapter, uint16_t* out, void* workspace, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  m2_status s = check_lora(lora, "m2_mixed_lora");
+  if (s) return s;
+  if (nseq < 0 || nseq > kMaxSeq) return fail(M2_ESHAPE, "m2_mixed_lora: nseq %d not in [0, %d]", nseq, kMaxSeq);
+  if (Bt > 0 && (!row_adapter || (uintptr_t)row_adapter % 4))
+    return fail(M2_EINVAL, "m2_mixed_lora: decode rows need row_adapter, 4-byte aligned");
+  LoraCall lc{};
+  lc.w = lora;
+  lc.dec_ids = row_adapter;
+  if (nseq > 0 && (s = seq_adapters(lora, seq_adapter, nseq, &lc.seq, "m2_mixed_lora"))) return s;
+  return mixed_impl(h, hidden, Bt, conv_pool, ssm_pool, n_slots, slot_idx, seqlens_host, nseq, has_initial, conv_state,
+                    ssm_state, out, workspace, ws_bytes, stream, &lc);
 }
 
 // ---------------------------------------------------------------- standalone ops

@@ -135,3 +135,55 @@ def test_binding_refuses_host_tensors_and_types(m2):
         m2.m2_beam_select(torch.zeros((5, 10)), torch.zeros((1, 4)))
     with pytest.raises(ValueError):
         m2.m2_state_reorder([], [], ids.reshape(1, 4), ids.reshape(1, 4))
+
+
+def _adapters(m2, **kw):
+    f = dict(n_adapters=2, rank=16, in_a=1 << 20, in_b=2 << 20, out_a=3 << 20, out_b=4 << 20, scale=None)
+    f.update(kw)
+    return m2.m2_lora(*[f[n] for n, _ in m2.m2_lora._fields_])
+
+
+@pytest.mark.parametrize("kw,status", [(dict(rank=12), "M2_ESHAPE"), (dict(n_adapters=0), "M2_ESHAPE"),
+                                       (dict(in_b=None), "M2_EINVAL"), (dict(out_a=None), "M2_EINVAL"),
+                                       (dict(in_a=None, in_b=None, out_a=None, out_b=None), "M2_EINVAL"),
+                                       (dict(out_b=(4 << 20) + 8), "M2_EINVAL"), (dict(scale=2), "M2_EINVAL")])
+def test_block_adapters_refused(m2, kw, status):
+    """A bad adapter set is refused by all three block calls and their
+    workspace queries, before the handle is looked at."""
+    ref = ctypes.byref(_adapters(m2, **kw))
+    want = getattr(m2, status)
+    lens, ids, p = (ctypes.c_int32 * 1)(4), (ctypes.c_int32 * 1)(0), 1 << 21
+    L = m2._lib
+    assert L.m2_prefill_lora(None, p, lens, 1, None, p, p, ref, ids, p, p, BIG, None) == want
+    assert "m2_prefill_lora" in m2.last_error()
+    assert L.m2_decode_lora(None, p, 1, p, p, 1, p, ref, p, p, p, BIG, None) == want
+    assert "m2_decode_lora" in m2.last_error()
+    assert L.m2_mixed_lora(None, p, 1, p, p, 1, p, p, lens, 1, None, p, p, ref, ids, p, p, BIG, None) == want
+    assert "m2_mixed_lora" in m2.last_error()
+
+
+def test_block_adapter_ids_refused(m2):
+    ref, p = ctypes.byref(_adapters(m2)), 1 << 21
+    lens = (ctypes.c_int32 * 2)(4, 4)
+    L = m2._lib
+    for bad in ((0, 2), (-2, 0)):
+        ids = (ctypes.c_int32 * 2)(*bad)
+        assert L.m2_prefill_lora(None, p, lens, 2, None, p, p, ref, ids, p, p, BIG, None) == m2.M2_EINVAL
+        assert "seq_adapter" in m2.last_error()
+        assert L.m2_mixed_lora(None, p, 0, None, None, 0, None, None, lens, 2, None, p, p, ref, ids, p, p, BIG,
+                               None) == m2.M2_EINVAL
+        assert "seq_adapter" in m2.last_error()
+    assert L.m2_prefill_lora(None, p, lens, 257, None, p, p, ref, None, p, p, BIG, None) == m2.M2_ESHAPE
+    assert L.m2_decode_lora(None, p, 1, p, p, 1, p, ref, None, p, p, BIG, None) == m2.M2_EINVAL
+    assert L.m2_decode_lora(None, p, 1, p, p, 1, p, ref, p, p, p, BIG, None) == m2.M2_EINVAL      # null handle
+    n = ctypes.c_size_t()
+    assert L.m2_prefill_lora_workspace_size(None, lens, 2, ref, ctypes.byref(n)) == m2.M2_EINVAL
+    assert L.m2_decode_lora_workspace_size(None, 1, ref, ctypes.byref(n)) == m2.M2_EINVAL
+    assert L.m2_mixed_lora_workspace_size(None, 1, lens, 2, ref, ctypes.byref(n)) == m2.M2_EINVAL
+
+
+def test_lora_struct_matches_the_header(m2):
+    import re
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "m2.h")).read(), flags=re.S)
+    body = re.search(r"typedef struct m2_lora \{(.*?)\} m2_lora;", src, flags=re.S).group(1)
+    assert re.findall(r"(\w+)\s*;", body) == [n for n, _ in m2.m2_lora._fields_]
