@@ -296,12 +296,14 @@ __global__ void __launch_bounds__(kBeThreads) k_beam_rows(const T* __restrict__ 
   uint64_t* out = keys + (size_t)request * beams * splits * k + split * beams + (row - request * beams);
   const int next = splits * beams;   // from one rank to the next
   if (n <= kCap) {
-    for (int i = tid; i < n; i += kBeThreads) {
-      const uint64_t mine = cand[i];
+    for (int i0 = 0; i0 < n; i0 += kBeThreads / 8) {   // eight threads count a candidate's betters
+      const int i = i0 + tid / 8;
+      const uint64_t mine = i < n ? cand[i] : ~0ull;
       int rank = 0;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) rank += cand[j] > mine;
-      if (rank < k) out[(size_t)rank * next] = mine;
+      for (int j = tid % 8; j < n; j += 8) rank += cand[j] > mine;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      if (i < n && tid % 8 == 0 && rank < k) out[(size_t)rank * next] = mine;
     }
     for (int i = n + tid; i < k; i += kBeThreads) out[(size_t)i * next] = 0;
   } else {   // many equal values: the greatest key below the last one, k times
@@ -397,26 +399,25 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
   }
   __syncthreads();
 
-  // candidate c with key `key`: lower and upper bound of its value as ordered
-  // f32 (0: no candidate)
-  auto bounds = [&](int c, uint64_t key, uint32_t* hi) -> uint32_t {
-    const int b = c % beams;
+  // candidate c with key `key`, of beam b = c % beams: lower and upper bound
+  // of its value as ordered f32 (0: no candidate)
+  auto bounds = [&](int c, int b, uint64_t key, uint32_t* hi) -> uint32_t {
     *hi = 0;
-    if (kind[b] == 0) return 0;
-    if (kind[b] == 2) return c < beams ? *hi = ord32(offs[b] + 0.f) : 0;
+    const int kd = kind[b];
+    const float off = offs[b];
+    if (kd != 1) return kd == 2 && c < beams ? *hi = ord32(off + 0.f) : 0;
     if (key == 0) return 0;
     float x = unord32((uint32_t)(key >> 32));
     if (isinf(top[b])) {
       if (x != top[b]) return 0;
       x = 0.f;
     }
-    const float v = x + offs[b], err = 0x1p-22f * (fabsf(x) + fabsf(offs[b]));
+    const float v = x + off, err = 0x1p-22f * (fabsf(x) + fabsf(off));
     *hi = ord32(v + err + 0.f);
     return ord32(v - err + 0.f);
   };
   // its 64-bit value and place (beam, token), which orders like beam * vocab + token
-  auto value = [&](int c, uint64_t key, uint64_t* flat) -> uint64_t {
-    const int b = c % beams;
+  auto value = [&](int b, uint64_t key, uint64_t* flat) -> uint64_t {
     if (kind[b] == 2) {
       *flat = ((uint64_t)b << 32) | (uint32_t)eos;
       return ord64(score[b] + 0.);
@@ -425,13 +426,22 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
     const double x = isinf(top[b]) ? 0. : (double)unord32((uint32_t)(key >> 32));
     return ord64(score[b] + (x - lse[b]) + 0.);
   };
-  uint32_t mine = 0, hi;
+  uint32_t mine = 0, hi, hi_held[kKeep];
+  int b_held[kKeep];
+  {
+    const int step = blockDim.x % beams;
+    int b = tid % beams;
 #pragma unroll
-  for (int i = 0; i < kKeep; ++i) {
-    const int c = tid + i * blockDim.x;
-    if (c < total) mine = max(mine, bounds(c, held[i], &hi));
+    for (int i = 0; i < kKeep; ++i) {
+      const int c = tid + i * blockDim.x;
+      b_held[i] = b;
+      hi_held[i] = 0;
+      if (c < total) mine = max(mine, bounds(c, b, held[i], &hi_held[i]));
+      b += step;
+      b -= b >= beams ? beams : 0;
+    }
   }
-  for (int c = tid + kKeep * blockDim.x; c < total; c += blockDim.x) mine = max(mine, bounds(c, mykeys[c], &hi));
+  for (int c = tid + kKeep * blockDim.x; c < total; c += blockDim.x) mine = max(mine, bounds(c, c % beams, mykeys[c], &hi));
   uint32_t tau = __reduce_max_sync(0xffffffffu, mine);
   for (int i = (k + nw - 1) / nw; i > 1; --i) {
     const uint32_t who = __ballot_sync(0xffffffffu, mine == tau);
@@ -442,19 +452,19 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
   __syncthreads();
   tau = __reduce_min_sync(0xffffffffu, lane < nw ? wtau[lane] : 0xffffffffu);
   if (tau == 0) tau = 1;
-  auto keep = [&](int c, uint64_t key) {
-    bounds(c, key, &hi);
-    if (hi < tau) return;
+  auto keep = [&](int b, uint64_t key) {
     const int at = atomicAdd(&n_cand, 1);
     uint64_t f;
-    if (at < kCap) cval[at] = value(c, key, &f), cflat[at] = f;
+    if (at < kCap) cval[at] = value(b, key, &f), cflat[at] = f;
   };
 #pragma unroll
-  for (int i = 0; i < kKeep; ++i) {
-    const int c = tid + i * blockDim.x;
-    if (c < total) keep(c, held[i]);
+  for (int i = 0; i < kKeep; ++i)
+    if (hi_held[i] >= tau) keep(b_held[i], held[i]);
+  for (int c = tid + kKeep * blockDim.x; c < total; c += blockDim.x) {
+    const uint64_t key = mykeys[c];
+    bounds(c, c % beams, key, &hi);
+    if (hi >= tau) keep(c % beams, key);
   }
-  for (int c = tid + kKeep * blockDim.x; c < total; c += blockDim.x) keep(c, mykeys[c]);
   __syncthreads();
   const int n = n_cand;
   const size_t o0 = (size_t)blockIdx.x * k;
@@ -472,11 +482,18 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
     if (out_done) out_done[o0 + rank] = 0;
   };
   if (n <= kCap) {
-    for (int i = tid; i < n; i += blockDim.x) {
-      const uint64_t v = cval[i], fl = cflat[i];
+    for (int i0 = 0; i0 < n; i0 += blockDim.x / 8) {   // eight threads count a candidate's betters
+      const int i = i0 + tid / 8;
+      const uint64_t v = i < n ? cval[i] : ~0ull, fl = i < n ? cflat[i] : 0;
       int rank = 0;
-      for (int j = 0; j < n; ++j) rank += cval[j] > v || (cval[j] == v && cflat[j] < fl);
-      if (rank < k) put(rank, v, fl);
+      for (int j = tid % 8; j < n; j += 8) {
+        const uint64_t w = cval[j];
+        rank += w > v;
+        if (w == v) rank += cflat[j] < fl;
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      if (i < n && tid % 8 == 0 && rank < k) put(rank, v, fl);
     }
     for (int i = n + tid; i < k; i += blockDim.x) none(i);
   } else {   // many equal values: the best after the last one, k times
@@ -485,10 +502,10 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
       uint64_t bv = 0, bf = ~0ull;
       for (int c = tid; c < total; c += blockDim.x) {
         const uint64_t key = mykeys[c];
-        bounds(c, key, &hi);
+        bounds(c, c % beams, key, &hi);
         if (hi < tau) continue;
         uint64_t f;
-        const uint64_t v = value(c, key, &f);
+        const uint64_t v = value(c % beams, key, &f);
         if (v > lv || (v == lv && f <= lf)) continue;
         if (v > bv || (v == bv && f < bf)) bv = v, bf = f;
       }
