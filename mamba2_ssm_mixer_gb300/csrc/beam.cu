@@ -154,7 +154,7 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 // 16-byte boundary.  Keys go to [request][rank][split][beam], the order in
 // which the merge's warps each meet every beam and every rank.
 template <typename T, int VPT, bool kAligned>
-__global__ void __launch_bounds__(kBeThreads) k_beam_rows(const T* __restrict__ logits, size_t stride, int vocab,
+__global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 5 : 6) k_beam_rows(const T* __restrict__ logits, size_t stride, int vocab,
                                                           const float* __restrict__ scores,
                                                           const uint8_t* __restrict__ done, int k, int beams,
                                                           int chunk, uint64_t* __restrict__ keys,
@@ -181,6 +181,10 @@ __global__ void __launch_bounds__(kBeThreads) k_beam_rows(const T* __restrict__ 
 
   uint4 q[VPT];
   float vm[VPT], mx = -INFINITY;
+  if (first + kBeThreads * V * VPT <= end) {   // a full chunk
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) q[j] = load16(base + first + (j * kBeThreads + tid) * V, off);
+  } else
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int at = first + (j * kBeThreads + tid) * V;
