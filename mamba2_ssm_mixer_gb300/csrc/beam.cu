@@ -239,13 +239,17 @@ __global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 5 : 6) k_beam_rows(cons
   repack(q);
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  // the warp's ceil(k / 8)-th largest thread maximum
-  uint32_t tau = owm, left = om;
-  for (int i = (k + kBeWarps - 1) / kBeWarps; i > 1; --i) {
-    const uint32_t who = __ballot_sync(0xffffffffu, left == tau);
-    if (lane == __ffs(who) - 1) left = 0;
-    tau = __reduce_max_sync(0xffffffffu, left);
-  }
+  // the warp's j-th largest thread maximum (0: it has not as many threads)
+  auto nth_max = [&](int j) {
+    uint32_t left = om, v = owm;
+    for (; j > 1; --j) {
+      const uint32_t who = __ballot_sync(0xffffffffu, left == v);
+      if (lane == __ffs(who) - 1) left = 0;
+      v = __reduce_max_sync(0xffffffffu, left);
+    }
+    return v;
+  };
+  const uint32_t tau = nth_max((k + kBeWarps - 1) / kBeWarps);
   if (lane == 0) wm[warp] = m, ws[warp] = s, wtau[warp] = tau;
   __syncthreads();
   const uint4 t0 = reinterpret_cast<const uint4*>(wtau)[0], t1 = reinterpret_cast<const uint4*>(wtau)[1];
@@ -262,16 +266,19 @@ __global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 5 : 6) k_beam_rows(cons
     for (int o = 1; o < 8; o <<= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
     if (lane == 0) sums[row * splits + split] = ChunkSum{M, S};
   }
-  if (t <= kOrdNegInf) {   // a warp has too few unmasked tokens: the k-th largest of all thread maxima
-    uint64_t* mine = cand;
-    mine[tid] = ((uint64_t)om << 32) | (uint32_t)(kBeThreads - tid);
+  if (t <= kOrdNegInf) {   // some warps have no unmasked token: the same over those that have
+    int active = 0;
+#pragma unroll
+    for (int i = 0; i < kBeWarps; ++i) active += wm[i] > -INFINITY;
+    const int j = active ? (k + active - 1) / active : 33;
+    const uint32_t again = j <= 32 && m > -INFINITY ? nth_max(j) : 0xffffffffu;
     __syncthreads();
-    int above = 0;
-    for (int i = 0; i < kBeThreads; ++i) above += mine[i] > mine[tid];
+    if (lane == 0) wtau[warp] = again;
     __syncthreads();
-    if (above == k - 1) wtau[0] = om;
-    __syncthreads();
-    t = wtau[0];
+    t = j <= 32 ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int i = 0; i < kBeWarps; ++i) t = min(t, wtau[i]);
+    // (still none: too few threads have any, and all their tokens survive)
   }
   // survivors: >= tau and above -inf.  First the few vectors that hold some,
   // then their elements, one a thread (in place, each warp would step through
@@ -446,15 +453,17 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
     }
   }
   for (int c = tid + kKeep * blockDim.x; c < total; c += blockDim.x) mine = max(mine, bounds(c, c % beams, mykeys[c], &hi));
+  // (tau from the first 8 warps: theirs are the chunks' best)
+  const int tw = min(nw, 8);
   uint32_t tau = __reduce_max_sync(0xffffffffu, mine);
-  for (int i = (k + nw - 1) / nw; i > 1; --i) {
+  for (int i = (k + tw - 1) / tw; i > 1; --i) {
     const uint32_t who = __ballot_sync(0xffffffffu, mine == tau);
     if (lane == __ffs(who) - 1) mine = 0;
     tau = __reduce_max_sync(0xffffffffu, mine);
   }
   if (lane == 0) wtau[warp] = tau;
   __syncthreads();
-  tau = __reduce_min_sync(0xffffffffu, lane < nw ? wtau[lane] : 0xffffffffu);
+  tau = __reduce_min_sync(0xffffffffu, lane < tw ? wtau[lane] : 0xffffffffu);
   if (tau == 0) tau = 1;
   auto keep = [&](int b, uint64_t key) {
     const int at = atomicAdd(&n_cand, 1);
