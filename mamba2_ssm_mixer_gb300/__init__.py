@@ -160,6 +160,9 @@ def _stream(stream):
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None):
+    if type(t) is torch.Tensor and t.dtype == dtype and (shape is None or t.shape == shape) and t.is_cuda and \
+            t.is_contiguous():
+        return   # (the common case first: these checks are a fair part of a short call)
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -639,6 +642,7 @@ def m2_rmsnorm_residual_quant(h: torch.Tensor, add: torch.Tensor | None, w: torc
 # (a call of a few microseconds would spend a third of itself on that).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on_device(ref: torch.Tensor, stream, others, call):
@@ -651,7 +655,7 @@ def _on_device(ref: torch.Tensor, stream, others, call):
     for t in others:
         if t is not None and t.device != dev:
             raise ValueError(f"tensors of one call are on {dev} and {t.device}")
-    if stream is None and dev.index == torch.cuda.current_device():
+    if stream is None and dev.index == _current_device():
         return call(_raw_stream(dev.index))
     with torch.cuda.device(dev):
         if stream is None:
