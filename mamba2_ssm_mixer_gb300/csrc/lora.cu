@@ -99,11 +99,11 @@ __device__ __forceinline__ void cp_wait() {
 // blocks over the cluster's 32 warps, the parts summed in shared memory, then
 // over the CTAs' shared memories.  B t: 16 columns per warp and step, the
 // first steps' B and y on their way before t is known.
-// A decode batch is bound by reading each adapter once and by latency: 64 rows
-// with 64 adapters of rank 16 (2688 -> 10304) in 10.0 us, floor 4.4; one row
-// 3.7 us.  Clusters of 8 and of 2 took 13.2 and 11.3; a form on FMA units, with
-// ten times the instructions for unpacking, 16.8; the kernels below, with their
-// sorting launch, 30.
+// A decode batch is bound by reading each adapter once and by latency.
+// Adapters of rank 16, 2688 -> 10304: 1 to 8 rows 4.6 us, 64 rows with 64
+// adapters 10.8 (floor 4.4); a form on FMA units, with ten times the
+// instructions for unpacking, took 16.8 for those, clusters of 8 and of 2 13.2
+// and 11.3, bringing B's slice to L2 ahead 0.3 to 1.2 more.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kFewRows = 256, kFewMost = 512;   // see few_rows
@@ -115,12 +115,12 @@ constexpr int kUnit = 8;   // rows that share the reads of an adapter
 // NT: rank / 16 rounded up to a power of two.  kPair: y and out move two
 // columns at a time (N even, 4-byte aligned).
 template <int NT, bool kPair>
-__global__ void __launch_bounds__(kLoThreads) k_lora_few(const uint16_t* y, const uint16_t* __restrict__ x,
+__global__ void __launch_bounds__(kLoThreads, NT <= 4 ? 2 : 1) k_lora_few(const uint16_t* y, const uint16_t* __restrict__ x,
                                                          const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
                                                          const float* __restrict__ scale,
                                                          const int32_t* __restrict__ ids, int n_adapters, int rank,
                                                          uint16_t* out, int M, int N, int K, int* err) {
-  constexpr int kAheadF = NT == 1 ? 8 : NT == 2 ? 4 : NT == 4 ? 2 : 1;   // steps of B and y under way
+  constexpr int kAheadF = NT == 1 ? 8 : NT == 2 ? 4 : 1;   // steps of B and y under way
   __shared__ int rows_s[kUnit];
   __shared__ __align__(16) float red[kLoWarps][NT * 128];
   __shared__ float part[NT * 128];
@@ -825,11 +825,14 @@ LoraWs carve_lora(void* base, int M, int rank, int n_adapters) {
 template <int NT, bool kPair>
 cudaError_t launch_few(const uint16_t* y, const uint16_t* x, const LoraWeights& w, const int32_t* ids, uint16_t* out,
                        int M, int N, int K, int* err, cudaStream_t st) {
-  // slices of N: enough clusters for every SM, but no less than a step of each warp
+  // slices of N: clusters for most SMs, one CTA each (a second on some SMs
+  // holds up its cluster: 152 CTAs took 5.8 us where 128 took 5.1), but no
+  // less than a step of each warp
   const int sms = device_sm_count(), least = kFewCluster * kLoWarps * 16;
-  int slices = (sms + kFewCluster * M - 1) / (kFewCluster * M);
+  int slices = sms * 27 / 32 / (kFewCluster * M);
   const int most = (N + least - 1) / least;
   if (slices > most) slices = most;
+  if (slices < 1) slices = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(kFewCluster * slices), (unsigned)M);
   cfg.blockDim = dim3(kLoThreads);
