@@ -515,7 +515,9 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
     xin[i] = r0 + 32 * i < tile.rows;
     xr[i] = x + (size_t)(xin[i] ? src[i] : 0) * K + piece * 8;
   }
-  const uint16_t* ar = a + (size_t)tile.adapter * rank * K + piece * 8;
+  const uint16_t* ar = a + ((size_t)tile.adapter * rank + r0) * K + piece * 8;
+  const size_t anext = (size_t)32 * K;
+  const uint32_t xdst = swz(r0, piece);   // (rows 32 apart swizzle alike)
   auto load = [&](int kb, int s) {
     const int k = (kb0 + kb) * kDownK;
     const bool kin = k + piece * 8 < K;
@@ -523,9 +525,11 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool in = kin && xin[i];
-      cp16(base + swz(r0 + 32 * i, piece), in ? xr[i] + k : x, in);
+      cp16(base + xdst + 32 * 128 * i, in ? xr[i] + k : x, in);
     }
-    for (int r = r0; r < rank; r += 32) cp16(base + kTile * 128 + swz(r, piece), kin ? ar + (size_t)r * K + k : a, kin);
+    const uint16_t* ap = ar + k;
+    uint32_t adst = base + kTile * 128 + xdst;
+    for (int r = r0; r < rank; r += 32, ap += anext, adst += 32 * 128) cp16(adst, kin ? ap : a, kin);
   };
 #pragma unroll
   for (int s = 0; s < kDownStages - 1; ++s) {
@@ -538,6 +542,12 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
   for (int i = 0; i < 2 * NK; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   const int am = mg * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, ac = lane >> 4;     // x fragment: row, piece
   const int bm = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;               // A fragment: rank row, piece
+  uint32_t xoff[2], aoff[2];   // of the block's two 16-wide steps (rank rows 16 apart swizzle alike)
+#pragma unroll
+  for (int k16 = 0; k16 < 2; ++k16) {
+    const int c = kh * 4 + k16 * 2;
+    xoff[k16] = swz(am, c + ac), aoff[k16] = kTile * 128 + swz(bm, c + bc);
+  }
   for (int kb = 0; kb < nk; ++kb) {
     cp_wait<kDownStages - 2>();
     __syncthreads();
@@ -545,17 +555,16 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
     if (kb + kDownStages - 1 < nk) load(kb + kDownStages - 1, (kb + kDownStages - 1) % kDownStages);
     cp_commit();
     if (mg * 16 >= tile.rows) continue;   // no rows for this warp
-    const uint32_t xs = s0 + s * stage, as = xs + kTile * 128;
+    const uint32_t xs = s0 + s * stage;
 #pragma unroll
     for (int k16 = 0; k16 < 2; ++k16) {
-      const int c = kh * 4 + k16 * 2;
       uint32_t af[4];
-      ldsm4(af, xs + swz(am, c + ac));
+      ldsm4(af, xs + xoff[k16]);
 #pragma unroll
       for (int p = 0; p < NK; ++p)
         if (p * 16 < rank) {
           uint32_t bf[4];
-          ldsm4(bf, as + swz(p * 16 + bm, c + bc));
+          ldsm4(bf, xs + aoff[k16] + p * 16 * 128);
           mma16816(acc[2 * p], af, bf[0], bf[1]);
           if (p * 16 + 8 < rank) mma16816(acc[2 * p + 1], af, bf[2], bf[3]);
         }
@@ -683,11 +692,14 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
   const uint32_t s0 = smem_u32(bsm);
   {
     const uint16_t* bt = b + ((size_t)tile.adapter * N + c0) * rank;
+    const int n_step = kLoThreads / rv, v_step = kLoThreads - n_step * rv;
+    int n = tid / rv, v = tid - n * rv;   // (stepped, not divided, from piece to piece)
     for (int i = tid; i < kCols * rv; i += kLoThreads) {
-      const int n = i / rv, v = i - n * rv;
       const int pos = (n & ~31) | ((n >> 1) & 3) << 3 | ((n >> 3) & 3) << 1 | (n & 1);
       const bool in = c0 + n < c_hi;
       cp16(s0 + (uint32_t)(pos * pitch + v * 16), in ? bt + (size_t)i * 8 : b, in);
+      n += n_step, v += v_step;
+      if (v >= rv) v -= rv, ++n;
     }
     cp_commit();
     if (rank & 8)   // the last 16-wide step reads 8 entries past the rank: zeros
@@ -802,10 +814,7 @@ struct LoraWs {
 // CTAs sharing a tile's K: two per SM for the fewest tiles the rows can make.
 int lora_splits(int M, int K) {
   const int tiles = (M + kTile - 1) / kTile, kblocks = (K + kDownK - 1) / kDownK;
-  #ifndef V_DT
-#define V_DT 2
-#endif
-  const int s = (V_DT * device_sm_count() + tiles - 1) / tiles;
+  const int s = (2 * device_sm_count() + tiles - 1) / tiles;
   return std::max(1, std::min({s, 8, kblocks / 4}));   // (four blocks each at least: the stages)
 }
 
