@@ -197,7 +197,8 @@ m2_status m2_set_taps(m2_handle* h, const m2_taps* taps);
  * Read and clear the handle's device error word (synchronises the device).
  * M2_EINVAL: a decode row named a slot outside [0, n_slots), or a slot an
  * earlier row of the same call already named (that row was skipped, its
- * output zeroed); M2_ETIMEOUT: a bounded wait ran out (the kernel returned
+ * output zeroed), or an adapter outside [-1, n_adapters) (taken as -1);
+ * M2_ETIMEOUT: a bounded wait ran out (the kernel returned
  * early: outputs of that call are incomplete).
  */
 m2_status m2_check(m2_handle* h);
@@ -464,8 +465,8 @@ m2_status m2_lora_add_workspace_size(int M, int N, int K, int rank, int n_adapte
  *   workspace    device, >= m2_lora_add_workspace_size bytes, 256-byte aligned
  *                (may be NULL when that is 0)
  * rank: a multiple of 8 in [8, 128] (adapters of lower rank are padded with
- * zero rows of a_w and columns of b); K: a multiple of 16; N >= 1; M from 0
- * to 2^24; n_adapters in [1, 4096].  x, a_w and b 16-byte aligned, y and out
+ * zero rows of a_w and columns of b); K: a multiple of 16 in [16, 2^24]; N in
+ * [1, 2^24]; M in [0, 2^24]; n_adapters in [1, 4096].  x, a_w and b 16-byte aligned, y and out
  * 2-byte.  Errors: M2_EINVAL, M2_ESHAPE, M2_ENOMEM, M2_EDEVICE, M2_ECUDA.
  */
 m2_status m2_lora_add(const uint16_t* y, const uint16_t* x, const uint16_t* a_w, const uint16_t* b, const float* scale,

@@ -424,6 +424,10 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
       x = 0.f;
     }
     const float v = x + off, err = 0x1p-22f * (fabsf(x) + fabsf(off));
+    if (!(fabsf(v) + err < 3.0e38f)) {   // past f32: bounded by nothing
+      *hi = ord32(INFINITY);
+      return kOrdNegInf;
+    }
     *hi = ord32(v + err + 0.f);
     return ord32(v - err + 0.f);
   };

@@ -1284,8 +1284,8 @@ static bool overlap(const void* p, size_t pn, const void* q, size_t qn) {
 }
 
 static m2_status check_lora_shape(int M, int N, int K, int rank, int n_adapters, const char* who) {
-  if (M < 0 || M > (1 << 24) || N < 1 || K < 16 || K % 16)
-    return fail(M2_ESHAPE, "%s: M %d, N %d, K %d (M up to 2^24, N >= 1, K a multiple of 16)", who, M, N, K);
+  if (M < 0 || M > (1 << 24) || N < 1 || N > (1 << 24) || K < 16 || K > (1 << 24) || K % 16)
+    return fail(M2_ESHAPE, "%s: M %d, N %d, K %d (each up to 2^24, N >= 1, K a multiple of 16)", who, M, N, K);
   if (rank < 8 || rank > kLoraMaxRank || rank % 8)
     return fail(M2_ESHAPE, "%s: rank %d must be a multiple of 8 in [8, %d]", who, rank, kLoraMaxRank);
   if (n_adapters < 1 || n_adapters > kLoraMaxAdapters)

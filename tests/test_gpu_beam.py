@@ -181,6 +181,21 @@ def test_large_logits_and_scores():
         assert np.allclose(step.scores[i].cpu().numpy(), val[i].reshape(-1)[want], rtol=2.0 ** -24, atol=2.0 ** -11)
 
 
+def test_values_past_f32():
+    """Logits at the type's lowest next to scores at the top of f32: the sums
+    the merge bounds its candidates with overflow, the values do not."""
+    low = float(torch.finfo(F32).min)
+    logits = torch.full((4, 700), low, device="cuda")
+    logits[1, :5] = -1.0e38
+    logits[3] = 0.0
+    scores = np.array([[3.3e38, 3.2e38, 3.0e38, 3.25e38]], np.float32)
+    step = _go(logits, scores, 12)
+    val = _values(logits.cpu().numpy().reshape(1, 4, 700), scores)[0].reshape(-1)
+    want = np.argsort(-val, kind="stable")[:12]
+    assert np.array_equal(step.parents[0].cpu().numpy() * 700 + step.tokens[0].cpu().numpy(), want)
+    assert np.allclose(step.scores[0].cpu().numpy(), val[want], rtol=2.0 ** -23, atol=0)
+
+
 def test_rows_past_32_bit_offsets():
     """Rows a gigabyte apart: offsets above 2^31 elements."""
     v, stride = 1000, 1 << 29

@@ -137,6 +137,12 @@ def test_a_wrong_request_is_left_alone_and_reported(bad):
     m2.check_standalone()
 
 
+def test_no_requests():
+    conv, ssm = _pools(1, 2, torch.float32)
+    none = torch.empty((0, 4), dtype=torch.int32, device="cuda")
+    assert m2.m2_state_reorder(conv, ssm, none, none).shape == (0, 4)
+
+
 def test_the_most_rows():
     """4096 rows, every slot named: the plan alone (each beam goes on as
     itself, permuted), and one copy."""

@@ -30,7 +30,7 @@ def _lora(m2, **kw):
                                a["N"], a["K"], a["ws"], a["wsn"], None)
 
 
-@pytest.mark.parametrize("kw", [dict(rank=12), dict(rank=0), dict(rank=136), dict(K=24), dict(K=0), dict(N=0), dict(M=-1),
+@pytest.mark.parametrize("kw", [dict(rank=12), dict(rank=0), dict(rank=136), dict(K=24), dict(K=0), dict(N=0), dict(N=(1 << 24) + 1), dict(K=(1 << 24) + 16), dict(M=-1),
                                 dict(M=(1 << 24) + 1), dict(n=0), dict(n=4097)])
 def test_lora_add_refuses_shapes(m2, kw):
     assert _lora(m2, **kw) == m2.M2_ESHAPE
