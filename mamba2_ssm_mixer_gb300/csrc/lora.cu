@@ -620,7 +620,10 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
 namespace {
 template <int NK>
 struct Up {
-  static constexpr int kCols = NK <= 4 ? 256 : 128;
+  #ifndef V_UC
+#define V_UC 256
+#endif
+  static constexpr int kCols = NK <= 2 ? V_UC : NK == 4 ? 256 : 128;
   static constexpr int kRowBytes = kCols * 2 + 64;   // of an unaligned row in shared memory (pieces, and no bank conflicts)
 };
 }  // namespace
@@ -635,8 +638,9 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
   const int at = blockIdx.x / chunks, c0 = (blockIdx.x - at * chunks) * kCols, c_hi = min(N, c0 + kCols);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3, mg = warp & 3;
-  pdl_wait();
-  pdl_trigger();
+  // What k_lora_group wrote, y and B are read ahead of the wait: the kernel
+  // waited for (k_lora_down, which writes none of them) itself waited for
+  // everything before it prior to letting this one start.
   const int have = *n_tiles;
   const TileInfo tile = info[at];
   int row[2];
@@ -645,11 +649,16 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
   // (unaligned: the warp moves rows warp + 8 i of the tile, known to lane i)
   int moved = 0;
   if constexpr (!kVec) moved = row_of[(size_t)at * kTile + warp + kLoWarps * (lane & 7)];
-  if (at >= have) return;   // (what was read past the last tile is not used)
+  if (at >= have) {   // (what was read past the last tile is not used)
+    pdl_wait();
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     if (mg * 16 + g + 8 * h >= tile.rows) row[h] = -1;
   if (tile.adapter < 0) {
+    pdl_wait();
+    pdl_trigger();
     if (out == y) return;
     for (int r = warp; r < tile.rows; r += kLoWarps) {
       const size_t o = (size_t)row_of[(size_t)at * kTile + r] * N;
@@ -706,6 +715,8 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
       for (int n = tid; n < kCols; n += kLoThreads)
         *reinterpret_cast<uint4*>(bsm + n * pitch + rank * 2) = make_uint4(0u, 0u, 0u, 0u);
   }
+  pdl_wait();
+  pdl_trigger();
   uint4 th[NK], tl[NK];   // t of the warp's 16 rows
   const uint4* fp = frag + ((size_t)at * 4 + mg) * NK * 64 + lane;
 #pragma unroll
