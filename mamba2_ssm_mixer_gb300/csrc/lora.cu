@@ -489,12 +489,23 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
                                                           const int32_t* __restrict__ row_of,
                                                           const TileInfo* __restrict__ info,
                                                           const int* __restrict__ n_tiles, int rank, int K, int splits,
-                                                          uint4* __restrict__ frag) {
+                                                          size_t x_ahead, uint4* __restrict__ frag) {
   extern __shared__ __align__(128) uint8_t ld_smem[];
   constexpr int kItems = 4 * NK * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int at = blockIdx.x / splits, split = blockIdx.x - at * splits;
   const int piece = tid & 7, r0 = tid >> 3;                  // this thread's pieces: rows r0 + 32 i
+  // While one CTA groups the rows the others bring x to L2, each a share (x is
+  // older than the grouping kernel, which waited for it before letting this
+  // one start).
+  if (warp == 0) {
+    const size_t share = (x_ahead / gridDim.x / 32) & ~(size_t)15;
+    if (share)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                       reinterpret_cast<uint64_t>(x) + ((size_t)blockIdx.x * 32 + lane) * share),
+                   "r"((uint32_t)share)
+                   : "memory");
+  }
   pdl_wait();
   pdl_trigger();
   const int have = *n_tiles;
@@ -620,10 +631,7 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
 namespace {
 template <int NK>
 struct Up {
-  #ifndef V_UC
-#define V_UC 256
-#endif
-  static constexpr int kCols = NK <= 2 ? V_UC : NK == 4 ? 256 : 128;
+  static constexpr int kCols = NK <= 4 ? 256 : 128;
   static constexpr int kRowBytes = kCols * 2 + 64;   // of an unaligned row in shared memory (pieces, and no bank conflicts)
 };
 }  // namespace
@@ -877,6 +885,8 @@ cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights&
   static_assert(kDownStages * (kTile + 8) * 128 >= 4 * 4 * 32 * 16, "the parts fit where the stages were");
   cudaError_t e = ensure_smem_optin((const void*)k_lora_down<NK>, kDownStages * (kTile + 16 * NK) * 128);
   if (e != cudaSuccess) return e;
+  constexpr size_t kXAhead = (size_t)64 << 20;   // half of L2: a larger x would push itself out
+  const size_t x_bytes = (size_t)M * K * 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)splits * (unsigned)max_tiles);
   cfg.blockDim = dim3(kLoThreads);
@@ -891,7 +901,7 @@ cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights&
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, k_lora_down<NK>, x, w.a, w.scale, (const int32_t*)ws.row_of, (const TileInfo*)ws.info,
-                         (const int*)ws.n_tiles, w.rank, K, splits, ws.frag);
+                         (const int*)ws.n_tiles, w.rank, K, splits, x_bytes <= kXAhead ? x_bytes : 0, ws.frag);
   if (e != cudaSuccess) return e;
   constexpr int kCols = Up<NK>::kCols;
   const int chunks = (N + kCols - 1) / kCols;
