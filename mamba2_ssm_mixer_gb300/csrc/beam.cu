@@ -4,13 +4,18 @@
 //
 // k_beam_rows: a CTA takes one chunk of one row, held packed in registers: each
 // warp's maximum and sum of exponentials (online softmax, joined later), and
-// the chunk's k best tokens.  The k best need no sort: if every one of the 8 warps
-// has ceil(k / 8) threads whose own maximum is at least tau, then at least k
-// elements of the chunk are >= tau, so only those are looked at further (for
-// unordered logits a small multiple of k).  tau is the least, over the warps,
-// of the warp's ceil(k / 8)-th largest thread maximum: a few warp reductions.
-// The survivors are ranked by counting.  Where equal values leave more
-// survivors than fit, the k best are taken one after another instead.
+// the chunk's k best tokens.  The k best need no sort: if every one of the 8
+// warps has ceil(k / 8) threads whose own maximum is at least tau, then at
+// least k elements of the chunk are >= tau, so only those are looked at further
+// (for unordered logits a small multiple of k).  tau is the least, over the
+// warps, of the warp's ceil(k / 8)-th largest thread maximum: a few warp
+// reductions.  The survivors are ranked by counting.  Where equal values leave
+// more survivors than fit, the k best are taken one after another instead.
+// Bound by instruction issue (unpacking, one multiply-add, one exp2 and one add
+// per token, half of them on pairs) at about twice the time of reading the
+// logits: 64 x 8 rows of 131072 bf16 tokens, with the merge, in 34.7 us; 16 KB
+// chunks instead of 32 took 43, a first form that kept the row unpacked in
+// registers and summed in f64 181.
 // k_beam_merge: a CTA per request joins the chunks' sums to lse_b, and selects
 // among the chunks' survivors by the 64-bit value in the same way.
 //

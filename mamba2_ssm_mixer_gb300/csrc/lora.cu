@@ -5,21 +5,19 @@
 // small change (2 rank (K + N) operations per row); what bounds the call is
 // reading y and writing out once, or, in a decode batch, reading each named
 // adapter once.  Two forms:
-//  - up to kFewRows rows: one kernel, one 8-CTA cluster per (up to kUnit rows
+//  - up to kFewRows rows: one kernel, one 4-CTA cluster per (up to kUnit rows
 //    of one adapter, slice of N).  Which rows share an adapter is found by
 //    each cluster itself from the batch's ids (a ballot), so there is no
 //    sorting launch and no workspace, and a shared adapter is read once per
-//    kUnit rows.  Each CTA forms rank / 8 of t's entries over all of K, hands
-//    them to the cluster through distributed shared memory, and adds its part
-//    of N.  All in f32.
-//  - more rows: k_lora_group sorts the rows by adapter into tiles of 64,
-//    k_lora_down forms t on the tensor cores (K split over CTAs, the parts
-//    added in order), k_lora_up streams y through registers in 16-byte pieces
-//    and adds B t from tensor-core fragments.
-// mma.sync is enough: the tensor work is a few per cent of the stream's time.
+//    kUnit rows.
+//  - more rows: k_lora_group deals the rows out to tiles of 64 of one adapter
+//    (while the next kernel's CTAs bring x to L2), k_lora_down forms t on the
+//    tensor cores, K split over a cluster, and k_lora_up streams y past B t.
 // t is summed in f32 and enters the second product as two bf16 parts (its
 // rounding and the remainder, 2^-17 of it in all), so no accuracy is lost to
-// the 16-bit operands.
+// the 16-bit operands.  mma.sync: up to rank 32 the tensor work hides behind
+// the stream of y (8192 rows, 2688 -> 10304: rank 16 70 us, floor 57; rank 32
+// 76); at rank 64 and 128 its two passes show (97 and 198).
 #include <algorithm>
 #include <type_traits>
 
@@ -90,20 +88,23 @@ __device__ __forceinline__ void cp_wait() {
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Up to kFewRows rows.  Grid (8 x slices of N, M), clusters of 4 along x; the
+// Up to kFewRows rows.  Grid (4 x slices of N, M), clusters of 4 along x; the
 // cluster of row m goes on if m is the first of a run of 8 among the rows of
-// its adapter in its window of 256 rows (a ballot in every warp, no barrier).  Both products put the adapter's matrix on the 16-wide side of
-// m16n8k16 and the rows (up to 8) on the other, and take their operands
-// straight from global memory: the order of the summed index inside an MMA is
-// free, so each lane loads whole 8- or 16-byte pieces.  A x: K in 32-wide
-// blocks over the cluster's 32 warps, the parts summed in shared memory, then
-// over the CTAs' shared memories.  B t: 16 columns per warp and step, the
-// first steps' B and y on their way before t is known.
-// A decode batch is bound by reading each adapter once and by latency.
-// Adapters of rank 16, 2688 -> 10304: 1 to 8 rows 4.6 us, 64 rows with 64
-// adapters 10.8 (floor 4.4); a form on FMA units, with ten times the
-// instructions for unpacking, took 16.8 for those, clusters of 8 and of 2 13.2
-// and 11.3, bringing B's slice to L2 ahead 0.3 to 1.2 more.
+// its adapter in its window of 256 rows (a ballot in every warp, no barrier).
+// Both products put the adapter's matrix on the 16-wide side of m16n8k16 and
+// the rows (up to 8) on the other, and take their operands straight from
+// global memory: the order of the summed index inside an MMA is free, so each
+// lane loads whole 8- or 16-byte pieces.  A x: K in 32-wide blocks over the
+// cluster's 32 warps, the parts summed in shared memory, then over the CTAs'
+// shared memories.  B t: 16 columns per warp and step, the first steps' B and
+// y on their way before t is known.
+// A decode batch is bound by reading each adapter once and, more, by latency
+// (ids, operands, the cluster's sum, the columns: each a trip).  Adapters of
+// rank 16, 2688 -> 10304: 1 to 8 rows 4.6 us, 64 rows with 64 adapters 10.9
+// (floor 4.4); a form on FMA units, with ten times the instructions for
+// unpacking, took 16.8 for those, clusters of 8 and of 2 13.2 and 11.3, 32
+// columns per step 10.7 (but 0.7 more at rank 64), bringing B's slice to L2
+// ahead 0.3 to 1.2 more.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kFewRows = 256, kFewMost = 512;   // see few_rows
@@ -115,11 +116,10 @@ constexpr int kUnit = 8;   // rows that share the reads of an adapter
 // NT: rank / 16 rounded up to a power of two.  kPair: y and out move two
 // columns at a time (N even, 4-byte aligned).
 template <int NT, bool kPair>
-__global__ void __launch_bounds__(kLoThreads, NT <= 4 ? 2 : 1) k_lora_few(const uint16_t* y, const uint16_t* __restrict__ x,
-                                                         const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
-                                                         const float* __restrict__ scale,
-                                                         const int32_t* __restrict__ ids, int n_adapters, int rank,
-                                                         uint16_t* out, int M, int N, int K, int* err) {
+__global__ void __launch_bounds__(kLoThreads, NT <= 4 ? 2 : 1) k_lora_few(
+    const uint16_t* y, const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
+    const float* __restrict__ scale, const int32_t* __restrict__ ids, int n_adapters, int rank, uint16_t* out, int M,
+    int N, int K, int* err) {
   constexpr int kAheadF = NT == 1 ? 8 : NT == 2 ? 4 : 1;   // steps of B and y under way
   __shared__ int rows_s[kUnit];
   __shared__ __align__(16) float red[kLoWarps][NT * 128];
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
 }
 
 // ---------------------------------------------------------------------------
-// out of a tile and kUpCols columns: y + B t.  Column n of a 32-column group
+// out of a tile and Up::kCols columns: y + B t.  Column n of a 32-column group
 // sits at MMA j = (n % 8) / 2, column 2 (n / 8) + n % 2, so that a thread's
 // accumulators of the four MMAs are 8 consecutive columns: y and out move in
 // 16-byte pieces, 64 bytes of a row per four lanes.  Many small CTAs: the
