@@ -11,11 +11,13 @@
 // warps, of the warp's ceil(k / 8)-th largest thread maximum: a few warp
 // reductions.  The survivors are ranked by counting.  Where equal values leave
 // more survivors than fit, the k best are taken one after another instead.
-// Bound by instruction issue (unpacking, one multiply-add, one exp2 and one add
-// per token, half of them on pairs) at about twice the time of reading the
-// logits: 64 x 8 rows of 131072 bf16 tokens, with the merge, in 34.7 us; 16 KB
-// chunks instead of 32 took 43, a first form that kept the row unpacked in
-// registers and summed in f64 181.
+// Bound by a chunk's way through the CTA (load, sum, select: the sums alone take
+// 25 us of the 33 below, issue and exp2 unit half used): 64 x 8 rows of 131072
+// bf16 tokens, with the merge, in 33 us (floor 18.5); 16 KB chunks instead of
+// 32 take 36 (more selections), three and six CTAs per SM instead of four 37
+// and 43.  A CTA over several chunks that keeps its list from one to the next
+// took 47 to 64, a first form that kept the row unpacked in registers and
+// summed in f64 181.
 // k_beam_merge: a CTA per request joins the chunks' sums to lse_b, and selects
 // among the chunks' survivors by the 64-bit value in the same way.
 //
@@ -34,7 +36,8 @@ namespace {
 constexpr int kBeThreads = 256;
 constexpr int kBeWarps = kBeThreads / 32;
 constexpr int kCap = 1024;   // survivors ranked by counting
-constexpr int kCapV = 512;   // vectors with survivors among their elements
+constexpr int kCapV = 64;    // a warp's vectors with survivors among their elements
+constexpr int kRankStep = 8; // keys a ranking thread compares per step
 
 struct ChunkSum {
   float m, s;   // maximum and sum of exp(x - m) of one chunk
@@ -159,29 +162,29 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 // 16-byte boundary.  Keys go to [request][rank][split][beam], the order in
 // which the merge's warps each meet every beam and every rank.
 template <typename T, int VPT, bool kAligned>
-__global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 5 : 6) k_beam_rows(const T* __restrict__ logits, size_t stride, int vocab,
+__global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 4 : 6) k_beam_rows(const T* __restrict__ logits, size_t stride, int vocab,
                                                           const float* __restrict__ scores,
                                                           const uint8_t* __restrict__ done, int k, int beams,
                                                           int chunk, uint64_t* __restrict__ keys,
                                                           ChunkSum* __restrict__ sums) {
   using E = Elem<T>;
   constexpr int V = E::kVec;
-  __shared__ uint64_t cand[kCap];
-  __shared__ uint4 vecs[kCapV];
-  __shared__ int vec_at[kCapV];
+  __shared__ __align__(16) uint64_t cand[kCap + kRankStep];
+  __shared__ uint4 vecs[kBeWarps][kCapV];
+  __shared__ int vec_at[kBeWarps][kCapV];
   __shared__ float wm[kBeWarps], ws[kBeWarps];
   __shared__ __align__(16) uint32_t wtau[kBeWarps];
-  __shared__ int n_vec, n_cand;
+  __shared__ int n_cand;
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.y, split = blockIdx.x, splits = gridDim.x;
+  const int row = blockIdx.z * beams + blockIdx.y, split = blockIdx.x, splits = gridDim.x;
   const float score = scores[row];
   const bool ended = done && done[row];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* base = logits + (size_t)row * stride;
   const uint32_t off = kAligned ? 0u : (uint32_t)((uintptr_t)base & 15u);
   const int first = split * chunk, end = min(vocab, first + chunk);
-  if (tid == 0) n_vec = n_cand = 0;
+  if (tid == 0) n_cand = 0;
   if (!isfinite(score) || ended) return;   // no candidates here (the merge reads nothing either)
 
   uint4 q[VPT];
@@ -285,43 +288,57 @@ __global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 5 : 6) k_beam_rows(cons
     for (int i = 0; i < kBeWarps; ++i) t = min(t, wtau[i]);
     // (still none: too few threads have any, and all their tokens survive)
   }
-  // survivors: >= tau and above -inf.  First the few vectors that hold some,
-  // then their elements, one a thread (in place, each warp would step through
-  // all elements of its vectors for one lane's sake).
+  // survivors: >= tau and above -inf.  First the few vectors that hold some
+  // are put side by side, then their elements are looked at, one a lane (in
+  // place, the warp would step through all elements of a vector for one
+  // lane's sake).
   const float low = unord32(max(t, kOrdNegInf + 1u));
+  int nv = 0;
 #pragma unroll
-  for (int j = 0; j < VPT; ++j)
-    if (vm[j] >= low) {
-      const int at = atomicAdd(&n_vec, 1);
-      if (at < kCapV) vecs[at] = q[j], vec_at[at] = first + (j * kBeThreads + tid) * V;
+  for (int j = 0; j < VPT; ++j) {
+    const uint32_t hit = __ballot_sync(0xffffffffu, vm[j] >= low);
+    if (hit) {
+      const int at = nv + __popc(hit & ((1u << lane) - 1u));
+      if (vm[j] >= low && at < kCapV) vecs[warp][at] = q[j], vec_at[warp][at] = first + (j * kBeThreads + tid) * V;
+      nv += __popc(hit);
     }
-  __syncthreads();
-  const int nv = n_vec;
-  if (nv <= kCapV)
-    for (int i = tid; i < nv * V; i += kBeThreads) {
-      const float x = E::load(reinterpret_cast<const T*>(vecs) + i);
+  }
+  __syncwarp();
+  if (nv > kCapV) {
+    if (lane == 0) atomicAdd(&n_cand, kCap + 1);
+  } else {
+    for (int i = lane; i < nv * V; i += 32) {
+      const float x = E::load(reinterpret_cast<const T*>(vecs[warp]) + i);
       if (x >= low) {
         const int at = atomicAdd(&n_cand, 1);
-        const uint32_t token = (uint32_t)(vec_at[i / V] + i % V);
+        const uint32_t token = (uint32_t)(vec_at[warp][i / V] + i % V);
         if (at < kCap) cand[at] = ((uint64_t)ord32(x + 0.f) << 32) | (0xffffffffu - token);
       }
     }
+  }
   __syncthreads();
-  const int n = nv <= kCapV ? n_cand : kCap + 1;
-  const int request = row / beams;
-  uint64_t* out = keys + (size_t)request * beams * splits * k + split * beams + (row - request * beams);
+  const int n = n_cand;
+  uint64_t* out = keys + (size_t)blockIdx.z * beams * splits * k + split * beams + blockIdx.y;
   const int next = splits * beams;   // from one rank to the next
   if (n <= kCap) {
-    for (int i0 = 0; i0 < n; i0 += kBeThreads / 8) {   // eight threads count a candidate's betters
-      const int i = i0 + tid / 8;
-      const uint64_t mine = i < n ? cand[i] : ~0ull;
+    // a thread counts the betters of its candidate, a few keys at a time
+    // (zeros past the last: each warp that counts puts them there itself)
+    for (int i0 = warp * 32; i0 < n; i0 += kBeThreads) {
+      if (lane < kRankStep) cand[n + lane] = 0;
+      __syncwarp();
+      const uint64_t mine = i0 + lane < n ? cand[i0 + lane] : ~0ull;
       int rank = 0;
-      for (int j = tid % 8; j < n; j += 8) rank += cand[j] > mine;
+      for (int j = 0; j < n; j += kRankStep) {
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-      if (i < n && tid % 8 == 0 && rank < k) out[(size_t)rank * next] = mine;
+        for (int e = 0; e < kRankStep; e += 2) {
+          const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(&cand[j + e]);
+          rank += w.x > mine;
+          rank += w.y > mine;
+        }
+      }
+      if (i0 + lane < n && rank < k) out[rank * next] = mine;
     }
-    for (int i = n + tid; i < k; i += kBeThreads) out[(size_t)i * next] = 0;
+    for (int i = n + tid; i < k; i += kBeThreads) out[i * next] = 0;
   } else {   // many equal values: the greatest key below the last one, k times
     uint64_t last = ~0ull;
     for (int i = 0; i < k; ++i) {
@@ -344,7 +361,7 @@ __global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 5 : 6) k_beam_rows(cons
       __syncthreads();
 #pragma unroll
       for (int w = 0; w < kBeWarps; ++w) best = cand[w] > best ? cand[w] : best;
-      if (tid == 0) out[(size_t)i * next] = best;
+      if (tid == 0) out[i * next] = best;
       last = best;
     }
   }
@@ -565,7 +582,7 @@ template <typename T, int VPT, bool kAligned>
 cudaError_t launch_rows(const void* logits, size_t stride, int rows, int vocab, const float* scores, const uint8_t* done,
                         int k, int beams, int splits, uint64_t* keys, ChunkSum* sums, cudaStream_t st) {
   const int vec = Elem<T>::kVec, chunk = ((vocab + splits - 1) / splits + vec - 1) / vec * vec;   // even parts
-  return launch_pdl(k_beam_rows<T, VPT, kAligned>, dim3((unsigned)splits, (unsigned)rows), dim3(kBeThreads), 0, st,
+  return launch_pdl(k_beam_rows<T, VPT, kAligned>, dim3((unsigned)splits, (unsigned)beams, (unsigned)(rows / beams)), dim3(kBeThreads), 0, st,
                     static_cast<const T*>(logits), stride, vocab, scores, done, k, beams, chunk, keys, sums);
 }
 
