@@ -12,7 +12,8 @@
 //    kUnit rows.
 //  - more rows: k_lora_group deals the rows out to tiles of 64 of one adapter
 //    (while the next kernel's CTAs bring x to L2), k_lora_down forms t on the
-//    tensor cores, K split over a cluster, and k_lora_up streams y past B t.
+//    tensor cores, K split over a cluster, and k_lora_up streams y past B t;
+//    or, up to rank 32 and a middling batch, k_lora_tile does both.
 // t is summed in f32 and enters the second product as two bf16 parts (its
 // rounding and the remainder, 2^-17 of it in all), so no accuracy is lost to
 // the 16-bit operands.  mma.sync: up to rank 32 the tensor work hides behind
@@ -480,45 +481,29 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank)
       : "memory");
   return v;
 }
-}  // namespace
 
 // NK: 16-wide steps of the rank (rank / 16 rounded up to a power of two).
 template <int NK>
-__global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a,
-                                                          const float* __restrict__ scale,
-                                                          const int32_t* __restrict__ row_of,
-                                                          const TileInfo* __restrict__ info,
-                                                          const int* __restrict__ n_tiles, int rank, int K, int splits,
-                                                          size_t x_ahead, uint4* __restrict__ frag) {
-  extern __shared__ __align__(128) uint8_t ld_smem[];
-  constexpr int kItems = 4 * NK * 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int at = blockIdx.x / splits, split = blockIdx.x - at * splits;
-  const int piece = tid & 7, r0 = tid >> 3;                  // this thread's pieces: rows r0 + 32 i
-  // While one CTA groups the rows the others bring x to L2, each a share (x is
-  // older than the grouping kernel, which waited for it before letting this
-  // one start).
-  if (warp == 0) {
-    const size_t share = (x_ahead / gridDim.x / 32) & ~(size_t)15;
-    if (share)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                       reinterpret_cast<uint64_t>(x) + ((size_t)blockIdx.x * 32 + lane) * share),
-                   "r"((uint32_t)share)
-                   : "memory");
-  }
-  pdl_wait();
-  pdl_trigger();
-  const int have = *n_tiles;
-  const TileInfo tile = info[at];
-  int src[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) src[i] = row_of[(size_t)at * kTile + r0 + 32 * i];
-  if (at >= have || tile.adapter < 0) return;   // (what was read past the last tile is not used)
+struct Down {
+  static constexpr int kItems = 4 * NK * 32;
+};
+
+// The part of a tile's A x that K block range `split` of `splits` makes, in
+// shared memory as [K half][8-wide half of the step][16-row group][step][lane].
+// src: the rows of this thread's pieces.  after(i), i < kDownStages - 1, may
+// issue copies in place of the last blocks' (one group each, not waited for).
+template <int NK, typename F>
+__device__ __forceinline__ float4* down_part(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, int rank,
+                                             int K, int split, int splits, const TileInfo& tile, const int (&src)[2],
+                                             uint8_t* smem, F after) {
+  constexpr int kItems = Down<NK>::kItems;
   const int arows = (rank + 15) & ~15;                       // rows of an A stage (the last 8 may be unused)
   const uint32_t stage = (uint32_t)(kTile + arows) * 128;
-  const uint32_t s0 = smem_u32(ld_smem);
+  const uint32_t s0 = smem_u32(smem);
   const int kblocks = (K + kDownK - 1) / kDownK;
   const int kb0 = kblocks * split / splits, nk = kblocks * (split + 1) / splits - kb0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int piece = tid & 7, r0 = tid >> 3;   // this thread's pieces: rows r0 + 32 i
   const uint16_t* xr[2];
   bool xin[2];
 #pragma unroll
@@ -545,6 +530,7 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
 #pragma unroll
   for (int s = 0; s < kDownStages - 1; ++s) {
     if (s < nk) load(s, s);
+    else after(s - nk);
     cp_commit();
   }
   const int mg = warp & 3, kh = warp >> 2;
@@ -564,6 +550,7 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
     __syncthreads();
     const int s = kb % kDownStages;
     if (kb + kDownStages - 1 < nk) load(kb + kDownStages - 1, (kb + kDownStages - 1) % kDownStages);
+    else after(kb + kDownStages - 1 - nk);
     cp_commit();
     if (mg * 16 >= tile.rows) continue;   // no rows for this warp
     const uint32_t xs = s0 + s * stage;
@@ -581,12 +568,78 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
         }
     }
   }
-  cp_wait<0>();
   __syncthreads();
-  float4* part = reinterpret_cast<float4*>(ld_smem);   // [K half][8-wide half of the step][16-row group][step][lane]
+  float4* part = reinterpret_cast<float4*>(smem);
 #pragma unroll
   for (int i = 0; i < 2 * NK; ++i)
     part[(kh * 2 + (i & 1)) * kItems + (mg * NK + i / 2) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  return part;
+}
+
+__device__ __forceinline__ void st_cluster_u4(uint32_t addr, uint32_t rank, const uint4& v) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+      "st.shared::cluster.v4.u32 [ra], {%2, %3, %4, %5};\n\t}" ::"r"(addr),
+      "r"(rank), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+      : "memory");
+}
+
+// t of item i of a tile (see k_lora_down) from the cluster's parts.
+template <int NK>
+__device__ __forceinline__ void gather_t(const float4* part, int i, int splits, float sc, uint4* hi, uint4* lo) {
+  float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int c = 0; c < splits; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4* p = part + e * Down<NK>::kItems + i;
+      const float4 w = splits > 1 ? ld_cluster_f32x4(smem_u32(p), (uint32_t)c) : *p;
+      float4& t = v[e & 1];
+      t.x += w.x, t.y += w.y, t.z += w.z, t.w += w.w;
+    }
+  // rows g, g + 8 of entries 2 q, + 1; the same of 8 + 2 q, + 1
+  split_bf16x2(v[0].x * sc, v[0].y * sc, &hi->x, &lo->x);
+  split_bf16x2(v[0].z * sc, v[0].w * sc, &hi->y, &lo->y);
+  split_bf16x2(v[1].x * sc, v[1].y * sc, &hi->z, &lo->z);
+  split_bf16x2(v[1].z * sc, v[1].w * sc, &hi->w, &lo->w);
+}
+
+// While one CTA groups the rows the next kernel's bring x to L2, each a share
+// (x is older than the grouping kernel, which waited for it before letting
+// this one start).
+__device__ __forceinline__ void x_to_l2(const uint16_t* x, size_t bytes) {
+  if (threadIdx.x >= 32) return;
+  const size_t share = (bytes / gridDim.x / 32) & ~(size_t)15;
+  if (share)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                     reinterpret_cast<uint64_t>(x) + ((size_t)blockIdx.x * 32 + threadIdx.x) * share),
+                 "r"((uint32_t)share)
+                 : "memory");
+}
+
+}  // namespace
+
+template <int NK>
+__global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a,
+                                                          const float* __restrict__ scale,
+                                                          const int32_t* __restrict__ row_of,
+                                                          const TileInfo* __restrict__ info,
+                                                          const int* __restrict__ n_tiles, int rank, int K, int splits,
+                                                          size_t x_ahead, uint4* __restrict__ frag) {
+  extern __shared__ __align__(128) uint8_t ld_smem[];
+  constexpr int kItems = Down<NK>::kItems;
+  const int tid = threadIdx.x;
+  const int at = blockIdx.x / splits, split = blockIdx.x - at * splits;
+  x_to_l2(x, x_ahead);
+  pdl_wait();
+  pdl_trigger();
+  const int have = *n_tiles;
+  const TileInfo tile = info[at];
+  int src[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) src[i] = row_of[(size_t)at * kTile + (tid >> 3) + 32 * i];
+  if (at >= have || tile.adapter < 0) return;   // (what was read past the last tile is not used)
+  const float4* part = down_part<NK>(x, a, rank, K, split, splits, tile, src, ld_smem, [](int) {});
   const float sc = scale ? scale[tile.adapter] : 1.f;
   if (splits > 1) {
     lo_cluster_arrive();
@@ -596,19 +649,8 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
   }
   uint4* out = frag + (size_t)at * kItems * 2;
   for (int i = split * kLoThreads + tid; i < kItems; i += splits * kLoThreads) {
-    float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int c = 0; c < splits; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 w = splits > 1 ? ld_cluster_f32x4(smem_u32(part + e * kItems + i), (uint32_t)c) : part[e * kItems + i];
-        float4& t = v[e & 1];
-        t.x += w.x, t.y += w.y, t.z += w.z, t.w += w.w;
-      }
-    uint4 hi, lo;   // rows g, g + 8 of entries 2 q, + 1; the same of 8 + 2 q, + 1
-    split_bf16x2(v[0].x * sc, v[0].y * sc, &hi.x, &lo.x);
-    split_bf16x2(v[0].z * sc, v[0].w * sc, &hi.y, &lo.y);
-    split_bf16x2(v[1].x * sc, v[1].y * sc, &hi.z, &lo.z);
-    split_bf16x2(v[1].z * sc, v[1].w * sc, &hi.w, &lo.w);
+    uint4 hi, lo;
+    gather_t<NK>(part, i, splits, sc, &hi, &lo);
     uint4* o = out + (size_t)(i >> 5) * 64 + (i & 31);
     o[0] = hi;
     o[32] = lo;
@@ -617,6 +659,149 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
     lo_cluster_arrive();
     lo_cluster_wait();
   }
+}
+
+// ---------------------------------------------------------------------------
+// Both products of a tile in one kernel, where the tiles' clusters fit on the
+// GPU at once (see lora_one_kernel): the CTAs that shared K share the columns,
+// in 64-wide steps through a ring of stages.  The first steps' y and B are under
+// way while t is joined.  No launch and no tail between the products: 5669 rows
+// 4096 -> 2688 in 31.6 us at rank 32, 27.9 at rank 16 (with the two kernels 33.5
+// and 31.9; floor 16.3).  Bringing each row's y to L2 further ahead took 3 more.
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kStepCols = 64;
+constexpr int kStepStages = kDownStages;   // (the first kDownStages - 1 go out in down_part's last groups)
+
+template <int NK>
+struct Step {
+  static constexpr int kY = 2 * kLoThreads * 16;
+  static constexpr int kBytes = kY + kStepCols * (32 * NK + 16);
+};
+}  // namespace
+
+template <int NK>
+__global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
+    const uint16_t* y, const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
+    const float* __restrict__ scale, const int32_t* __restrict__ row_of, const TileInfo* __restrict__ info,
+    const int* __restrict__ n_tiles, int rank, int N, int K, int splits, size_t x_ahead, uint16_t* out) {
+  extern __shared__ __align__(128) uint8_t lt_smem[];
+  constexpr int kItems = Down<NK>::kItems;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3, mg = warp & 3;
+  const int at = blockIdx.x / splits, split = blockIdx.x - at * splits;
+  x_to_l2(x, x_ahead);
+  pdl_wait();
+  pdl_trigger();
+  const int have = *n_tiles;
+  const TileInfo tile = info[at];
+  int src[2], row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    src[i] = row_of[(size_t)at * kTile + (tid >> 3) + 32 * i];
+    row[i] = row_of[(size_t)at * kTile + mg * 16 + g + 8 * i];
+  }
+  if (at >= have) return;   // (what was read past the last tile is not used)
+  const int units = (N + kStepCols - 1) / kStepCols;
+  const int u0 = (int)((long long)units * split / splits), nu = (int)((long long)units * (split + 1) / splits) - u0;
+  if (tile.adapter < 0) {
+    if (out == y) return;
+    for (int r = warp; r < tile.rows; r += kLoWarps) {
+      const size_t o = (size_t)row_of[(size_t)at * kTile + r] * N;
+      for (int c = u0 * kStepCols + lane * 8; c < min(N, (u0 + nu) * kStepCols); c += 256)
+        *reinterpret_cast<uint4*>(out + o + c) = *reinterpret_cast<const uint4*>(y + o + c);
+    }
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (mg * 16 + g + 8 * h >= tile.rows) row[h] = -1;
+  // a step: y into slots of each thread's own, B with column n of a 32-column
+  // group at MMA j = (n % 8) / 2, column 2 (n / 8) + n % 2 (as in k_lora_up)
+  const int arows = (rank + 15) & ~15, pitch = rank * 2 + 16, rv = rank / 8;
+  uint8_t* steps = lt_smem + kDownStages * (kTile + arows) * 128;
+  const int bn = tid / rv, bv = tid - bn * rv;   // this thread's piece of B
+  const int bpos = (bn & ~31) | ((bn >> 1) & 3) << 3 | ((bn >> 3) & 3) << 1 | (bn & 1);
+  const uint16_t* bt = b + (size_t)tile.adapter * N * rank + bv * 8;
+  const int cw = (warp >> 2) * 32 + q * 8;       // this thread's columns of a step
+  auto load = [&](int u) {
+    if (u >= nu) return;
+    uint8_t* st = steps + (u % kStepStages) * Step<NK>::kBytes;
+    const int c0 = (u0 + u) * kStepCols;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (row[h] >= 0 && c0 + cw < N)
+        cp16(smem_u32(st + (h * kLoThreads + tid) * 16), y + (size_t)row[h] * N + c0 + cw, true);
+    if (bn < kStepCols) {
+      const bool in = c0 + bn < N;
+      cp16(smem_u32(st + Step<NK>::kY + bpos * pitch + bv * 16), in ? bt + (size_t)(c0 + bn) * rank : b, in);
+    }
+  };
+  if (rank & 8)   // the last 16-wide step reads 8 entries past the rank: zeros
+    for (int i = tid; i < kStepStages * kStepCols; i += kLoThreads)
+      *reinterpret_cast<uint4*>(steps + i / kStepCols * Step<NK>::kBytes + Step<NK>::kY + i % kStepCols * pitch + rank * 2) =
+          make_uint4(0u, 0u, 0u, 0u);
+  const float4* part = down_part<NK>(x, a, rank, K, split, splits, tile, src, lt_smem, load);
+  const float sc = scale ? scale[tile.adapter] : 1.f;
+  lo_cluster_arrive();
+  lo_cluster_wait();
+  // each CTA joins its share of the items and hands them to all (every CTA
+  // joining all of them took 3 to 20 us more)
+  uint4* tf = reinterpret_cast<uint4*>(lt_smem + 4 * kItems * 16);
+  for (int i = kItems * split / splits + tid; i < kItems * (split + 1) / splits; i += kLoThreads) {
+    uint4 hi, lo;
+    gather_t<NK>(part, i, splits, sc, &hi, &lo);
+    for (int c = 0; c < splits; ++c) {
+      st_cluster_u4(smem_u32(tf + i), (uint32_t)c, hi);
+      st_cluster_u4(smem_u32(tf + kItems + i), (uint32_t)c, lo);
+    }
+  }
+  lo_cluster_arrive();
+  lo_cluster_wait();
+  uint4 th[NK], tl[NK];   // t of the warp's 16 rows
+#pragma unroll
+  for (int s = 0; s < NK; ++s) th[s] = tf[(mg * NK + s) * 32 + lane], tl[s] = tf[kItems + (mg * NK + s) * 32 + lane];
+  const uint32_t boff = Step<NK>::kY + (uint32_t)((warp >> 2) * 32 + (lane & 7) + (lane >> 4) * 8) * pitch +
+                        (uint32_t)((lane >> 3) & 1) * 16;
+  for (int u = 0; u < nu; ++u) {
+    cp_wait<kStepStages - 2>();
+    __syncthreads();
+    load(u + kStepStages - 1);
+    cp_commit();
+    if (mg * 16 >= tile.rows) continue;   // no rows for this warp
+    const uint8_t* st = steps + (u % kStepStages) * Step<NK>::kBytes;
+    const uint32_t bs = smem_u32(st) + boff;
+    float acc[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+    for (int s = 0; s < NK; ++s)
+      if (s * 16 < rank) {
+#pragma unroll
+        for (int jp = 0; jp < 2; ++jp) {
+          const uint32_t lo[4] = {tl[s].x, tl[s].y, tl[s].z, tl[s].w}, hi[4] = {th[s].x, th[s].y, th[s].z, th[s].w};
+          uint32_t bf[4];
+          ldsm4(bf, bs + (uint32_t)(jp * 16) * pitch + s * 32);
+          mma16816(acc[2 * jp], lo, bf[0], bf[1]);
+          mma16816(acc[2 * jp + 1], lo, bf[2], bf[3]);
+          mma16816(acc[2 * jp], hi, bf[0], bf[1]);
+          mma16816(acc[2 * jp + 1], hi, bf[2], bf[3]);
+        }
+      }
+    const int n = (u0 + u) * kStepCols + cw;
+    if (n >= N) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (row[h] < 0) continue;
+      const uint4 yv = *reinterpret_cast<const uint4*>(st + (h * kLoThreads + tid) * 16);
+      *reinterpret_cast<uint4*>(out + (size_t)row[h] * N + n) =
+          make_uint4(pack_bf16x2(lo_f(yv.x) + acc[0][2 * h], hi_f(yv.x) + acc[0][2 * h + 1]),
+                     pack_bf16x2(lo_f(yv.y) + acc[1][2 * h], hi_f(yv.y) + acc[1][2 * h + 1]),
+                     pack_bf16x2(lo_f(yv.z) + acc[2][2 * h], hi_f(yv.z) + acc[2][2 * h + 1]),
+                     pack_bf16x2(lo_f(yv.w) + acc[3][2 * h], hi_f(yv.w) + acc[3][2 * h + 1]));
+    }
+  }
+  cp_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -837,6 +1022,23 @@ int lora_splits(int M, int K) {
   return std::max(1, std::min({s, 8, kblocks / 4}));   // (four blocks each at least: the stages)
 }
 
+// CTAs per tile of the one-kernel form (0: the two-kernel form).  It wins
+// where the tiles' clusters fit on the GPU at once, two CTAs per SM, with two
+// CTAs a tile at least; a CTA's columns are a loop, so not where few CTAs have
+// many steps; and a long stream of y runs better with many small CTAs.  us, one
+// kernel / two, 4096 -> 2688 rank 32: 600 rows 15.6 / 16.8, 2048 17.4 / 21.4,
+// 5669 31.6 / 33.5, 9600 (more tiles than that) 64 / 48; 2688 -> 10304 rank 16:
+// 1024 rows (128 CTAs of 20 steps) 21.5 / 18.9, 2048 24 / 27, 5669 53.8 / 54.1,
+// 8192 73.5 / 70.3.
+int lora_one_kernel(int M, int N, int K, int max_tiles) {
+  const int sms = device_sm_count(), kblocks = (K + kDownK - 1) / kDownK;
+  const int splits = std::min({2 * sms / max_tiles, 8, kblocks / 4});
+  if (splits < 2 || (long long)M * N > 1ll << 26) return 0;
+  const int steps = (N + kStepCols * splits - 1) / (kStepCols * splits);
+  const int tiles = (M + kTile - 1) / kTile;   // the fewest; there may be as many as max_tiles
+  return (tiles + max_tiles) / 2 * splits >= sms || steps <= 8 ? splits : 0;
+}
+
 LoraWs carve_lora(void* base, int M, int rank, int n_adapters) {
   char* p = static_cast<char*>(base);
   const size_t tiles = (size_t)lora_max_tiles(M, n_adapters);
@@ -879,8 +1081,10 @@ cudaError_t launch_few(const uint16_t* y, const uint16_t* x, const LoraWeights& 
 
 template <int NK>
 cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights& w, uint16_t* out, int M, int N, int K,
-                        const LoraWs& ws, int max_tiles, cudaStream_t st) {
-  const int splits = lora_splits(M, K);
+                        const LoraWs& ws, int max_tiles, cudaStream_t st, int* launches) {
+  const bool vec = N % 8 == 0 && (uintptr_t)y % 16 == 0 && (uintptr_t)out % 16 == 0;
+  const int one = NK <= 2 && vec ? lora_one_kernel(M, N, K, max_tiles) : 0;
+  const int splits = one ? one : lora_splits(M, K);
   const size_t dsm = (size_t)kDownStages * (kTile + ((w.rank + 15) & ~15)) * 128;
   static_assert(kDownStages * (kTile + 8) * 128 >= 4 * 4 * 32 * 16, "the parts fit where the stages were");
   cudaError_t e = ensure_smem_optin((const void*)k_lora_down<NK>, kDownStages * (kTile + 16 * NK) * 128);
@@ -900,13 +1104,24 @@ cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights&
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  if constexpr (NK <= 2) {
+    if (one) {
+      *launches = 2;
+      if ((e = ensure_smem_optin((const void*)k_lora_tile<NK>,
+                                 kDownStages * (kTile + 16 * NK) * 128 + kStepStages * Step<NK>::kBytes)) != cudaSuccess)
+        return e;
+      cfg.dynamicSmemBytes = dsm + kStepStages * Step<NK>::kBytes;
+      return cudaLaunchKernelEx(&cfg, k_lora_tile<NK>, y, x, w.a, w.b, w.scale, (const int32_t*)ws.row_of,
+                                (const TileInfo*)ws.info, (const int*)ws.n_tiles, w.rank, N, K, splits,
+                                x_bytes <= kXAhead ? x_bytes : 0, out);
+    }
+  }
   e = cudaLaunchKernelEx(&cfg, k_lora_down<NK>, x, w.a, w.scale, (const int32_t*)ws.row_of, (const TileInfo*)ws.info,
                          (const int*)ws.n_tiles, w.rank, K, splits, x_bytes <= kXAhead ? x_bytes : 0, ws.frag);
   if (e != cudaSuccess) return e;
   constexpr int kCols = Up<NK>::kCols;
   const int chunks = (N + kCols - 1) / kCols;
   if ((long long)chunks * max_tiles > 0x7fffffffll) return cudaErrorInvalidValue;
-  const bool vec = N % 8 == 0 && (uintptr_t)y % 16 == 0 && (uintptr_t)out % 16 == 0;
   constexpr int kRows = kTile * Up<NK>::kRowBytes;   // (more than the aligned form's kCols / 32 slots per thread)
   static_assert(kRows >= kCols / 32 * kLoThreads * 16, "");
   const size_t usm = (size_t)kCols * (w.rank * 2 + 16) + (vec ? kCols / 32 * kLoThreads * 16 : kRows);
@@ -957,10 +1172,10 @@ cudaError_t launch_lora_add(const uint16_t* y, const uint16_t* x, const LoraWeig
                  lw.n_tiles, err);
   if (e != cudaSuccess) return e;
   const int max_tiles = lora_max_tiles(M, w.n_adapters);
-  if (w.rank <= 16) return launch_many<1>(y, x, w, out, M, N, K, lw, max_tiles, st);
-  if (w.rank <= 32) return launch_many<2>(y, x, w, out, M, N, K, lw, max_tiles, st);
-  if (w.rank <= 64) return launch_many<4>(y, x, w, out, M, N, K, lw, max_tiles, st);
-  return launch_many<8>(y, x, w, out, M, N, K, lw, max_tiles, st);
+  if (w.rank <= 16) return launch_many<1>(y, x, w, out, M, N, K, lw, max_tiles, st, launches);
+  if (w.rank <= 32) return launch_many<2>(y, x, w, out, M, N, K, lw, max_tiles, st, launches);
+  if (w.rank <= 64) return launch_many<4>(y, x, w, out, M, N, K, lw, max_tiles, st, launches);
+  return launch_many<8>(y, x, w, out, M, N, K, lw, max_tiles, st, launches);
 }
 
 // Adapter of every row of a packed call: the decode rows' own, then each

@@ -82,6 +82,32 @@ def test_matches_the_formula(M, N, K, rank, na):
     _check(to_np(_run(*args)), val, err, y, ids)
 
 
+# batches whose tiles take both products in one kernel: fewer 64-column steps
+# than CTAs, a last step of 8 columns, ranks that end inside a 16-wide step, K
+# that ends inside a block, as many tiles as it takes and one more
+@pytest.mark.parametrize("M,N,K,rank,na", [
+    (513, 8, 512, 8, 1), (520, 72, 528, 24, 3), (640, 1000, 1040, 8, 5), (1100, 200, 2688, 32, 2), (2100, 5128, 512, 16, 4),
+    (4097, 128, 1552, 32, 9), (9536, 264, 528, 16, 2), (9537, 264, 528, 16, 2), (600, 520, 4096, 16, 60)])
+@pytest.mark.parametrize("place", ["in place", None])
+def test_middling_batches(M, N, K, rank, na, place):
+    args = _inputs(M, N, K, rank, na, M + N)
+    x, y, a, b, scale, ids = args
+    val, err = _ref(*args)
+    _check(to_np(_run(*args, out=place)), val, err, y, ids)
+
+
+@pytest.mark.parametrize("M,N,K,rank,na", [(900, 136, 544, 24, 3), (600, 72, 512, 32, 12)])
+def test_middling_batches_of_integers_are_exact(M, N, K, rank, na):
+    """|t| <= 12 K <= 2^13 and the sums stay below 2^24: only the final rounding."""
+    rng = np.random.default_rng(M + N)
+    x, y = rng.integers(-4, 5, (M, K)).astype(float), rng.integers(-64, 65, (M, N)).astype(float)
+    a, b = rng.integers(-3, 4, (na, rank, K)).astype(float), rng.integers(-8, 9, (na, N, rank)).astype(float)
+    scale = 2.0 ** rng.integers(-2, 3, na)
+    ids = rng.integers(-1, na, M).astype(np.int32)
+    val, _ = _ref(x, y, a, b, scale, ids)
+    assert np.array_equal(to_np(_run(x, y, a, b, scale, ids)), _bf16(val))
+
+
 @pytest.mark.parametrize("M", [5, 400])
 def test_in_place_and_without_scale(M):
     x, y, a, b, scale, ids = _inputs(M, 2688, 4096, 16, 6, 11 + M)
