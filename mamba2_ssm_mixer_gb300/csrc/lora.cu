@@ -140,8 +140,21 @@ __global__ void __launch_bounds__(kLoThreads, NT <= 4 ? 2 : 1) k_lora_few(
   for (int i = 0; i < kWindow / 32; ++i) other[i] = w0 + 32 * i + lane < M ? ids[w0 + 32 * i + lane] : -1;
   if (id < 0 || id >= n_adapters) {   // the same for the whole cluster
     if (id != -1 && blockIdx.x == 0 && tid == 0) atomicOr(err, kErrAdapter);
-    if (out != y)
-      for (int n = n_lo + tid; n < n_hi; n += kLoThreads) out[(size_t)m * N + n] = y[(size_t)m * N + n];
+    if (out != y) {   // (loads ahead of the stores: y and out may be one buffer for all the compiler knows)
+      constexpr int kCopies = 4;
+      using E = typename std::conditional<kPair, uint32_t, uint16_t>::type;
+      constexpr int kE = sizeof(E) / 2;
+      const E* from = reinterpret_cast<const E*>(y + (size_t)m * N);
+      E* to = reinterpret_cast<E*>(out + (size_t)m * N);
+      for (int n0 = n_lo / kE + tid; n0 < n_hi / kE; n0 += kCopies * kLoThreads) {
+        E v[kCopies];
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) v[i] = from[min(n0 + i * kLoThreads, n_hi / kE - 1)];
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+          if (n0 + i * kLoThreads < n_hi / kE) to[n0 + i * kLoThreads] = v[i];
+      }
+    }
     return;
   }
   uint32_t same[kWindow / 32];
@@ -704,15 +717,8 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
   if (at >= have) return;   // (what was read past the last tile is not used)
   const int units = (N + kStepCols - 1) / kStepCols;
   const int u0 = (int)((long long)units * split / splits), nu = (int)((long long)units * (split + 1) / splits) - u0;
-  if (tile.adapter < 0) {
-    if (out == y) return;
-    for (int r = warp; r < tile.rows; r += kLoWarps) {
-      const size_t o = (size_t)row_of[(size_t)at * kTile + r] * N;
-      for (int c = u0 * kStepCols + lane * 8; c < min(N, (u0 + nu) * kStepCols); c += 256)
-        *reinterpret_cast<uint4*>(out + o + c) = *reinterpret_cast<const uint4*>(y + o + c);
-    }
-    return;
-  }
+  const bool bare = tile.adapter < 0;   // rows without an adapter: y moves as it is
+  if (bare && out == y) return;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     if (mg * 16 + g + 8 * h >= tile.rows) row[h] = -1;
@@ -722,7 +728,7 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
   uint8_t* steps = lt_smem + kDownStages * (kTile + arows) * 128;
   const int bn = tid / rv, bv = tid - bn * rv;   // this thread's piece of B
   const int bpos = (bn & ~31) | ((bn >> 1) & 3) << 3 | ((bn >> 3) & 3) << 1 | (bn & 1);
-  const uint16_t* bt = b + (size_t)tile.adapter * N * rank + bv * 8;
+  const uint16_t* bt = b + (size_t)(bare ? 0 : tile.adapter) * N * rank + bv * 8;
   const int cw = (warp >> 2) * 32 + q * 8;       // this thread's columns of a step
   auto load = [&](int u) {
     if (u >= nu) return;
@@ -732,7 +738,7 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
     for (int h = 0; h < 2; ++h)
       if (row[h] >= 0 && c0 + cw < N)
         cp16(smem_u32(st + (h * kLoThreads + tid) * 16), y + (size_t)row[h] * N + c0 + cw, true);
-    if (bn < kStepCols) {
+    if (bn < kStepCols && !bare) {
       const bool in = c0 + bn < N;
       cp16(smem_u32(st + Step<NK>::kY + bpos * pitch + bv * 16), in ? bt + (size_t)(c0 + bn) * rank : b, in);
     }
@@ -741,26 +747,31 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
     for (int i = tid; i < kStepStages * kStepCols; i += kLoThreads)
       *reinterpret_cast<uint4*>(steps + i / kStepCols * Step<NK>::kBytes + Step<NK>::kY + i % kStepCols * pitch + rank * 2) =
           make_uint4(0u, 0u, 0u, 0u);
-  const float4* part = down_part<NK>(x, a, rank, K, split, splits, tile, src, lt_smem, load);
-  const float sc = scale ? scale[tile.adapter] : 1.f;
-  lo_cluster_arrive();
-  lo_cluster_wait();
-  // each CTA joins its share of the items and hands them to all (every CTA
-  // joining all of them took 3 to 20 us more)
-  uint4* tf = reinterpret_cast<uint4*>(lt_smem + 4 * kItems * 16);
-  for (int i = kItems * split / splits + tid; i < kItems * (split + 1) / splits; i += kLoThreads) {
-    uint4 hi, lo;
-    gather_t<NK>(part, i, splits, sc, &hi, &lo);
-    for (int c = 0; c < splits; ++c) {
-      st_cluster_u4(smem_u32(tf + i), (uint32_t)c, hi);
-      st_cluster_u4(smem_u32(tf + kItems + i), (uint32_t)c, lo);
-    }
-  }
-  lo_cluster_arrive();
-  lo_cluster_wait();
   uint4 th[NK], tl[NK];   // t of the warp's 16 rows
+  if (bare) {
 #pragma unroll
-  for (int s = 0; s < NK; ++s) th[s] = tf[(mg * NK + s) * 32 + lane], tl[s] = tf[kItems + (mg * NK + s) * 32 + lane];
+    for (int u = 0; u < kStepStages - 1; ++u) load(u), cp_commit();
+  } else {
+    const float4* part = down_part<NK>(x, a, rank, K, split, splits, tile, src, lt_smem, load);
+    const float sc = scale ? scale[tile.adapter] : 1.f;
+    lo_cluster_arrive();
+    lo_cluster_wait();
+    // each CTA joins its share of the items and hands them to all (every CTA
+    // joining all of them took 3 to 20 us more)
+    uint4* tf = reinterpret_cast<uint4*>(lt_smem + 4 * kItems * 16);
+    for (int i = kItems * split / splits + tid; i < kItems * (split + 1) / splits; i += kLoThreads) {
+      uint4 hi, lo;
+      gather_t<NK>(part, i, splits, sc, &hi, &lo);
+      for (int c = 0; c < splits; ++c) {
+        st_cluster_u4(smem_u32(tf + i), (uint32_t)c, hi);
+        st_cluster_u4(smem_u32(tf + kItems + i), (uint32_t)c, lo);
+      }
+    }
+    lo_cluster_arrive();
+    lo_cluster_wait();
+#pragma unroll
+    for (int s = 0; s < NK; ++s) th[s] = tf[(mg * NK + s) * 32 + lane], tl[s] = tf[kItems + (mg * NK + s) * 32 + lane];
+  }
   const uint32_t boff = Step<NK>::kY + (uint32_t)((warp >> 2) * 32 + (lane & 7) + (lane >> 4) * 8) * pitch +
                         (uint32_t)((lane >> 3) & 1) * 16;
   for (int u = 0; u < nu; ++u) {
@@ -776,7 +787,7 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
     for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 #pragma unroll
     for (int s = 0; s < NK; ++s)
-      if (s * 16 < rank) {
+      if (s * 16 < rank && !bare) {
 #pragma unroll
         for (int jp = 0; jp < 2; ++jp) {
           const uint32_t lo[4] = {tl[s].x, tl[s].y, tl[s].z, tl[s].w}, hi[4] = {th[s].x, th[s].y, th[s].z, th[s].w};
@@ -795,6 +806,7 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
       if (row[h] < 0) continue;
       const uint4 yv = *reinterpret_cast<const uint4*>(st + (h * kLoThreads + tid) * 16);
       *reinterpret_cast<uint4*>(out + (size_t)row[h] * N + n) =
+          bare ? yv :
           make_uint4(pack_bf16x2(lo_f(yv.x) + acc[0][2 * h], hi_f(yv.x) + acc[0][2 * h + 1]),
                      pack_bf16x2(lo_f(yv.y) + acc[1][2 * h], hi_f(yv.y) + acc[1][2 * h + 1]),
                      pack_bf16x2(lo_f(yv.z) + acc[2][2 * h], hi_f(yv.z) + acc[2][2 * h + 1]),
@@ -849,19 +861,9 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     if (mg * 16 + g + 8 * h >= tile.rows) row[h] = -1;
-  if (tile.adapter < 0) {
+  const bool bare = tile.adapter < 0;   // rows without an adapter: y moves as it is
+  if (bare && out == y) {
     pdl_wait();
-    pdl_trigger();
-    if (out == y) return;
-    for (int r = warp; r < tile.rows; r += kLoWarps) {
-      const size_t o = (size_t)row_of[(size_t)at * kTile + r] * N;
-      if constexpr (kVec) {
-        for (int c = c0 + lane * 8; c < c_hi; c += 256)
-          *reinterpret_cast<uint4*>(out + o + c) = *reinterpret_cast<const uint4*>(y + o + c);
-      } else {
-        for (int c = c0 + lane; c < c_hi; c += 32) out[o + c] = y[o + c];
-      }
-    }
     return;
   }
   // y, asked for at once and held by no registers.  Aligned: each thread's
@@ -892,7 +894,7 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
   const int pitch = rank * 2 + 16, rv = rank / 8;
   uint8_t* bsm = lu_smem + (kVec ? kGroups * 2 * kLoThreads * 16 : kTile * Up<NK>::kRowBytes);
   const uint32_t s0 = smem_u32(bsm);
-  {
+  if (!bare) {
     const uint16_t* bt = b + ((size_t)tile.adapter * N + c0) * rank;
     const int n_step = kLoThreads / rv, v_step = kLoThreads - n_step * rv;
     int n = tid / rv, v = tid - n * rv;   // (stepped, not divided, from piece to piece)
@@ -903,14 +905,14 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
       n += n_step, v += v_step;
       if (v >= rv) v -= rv, ++n;
     }
-    cp_commit();
     if (rank & 8)   // the last 16-wide step reads 8 entries past the rank: zeros
       for (int n = tid; n < kCols; n += kLoThreads)
         *reinterpret_cast<uint4*>(bsm + n * pitch + rank * 2) = make_uint4(0u, 0u, 0u, 0u);
   }
+  cp_commit();
   pdl_wait();
   pdl_trigger();
-  uint4 th[NK], tl[NK];   // t of the warp's 16 rows
+  uint4 th[NK], tl[NK];   // t of the warp's 16 rows (a bare tile's is not written, and not used)
   const uint4* fp = frag + ((size_t)at * 4 + mg) * NK * 64 + lane;
 #pragma unroll
   for (int s = 0; s < NK; ++s) th[s] = __ldg(fp + s * 64), tl[s] = __ldg(fp + s * 64 + 32);
@@ -941,7 +943,7 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
     for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 #pragma unroll
     for (int s = 0; s < NK; ++s)
-      if (s * 16 < rank) {
+      if (s * 16 < rank && !bare) {
 #pragma unroll
         for (int jp = 0; jp < 2; ++jp) {
           const uint32_t lo[4] = {tl[s].x, tl[s].y, tl[s].z, tl[s].w}, hi[4] = {th[s].x, th[s].y, th[s].z, th[s].w};
@@ -961,6 +963,7 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
         if (n >= c_hi) continue;
         const uint4 yv = ys[(u * 2 + h) * kLoThreads];
         *reinterpret_cast<uint4*>(out + o) =
+            bare ? yv :
             make_uint4(pack_bf16x2(lo_f(yv.x) + acc[0][2 * h], hi_f(yv.x) + acc[0][2 * h + 1]),
                        pack_bf16x2(lo_f(yv.y) + acc[1][2 * h], hi_f(yv.y) + acc[1][2 * h + 1]),
                        pack_bf16x2(lo_f(yv.z) + acc[2][2 * h], hi_f(yv.z) + acc[2][2 * h + 1]),
@@ -968,6 +971,7 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
       } else {
         // (columns past the last are computed in place too, and not stored)
         uint4* rp = reinterpret_cast<uint4*>(lu_smem + (mg * 16 + g + 8 * h) * Up<NK>::kRowBytes) + (n - c0) / 8;
+        if (bare) continue;
         const uint4 yv = *rp;
         *rp = make_uint4(pack_bf16x2(lo_f(yv.x) + acc[0][2 * h], hi_f(yv.x) + acc[0][2 * h + 1]),
                          pack_bf16x2(lo_f(yv.y) + acc[1][2 * h], hi_f(yv.y) + acc[1][2 * h + 1]),
