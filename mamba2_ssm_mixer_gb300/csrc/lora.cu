@@ -480,6 +480,10 @@ namespace {
 constexpr int kDownStages = 4;
 constexpr int kDownK = 64;
 
+// Bytes from one column of B to the next in shared memory: whole 16-wide steps
+// and 16 more, so that the 8 columns of a fragment lie in different banks.
+__host__ __device__ __forceinline__ int b_pitch(int rank) { return ((rank + 15) & ~15) * 2 + 16; }
+
 // 16-byte piece `c` (0..7) of 128-byte row r of a swizzled tile.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
@@ -724,7 +728,7 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
     if (mg * 16 + g + 8 * h >= tile.rows) row[h] = -1;
   // a step: y into slots of each thread's own, B with column n of a 32-column
   // group at MMA j = (n % 8) / 2, column 2 (n / 8) + n % 2 (as in k_lora_up)
-  const int arows = (rank + 15) & ~15, pitch = rank * 2 + 16, rv = rank / 8;
+  const int arows = (rank + 15) & ~15, pitch = b_pitch(rank), rv = rank / 8;
   uint8_t* steps = lt_smem + kDownStages * (kTile + arows) * 128;
   const int bn = tid / rv, bv = tid - bn * rv;   // this thread's piece of B
   const int bpos = (bn & ~31) | ((bn >> 1) & 3) << 3 | ((bn >> 3) & 3) << 1 | (bn & 1);
@@ -891,7 +895,7 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
         cp16(smem_u32(lu_smem + r * Up<NK>::kRowBytes + j * 16), (const void*)(first + j * 16), true);
     }
   }
-  const int pitch = rank * 2 + 16, rv = rank / 8;
+  const int pitch = b_pitch(rank), rv = rank / 8;
   uint8_t* bsm = lu_smem + (kVec ? kGroups * 2 * kLoThreads * 16 : kTile * Up<NK>::kRowBytes);
   const uint32_t s0 = smem_u32(bsm);
   if (!bare) {
@@ -1128,7 +1132,7 @@ cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights&
   if ((long long)chunks * max_tiles > 0x7fffffffll) return cudaErrorInvalidValue;
   constexpr int kRows = kTile * Up<NK>::kRowBytes;   // (more than the aligned form's kCols / 32 slots per thread)
   static_assert(kRows >= kCols / 32 * kLoThreads * 16, "");
-  const size_t usm = (size_t)kCols * (w.rank * 2 + 16) + (vec ? kCols / 32 * kLoThreads * 16 : kRows);
+  const size_t usm = (size_t)kCols * b_pitch(w.rank) + (vec ? kCols / 32 * kLoThreads * 16 : kRows);
   const dim3 grid((unsigned)(chunks * max_tiles));
   const auto kernel = vec ? k_lora_up<NK, true> : k_lora_up<NK, false>;
   if ((e = ensure_smem_optin((const void*)kernel, kCols * (32 * NK + 16) + kRows)) != cudaSuccess)
