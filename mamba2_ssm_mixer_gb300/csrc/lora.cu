@@ -77,6 +77,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// y's 8 columns, as words of MMAs 0 to 3, plus accumulator row h (0, or 1: + 8)
+__device__ __forceinline__ void add_pairs(uint4* y, const float (&acc)[4][4], int h) {
+  y->x = pack_bf16x2(lo_f(y->x) + acc[0][2 * h], hi_f(y->x) + acc[0][2 * h + 1]);
+  y->y = pack_bf16x2(lo_f(y->y) + acc[1][2 * h], hi_f(y->y) + acc[1][2 * h + 1]);
+  y->z = pack_bf16x2(lo_f(y->z) + acc[2][2 * h], hi_f(y->z) + acc[2][2 * h + 1]);
+  y->w = pack_bf16x2(lo_f(y->w) + acc[3][2 * h], hi_f(y->w) + acc[3][2 * h + 1]);
+}
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
@@ -484,6 +491,48 @@ constexpr int kDownK = 64;
 // and 16 more, so that the 8 columns of a fragment lie in different banks.
 __host__ __device__ __forceinline__ int b_pitch(int rank) { return ((rank + 15) & ~15) * 2 + 16; }
 
+// How a thread's 8 columns of a 32-column group lie, in pieces of kW columns
+// that every row of y and out is aligned to: piece p at column 4 kW p + kW q of
+// the group, so that four lanes touch 8 kW bytes of a row at once.  Their words
+// are, in order, the accumulator pairs of MMAs 0 to 3.
+template <int kW>
+struct Cols {
+  static constexpr int kPieces = 8 / kW;
+  __device__ static int at(int p, int q) { return 4 * kW * p + kW * q; }
+  // where column n of B lies among the operands: MMA j, its column 2 q + n % 2
+  __device__ static int place(int n) {
+    const int j = (n & 31) / (4 * kW) * (kW / 2) + (n % kW) / 2, q = (n & 31) % (4 * kW) / kW;
+    return (n & ~31) | (j << 3) | (q << 1) | (n & 1);
+  }
+  // y's pieces into a 16-byte slot; c: the group's first column
+  __device__ static void fetch(uint32_t slot, const uint16_t* row, int c, int q, int c_hi) {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const int n = c + at(p, q);
+      if (n >= c_hi) continue;
+      if constexpr (kW == 8)
+        cp16(slot, row + n, true);
+      else if constexpr (kW == 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(slot + p * 8), "l"(row + n) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slot + p * 4), "l"(row + n) : "memory");
+    }
+  }
+  __device__ static void store(uint16_t* row, int c, int q, int c_hi, const uint4& v) {
+    if constexpr (kW == 8) {
+      if (c + at(0, q) < c_hi) *reinterpret_cast<uint4*>(row + c + at(0, q)) = v;
+    } else if constexpr (kW == 4) {
+      if (c + at(0, q) < c_hi) *reinterpret_cast<uint2*>(row + c + at(0, q)) = make_uint2(v.x, v.y);
+      if (c + at(1, q) < c_hi) *reinterpret_cast<uint2*>(row + c + at(1, q)) = make_uint2(v.z, v.w);
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        if (c + at(p, q) < c_hi) *reinterpret_cast<uint32_t*>(row + c + at(p, q)) = w[p];
+    }
+  }
+};
+
 // 16-byte piece `c` (0..7) of 128-byte row r of a swizzled tile.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
@@ -685,6 +734,9 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
 // way while t is joined.  No launch and no tail between the products: 5669 rows
 // 4096 -> 2688 in 31.6 us at rank 32, 27.9 at rank 16 (with the two kernels 33.5
 // and 31.9; floor 16.3).  Bringing each row's y to L2 further ahead took 3 more.
+// kW: columns per piece of y and out (8, or 4 or 2 where rows of N % 4 or N % 2
+// columns start on no more: 1336 x 2498 of 63 adapters, rank 24, in 23.6 us, with
+// the two kernels 26).
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kStepCols = 64;
@@ -697,7 +749,7 @@ struct Step {
 };
 }  // namespace
 
-template <int NK>
+template <int NK, int kW>
 __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
     const uint16_t* y, const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, const uint16_t* __restrict__ b,
     const float* __restrict__ scale, const int32_t* __restrict__ row_of, const TileInfo* __restrict__ info,
@@ -726,22 +778,20 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     if (mg * 16 + g + 8 * h >= tile.rows) row[h] = -1;
-  // a step: y into slots of each thread's own, B with column n of a 32-column
-  // group at MMA j = (n % 8) / 2, column 2 (n / 8) + n % 2 (as in k_lora_up)
+  // a step: y into slots of each thread's own, B in the order of the MMAs
   const int arows = (rank + 15) & ~15, pitch = b_pitch(rank), rv = rank / 8;
   uint8_t* steps = lt_smem + kDownStages * (kTile + arows) * 128;
   const int bn = tid / rv, bv = tid - bn * rv;   // this thread's piece of B
-  const int bpos = (bn & ~31) | ((bn >> 1) & 3) << 3 | ((bn >> 3) & 3) << 1 | (bn & 1);
+  const int bpos = Cols<kW>::place(bn);
   const uint16_t* bt = b + (size_t)(bare ? 0 : tile.adapter) * N * rank + bv * 8;
-  const int cw = (warp >> 2) * 32 + q * 8;       // this thread's columns of a step
+  const int cw = (warp >> 2) * 32;               // this warp's columns of a step
   auto load = [&](int u) {
     if (u >= nu) return;
     uint8_t* st = steps + (u % kStepStages) * Step<NK>::kBytes;
     const int c0 = (u0 + u) * kStepCols;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (row[h] >= 0 && c0 + cw < N)
-        cp16(smem_u32(st + (h * kLoThreads + tid) * 16), y + (size_t)row[h] * N + c0 + cw, true);
+      if (row[h] >= 0) Cols<kW>::fetch(smem_u32(st + (h * kLoThreads + tid) * 16), y + (size_t)row[h] * N, c0 + cw, q, N);
     if (bn < kStepCols && !bare) {
       const bool in = c0 + bn < N;
       cp16(smem_u32(st + Step<NK>::kY + bpos * pitch + bv * 16), in ? bt + (size_t)(c0 + bn) * rank : b, in);
@@ -803,29 +853,25 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
           mma16816(acc[2 * jp + 1], hi, bf[2], bf[3]);
         }
       }
-    const int n = (u0 + u) * kStepCols + cw;
-    if (n >= N) continue;
+    const int c = (u0 + u) * kStepCols + cw;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (row[h] < 0) continue;
-      const uint4 yv = *reinterpret_cast<const uint4*>(st + (h * kLoThreads + tid) * 16);
-      *reinterpret_cast<uint4*>(out + (size_t)row[h] * N + n) =
-          bare ? yv :
-          make_uint4(pack_bf16x2(lo_f(yv.x) + acc[0][2 * h], hi_f(yv.x) + acc[0][2 * h + 1]),
-                     pack_bf16x2(lo_f(yv.y) + acc[1][2 * h], hi_f(yv.y) + acc[1][2 * h + 1]),
-                     pack_bf16x2(lo_f(yv.z) + acc[2][2 * h], hi_f(yv.z) + acc[2][2 * h + 1]),
-                     pack_bf16x2(lo_f(yv.w) + acc[3][2 * h], hi_f(yv.w) + acc[3][2 * h + 1]));
+      uint4 v = *reinterpret_cast<const uint4*>(st + (h * kLoThreads + tid) * 16);
+      if (!bare) add_pairs(&v, acc, h);
+      Cols<kW>::store(out + (size_t)row[h] * N, c, q, N, v);
     }
   }
   cp_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
-// out of a tile and Up::kCols columns: y + B t.  Column n of a 32-column group
-// sits at MMA j = (n % 8) / 2, column 2 (n / 8) + n % 2, so that a thread's
-// accumulators of the four MMAs are 8 consecutive columns: y and out move in
-// 16-byte pieces, 64 bytes of a row per four lanes.  Many small CTAs: the
-// stream runs at the copy rate when its tail is short (a pure copy in this
+// out of a tile and Up::kCols columns: y + B t.  The columns of B are dealt out
+// to the MMAs so that a thread's accumulators are 8 consecutive columns: y and
+// out move in 16-byte pieces, 64 bytes of a row per four lanes, or, where rows
+// start on less (!kVec), through rows in shared memory (44 us against 27.5 for
+// 6614 x 5020 and x 5024, rank 24; in 8-byte pieces straight 45: their stores
+// end inside sectors).  Many small CTAs: the stream runs at the copy rate when its tail is short (a pure copy in this
 // pattern: 41 CTAs per tile 6580 GB/s, 3 to 6 of them 5200 to 5600), so what a
 // CTA needs before its first load of y is two dependent reads deep.
 // ---------------------------------------------------------------------------
@@ -903,7 +949,7 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
     const int n_step = kLoThreads / rv, v_step = kLoThreads - n_step * rv;
     int n = tid / rv, v = tid - n * rv;   // (stepped, not divided, from piece to piece)
     for (int i = tid; i < kCols * rv; i += kLoThreads) {
-      const int pos = (n & ~31) | ((n >> 1) & 3) << 3 | ((n >> 3) & 3) << 1 | (n & 1);
+      const int pos = Cols<8>::place(n);
       const bool in = c0 + n < c_hi;
       cp16(s0 + (uint32_t)(pos * pitch + v * 16), in ? bt + (size_t)i * 8 : b, in);
       n += n_step, v += v_step;
@@ -941,7 +987,6 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
                       (uint32_t)((lane >> 3) & 1) * 16;
 #pragma unroll
   for (int u = 0; u < kGroups; ++u) {
-    const int n = cw + u * 32 + q * 8;
     float acc[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
@@ -962,25 +1007,18 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (row[h] < 0) continue;
-      const size_t o = (size_t)row[h] * N + n;
       if constexpr (kVec) {
+        const int n = cw + u * 32 + q * 8;
         if (n >= c_hi) continue;
-        const uint4 yv = ys[(u * 2 + h) * kLoThreads];
-        *reinterpret_cast<uint4*>(out + o) =
-            bare ? yv :
-            make_uint4(pack_bf16x2(lo_f(yv.x) + acc[0][2 * h], hi_f(yv.x) + acc[0][2 * h + 1]),
-                       pack_bf16x2(lo_f(yv.y) + acc[1][2 * h], hi_f(yv.y) + acc[1][2 * h + 1]),
-                       pack_bf16x2(lo_f(yv.z) + acc[2][2 * h], hi_f(yv.z) + acc[2][2 * h + 1]),
-                       pack_bf16x2(lo_f(yv.w) + acc[3][2 * h], hi_f(yv.w) + acc[3][2 * h + 1]));
-      } else {
+        uint4 v = ys[(u * 2 + h) * kLoThreads];
+        if (!bare) add_pairs(&v, acc, h);
+        *reinterpret_cast<uint4*>(out + (size_t)row[h] * N + n) = v;
+      } else if (!bare) {
         // (columns past the last are computed in place too, and not stored)
-        uint4* rp = reinterpret_cast<uint4*>(lu_smem + (mg * 16 + g + 8 * h) * Up<NK>::kRowBytes) + (n - c0) / 8;
-        if (bare) continue;
-        const uint4 yv = *rp;
-        *rp = make_uint4(pack_bf16x2(lo_f(yv.x) + acc[0][2 * h], hi_f(yv.x) + acc[0][2 * h + 1]),
-                         pack_bf16x2(lo_f(yv.y) + acc[1][2 * h], hi_f(yv.y) + acc[1][2 * h + 1]),
-                         pack_bf16x2(lo_f(yv.z) + acc[2][2 * h], hi_f(yv.z) + acc[2][2 * h + 1]),
-                         pack_bf16x2(lo_f(yv.w) + acc[3][2 * h], hi_f(yv.w) + acc[3][2 * h + 1]));
+        uint4* rp = reinterpret_cast<uint4*>(lu_smem + (mg * 16 + g + 8 * h) * Up<NK>::kRowBytes) + (cw - c0 + u * 32) / 8 + q;
+        uint4 v = *rp;
+        add_pairs(&v, acc, h);
+        *rp = v;
       }
     }
   }
@@ -1090,8 +1128,13 @@ cudaError_t launch_few(const uint16_t* y, const uint16_t* x, const LoraWeights& 
 template <int NK>
 cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights& w, uint16_t* out, int M, int N, int K,
                         const LoraWs& ws, int max_tiles, cudaStream_t st, int* launches) {
-  const bool vec = N % 8 == 0 && (uintptr_t)y % 16 == 0 && (uintptr_t)out % 16 == 0;
-  const int one = NK <= 2 && vec ? lora_one_kernel(M, N, K, max_tiles) : 0;
+  // columns per piece of y and out: every row starts on such a piece
+  const uintptr_t where = (uintptr_t)y | (uintptr_t)out;
+  const int width = N % 8 == 0 && where % 16 == 0  ? 8
+                    : N % 4 == 0 && where % 8 == 0 ? 4
+                    : N % 2 == 0 && where % 4 == 0 ? 2
+                                                   : 0;
+  const int one = NK <= 2 && width ? lora_one_kernel(M, N, K, max_tiles) : 0;
   const int splits = one ? one : lora_splits(M, K);
   const size_t dsm = (size_t)kDownStages * (kTile + ((w.rank + 15) & ~15)) * 128;
   static_assert(kDownStages * (kTile + 8) * 128 >= 4 * 4 * 32 * 16, "the parts fit where the stages were");
@@ -1115,11 +1158,12 @@ cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights&
   if constexpr (NK <= 2) {
     if (one) {
       *launches = 2;
-      if ((e = ensure_smem_optin((const void*)k_lora_tile<NK>,
+      const auto kernel = width == 8 ? k_lora_tile<NK, 8> : width == 4 ? k_lora_tile<NK, 4> : k_lora_tile<NK, 2>;
+      if ((e = ensure_smem_optin((const void*)kernel,
                                  kDownStages * (kTile + 16 * NK) * 128 + kStepStages * Step<NK>::kBytes)) != cudaSuccess)
         return e;
       cfg.dynamicSmemBytes = dsm + kStepStages * Step<NK>::kBytes;
-      return cudaLaunchKernelEx(&cfg, k_lora_tile<NK>, y, x, w.a, w.b, w.scale, (const int32_t*)ws.row_of,
+      return cudaLaunchKernelEx(&cfg, kernel, y, x, w.a, w.b, w.scale, (const int32_t*)ws.row_of,
                                 (const TileInfo*)ws.info, (const int*)ws.n_tiles, w.rank, N, K, splits,
                                 x_bytes <= kXAhead ? x_bytes : 0, out);
     }
@@ -1132,9 +1176,9 @@ cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights&
   if ((long long)chunks * max_tiles > 0x7fffffffll) return cudaErrorInvalidValue;
   constexpr int kRows = kTile * Up<NK>::kRowBytes;   // (more than the aligned form's kCols / 32 slots per thread)
   static_assert(kRows >= kCols / 32 * kLoThreads * 16, "");
-  const size_t usm = (size_t)kCols * b_pitch(w.rank) + (vec ? kCols / 32 * kLoThreads * 16 : kRows);
+  const size_t usm = (size_t)kCols * b_pitch(w.rank) + (width == 8 ? kCols / 32 * kLoThreads * 16 : kRows);
   const dim3 grid((unsigned)(chunks * max_tiles));
-  const auto kernel = vec ? k_lora_up<NK, true> : k_lora_up<NK, false>;
+  const auto kernel = width == 8 ? k_lora_up<NK, true> : k_lora_up<NK, false>;
   if ((e = ensure_smem_optin((const void*)kernel, kCols * (32 * NK + 16) + kRows)) != cudaSuccess)
     return e;
   return launch_pdl(kernel, grid, dim3(kLoThreads), usm, st, y, ws.frag, w.b, ws.row_of, ws.info, ws.n_tiles, w.rank, N,

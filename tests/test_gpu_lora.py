@@ -96,6 +96,19 @@ def test_middling_batches(M, N, K, rank, na, place):
     _check(to_np(_run(*args, out=place)), val, err, y, ids)
 
 
+@pytest.mark.parametrize("N", [1000, 1001, 1002, 1004, 262, 260, 30])
+@pytest.mark.parametrize("M,K,rank,na", [(700, 528, 24, 3), (700, 1040, 16, 5), (1300, 272, 56, 4), (600, 64, 8, 9)])
+def test_widths(M, N, K, rank, na):
+    """Rows of y and out that start on 16, 8, 4 and 2 bytes."""
+    args = _inputs(M, N, K, rank, na, M + N + rank)
+    x, y, a, b, scale, ids = args
+    val, err = _ref(*args)
+    _check(to_np(_run(*args)), val, err, y, ids)
+    _check(to_np(_run(*args, out="in place")), val, err, y, ids)
+    off = torch.empty(M * N + 1, dtype=torch.bfloat16, device="cuda")[1:].view(M, N)
+    _check(to_np(_run(*args, out=off)), val, err, y, ids)
+
+
 @pytest.mark.parametrize("M,N,K,rank,na", [(900, 136, 544, 24, 3), (600, 72, 512, 32, 12)])
 def test_middling_batches_of_integers_are_exact(M, N, K, rank, na):
     """|t| <= 12 K <= 2^13 and the sums stay below 2^24: only the final rounding."""
