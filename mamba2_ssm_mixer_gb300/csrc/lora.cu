@@ -500,9 +500,9 @@ struct Cols {
   static constexpr int kPieces = 8 / kW;
   __device__ static int at(int p, int q) { return 4 * kW * p + kW * q; }
   // where column n of B lies among the operands: MMA j, its column 2 q + n % 2
-  __device__ static int place(int n) {
-    const int j = (n & 31) / (4 * kW) * (kW / 2) + (n % kW) / 2, q = (n & 31) % (4 * kW) / kW;
-    return (n & ~31) | (j << 3) | (q << 1) | (n & 1);
+  __device__ static uint32_t place(uint32_t n) {
+    const uint32_t j = (n & 31) / (4 * kW) * (kW / 2) + (n % kW) / 2, q = (n & 31) % (4 * kW) / kW;
+    return (n & ~31u) | (j << 3) | (q << 1) | (n & 1);
   }
   // y's pieces into a 16-byte slot; c: the group's first column
   __device__ static void fetch(uint32_t slot, const uint16_t* row, int c, int q, int c_hi) {
@@ -620,18 +620,35 @@ __device__ __forceinline__ float4* down_part(const uint16_t* __restrict__ x, con
     cp_commit();
     if (mg * 16 >= tile.rows) continue;   // no rows for this warp
     const uint32_t xs = s0 + s * stage;
+    if constexpr (NK <= 2) {   // the block's operands ahead of its MMAs (at NK 4 and 8 this took 5 to 10% more)
+      uint32_t af[2][4], bf[2][NK][4];
 #pragma unroll
-    for (int k16 = 0; k16 < 2; ++k16) {
-      uint32_t af[4];
-      ldsm4(af, xs + xoff[k16]);
+      for (int k16 = 0; k16 < 2; ++k16) {
+        ldsm4(af[k16], xs + xoff[k16]);
 #pragma unroll
-      for (int p = 0; p < NK; ++p)
-        if (p * 16 < rank) {
-          uint32_t bf[4];
-          ldsm4(bf, xs + aoff[k16] + p * 16 * 128);
-          mma16816(acc[2 * p], af, bf[0], bf[1]);
-          if (p * 16 + 8 < rank) mma16816(acc[2 * p + 1], af, bf[2], bf[3]);
+        for (int p = 0; p < NK; ++p) ldsm4(bf[k16][p], xs + aoff[k16] + p * 16 * 128);
+      }
+#pragma unroll
+      for (int k16 = 0; k16 < 2; ++k16)
+#pragma unroll
+        for (int p = 0; p < NK; ++p) {
+          mma16816(acc[2 * p], af[k16], bf[k16][p][0], bf[k16][p][1]);
+          if (p * 16 + 8 < rank) mma16816(acc[2 * p + 1], af[k16], bf[k16][p][2], bf[k16][p][3]);
         }
+    } else {
+#pragma unroll
+      for (int k16 = 0; k16 < 2; ++k16) {
+        uint32_t af[4];
+        ldsm4(af, xs + xoff[k16]);
+#pragma unroll
+        for (int p = 0; p < NK; ++p)
+          if (p * 16 < rank) {
+            uint32_t bf[4];
+            ldsm4(bf, xs + aoff[k16] + p * 16 * 128);
+            mma16816(acc[2 * p], af, bf[0], bf[1]);
+            if (p * 16 + 8 < rank) mma16816(acc[2 * p + 1], af, bf[2], bf[3]);
+          }
+      }
     }
   }
   __syncthreads();
@@ -842,16 +859,14 @@ __global__ void __launch_bounds__(kLoThreads, 2) k_lora_tile(
 #pragma unroll
     for (int s = 0; s < NK; ++s)
       if (s * 16 < rank && !bare) {
+        const uint32_t lo[4] = {tl[s].x, tl[s].y, tl[s].z, tl[s].w}, hi[4] = {th[s].x, th[s].y, th[s].z, th[s].w};
+        uint32_t bf[2][4];
 #pragma unroll
-        for (int jp = 0; jp < 2; ++jp) {
-          const uint32_t lo[4] = {tl[s].x, tl[s].y, tl[s].z, tl[s].w}, hi[4] = {th[s].x, th[s].y, th[s].z, th[s].w};
-          uint32_t bf[4];
-          ldsm4(bf, bs + (uint32_t)(jp * 16) * pitch + s * 32);
-          mma16816(acc[2 * jp], lo, bf[0], bf[1]);
-          mma16816(acc[2 * jp + 1], lo, bf[2], bf[3]);
-          mma16816(acc[2 * jp], hi, bf[0], bf[1]);
-          mma16816(acc[2 * jp + 1], hi, bf[2], bf[3]);
-        }
+        for (int jp = 0; jp < 2; ++jp) ldsm4(bf[jp], bs + (uint32_t)(jp * 16) * pitch + s * 32);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma16816(acc[j], lo, bf[j / 2][j % 2 * 2], bf[j / 2][j % 2 * 2 + 1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma16816(acc[j], hi, bf[j / 2][j % 2 * 2], bf[j / 2][j % 2 * 2 + 1]);
       }
     const int c = (u0 + u) * kStepCols + cw;
 #pragma unroll
@@ -911,17 +926,29 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     if (mg * 16 + g + 8 * h >= tile.rows) row[h] = -1;
-  const bool bare = tile.adapter < 0;   // rows without an adapter: y moves as it is
-  if (bare && out == y) {
+  const int cw = c0 + (warp >> 2) * (kCols / 2);
+  uint4* ys = reinterpret_cast<uint4*>(lu_smem) + tid;   // [group][half][thread]
+  if (tile.adapter < 0 && (kVec || out == y)) {   // rows without an adapter: y moves as it is
     pdl_wait();
+    pdl_trigger();
+    if (out == y) return;
+    uint4 v[kGroups][2];
+#pragma unroll
+    for (int i = 0; i < 2 * kGroups; ++i)
+      v[i / 2][i % 2] = row[i % 2] >= 0 && cw + i / 2 * 32 + q * 8 < c_hi
+                            ? *reinterpret_cast<const uint4*>(y + (size_t)row[i % 2] * N + cw + i / 2 * 32 + q * 8)
+                            : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 2 * kGroups; ++i)
+      if (row[i % 2] >= 0 && cw + i / 2 * 32 + q * 8 < c_hi)
+        *reinterpret_cast<uint4*>(out + (size_t)row[i % 2] * N + cw + i / 2 * 32 + q * 8) = v[i / 2][i % 2];
     return;
   }
+  const bool bare = !kVec && tile.adapter < 0;
   // y, asked for at once and held by no registers.  Aligned: each thread's
   // pieces into slots of its own.  Otherwise each row's aligned 16-byte pieces
   // (all of which hold bytes of the row's columns) into a row of shared memory,
   // shifted there by the warp that fetched them, and back on the way out.
-  const int cw = c0 + (warp >> 2) * (kCols / 2);
-  uint4* ys = reinterpret_cast<uint4*>(lu_smem) + tid;   // [group][half][thread]
   if constexpr (kVec) {
 #pragma unroll
     for (int u = 0; u < kGroups; ++u)
@@ -985,6 +1012,7 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
   if (kVec && mg * 16 >= tile.rows) return;   // no rows for this warp
   const uint32_t bs = s0 + (uint32_t)((warp >> 2) * (kCols / 2) + (lane & 7) + (lane >> 4) * 8) * pitch +
                       (uint32_t)((lane >> 3) & 1) * 16;
+  if (kVec || !bare)
 #pragma unroll
   for (int u = 0; u < kGroups; ++u) {
     float acc[4][4];
@@ -992,17 +1020,15 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
     for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 #pragma unroll
     for (int s = 0; s < NK; ++s)
-      if (s * 16 < rank && !bare) {
+      if (s * 16 < rank) {
+        const uint32_t lo[4] = {tl[s].x, tl[s].y, tl[s].z, tl[s].w}, hi[4] = {th[s].x, th[s].y, th[s].z, th[s].w};
+        uint32_t bf[2][4];
 #pragma unroll
-        for (int jp = 0; jp < 2; ++jp) {
-          const uint32_t lo[4] = {tl[s].x, tl[s].y, tl[s].z, tl[s].w}, hi[4] = {th[s].x, th[s].y, th[s].z, th[s].w};
-          uint32_t bf[4];
-          ldsm4(bf, bs + (uint32_t)(u * 32 + jp * 16) * pitch + s * 32);
-          mma16816(acc[2 * jp], lo, bf[0], bf[1]);
-          mma16816(acc[2 * jp + 1], lo, bf[2], bf[3]);
-          mma16816(acc[2 * jp], hi, bf[0], bf[1]);
-          mma16816(acc[2 * jp + 1], hi, bf[2], bf[3]);
-        }
+        for (int jp = 0; jp < 2; ++jp) ldsm4(bf[jp], bs + (uint32_t)(u * 32 + jp * 16) * pitch + s * 32);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma16816(acc[j], lo, bf[j / 2][j % 2 * 2], bf[j / 2][j % 2 * 2 + 1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma16816(acc[j], hi, bf[j / 2][j % 2 * 2], bf[j / 2][j % 2 * 2 + 1]);
       }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -1011,9 +1037,9 @@ __global__ void __launch_bounds__(kLoThreads, NK <= 2 ? 4 : NK == 4 ? 3 : 2) k_l
         const int n = cw + u * 32 + q * 8;
         if (n >= c_hi) continue;
         uint4 v = ys[(u * 2 + h) * kLoThreads];
-        if (!bare) add_pairs(&v, acc, h);
+        add_pairs(&v, acc, h);
         *reinterpret_cast<uint4*>(out + (size_t)row[h] * N + n) = v;
-      } else if (!bare) {
+      } else {
         // (columns past the last are computed in place too, and not stored)
         uint4* rp = reinterpret_cast<uint4*>(lu_smem + (mg * 16 + g + 8 * h) * Up<NK>::kRowBytes) + (cw - c0 + u * 32) / 8 + q;
         uint4 v = *rp;
