@@ -18,7 +18,7 @@
 // rounding and the remainder, 2^-17 of it in all), so no accuracy is lost to
 // the 16-bit operands.  mma.sync: up to rank 32 the tensor work hides behind
 // the stream of y (8192 rows, 2688 -> 10304: rank 16 70 us, floor 57; rank 32
-// 76); at rank 64 and 128 its two passes show (97 and 198).
+// 77); at rank 64 and 128 its two passes show (98 and 200).
 #include <algorithm>
 #include <type_traits>
 
@@ -749,10 +749,10 @@ __global__ void __launch_bounds__(kLoThreads) k_lora_down(const uint16_t* __rest
 // GPU at once (see lora_one_kernel): the CTAs that shared K share the columns,
 // in 64-wide steps through a ring of stages.  The first steps' y and B are under
 // way while t is joined.  No launch and no tail between the products: 5669 rows
-// 4096 -> 2688 in 31.6 us at rank 32, 27.9 at rank 16 (with the two kernels 33.5
-// and 31.9; floor 16.3).  Bringing each row's y to L2 further ahead took 3 more.
+// 4096 -> 2688 in 30.5 us at rank 32, 28.0 at rank 16 (with the two kernels 34.0
+// and 32.4; floor 16.3).  Bringing each row's y to L2 further ahead took 3 more.
 // kW: columns per piece of y and out (8, or 4 or 2 where rows of N % 4 or N % 2
-// columns start on no more: 1336 x 2498 of 63 adapters, rank 24, in 23.6 us, with
+// columns start on no more: 1336 x 2498 of 63 adapters, rank 24, in 23.3 us, with
 // the two kernels 26).
 // ---------------------------------------------------------------------------
 namespace {
@@ -1098,10 +1098,10 @@ int lora_splits(int M, int K) {
 // where the tiles' clusters fit on the GPU at once, two CTAs per SM, with two
 // CTAs a tile at least; a CTA's columns are a loop, so not where few CTAs have
 // many steps; and a long stream of y runs better with many small CTAs.  us, one
-// kernel / two, 4096 -> 2688 rank 32: 600 rows 15.6 / 16.8, 2048 17.4 / 21.4,
-// 5669 31.6 / 33.5, 9600 (more tiles than that) 64 / 48; 2688 -> 10304 rank 16:
-// 1024 rows (128 CTAs of 20 steps) 21.5 / 18.9, 2048 24 / 27, 5669 53.8 / 54.1,
-// 8192 73.5 / 70.3.
+// kernel / two, 4096 -> 2688 rank 32: 600 rows 15.3 / 16.9, 2048 17.1 / 21.7,
+// 5669 30.5 / 34.0, 9600 (more tiles than that) 64 / 48; 2688 -> 10304 rank 16:
+// 1024 rows (128 CTAs of 20 steps) 21.5 / 19.2, 2048 24.3 / 27.5, 5669 53.6 /
+// 54.5, 8192 73.5 / 70.6.
 int lora_one_kernel(int M, int N, int K, int max_tiles) {
   const int sms = device_sm_count(), kblocks = (K + kDownK - 1) / kDownK;
   const int splits = std::min({2 * sms / max_tiles, 8, kblocks / 4});
