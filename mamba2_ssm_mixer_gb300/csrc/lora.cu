@@ -5,7 +5,7 @@
 // small change (2 rank (K + N) operations per row); what bounds the call is
 // reading y and writing out once, or, in a decode batch, reading each named
 // adapter once.  Two forms:
-//  - up to kFewRows rows: one kernel, one 4-CTA cluster per (up to kUnit rows
+//  - few rows (see few_rows): one kernel, one 4-CTA cluster per (up to kUnit rows
 //    of one adapter, slice of N).  Which rows share an adapter is found by
 //    each cluster itself from the batch's ids (a ballot), so there is no
 //    sorting launch and no workspace, and a shared adapter is read once per
@@ -96,7 +96,7 @@ __device__ __forceinline__ void cp_wait() {
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Up to kFewRows rows.  Grid (4 x slices of N, M), clusters of 4 along x; the
+// Few rows.  Grid (4 x slices of N, M), clusters of 4 along x; the
 // cluster of row m goes on if m is the first of a run of 8 among the rows of
 // its adapter in its window of 256 rows (a ballot in every warp, no barrier).
 // Both products put the adapter's matrix on the 16-wide side of m16n8k16 and
@@ -115,7 +115,7 @@ __device__ __forceinline__ void cp_wait() {
 // ahead 0.3 to 1.2 more.
 // ---------------------------------------------------------------------------
 namespace {
-constexpr int kFewRows = 256, kFewMost = 512;   // see few_rows
+constexpr int kFewRows = 320, kFewMost = 1024;   // see few_rows
 constexpr int kWindow = 256;
 constexpr int kFewCluster = 4;
 constexpr int kUnit = 8;   // rows that share the reads of an adapter
@@ -1214,12 +1214,13 @@ cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights&
 }  // namespace
 
 // Which form: units of an adapter's rows up to kFewRows rows; beyond, up to
-// kFewMost, while the adapters are so many that a 64-row tile would be nearly
-// empty.  Measured (us, units / tiles), 2688 -> 10304: rank 16, 1 adapter:
-// 64 rows 9 / 13, 256 rows 13 / 13; 64 adapters: 64 rows 11 / 30, 256 rows
-// 18 / 31, 384 rows 25 / 31; 256 adapters: 512 rows 64 / 87; 4096 -> 2688, rank
-// 64, 64 adapters: 256 rows 29 / 48, 384 rows 45 / 40.
-static bool few_rows(int M, int n_adapters) { return M <= kFewRows || (M <= kFewMost && M < 4 * n_adapters); }
+// kFewMost, while the adapters are so many that 64-row tiles would be nearly
+// empty.  Measured (us, units / tiles): 2688 -> 10304 rank 16, 1 adapter: 256
+// rows 13 / 13, 320 14.5 / 12.9, 384 16.4 / 13.7; 64 adapters: 256 rows 17 / 29,
+// 384 21 / 30, 512 23 / 25, 640 31 / 31; 256 adapters: 1024 rows 52 / 82.  4096 ->
+// 2688 rank 32, 1 adapter: 320 rows 12.0 / 13.3, 384 13.9 / 13.3; 64 adapters:
+// 384 rows 17 / 23, 640 26 / 23; 128: 896 rows 30.5 / 32, 1024 32 / 28.
+static bool few_rows(int M, int n_adapters) { return M <= kFewRows || (M <= kFewMost && M <= 7 * n_adapters); }
 
 size_t lora_workspace_bytes(int M, int N, int K, int rank, int n_adapters) {
   (void)N, (void)K;

@@ -74,7 +74,8 @@ def _run(x, y, a, b, scale, ids, out=None, **kw):
     (130, 64, 64, 8, 200), (255, 1000, 272, 32, 12), (257, 1001, 528, 56, 7), (300, 10304, 2688, 16, 3),
     (513, 2688, 4096, 32, 2), (1000, 264, 2688, 104, 40), (2049, 136, 112, 16, 1), (5000, 33, 32, 8, 4096),
     (400, 1003, 272, 16, 120), (512, 520, 160, 72, 300), (900, 777, 1024, 24, 11), (300, 515, 96, 128, 2),
-    (700, 4099, 64, 64, 3)])
+    (700, 4099, 64, 64, 3), (320, 2688, 512, 32, 2), (321, 515, 96, 128, 2), (321, 515, 96, 32, 46), (1024, 264, 272, 16, 150),
+    (1023, 1001, 96, 72, 256), (1024, 130, 528, 8, 146), (1025, 72, 528, 24, 700)])
 def test_matches_the_formula(M, N, K, rank, na):
     args = _inputs(M, N, K, rank, na, M * 7 + N)
     x, y, a, b, scale, ids = args
@@ -172,7 +173,7 @@ def test_a_row_does_not_reach_another(M):
     _check(got[keep], val[keep], err[keep], args[1][keep], args[5][keep])
 
 
-@pytest.mark.parametrize("M", [8, 300])
+@pytest.mark.parametrize("M", [8, 300, 700])
 def test_an_unknown_adapter_is_reported_and_taken_as_none(M):
     x, y, a, b, scale, ids = _inputs(M, 128, 64, 8, 3, M + 2)
     ids[:] = np.arange(M) % 3
