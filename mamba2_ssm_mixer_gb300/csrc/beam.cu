@@ -479,8 +479,9 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
     }
   }
   for (int c = tid + kKeep * blockDim.x; c < total; c += blockDim.x) mine = max(mine, bounds(c, c % beams, mykeys[c], &hi));
-  // (tau from the first 8 warps: theirs are the chunks' best)
-  const int tw = min(nw, 8);
+  // (tau from the first 8 warps, theirs are the chunks' best, or from those
+  // whose lanes all have a key: an empty warp would leave no threshold)
+  const int tw = min(8, max(1, min(nw, total / 32)));
   uint32_t tau = __reduce_max_sync(0xffffffffu, mine);
   for (int i = (k + tw - 1) / tw; i > 1; --i) {
     const uint32_t who = __ballot_sync(0xffffffffu, mine == tau);
