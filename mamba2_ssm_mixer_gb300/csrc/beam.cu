@@ -136,16 +136,6 @@ __device__ __forceinline__ void repack(uint4 (&q)[VPT]) {
   for (int j = 0; j < VPT; ++j) asm volatile("" : "+r"(q[j].x), "+r"(q[j].y), "+r"(q[j].z), "+r"(q[j].w));
 }
 
-// 16 bytes from p, whose address may sit `off` bytes past a 16-byte boundary
-// (off uniform over the row): two aligned loads and byte shifts.  Both loads
-// hold at least one byte of the 16.
-__device__ __forceinline__ uint4 load16(const void* p, uint32_t off) {
-  const uint4* q = reinterpret_cast<const uint4*>((const char*)p - off);
-  const uint4 a = __ldg(q);
-  if (off == 0) return a;
-  return bytes16_at(a, __ldg(q + 1), off);
-}
-
 __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -189,20 +179,38 @@ __global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 4 : 6) k_beam_rows(cons
 
   uint4 q[VPT];
   float vm[VPT], mx = -INFINITY;
-  if (first + kBeThreads * V * VPT <= end) {   // a full chunk
+  const bool full = first + kBeThreads * V * VPT <= end;
+  const int whole = (end - first) / V;   // vectors that lie in the chunk
+  if (whole > 0) {
+    // loads without conditions, past the chunk from its last vector instead,
+    // and a few ahead of their shifts: else each waits for the one before
+    const uint4* p = reinterpret_cast<const uint4*>((const char*)(base + first) - off);
+    const int more = off != 0;
+    constexpr int kBatch = kAligned || VPT < 4 ? VPT : 4;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) q[j] = load16(base + first + (j * kBeThreads + tid) * V, off);
-  } else
+    for (int j0 = 0; j0 < VPT; j0 += kBatch) {
+      uint4 next[kBatch];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int at = first + (j * kBeThreads + tid) * V;
-    if (at + V <= end) {
-      q[j] = load16(base + at, off);
-    } else {
-      q[j] = make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+      for (int j = 0; j < kBatch; ++j) {
+        const int at = full ? (j0 + j) * kBeThreads + tid : min((j0 + j) * kBeThreads + tid, whole - 1);
+        q[j0 + j] = __ldg(p + at);
+        if constexpr (!kAligned) next[j] = __ldg(p + at + more);
+      }
+      if constexpr (!kAligned)
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (at + e < end) E::put(&q[j], e, base[at + e]);
+        for (int j = 0; j < kBatch; ++j) q[j0 + j] = bytes16_at(q[j0 + j], next[j], off);
+    }
+  }
+  if (!full) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int i = j * kBeThreads + tid;
+      if (i >= whole) {
+        q[j] = make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (first + i * V + e < end) E::put(&q[j], e, base[first + i * V + e]);
+      }
     }
   }
 #pragma unroll
