@@ -545,7 +545,13 @@ m2_status m2_beam_select_workspace_size(int batch, int beams, int vocab, int k, 
  *   out_done    uint8 [batch, k] device or NULL: 1 where the parent was
  *               finished or the token is eos, else 0
  * A logit of -inf is masked (no continuation); a NaN is treated as masked.  A
- * row of +inf logits shares the probability equally among them.  Where a
+ * row of +inf logits shares the probability equally among them.  Finite logits
+ * may be of any size: log sum exp is kept relative to the row's largest logit,
+ * so a row of n equal ones gives each token scores[b] - log n.  The exception
+ * is a row whose largest logit is at or below -2^127 (nothing in it but the
+ * lowest values that masks are filled with): its sum counts as one there, its
+ * tokens equal to the largest keep scores[b].  Mask with -inf for a beam
+ * without continuations.  Where a
  * request has fewer than k continuations, the rest is token -1, parent -1,
  * score -inf, done 0.
  * out_scores may be scores, and out_done done, when k == beams; otherwise no

@@ -18,7 +18,7 @@
 // and 43.  A CTA over several chunks that keeps its list from one to the next
 // took 47 to 64, a first form that kept the row unpacked in registers and
 // summed in f64 181.
-// k_beam_merge: a CTA per request joins the chunks' sums to lse_b, and selects
+// k_beam_merge: a CTA per request joins the chunks' sums of a row, and selects
 // among the chunks' survivors by the 64-bit value in the same way.
 //
 // Order: greater value first, then the lower beam * vocab + token.  Within a
@@ -26,6 +26,8 @@
 // lse from f32 sums in an order that depends on the token's index alone (not
 // on the row's address), so equal rows get equal values and a true tie stays
 // one.
+#include <type_traits>
+
 #include "launch_util.h"
 #include "m2_kernels.h"
 
@@ -80,6 +82,11 @@ __device__ __forceinline__ float2 unpair(uint64_t v) {
 __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
@@ -218,39 +225,54 @@ __global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 4 : 6) k_beam_rows(cons
   const uint32_t om = ord32(mx + 0.f);   // + 0: -0 and +0 are equal logits
   const uint32_t owm = __reduce_max_sync(0xffffffffu, om);
   const float m = unord32(owm);
-  // sum of exp(x - m) = 2^r sum 2^(c x - cm), cm = c m rounded, r its rounding
-  // error: one multiply-add per element, and the error of c scales x - m only
+  // sum of exp(x - m) = 2^-r sum 2^(c x - cm), cm = c m rounded, r = c m - cm:
+  // one multiply-add per element, and the error of c scales x - m only.  2^-r
+  // is taken to first order, which is right to 2^-24 while |r| <= 2^-11, up to
+  // |m| = 2^13 / c at least; r grows with m, so past that x - m comes first, in
+  // one instruction more (half a us of 35 for 64 x 8 x 131072).
   constexpr float kLog2e = 1.4426950408889634f;
-  const float cm = m * kLog2e;
-  uint64_t acc = pair(0.f, 0.f);
+  const float cm = m * kLog2e, r = fmaf(m, kLog2e, -cm);
+  auto sum = [&](auto shifted) {
+    constexpr bool kShifted = decltype(shifted)::value;
+    uint64_t acc = pair(0.f, 0.f);
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+    for (int j = 0; j < VPT; ++j) {
+      const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      uint64_t x;
-      if constexpr (V == 8)
-        x = pair(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-      else
-        x = pair(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
-      const float2 t = unpair(fma_pair(x, pair(kLog2e, kLog2e), pair(-cm, -cm)));
-      acc = add_pair(acc, pair(exp2_fast(t.x), exp2_fast(t.y)));
+      for (int e = 0; e < V / 2; ++e) {
+        uint64_t x;
+        if constexpr (V == 8)
+          x = pair(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+        else
+          x = pair(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+        const float2 t = unpair(kShifted ? mul_pair(add_pair(x, pair(-m, -m)), pair(kLog2e, kLog2e))
+                                         : fma_pair(x, pair(kLog2e, kLog2e), pair(-cm, -cm)));
+        acc = add_pair(acc, pair(exp2_fast(t.x), exp2_fast(t.y)));
+      }
     }
+    const float2 acc2 = unpair(acc);
+    return acc2.x + acc2.y;
+  };
+  float s;
+  if (fabsf(r) <= 0x1p-11f) {   // (the same for the warp)
+    s = sum(std::false_type());
+    s = fmaf(s, -0.6931471805599453f * r, s);
+  } else {
+    s = sum(std::true_type());
   }
-  const float2 acc2 = unpair(acc);
-  float s = acc2.x + acc2.y;
-  const float r = fmaf(m, kLog2e, -cm);
-  s = fmaf(s, -0.6931471805599453f * r, s);
   repack(q);
-  if (isnan(s)) {   // a NaN (no candidate), a warp of -inf, +inf (takes all the probability), c x past the f32 range
+  if (isnan(s)) {   // a NaN (no candidate), a warp of -inf, +inf (takes all the probability)
     s = 0.f;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
+    for (int j = 0; j < VPT; ++j) {
+      float sj = 0.f;   // (a vector's sum of its own: as few additions in a row as above)
 #pragma unroll 1
       for (int e = 0; e < V; ++e) {
         const float x = E::at(q[j], e);
-        if (x > -INFINITY) s += x == m ? 1.f : exp2_fast((x - m) * kLog2e);
+        if (x > -INFINITY) sj += x == m ? 1.f : exp2_fast((x - m) * kLog2e);
       }
+      s += sj;
+    }
   }
   repack(q);
 #pragma unroll
@@ -375,19 +397,24 @@ __global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 4 : 6) k_beam_rows(cons
   }
 }
 
-// One request.  The chunks' keys are first bounded in f32: value(b, v) lies
-// within 2^-22 (|score_b - lse_b| + |x|) of its f32 sum (f64 runs at a small
-// fraction of the f32 rate); tau is taken over the lower bounds, and only the
-// few whose upper bound reaches it are valued in 64 bits and ranked.
+// One request.  With m the row's maximum and l = lse - m, value(b, v) is
+// score + ((x - m) - l): l keeps its digits whatever the size of m, where a
+// 64-bit lse of a row near 1e12 or more would have none for it.  (A row whose
+// maximum is at the bottom of f32, below -2^127, holds nothing but the lowest
+// values that masks are filled with: l is 0 there, as in a 64-bit lse.)
+// The chunks' keys are first bounded in f32: value(b, v) lies within 2^-22
+// (|score - l| + |x - m|) of its f32 sum (f64 runs at a small fraction of the
+// f32 rate); tau is taken over the lower bounds, and only the few whose upper
+// bound reaches it are valued in 64 bits and ranked.
 constexpr int kKeep = 4;   // keys a thread holds in registers between the two looks at them
 __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict__ keys,
                                                      const ChunkSum* __restrict__ sums, const float* scores,
                                                      const uint8_t* done, int beams, int eos, int k, int splits, int32_t* __restrict__ tokens,
                                                      int32_t* __restrict__ parents, float* out_scores,
                                                      uint8_t* out_done) {
-  __shared__ double score[kBeamMaxBeams], lse[kBeamMaxBeams];
-  __shared__ float offs[kBeamMaxBeams];     // f32 of score - lse
-  __shared__ float top[kBeamMaxBeams];      // the row's maximum (+inf: lse holds the log of their count)
+  __shared__ double score[kBeamMaxBeams], lsum[kBeamMaxBeams];   // l: log of sum exp(x - m)
+  __shared__ float offs[kBeamMaxBeams];     // f32 of score - l
+  __shared__ float top[kBeamMaxBeams];      // m (+inf: l is the log of their count)
   __shared__ int kind[kBeamMaxBeams];       // 0: no candidates, 1: live, 2: finished
   __shared__ uint32_t wtau[32];
   __shared__ uint64_t cval[kCap], cflat[kCap];
@@ -430,11 +457,11 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
       int e;
       float f = frexpf(s, &e);
       if (f < 0.70710678f) f *= 2.f, --e;
-      const double l = (double)e * 0.693147180559945309 + (double)logf(f) + (isinf(m) ? 0. : (double)m);
+      const double l = m > -0x1p127f ? (double)e * 0.693147180559945309 + (double)logf(f) : 0.;
       kind[b] = s > 0.f ? 1 : 0;
       top[b] = m;
       score[b] = (double)sc;
-      lse[b] = l;
+      lsum[b] = l;
       offs[b] = (float)((double)sc - l);
     }
   }
@@ -448,12 +475,10 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
     const float off = offs[b];
     if (kd != 1) return kd == 2 && c < beams ? *hi = ord32(off + 0.f) : 0;
     if (key == 0) return 0;
-    float x = unord32((uint32_t)(key >> 32));
-    if (isinf(top[b])) {
-      if (x != top[b]) return 0;
-      x = 0.f;
-    }
-    const float v = x + off, err = 0x1p-22f * (fabsf(x) + fabsf(off));
+    const float x = unord32((uint32_t)(key >> 32)), m = top[b];
+    if (isinf(m) && x != m) return 0;
+    const float d = isinf(m) ? 0.f : x - m;
+    const float v = d + off, err = 0x1p-22f * (fabsf(d) + fabsf(off));
     if (!(fabsf(v) + err < 3.0e38f)) {   // past f32: bounded by nothing
       *hi = ord32(INFINITY);
       return kOrdNegInf;
@@ -468,8 +493,8 @@ __global__ void __launch_bounds__(1024) k_beam_merge(const uint64_t* __restrict_
       return ord64(score[b] + 0.);
     }
     *flat = ((uint64_t)b << 32) | (0xffffffffu - (uint32_t)key);
-    const double x = isinf(top[b]) ? 0. : (double)unord32((uint32_t)(key >> 32));
-    return ord64(score[b] + (x - lse[b]) + 0.);
+    const double d = isinf(top[b]) ? 0. : (double)unord32((uint32_t)(key >> 32)) - (double)top[b];
+    return ord64(score[b] + (d - lsum[b]) + 0.);
   };
   uint32_t mine = 0, hi, hi_held[kKeep];
   int b_held[kKeep];

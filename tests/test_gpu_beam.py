@@ -244,3 +244,63 @@ def test_repeats_on_streams_and_in_a_graph():
 def test_no_requests():
     step = m2.m2_beam_select(torch.empty((0, 50), dtype=BF, device="cuda"), torch.empty((0, 4), device="cuda"))
     assert step.tokens.shape == (0, 4)
+
+
+# ---- logits of any finite size.  A shift of a row by a constant leaves its
+# values: they are taken here as scores + ((x - max) - log sum exp(x - max)),
+# which keeps log sum exp where x - log sum exp(x) in 64 bits has no room for
+# it.  The bound is the one above: the exponent is (x - max) log2 e, x - max
+# rounded once at most, however large the row's maximum is.
+
+
+def _shifted(x, scores):
+    x = np.asarray(x, np.float64)
+    m = x.max(-1, keepdims=True)
+    d = x - m
+    with np.errstate(under="ignore"):
+        logp = d - np.log(np.exp(d).sum(-1, keepdims=True))
+    return np.asarray(scores, np.float64)[..., None] + logp
+
+
+def _check_values(step, val, k):
+    """Every request has its k best (finite logits: there are that many), in
+    order, and their scores."""
+    nb, kb, v = val.shape
+    tok, par, sc = (t.cpu().numpy() for t in step[:3])
+    for i in range(nb):
+        flat = val[i].reshape(-1)
+        order = np.argsort(-flat, kind="stable")[:k + 1]
+        best = flat[order]
+        assert (tok[i] >= 0).all() and (par[i] >= 0).all(), (i, "continuations lost", tok[i], par[i])
+        got = par[i].astype(np.int64) * v + tok[i]
+        assert len(set(got.tolist())) == k
+        bound = LSE + 2.0 ** -24 * np.abs(flat[got])
+        assert np.all(np.abs(sc[i] - flat[got]) <= bound), (i, sc[i], flat[got])
+        assert np.all(np.abs(flat[got] - best[:k]) <= 2 * LSE)
+        apart = np.concatenate([[np.inf], -np.diff(best), [np.inf]])
+        clear = ((apart > 4 * LSE) | (apart == 0))
+        clear = clear[:k] & clear[1:k + 1]
+        assert np.array_equal(got[clear], order[:k][clear]), (i, got, order)
+
+
+SIZES = [5e3, 1.1e4, 2e4, 1e5, 1e6, 1e7, 1e8, 1e9, 1e12, 1e30, 1e38]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("v,pad", [(257, 0), (9001, 3), (70000, 0)])
+@pytest.mark.parametrize("size", [s * c for c in SIZES for s in (1, -1)])
+def test_large_finite_logits(size, v, pad, dtype):
+    """Rows uniform at a large value (all beams, or one beside live ones), a
+    few or most tokens masked with it, one token forced with it, and rows
+    shifted by it."""
+    nb, kb = 6, 3
+    logits, _, scores = _case(nb, kb, v, dtype, 91 + v, pad)
+    L = logits.view(nb, kb, v) if not pad else logits.as_strided((nb, kb, v), (kb * logits.stride(0), logits.stride(0), 1))
+    L[0] = size
+    L[1, 1] = size
+    L[2, :, ::2] = size
+    L[3, :, 12:] = size
+    L[4, 0, v // 3] = size
+    L[5] += size
+    x = logits.float().cpu().numpy().reshape(nb, kb, v)
+    _check_values(_go(logits, scores, 7), _shifted(x, scores), 7)
