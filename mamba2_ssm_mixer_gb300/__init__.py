@@ -332,7 +332,8 @@ class Mamba2Mixer:
                      has_initial=None, out=None, workspace=None, stream=None):
         """prefill (bf16 hidden) with an adapter per sequence: seq_adapter is a
         list of adapter numbers, -1 for none (m2_prefill_lora)."""
-        seqlens, T = list(seqlens), sum(seqlens)
+        seqlens = list(seqlens)
+        T = sum(seqlens)
         _need(hidden, "hidden", torch.bfloat16, (T, HIDDEN))
         _need(conv_state, "conv_state", torch.bfloat16, (len(seqlens), CONV_DIM, CONV_WIDTH - 1))
         _need(ssm_state, "ssm_state", self.state_dtype, (len(seqlens), NHEADS, HEADDIM, D_STATE))

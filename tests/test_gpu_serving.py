@@ -346,3 +346,14 @@ def test_a_search_step_in_a_graph(search):
         runs.append((*conv, *ssm, slots, scores, tok))
     assert all(torch.equal(a, b) for a, b in zip(*runs))
     m2.check_standalone()
+
+
+def test_prefill_takes_its_lengths_from_any_iterable(block):
+    _, blk, _ = block
+    lora, *_ = _adapters(seed=1)
+    lens = [9, 4]
+    h = bf16_dev(synth.make_hidden(6, sum(lens)))
+    outs = [blk.prefill_lora(h, n, bf16_dev(synth.make_conv_state(6, 2)), f32_dev(synth.make_ssm_state(6, 2)), lora, [1, -1])
+            for n in (lens, iter(lens))]
+    torch.cuda.synchronize()
+    assert torch.equal(*outs)
