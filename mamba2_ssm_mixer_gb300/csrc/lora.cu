@@ -14,9 +14,9 @@
 //    (while the next kernel's CTAs bring x to L2), k_lora_down forms t on the
 //    tensor cores, K split over a cluster, and k_lora_up streams y past B t;
 //    or, up to rank 32 and a middling batch, k_lora_tile does both.
-// t is summed in f32 and enters the second product as two bf16 parts (its
-// rounding and the remainder, 2^-17 of it in all), so no accuracy is lost to
-// the 16-bit operands.  mma.sync: up to rank 32 the tensor work hides behind
+// t is summed in f32 and enters the second product as two bf16 parts, 2^-16 of
+// it in all (an f32 operand would keep 2^-24; out keeps 2^-9 of the sum): the
+// 16-bit tensor rate, at twice the operations.  mma.sync: up to rank 32 the tensor work hides behind
 // the stream of y (8192 rows, 2688 -> 10304: rank 16 70 us, floor 57; rank 32
 // 77); at rank 64 and 128 its two passes show (98 and 200).
 #include <algorithm>
@@ -38,12 +38,20 @@ constexpr int kLoWarps = kLoThreads / 32;
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// a, b as two bf16 pairs: their rounding and the remainder.  An infinite or
-// NaN value has no remainder; its rounding carries it.
+// a, b as two bf16 pairs: their first 8 bits and the remainder, 2^-16 of them
+// in all.  Cut, not rounded, and with the least normal value for a remainder
+// of 0, so that the parts of what is not 0 have one sign and neither is 0: an
+// infinite weight then makes the same infinity of both, as the formula does
+// (0 x inf or inf - inf would be NaN).  2^-126 of a weight is past the last
+// digit of the first part's product, and of no account where that is not.
 __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t* hi, uint32_t* lo) {
-  *hi = pack_bf16x2(a, b);
-  const float ra = a - lo_f(*hi), rb = b - hi_f(*hi);
-  *lo = pack_bf16x2(isfinite(ra) ? ra : 0.f, isfinite(rb) ? rb : 0.f);
+  const uint32_t h = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  // (an infinite value has no remainder, a NaN is one in both parts)
+  const uint32_t r = pack_bf16x2(isinf(a) ? 0.f : a - lo_f(h), isinf(b) ? 0.f : b - hi_f(h));
+  const uint32_t la = (r & 0x7FFFu) || !(h & 0x7FFFu) ? 0u : (h & 0x8000u) | 0x0080u;
+  const uint32_t lb = (r & 0x7FFF0000u) || !(h & 0x7FFF0000u) ? 0u : (h & 0x80000000u) | 0x00800000u;
+  *hi = h;
+  *lo = r | la | lb;
 }
 
 __device__ __forceinline__ uint32_t lo_cluster_rank() {
@@ -132,7 +140,7 @@ __global__ void __launch_bounds__(kLoThreads, NT <= 4 ? 2 : 1) k_lora_few(
   __shared__ int rows_s[kUnit];
   __shared__ __align__(16) float red[kLoWarps][NT * 128];
   __shared__ float part[NT * 128];
-  __shared__ __align__(16) float t_s[kUnit][NT * 16 + 4];
+  __shared__ __align__(16) uint16_t t_s[2][kUnit][NT * 16 + 8];   // t's two bf16 parts
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int crank = (int)lo_cluster_rank();
   const int m = blockIdx.y;
@@ -276,18 +284,20 @@ __global__ void __launch_bounds__(kLoThreads, NT <= 4 ? 2 : 1) k_lora_few(
     for (int r = 1; r < kFewCluster; ++r) t += v[r];
     const int l = (i >> 2) & 31, e = i & 3;   // fragment entry: rank index l / 4 (+ 8), row 2 (l % 4) (+ 1)
     const int j = (i >> 7) * 16 + (l >> 2) + 8 * (e >> 1);
-    t_s[2 * (l & 3) + (e & 1)][j] = j < rank ? t * sc : 0.f;
+    uint32_t hi, lo;
+    split_bf16x2(j < rank ? t * sc : 0.f, 0.f, &hi, &lo);
+    t_s[0][2 * (l & 3) + (e & 1)][j] = (uint16_t)hi;
+    t_s[1][2 * (l & 3) + (e & 1)][j] = (uint16_t)lo;
   }
   lo_cluster_arrive();   // (waited for at the end: no CTA leaves while its part is read)
   __syncthreads();
 
-  // t of row g in two bf16 parts, in the order of B's pieces
-  uint32_t th[NT][2], tl[NT][2];
+  // t of row g, in the order of B's pieces
+  uint2 th[NT], tl[NT];
 #pragma unroll
   for (int s = 0; s < NT; ++s) {
-    const float4 v = *reinterpret_cast<const float4*>(&t_s[g][16 * s + 4 * q]);
-    split_bf16x2(v.x, v.y, &th[s][0], &tl[s][0]);
-    split_bf16x2(v.z, v.w, &th[s][1], &tl[s][1]);
+    th[s] = *reinterpret_cast<const uint2*>(&t_s[0][g][16 * s + 4 * q]);
+    tl[s] = *reinterpret_cast<const uint2*>(&t_s[1][g][16 * s + 4 * q]);
   }
   for (int n0 = n_first; n0 - 2 * g < n_hi; n0 += kAheadF * (16 * kLoWarps)) {
 #pragma unroll
@@ -297,8 +307,8 @@ __global__ void __launch_bounds__(kLoThreads, NT <= 4 ? 2 : 1) k_lora_few(
 #pragma unroll
       for (int s = 0; s < NT; ++s) {
         const uint32_t(&bf)[4] = {bv[u][s][0].x, bv[u][s][1].x, bv[u][s][0].y, bv[u][s][1].y};
-        mma16816(d, bf, tl[s][0], tl[s][1]);
-        mma16816(d, bf, th[s][0], th[s][1]);
+        mma16816(d, bf, tl[s].x, tl[s].y);
+        mma16816(d, bf, th[s].x, th[s].y);
       }
       const uint32_t y0 = yv[u][0], y1 = yv[u][1];
       fetch(u, n + kAheadF * (16 * kLoWarps));

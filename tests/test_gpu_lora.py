@@ -247,3 +247,34 @@ def test_repeats_bit_for_bit_on_streams_and_in_a_graph(M):
     torch.cuda.synchronize()
     assert torch.equal(out, want2) and not torch.equal(out, want)
     m2.check_standalone()
+
+
+@pytest.mark.parametrize("M,N,K,rank,na", [
+    (64, 264, 160, 16, 5), (9, 515, 96, 40, 3), (300, 200, 64, 128, 2), (130, 96, 2688, 24, 40),   # few rows
+    (640, 1000, 1040, 8, 5), (700, 1004, 528, 24, 3), (1100, 202, 1040, 32, 2),                     # both products in one
+    (700, 1000, 272, 56, 4), (700, 1001, 528, 24, 3), (400, 264, 64, 128, 2), (1300, 261, 96, 72, 3)])
+@pytest.mark.parametrize("whole", [False, True])
+def test_infinite_weights(M, N, K, rank, na, whole):
+    """Infinities and a NaN in b: the columns they reach are the formula's
+    infinities or NaN, every other one is as without them.  whole: integers,
+    an intermediate that bf16 holds exactly."""
+    x, y, a, b, scale, ids = _inputs(M, N, K, rank, na, M + 3 * N)
+    if whole:
+        rng = np.random.default_rng(M + N)
+        x[:], a[:] = 0.0, 0.0
+        x[:, :2], a[:, :, :2] = rng.integers(1, 8, (M, 2)), rng.integers(-7, 8, (na, rank, 2)) * 2.0 + 1.0
+        scale[:] = 0.5
+    b[0, 3, 1] = np.inf
+    b[0, N - 1, rank - 1] = -np.inf
+    b[1, 5, :2] = np.inf                        # two: an infinity or, of both signs, NaN
+    b[1, N // 2, 0] = np.nan
+    b[1, 7] = np.inf
+    with np.errstate(invalid="ignore"):
+        val, err = _ref(x, y, a, b, scale, ids)
+    got = to_np(_run(x, y, a, b, scale, ids)).astype(np.float64)
+    odd = ~np.isfinite(val)
+    assert odd.any() and np.array_equal(got[odd], val[odd], equal_nan=True)
+    b[~np.isfinite(b)] = 0.0
+    val, err = _ref(x, y, a, b, scale, ids)
+    over = np.abs(got - val) > err + (np.abs(val) + err) * 2.0 ** -8
+    assert not (over & ~odd).any()
