@@ -46,8 +46,10 @@ namespace m2 {
 
 // Launch with programmatic dependent launch allowed: the kernel may start
 // while the previous kernel on the stream is finishing.  Every kernel of this
-// library calls pdl_wait() before its first global-memory access, so it only
-// touches data after the previous kernel has completed and flushed.
+// library calls pdl_wait() before pdl_trigger() and before its first write, and
+// reads ahead of pdl_wait() only what the previous kernel does not write:
+// weights, or what kernels before that one wrote, which have completed, since
+// the previous kernel waited for them before it let this one start.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                        Args&&... args) {

@@ -1225,11 +1225,16 @@ cudaError_t launch_many(const uint16_t* y, const uint16_t* x, const LoraWeights&
 
 // Which form: units of an adapter's rows up to kFewRows rows; beyond, up to
 // kFewMost, while the adapters are so many that 64-row tiles would be nearly
-// empty.  Measured (us, units / tiles): 2688 -> 10304 rank 16, 1 adapter: 256
-// rows 13 / 13, 320 14.5 / 12.9, 384 16.4 / 13.7; 64 adapters: 256 rows 17 / 29,
-// 384 21 / 30, 512 23 / 25, 640 31 / 31; 256 adapters: 1024 rows 52 / 82.  4096 ->
-// 2688 rank 32, 1 adapter: 320 rows 12.0 / 13.3, 384 13.9 / 13.3; 64 adapters:
-// 384 rows 17 / 23, 640 26 / 23; 128: 896 rows 30.5 / 32, 1024 32 / 28.
+// empty if the rows named them all, which the host does not know: 1000 rows
+// that name 1 or 4 of 256 adapters take 36 us, of 64 adapters (tiles) 19 to 21
+// (2688 -> 10304 rank 16).  The tile form's grids follow the adapters there are
+// as well: 5669 rows that name 4 of 4, 512 and 4096 take 54, 62 and 165 us.
+// Measured with all adapters named (us, units / tiles): 2688 -> 10304 rank 16, 1
+// adapter: 256 rows 13 / 13, 320 14.5 / 12.9, 384 16.4 / 13.7; 64 adapters: 256
+// rows 17 / 29, 384 21 / 30, 512 23 / 25, 640 31 / 31; 256 adapters: 1024 rows
+// 52 / 82.  4096 -> 2688 rank 32, 1 adapter: 320 rows 12.0 / 13.3, 384 13.9 /
+// 13.3; 64 adapters: 384 rows 17 / 23, 640 26 / 23; 128: 896 rows 30.5 / 32,
+// 1024 32 / 28.
 static bool few_rows(int M, int n_adapters) { return M <= kFewRows || (M <= kFewMost && M <= 7 * n_adapters); }
 
 size_t lora_workspace_bytes(int M, int N, int K, int rank, int n_adapters) {

@@ -10,7 +10,7 @@
 // pools: the plan (a few integers per row) is computed by every CTA for
 // itself in shared memory, which costs less than a second launch.
 // Bound by moving the bytes: 23 layers x 32 copies of bf16 rows (1.6 GB) in
-// 237 us, 1.01 of the copy rate; 32 copies of f32 rows (137 MB) in 23 us, 0.87;
+// 238 to 246 us, 0.97 to 1.01 of the copy rate; 32 copies of f32 rows (137 MB) in 23 us, 0.87;
 // two copies 3.9 us.  Four CTAs per SM with eight loads each under way: 2, 3, 5
 // and 6 CTAs took 9 to 30 us more on the first.
 #include "launch_util.h"
