@@ -227,9 +227,9 @@ __global__ void __launch_bounds__(kBeThreads, VPT == 8 ? 4 : 6) k_beam_rows(cons
   const float m = unord32(owm);
   // sum of exp(x - m) = 2^-r sum 2^(c x - cm), cm = c m rounded, r = c m - cm:
   // one multiply-add per element, and the error of c scales x - m only.  2^-r
-  // is taken to first order, which is right to 2^-24 while |r| <= 2^-11, up to
-  // |m| = 2^13 / c at least; r grows with m, so past that x - m comes first, in
-  // one instruction more (half a us of 35 for 64 x 8 x 131072).
+  // is taken to first order, which is right to 2^-24 while |r| <= 2^-11: always
+  // up to |m| = 2^14 / c.  Past that x - m comes first, in one instruction more
+  // (half a us of 35 for 64 x 8 x 131072).
   constexpr float kLog2e = 1.4426950408889634f;
   const float cm = m * kLog2e, r = fmaf(m, kLog2e, -cm);
   auto sum = [&](auto shifted) {
