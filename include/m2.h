@@ -591,6 +591,100 @@ m2_status m2_state_reorder(uint16_t* const* conv_pools, void* const* ssm_pools, 
                            const int32_t* slot_idx, const int32_t* parents, int32_t* new_slot_idx, int batch, int beams,
                            void* stream);
 
+/* ------------------------------------------------------------------------
+ * The head: products of microscaled 4-bit operands, and the log probabilities
+ * of tokens from the logits.  (The pages have no counterpart to these entry
+ * points.)
+ *
+ * MXFP4 (OCP Microscaling Formats): a row's values in blocks of 32 share a
+ * scale 2^(s - 127), s an e8m0 code (255: NaN), and are e2m1 codes (sign, then
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6).  codes: uint8 [rows, K / 2], the even k in a
+ * byte's low half.  scales: tiles of 128 rows x 128 values, 512 bytes each,
+ * [ceil(rows / 128)][ceil(K / 128)]; row r and block b of a tile at byte
+ * (r % 32) * 16 + (r / 32) * 4 + b, zero past the rows and past K
+ * (mxfp4_scale_bytes; mxfp4_pack_scales makes them from row-major codes).
+ * K: a multiple of 32 in [32, 2^24]; rows up to 2^24; codes and scales 16-byte
+ * aligned.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of the scale tiles of a [rows, K] operand. */
+m2_status mxfp4_scale_bytes(int rows, int K, size_t* bytes);
+
+/* Scale tiles from row-major e8m0 codes uint8 [rows, K / 32] (any alignment). */
+m2_status mxfp4_pack_scales(const uint8_t* scales, int rows, int K, uint8_t* tiles, void* stream);
+
+/*
+ * bf16 to MXFP4: per block with largest magnitude a,
+ *   e = max(floor(log2 a) - 2, -127), scale code e + 127,
+ *   code = e2m1(x / 2^e), round to nearest even, 6 past the end.
+ * A block of zeros has scale code 0; one with an infinity or a NaN has scale
+ * code 255 and zero codes (all of it reads as NaN).  Bit-exact.
+ * x bf16 device, rows row_stride elements apart (a multiple of 8, >= K),
+ * 16-byte aligned.  The outputs overlap neither x nor each other.
+ * Errors: M2_EINVAL, M2_ESHAPE, M2_EDEVICE, M2_ECUDA.
+ */
+m2_status mxfp4_quant(const uint16_t* x, size_t row_stride, int rows, int K, uint8_t* codes, uint8_t* scales,
+                      void* stream);
+
+/*
+ * The values: out[r, k] = bf16(e2m1(code) * 2^(s - 127)), exact but for scale
+ * codes whose values pass bf16's range (infinity).  out bf16 [rows, K],
+ * 16-byte aligned, overlaps neither input.
+ */
+m2_status mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int rows, int K, uint16_t* out, void* stream);
+
+/*
+ * Product of MXFP4 operands on the tensor cores:
+ *   y[m, n] = sum_k a[m, k] * w[n, k]
+ * a [M, K], w [N, K] ([out, in]); f32 accumulation; y [M, N] bf16 or f32
+ * (out_dtype), rounded once, aligned to its element; it overlaps no input.
+ * M in [0, 2^24], N in [1, 2^24], M * N <= 2^40.
+ * A bounded wait that runs out is reported by m2_check_standalone().
+ * Errors: M2_EINVAL, M2_ESHAPE, M2_EDEVICE, M2_ECUDA.
+ */
+m2_status mxfp4_linear(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales,
+                       void* y, int out_dtype, int M, int N, int K, void* stream);
+
+/*
+ * The quantise-inside form: x bf16 [M, K] (rows row_stride elements apart, as
+ * mxfp4_quant) is quantised into the workspace, then as mxfp4_linear: the same
+ * bits.  workspace: device, 256-byte aligned, >= the size call's bytes.
+ */
+m2_status mxfp4_linear_bf16_workspace_size(int M, int N, int K, size_t* bytes);
+m2_status mxfp4_linear_bf16(const uint16_t* x, size_t row_stride, const uint8_t* w_codes, const uint8_t* w_scales, void* y,
+                            int out_dtype, int M, int N, int K, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Log probabilities of given tokens, from logits, in one pass:
+ *   logprobs[r] = logits[r, t] - log sum_u exp(logits[r, u]),   t = tokens[r]
+ *   ranks[r]    = 1 + the number of tokens before t in the order (greater
+ *                 logit, then lower token)
+ *   entropy[r]  = -sum_u p_u log p_u,   p = softmax(logits[r])
+ *   top_tokens[r, i], top_logprobs[r, i]: the first `top` tokens in that order
+ *   logits      bf16 or f32 (dtype) device, rows row_stride elements apart
+ *               (>= vocab), any alignment of the element type
+ *   tokens      int32 [rows] device or NULL; -1: none (logprob 0, rank 0); a
+ *               token outside [-1, vocab) is treated as -1 and
+ *               m2_check_standalone() reports M2_EINVAL
+ *   logprobs    f32 [rows] device, ranks int32 [rows] device; both NULL
+ *               when tokens is NULL, and not otherwise
+ *   entropy     f32 [rows] device or NULL
+ *   top_tokens  int32 [rows, top], top_logprobs f32 [rows, top] device (NULL
+ *               when top is 0)
+ * A logit of -inf is masked, a NaN is treated as masked: its logprob is -inf and
+ * its rank 1 + the number of unmasked tokens.  A row of +inf logits shares the
+ * probability equally among them (the others' logprob is -inf).  Finite logits
+ * may be of any size: the logarithm is kept relative to the row's largest.
+ * Where a row has fewer than `top` tokens with a probability, the rest is token
+ * -1, logprob -inf; a row without any has entropy 0.
+ * rows in [0, 2^24], vocab in [1, 2^24], top in [0, 64].  No output overlaps
+ * an input or another output.
+ * Errors: M2_EINVAL, M2_ESHAPE, M2_EDEVICE, M2_ECUDA.
+ */
+m2_status m2_token_logprobs(const void* logits, int dtype, size_t row_stride, int rows, int vocab, const int32_t* tokens,
+                            int top, float* logprobs, int32_t* ranks, float* entropy, int32_t* top_tokens,
+                            float* top_logprobs, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

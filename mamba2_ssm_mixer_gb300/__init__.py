@@ -40,7 +40,9 @@ EXPORTED = ["m2_last_error", "m2_create", "m2_destroy", "m2_get_stats", "m2_set_
             "fp8_dequant", "bf16_linear_workspace_size", "bf16_linear", "m2_check_standalone",
             "m2_selftest_timeout", "m2_lora_add_workspace_size", "m2_lora_add", "m2_beam_select_workspace_size",
             "m2_beam_select", "m2_state_reorder", "m2_prefill_lora_workspace_size", "m2_prefill_lora",
-            "m2_decode_lora_workspace_size", "m2_decode_lora", "m2_mixed_lora_workspace_size", "m2_mixed_lora"]
+            "m2_decode_lora_workspace_size", "m2_decode_lora", "m2_mixed_lora_workspace_size", "m2_mixed_lora",
+            "mxfp4_scale_bytes", "mxfp4_pack_scales", "mxfp4_quant", "mxfp4_dequant", "mxfp4_linear",
+            "mxfp4_linear_bf16_workspace_size", "mxfp4_linear_bf16", "m2_token_logprobs"]
 
 STAGES = ["quant_in", "in_proj", "conv", "conv_state", "ssd_cumsum", "ssd_chunk_state", "ssd_state_pass",
           "ssd_chunk_scan", "norm_quant", "out_proj", "decode_fused", "dec_quant_in", "dec_in_proj",
@@ -127,6 +129,14 @@ _sigs = {
     "m2_mixed_lora": ([_vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, ctypes.POINTER(m2_lora), _vp, _vp,
                        _vp, _sz, _vp], _i),
     "m2_state_reorder": ([_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _vp], _i),
+    "mxfp4_scale_bytes": ([_i, _i, ctypes.POINTER(_sz)], _i),
+    "mxfp4_pack_scales": ([_vp, _i, _i, _vp, _vp], _i),
+    "mxfp4_quant": ([_vp, _sz, _i, _i, _vp, _vp, _vp], _i),
+    "mxfp4_dequant": ([_vp, _vp, _i, _i, _vp, _vp], _i),
+    "mxfp4_linear": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
+    "mxfp4_linear_bf16_workspace_size": ([_i, _i, _i, ctypes.POINTER(_sz)], _i),
+    "mxfp4_linear_bf16": ([_vp, _sz, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp], _i),
+    "m2_token_logprobs": ([_vp, _i, _sz, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp], _i),
 }
 for _name, (_args, _ret) in _sigs.items():
     _fn = getattr(_lib, _name)
@@ -827,6 +837,260 @@ def m2_state_reorder(conv_pools, ssm_pools, slot_idx: torch.Tensor, parents: tor
     return _on_device(slot_idx, stream, (parents, out, *conv_pools, *ssm_pools), call)
 
 
+class Mxfp4(typing.NamedTuple):
+    """A [rows, K] matrix in microscaled 4-bit floating point (MXFP4): codes
+    uint8 [rows, K / 2] (two e2m1 codes to a byte, the even k in the low half)
+    and scales uint8 [ceil(rows / 128), ceil(K / 128), 512], the e8m0 scale
+    codes of blocks of 32 in the tensor cores' order (include/m2.h)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], 2 * self.codes.shape[1]
+
+
+def _scales_shape(rows: int, K: int):
+    return (rows + 127) // 128, (K + 127) // 128, 512
+
+
+def _need_mx(q: Mxfp4, name: str, shape=None):
+    if not isinstance(q, Mxfp4):
+        raise ValueError(f"{name} must be an Mxfp4, got {type(q).__name__}")
+    if q.codes.dim() != 2:
+        raise ValueError(f"{name}.codes must be [rows, K / 2], got {tuple(q.codes.shape)}")
+    rows, K = q.shape if shape is None else shape
+    if K < 32 or K % 32:
+        raise ValueError(f"{name}: K must be a multiple of 32, got {K}")
+    _need(q.codes, f"{name}.codes", torch.uint8, (rows, K // 2))
+    _need(q.scales, f"{name}.scales", torch.uint8, _scales_shape(rows, K))
+
+
+def _need_rows(x: torch.Tensor, name: str, dtypes, multiple: int = 1) -> int:
+    """The row stride of a matrix whose rows are contiguous (a slice of wider
+    rows is taken in place)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {x.dtype}")
+    if x.dim() != 2 or not x.shape[1]:
+        raise ValueError(f"{name} must be a matrix with columns, got {tuple(x.shape)}")
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    if rows <= 1:
+        return -(-cols // multiple) * multiple   # (nothing is read past the row)
+    if x.stride(0) < cols or x.stride(0) % multiple:
+        raise ValueError(f"{name}: row stride {x.stride(0)} must be a multiple of {multiple} and at least {cols}")
+    return x.stride(0)
+
+
+def _mx_dtype(dtype) -> int:
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"y must be bfloat16 or float32, got {dtype}")
+    return M2_DTYPE_BF16 if dtype == torch.bfloat16 else M2_DTYPE_F32
+
+
+def mxfp4_pack(codes: torch.Tensor, scales: torch.Tensor, stream=None) -> Mxfp4:
+    """A checkpoint's MXFP4 matrix for mxfp4_linear: codes uint8 [rows, K / 2]
+    (taken as they are) and row-major scale codes uint8 [rows, K / 32], whose
+    tiles are made here."""
+    if codes.dim() != 2:
+        raise ValueError(f"codes must be [rows, K / 2], got {tuple(codes.shape)}")
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    _need(codes, "codes", torch.uint8)
+    if K < 32 or K % 32:
+        raise ValueError(f"K must be a multiple of 32, got {K}")
+    _need(scales, "scales", torch.uint8, (rows, K // 32))
+
+    def call(handle):
+        tiles = torch.empty(_scales_shape(rows, K), dtype=torch.uint8, device=codes.device)
+        _check(_lib.mxfp4_pack_scales(scales.data_ptr(), rows, K, tiles.data_ptr(), handle))
+        return Mxfp4(codes, tiles)
+
+    return _on_device(codes, stream, (scales,), call)
+
+
+def mxfp4_quant(x: torch.Tensor, out: Mxfp4 | None = None, stream=None) -> Mxfp4:
+    """bf16 [rows, K] to MXFP4 (K a multiple of 32): per block of 32 the scale
+    2^(floor(log2 max|x|) - 2), codes rounded to nearest even, 6 past the end; a
+    block with an infinity or a NaN becomes NaN.  x's rows may be a slice of
+    wider ones (16-byte aligned)."""
+    stride = _need_rows(x, "x", (torch.bfloat16,), 8)
+    rows, K = x.shape
+    if K % 32:
+        raise ValueError(f"K must be a multiple of 32, got {K}")
+    if out is not None:
+        _need_mx(out, "out", (rows, K))
+
+    def call(handle):
+        q = out if out is not None else Mxfp4(torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device),
+                                              torch.empty(_scales_shape(rows, K), dtype=torch.uint8, device=x.device))
+        _check(_lib.mxfp4_quant(x.data_ptr(), stride, rows, K, q.codes.data_ptr(), q.scales.data_ptr(), handle))
+        return q
+
+    return _on_device(x, stream, out or (), call)
+
+
+def mxfp4_dequant(q: Mxfp4, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of an MXFP4 matrix, bf16 [rows, K]."""
+    _need_mx(q, "q")
+    rows, K = q.shape
+    if out is not None:
+        _need(out, "out", torch.bfloat16, (rows, K))
+
+    def call(handle):
+        o = out if out is not None else torch.empty((rows, K), dtype=torch.bfloat16, device=q.codes.device)
+        _check(_lib.mxfp4_dequant(q.codes.data_ptr(), q.scales.data_ptr(), rows, K, o.data_ptr(), handle))
+        return o
+
+    return _on_device(q.codes, stream, (q.scales, out), call)
+
+
+def mxfp4_linear(a: Mxfp4, w: Mxfp4, y: torch.Tensor | None = None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """y = a @ w^T of 4-bit operands on the tensor cores, f32 accumulation; y in
+    `dtype` (bfloat16 or float32)."""
+    _need_mx(a, "a")
+    M, K = a.shape
+    _need_mx(w, "w", (w.codes.shape[0], K))
+    N = w.codes.shape[0]
+    out_dtype = _mx_dtype(dtype if y is None else y.dtype)
+    if y is not None:
+        _need(y, "y", y.dtype, (M, N))
+
+    def call(handle):
+        o = torch.empty((M, N), dtype=dtype, device=a.codes.device) if y is None else y
+        _check(_lib.mxfp4_linear(a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+                                 o.data_ptr(), out_dtype, M, N, K, handle))
+        return o
+
+    return _on_device(a.codes, stream, (a.scales, *w, y), call)
+
+
+@functools.lru_cache(maxsize=1024)
+def mxfp4_linear_bf16_workspace_size(M: int, N: int, K: int) -> int:
+    n = _sz()
+    _check(_lib.mxfp4_linear_bf16_workspace_size(M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def mxfp4_linear_bf16(x: torch.Tensor, w: Mxfp4, y: torch.Tensor | None = None, dtype=torch.bfloat16, workspace=None,
+                      stream=None) -> torch.Tensor:
+    """mxfp4_linear of x's 4-bit form (mxfp4_quant), quantised inside; x bf16
+    [M, K], whose rows may be a slice of wider ones."""
+    stride = _need_rows(x, "x", (torch.bfloat16,), 8)
+    M, K = x.shape
+    _need_mx(w, "w", (w.codes.shape[0], K))
+    N = w.codes.shape[0]
+    out_dtype = _mx_dtype(dtype if y is None else y.dtype)
+    if y is not None:
+        _need(y, "y", y.dtype, (M, N))
+
+    def call(handle):
+        o = torch.empty((M, N), dtype=dtype, device=x.device) if y is None else y
+        ws, nbytes = _scratch(workspace, mxfp4_linear_bf16_workspace_size(M, N, K), x.device)
+        _check(_lib.mxfp4_linear_bf16(x.data_ptr(), stride, w.codes.data_ptr(), w.scales.data_ptr(), o.data_ptr(), out_dtype,
+                                      M, N, K, _ptr(ws), nbytes, handle))
+        return o
+
+    return _on_device(x, stream, (*w, y, workspace), call)
+
+
+class TokenLogprobs(typing.NamedTuple):
+    """What m2_token_logprobs returns: [rows], and [rows, top]; None for what
+    was not asked for."""
+    logprobs: torch.Tensor | None       # f32; 0 where the token is -1, -inf where it is masked
+    ranks: torch.Tensor | None          # int32, 1 for the likeliest token; 0 where the token is -1
+    entropy: torch.Tensor               # f32, in nats
+    top_tokens: torch.Tensor | None     # int32, likeliest first; -1 where a row has no further token
+    top_logprobs: torch.Tensor | None   # f32; -inf there
+
+
+def m2_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0,
+                      out: TokenLogprobs | None = None, stream=None) -> TokenLogprobs:
+    """Log probabilities of given tokens with their ranks, the rows' entropy and
+    the `top` likeliest tokens, ties to the lower token.  logits bf16 or f32
+    [rows, vocab], rows contiguous and at a constant stride (a slice of a padded
+    vocabulary); tokens int32 [rows], -1 for none.  -inf and NaN logits are
+    masked.  out: a TokenLogprobs of tensors to write."""
+    stride = _need_rows(logits, "logits", (torch.bfloat16, torch.float32))
+    rows, vocab = logits.shape
+    if top < 0:
+        raise ValueError(f"top must not be negative, got {top}")
+    if tokens is not None:
+        _need(tokens, "tokens", torch.int32, (rows,))
+    if out is not None:
+        for t, name, dtype, shape, wanted in ((out.logprobs, "out.logprobs", torch.float32, (rows,), tokens is not None),
+                                              (out.ranks, "out.ranks", torch.int32, (rows,), tokens is not None),
+                                              (out.entropy, "out.entropy", torch.float32, (rows,), True),
+                                              (out.top_tokens, "out.top_tokens", torch.int32, (rows, top), top > 0),
+                                              (out.top_logprobs, "out.top_logprobs", torch.float32, (rows, top), top > 0)):
+            if wanted or (t is not None and t.numel()):
+                if not wanted:
+                    raise ValueError(f"{name} is not asked for")
+                _need(t, name, dtype, shape)
+
+    def call(handle):
+        dev, o = logits.device, out
+        if o is None:
+            def new(dtype, *shape):
+                return torch.empty(shape, dtype=dtype, device=dev)
+            o = TokenLogprobs(new(torch.float32, rows) if tokens is not None else None,
+                              new(torch.int32, rows) if tokens is not None else None, new(torch.float32, rows),
+                              new(torch.int32, rows, top) if top else None,
+                              new(torch.float32, rows, top) if top else None)
+        lp, rk = (o.logprobs.data_ptr(), o.ranks.data_ptr()) if tokens is not None else (None, None)
+        tt, tl = (o.top_tokens.data_ptr(), o.top_logprobs.data_ptr()) if top else (None, None)
+        _check(_lib.m2_token_logprobs(logits.data_ptr(), M2_DTYPE_BF16 if logits.dtype == torch.bfloat16 else M2_DTYPE_F32,
+                                      stride, rows, vocab, _ptr(tokens), top, lp, rk, o.entropy.data_ptr(), tt, tl,
+                                      handle))
+        return o
+
+    return _on_device(logits, stream, (tokens, *(out or ())), call)
+
+
+class Mxfp4Head:
+    """The head of a stack with its output matrix in 4 bits: final RMSNorm, then
+    logits = mxfp4(rmsnorm(h) * norm_w) @ weight^T.  norm_w bf16 [n], weight an
+    Mxfp4 [vocab, n]; dtype: of the logits (float32 or bfloat16)."""
+
+    def __init__(self, norm_w: torch.Tensor, weight: Mxfp4, eps: float = 1e-5, dtype=torch.float32):
+        _need_mx(weight, "weight")
+        _need(norm_w, "norm_w", torch.bfloat16, (weight.shape[1],))
+        _mx_dtype(dtype)
+        self.norm_w, self.weight, self.eps, self.dtype = norm_w, weight, eps, dtype
+        self.vocab = weight.shape[0]
+
+    def logits(self, h: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """[rows, vocab] of hidden rows h bf16 [rows, n] (left as they are)."""
+        def go(_):   # (the call's stream is current)
+            return mxfp4_linear_bf16(m2_rmsnorm_residual(h, None, self.norm_w, self.eps), self.weight, y=out,
+                                     dtype=self.dtype)
+
+        return _on_device(h, stream, (self.norm_w, *self.weight, out), go)
+
+    def logprobs(self, h: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0, max_rows: int = 4096,
+                 stream=None) -> TokenLogprobs:
+        """m2_token_logprobs of h's logits, of which at most max_rows rows exist
+        at a time."""
+        if max_rows < 1:
+            raise ValueError(f"max_rows must be positive, got {max_rows}")
+        rows = h.shape[0]
+        if tokens is not None:
+            _need(tokens, "tokens", torch.int32, (rows,))
+
+        def go(_):
+            if rows <= max_rows:
+                return m2_token_logprobs(self.logits(h), tokens, top)
+            buf = torch.empty((max_rows, self.vocab), dtype=self.dtype, device=h.device)
+            parts = [m2_token_logprobs(self.logits(h[i:i + max_rows], out=buf[:min(max_rows, rows - i)]),
+                                       None if tokens is None else tokens[i:i + max_rows], top)
+                     for i in range(0, rows, max_rows)]
+            return TokenLogprobs(*[None if p[0] is None else torch.cat(p) for p in zip(*parts)])
+
+        return _on_device(h, stream, (tokens, self.norm_w, *self.weight), go)
+
+
 class Mamba2Stack:
     """Pre-norm residual stack of mixer blocks: for each layer l,
     h <- h + block_l(rmsnorm(h) * norm_w[l]).  Host-side composition of the
@@ -904,6 +1168,17 @@ class Mamba2Stack:
         (BeamStep, the slots for the next decode)."""
         step = m2_beam_select(logits, scores, eos_token=eos_token, done=done, stream=stream)
         return step, m2_state_reorder(conv_pools, ssm_pools, slot_idx, step.parents, stream=stream)
+
+    def score(self, hidden, seqlens, conv_states, ssm_states, head: Mxfp4Head, tokens, top: int = 0, has_initial=None,
+              workspace=None, max_rows: int = 4096, stream=None):
+        """Log probabilities along prompts: prefill, then the head's
+        TokenLogprobs of every row.  tokens int32 [sum(T)]: the token that
+        follows each row, -1 for none (the last row of a sequence)."""
+        def go(_):
+            h = self.prefill(hidden, seqlens, conv_states, ssm_states, has_initial=has_initial, workspace=workspace)
+            return head.logprobs(h, tokens, top, max_rows=max_rows)
+
+        return _on_device(hidden, stream, (tokens,), go)
 
     def decode(self, hidden, conv_pools, ssm_pools, slot_idx, workspace=None, stream=None):
         ws = workspace if workspace is not None else torch.empty(

@@ -38,6 +38,16 @@ cudaError_t gemm_tc_big_bf16(const uint16_t* A, const uint16_t* B, uint16_t* y, 
                              bool w_static, int* err, cudaStream_t st);
 constexpr int kSkinnyMaxRows = 256;
 
+// Products of microscaled 4-bit operands (gemm_mx.cu): y[M,N] = a . w^T, bf16 or
+// f32.  w_early: the kernel before this one in the stream writes neither w's
+// codes nor its scales.  No workspace.
+struct MxOperand {
+  const uint8_t* codes;    // [rows, K / 2]
+  const uint8_t* scales;   // tiles (mxfp4.cu)
+};
+cudaError_t gemm_mx(const MxOperand& a, const MxOperand& w, void* y, bool f32, int M, int N, int K, bool w_early, int* err,
+                    cudaStream_t st);
+
 // Failure-detection self-test: one CTA allocates TMEM, waits with the GEMMs'
 // bounded mbarrier wait (limit_ns) on a barrier nothing arrives at, takes
 // their abort path (error word, drain, TMEM freed) and returns.

@@ -1,0 +1,703 @@
+// Tensor-core GEMMs on microscaled 4-bit operands: y = A . B^T with A [M, K]
+// and B [N, K] in MXFP4 (e2m1 codes K-major, two to a byte; scale tiles as
+// mxfp4.cu lays them out), f32 accumulation in TMEM, y bf16 or f32.
+// tcgen05.mma kind::mxf4 takes 64 values (32 bytes) of K per instruction and
+// the blocks' scales from TMEM, where tcgen05.cp puts them from shared memory:
+// a stage of 256 values (128 swizzled bytes a row) is 4 MMAs and one 512-byte
+// copy per 128 rows of each operand and 128 values.  Copies and MMAs of one
+// thread run in the order issued, so one set of scale columns serves every
+// stage.
+//
+// k_mx_pair (more than 128 rows): persistent two-CTA clusters on 256 x BN
+//   output tiles, as the e4m3 kernel of gemm_tc.cu; each CTA keeps the scales
+//   of its own 128 rows of A and of all BN columns.
+// k_mx_fewrow (up to 128 rows): the weights are the MMA's 128-row operand, K
+//   is split over the CTAs of a cluster and the partial sums meet in
+//   distributed shared memory.
+// Waits are bounded as in gemm_tc.cu.
+#include <cudaTypedefs.h>
+
+#include <map>
+#include <mutex>
+
+#include "gemm.h"
+#include "launch_util.h"
+#include "m2_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace m2 {
+
+using namespace tc;
+
+namespace {
+
+constexpr int kBM = 128;         // MMA rows per CTA
+constexpr int kRowBytes = 128;   // bytes of K per stage and row
+constexpr int kBK = 256;         // values of K per stage
+constexpr int kThreads = 192;    // 6 warps: producer, MMA, 4 x epilogue
+constexpr uint32_t kSfTile = 512;
+
+struct __align__(8) Ctl {
+  uint64_t full[8];
+  uint64_t empty[8];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ void raise_abort(Ctl* ctl, int* err) {
+  *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+  if (err) atomicOr(err, kErrTimeout);
+}
+
+// Output staging: two buffers per epilogue warp, 32 rows of 128 bytes each in
+// the 128-byte swizzle of the output tensor map.
+constexpr uint32_t kEpiBuf = 32 * 128;
+constexpr uint32_t kEpiBytes = 4 * 2 * kEpiBuf;
+
+template <bool kF32>
+struct Out;
+template <>
+struct Out<false> {
+  using T = uint16_t;
+  static constexpr int kCols = 64;   // columns of a 128-byte slice
+  __device__ static T one(uint32_t v) { return f2bfbits(__uint_as_float(v)); }
+};
+template <>
+struct Out<true> {
+  using T = float;
+  static constexpr int kCols = 32;
+  __device__ static T one(uint32_t v) { return __uint_as_float(v); }
+};
+
+// One epilogue warp: 32 accumulator lanes (output rows row0 ..) over the
+// tile's BN columns from TMEM column `tcol`, output column n0.  With a store
+// map, 128-byte slices go through shared memory and TMA stores; else every
+// thread writes its own row.
+template <int BN, bool kF32>
+__device__ __forceinline__ void epilogue_rows(uint32_t tcol, uint8_t* bufs, int& buf, const CUtensorMap* tmC,
+                                              bool tma_store, typename Out<kF32>::T* __restrict__ C, int M, int N,
+                                              int row0, int n0, int lane) {
+  using O = Out<kF32>;
+  if (tma_store) {
+#pragma unroll 1
+    for (int c = 0; c < BN; c += O::kCols) {
+      // slices outside the output are neither staged nor stored (warp-uniform)
+      if (row0 >= M || n0 + c >= N) break;
+      uint32_t r[O::kCols];
+#pragma unroll
+      for (int h = 0; h < O::kCols; h += 32)
+        tmem_ld_32x32b_x32(tcol + (uint32_t)(c + h), *reinterpret_cast<uint32_t(*)[32]>(&r[h]));
+      tmem_ld_wait();
+      uint8_t* b = bufs + buf * kEpiBuf;
+      if (lane == 0) bulk_wait_read<1>();
+      __syncwarp();
+      const uint32_t row_addr = smem_u32(b) + (uint32_t)lane * 128u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t at = row_addr + (uint32_t)((j ^ (lane & 7)) << 4);
+        if constexpr (kF32) {
+          st_shared_v4(at, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        } else {
+          const uint32_t* v = &r[8 * j];
+          st_shared_v4(at, pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                       pack_bf16x2(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                       pack_bf16x2(__uint_as_float(v[4]), __uint_as_float(v[5])),
+                       pack_bf16x2(__uint_as_float(v[6]), __uint_as_float(v[7])));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(tmC, b, n0 + c, row0);
+        bulk_commit();
+      }
+      buf ^= 1;
+    }
+    return;
+  }
+  const int row = row0 + lane;
+  typename O::T* crow = C + (size_t)row * N;
+#pragma unroll 1
+  for (int c = 0; c < BN; c += 32) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(tcol + (uint32_t)c, r);
+    tmem_ld_wait();
+    const int n = n0 + c;
+    if (row < M) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (n + j < N) crow[n + j] = O::one(r[j]);
+    }
+  }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// 256 x BN tiles on CTA pairs.  CTA r of a pair stages rows [128 r, ..) of A
+// with their scales, columns [r BN / 2, ..) of B and the scales of all of the
+// tile's columns (two 128-row tiles of them: a tile of B starts on a multiple
+// of 64 rows, in the middle of a scale tile for odd ones, and the MMA then
+// reads from the third of the tile's columns on).  The rest as k_gemm_pair.
+// ---------------------------------------------------------------------------
+template <int BN, int STAGES, bool kF32>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_mx_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+              const __grid_constant__ CUtensorMap tmC, int tma_store, typename Out<kF32>::T* __restrict__ C, int M, int N,
+              int K, int* err) {
+  static_assert(BN % 64 == 0 && BN >= 64 && BN <= 192, "BN");
+  static_assert(STAGES <= 8, "STAGES");
+  constexpr int kPM = 2 * kBM;
+  constexpr uint32_t A_BYTES = kBM * kRowBytes;
+  constexpr uint32_t B_BYTES = (BN / 2) * kRowBytes;
+  constexpr uint32_t SA_BYTES = 2 * kSfTile;          // 128 rows x 256 values
+  constexpr uint32_t SB_BYTES = 4 * kSfTile;          // 256 rows x 256 values
+  constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+  static_assert(STAGE_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
+  constexpr uint32_t TMEM_COLS = 512;
+  constexpr uint32_t SFA_COL = 2 * BN, SFB_COL = SFA_COL + 8;   // 2 x 4 and 2 x 8 columns
+  static_assert(SFB_COL + 16 <= TMEM_COLS, "scale columns");
+  constexpr uint16_t kPair = 0x3;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_align<1024>(smem_raw);
+  uint8_t* epi = smem + STAGES * STAGE_BYTES;
+  Ctl* ctl = reinterpret_cast<Ctl*>(epi + kEpiBytes);
+  volatile int* abort = &ctl->abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int tiles_m = (M + kPM - 1) / kPM, tiles_n = (N + BN - 1) / BN;
+  const int num_tiles = tiles_m * tiles_n;
+  const int kblocks = (K + kBK - 1) / kBK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->tfull[i], 1);
+      mbar_init(&ctl->tempty[i], 2 * 4);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+    tma_prefetch(&tmA);
+    tma_prefetch(&tmB);
+    tma_prefetch(&tmSA);
+    tma_prefetch(&tmSB);
+    if (tma_store) tma_prefetch(&tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&ctl->tmem_base, TMEM_COLS);
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued_phase[STAGES];
+      bool issued[STAGES];
+      for (int s = 0; s < STAGES; ++s) issued[s] = false, issued_phase[s] = 0;
+      bool ok = true;
+      for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+        const int m0 = (tile % tiles_m) * kPM + (int)rank * kBM;
+        const int nt = (tile / tiles_m) * BN, n0 = nt + (int)rank * (BN / 2);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort)) {
+            raise_abort(ctl, err);
+            ok = false;
+            break;
+          }
+          uint8_t* sA = smem + stage * STAGE_BYTES;
+          const uint32_t full0 = cluster_map(smem_u32(&ctl->full[stage]), 0);
+          if (rank == 0) mbar_expect_tx(&ctl->full[stage], 2 * STAGE_BYTES);
+          tma_load_2d_pair(sA, &tmA, full0, kb * kRowBytes, m0);
+          tma_load_2d_pair(sA + A_BYTES, &tmB, full0, kb * kRowBytes, n0);
+          // (the maps of the scales are in 4-byte words: 256 words = two tiles)
+          tma_load_2d_pair(sA + A_BYTES + B_BYTES, &tmSA, full0, kb * 256, m0 / 128);
+          tma_load_2d_pair(sA + A_BYTES + B_BYTES + SA_BYTES, &tmSB, full0, kb * 256, nt / 128);
+          issued[stage] = true;
+          issued_phase[stage] = phase;
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
+      }
+      if (*abort) {
+        // the even CTA's full barriers count both CTAs' copies: let those in
+        // flight land before the pair exits
+        if (rank == 0)
+          for (int s = 0; s < STAGES; ++s)
+            if (issued[s]) mbar_wait(&ctl->full[s], issued_phase[s], nullptr, 100000000ull);
+      } else {
+        for (int s = 0; s < STAGES; ++s)
+          if (issued[s] && !mbar_wait(&ctl->empty[s], issued_phase[s], abort)) {
+            raise_abort(ctl, err);
+            break;
+          }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---------------- MMA issuer (even CTA only)
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+        if (!mbar_wait_cluster(&ctl->tempty[acc], acc_phase ^ 1u, abort)) {
+          raise_abort(ctl, err);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+        const uint32_t sfb0 = tmem_base + SFB_COL + (((tile / tiles_m) * BN) % 128) / 32;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(&ctl->full[stage], phase, abort)) {
+            raise_abort(ctl, err);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + stage * STAGE_BYTES);
+          const uint32_t sf_addr = a_addr + A_BYTES + B_BYTES;
+          const uint64_t adesc = desc_kmajor_sw128(a_addr);
+          const uint64_t bdesc = desc_kmajor_sw128(a_addr + A_BYTES);
+          const int left = K - kb * kBK;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {   // 128 values: their scales, then two MMAs
+            if (t * 128 < left) {
+              tmem_cp_32x128b_pair(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
+              tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t, desc_scale_tile(sf_addr + SA_BYTES + t * kSfTile));
+              tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t + 4,
+                                   desc_scale_tile(sf_addr + SA_BYTES + (2 + t) * kSfTile));
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (t * 128 + h * 64 < left)
+                  mma_mxf4_pair(d_tmem, adesc + 2 * (2 * t + h), bdesc + 2 * (2 * t + h), idesc_mxf4(kPM, BN, 2 * h),
+                                tmem_base + SFA_COL + 4 * t, sfb0 + 8 * t, (kb | t | h) != 0);
+            }
+          }
+          mma_commit_pair(&ctl->empty[stage], kPair);
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
+        if (!ok) break;
+        mma_commit_pair(&ctl->tfull[acc], kPair);
+        if (++acc == 2) acc = 0, acc_phase ^= 1u;
+      }
+      if (*abort) {
+        mma_commit_pair(&ctl->drain, kPair);
+        mbar_wait(&ctl->drain, 0, nullptr, 100000000ull);
+      }
+    }
+  } else {
+    // ---------------- epilogue (both CTAs): warps 2..5 own TMEM lane quarters (warp % 4)
+    const int quarter = warp & 3;
+    const uint32_t tempty0[2] = {cluster_map(smem_u32(&ctl->tempty[0]), 0),
+                                 cluster_map(smem_u32(&ctl->tempty[1]), 0)};
+    uint8_t* bufs = epi + quarter * 2 * kEpiBuf;
+    int buf = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int tile = pair; tile < num_tiles; tile += npairs) {
+      const int m0 = (tile % tiles_m) * kPM + (int)rank * kBM, n0 = (tile / tiles_m) * BN;
+      if (!__all_sync(0xffffffffu, mbar_wait(&ctl->tfull[acc], acc_phase, abort))) {
+        raise_abort(ctl, err);
+        break;
+      }
+      tc_fence_after();
+      epilogue_rows<BN, kF32>(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN), bufs, buf, &tmC,
+                              tma_store != 0, C, M, N, m0 + quarter * 32, n0, lane);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(tempty0[acc]);
+      if (++acc == 2) acc = 0, acc_phase ^= 1u;
+    }
+    if (lane == 0) bulk_wait<0>();
+  }
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: D^T[n, m] = W X^T for one 128-row block of W per cluster, K split
+// over its CTAs, as k_gemm_fewrow.  w_early: W and its scales are not written
+// by the kernel before this one in the stream, so the first stages of them are
+// requested before waiting for it.
+// ---------------------------------------------------------------------------
+template <int BNT, int STAGES, bool kF32>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_mx_fewrow(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
+                typename Out<kF32>::T* __restrict__ y, int Mtok, int N, int K, int S, int w_early, int* err) {
+  static_assert(BNT % 16 == 0 && BNT >= 16 && BNT <= 128, "BNT");
+  using O = Out<kF32>;
+  constexpr uint32_t A_BYTES = kBM * kRowBytes;
+  constexpr uint32_t B_BYTES = BNT * kRowBytes;
+  constexpr uint32_t SF_BYTES = 2 * kSfTile;
+  constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
+  static_assert(STAGE_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
+  constexpr uint32_t ACC_COLS = BNT < 32 ? 32 : BNT;
+  constexpr uint32_t SFA_COL = ACC_COLS, SFB_COL = ACC_COLS + 8;
+  constexpr uint32_t TMEM_COLS = BNT <= 32 ? 64 : (BNT <= 64 ? 128 : 256);
+  static_assert(SFB_COL + 8 <= TMEM_COLS, "scale columns");
+  constexpr int RED_LD = BNT + 4;
+  static_assert(kBM * RED_LD * 4 <= (int)(STAGES * STAGE_BYTES), "the exchange buffer fits in the ring");
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_align<1024>(smem_raw);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * STAGE_BYTES);
+  float* red = reinterpret_cast<float*>(smem);
+  volatile int* abort = &ctl->abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();            // of the S CTAs of a weight block
+  const int n0 = (int)(blockIdx.x / (unsigned)S) * kBM;
+  const int kblocks = (K + kBK - 1) / kBK;
+  const int kb0 = rank * kblocks / S;
+  const int nk = (rank + 1) * kblocks / S - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    mbar_init(&ctl->tfull[0], 1);
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+    tma_prefetch(&tmW);
+    tma_prefetch(&tmX);
+    tma_prefetch(&tmSW);
+    tma_prefetch(&tmSX);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, TMEM_COLS);
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer: ring slot i holds k-block kb0 + i
+      const int npre = nk < STAGES ? nk : STAGES;
+      auto load_w = [&](int i) {
+        uint8_t* s = smem + (i % STAGES) * STAGE_BYTES;
+        uint64_t* bar = &ctl->full[i % STAGES];
+        mbar_expect_tx(bar, STAGE_BYTES);
+        tma_load_2d(s, &tmW, bar, (kb0 + i) * kRowBytes, n0);
+        tma_load_2d(s + A_BYTES + B_BYTES, &tmSW, bar, (kb0 + i) * 256, n0 / 128);
+      };
+      auto load_x = [&](int i) {
+        uint8_t* s = smem + (i % STAGES) * STAGE_BYTES;
+        uint64_t* bar = &ctl->full[i % STAGES];
+        tma_load_2d(s + A_BYTES, &tmX, bar, (kb0 + i) * kRowBytes, 0);
+        tma_load_2d(s + A_BYTES + B_BYTES + SF_BYTES, &tmSX, bar, (kb0 + i) * 256, 0);
+      };
+      if (w_early)
+        for (int i = 0; i < npre; ++i) load_w(i);
+      pdl_wait();
+      pdl_trigger();
+      for (int i = 0; i < npre; ++i) {
+        if (!w_early) load_w(i);
+        load_x(i);
+      }
+      int issued = npre;
+      for (int i = npre; i < nk; ++i) {
+        if (!mbar_wait(&ctl->empty[i % STAGES], ((uint32_t)(i / STAGES) & 1u) ^ 1u, abort)) {
+          raise_abort(ctl, err);
+          break;
+        }
+        load_w(i);
+        load_x(i);
+        issued = i + 1;
+      }
+      if (*abort)   // let the copies in flight land before the CTA can exit
+        for (int j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
+          mbar_wait(&ctl->full[j % STAGES], (uint32_t)(j / STAGES) & 1u, nullptr, 100000000ull);
+    }
+  } else {
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 1) {
+      if (lane == 0) {
+        // ---------------- MMA issuer
+        bool ok = true;
+        for (int i = 0; i < nk; ++i) {
+          const int stg = i % STAGES;
+          if (!mbar_wait(&ctl->full[stg], (uint32_t)(i / STAGES) & 1u, abort)) {
+            raise_abort(ctl, err);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + stg * STAGE_BYTES);
+          const uint32_t sf_addr = a_addr + A_BYTES + B_BYTES;
+          const uint64_t adesc = desc_kmajor_sw128(a_addr);
+          const uint64_t bdesc = desc_kmajor_sw128(a_addr + A_BYTES);
+          const int left = K - (kb0 + i) * kBK;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t * 128 < left) {
+              tmem_cp_32x128b(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
+              tmem_cp_32x128b(tmem_base + SFB_COL + 4 * t, desc_scale_tile(sf_addr + SF_BYTES + t * kSfTile));
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (t * 128 + h * 64 < left)
+                  mma_mxf4(tmem_base, adesc + 2 * (2 * t + h), bdesc + 2 * (2 * t + h), idesc_mxf4(kBM, BNT, 2 * h),
+                           tmem_base + SFA_COL + 4 * t, tmem_base + SFB_COL + 4 * t, (i | t | h) != 0);
+            }
+          }
+          mma_commit(&ctl->empty[stg]);
+        }
+        if (ok && nk > 0) {
+          mma_commit(&ctl->tfull[0]);
+        } else {
+          mma_commit(&ctl->drain);
+          mbar_wait(&ctl->drain, 0, nullptr, 100000000ull);
+        }
+      }
+    } else {
+      // ---------------- epilogue warps 2..5: accumulator rows -> own exchange buffer
+      const int quarter = warp & 3;
+      float* dst = red + (quarter * 32 + lane) * RED_LD;
+      if (__all_sync(0xffffffffu, nk > 0 && mbar_wait(&ctl->tfull[0], 0, abort))) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < BNT; c += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(dst + c + 4 * q) =
+                make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
+                            __uint_as_float(r[4 * q + 3]));
+        }
+        tc_fence_before();
+      } else {
+        if (nk > 0) raise_abort(ctl, err);
+        for (int c = 0; c < BNT; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();   // every CTA's partial sits in its exchange buffer
+  {
+    const int r0 = rank * kBM / S, rows = (rank + 1) * kBM / S - r0;
+    const int quads = (Mtok + 3) >> 2;
+    const uint32_t red_s = smem_u32(red);
+    for (int idx = threadIdx.x; idx < rows * quads; idx += kThreads) {
+      const int nl = r0 + idx % rows, m = 4 * (idx / rows);
+      const uint32_t off = red_s + (uint32_t)((nl * RED_LD + m) * 4);
+      float4 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < S) v[r] = ld_dsmem_f32x4(cluster_map(off, (uint32_t)r));
+      float4 acc = v[0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r)
+        if (r < S) acc.x += v[r].x, acc.y += v[r].y, acc.z += v[r].z, acc.w += v[r].w;
+      const int n = n0 + nl;
+      if (n < N) {
+        typename O::T* yc = y + (size_t)m * N + n;
+        yc[0] = O::one(__float_as_uint(acc.x));
+        if (m + 1 < Mtok) yc[N] = O::one(__float_as_uint(acc.y));
+        if (m + 2 < Mtok) yc[2 * (size_t)N] = O::one(__float_as_uint(acc.z));
+        if (m + 3 < Mtok) yc[3 * (size_t)N] = O::one(__float_as_uint(acc.w));
+      }
+    }
+  }
+  cluster_sync();   // no CTA leaves while another still reads its buffer
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+cudaError_t encode(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
+                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle,
+                   CUtensorMapL2promotion promo) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {box_inner, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promo,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+// Codes [rows, K / 2] bytes: boxes of box_rows x 128 bytes, 128-byte swizzle.
+cudaError_t map_codes(CUtensorMap* map, const uint8_t* p, int rows, int K, int box_rows) {
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, (uint64_t)K / 2, rows, (uint64_t)K / 2, kRowBytes, box_rows,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+// Scale tiles as words [ceil(rows / 128), ceil(K / 128) x 128]: boxes of two
+// tiles (256 values of K) by box_rows rows of tiles.
+cudaError_t map_scales(CUtensorMap* map, const uint8_t* p, int rows, int K, int box_rows) {
+  const uint64_t words = (uint64_t)((K + 127) / 128) * 128;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, p, words, (rows + 127) / 128, words * 4, 256, box_rows,
+                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+// Output map: boxes of 128 bytes x 32 rows.  False when rows are not 16-byte
+// aligned; the kernels then store per thread.
+template <bool kF32>
+bool map_out(CUtensorMap* map, void* y, int M, int N) {
+  constexpr int es = kF32 ? 4 : 2;
+  if (((size_t)N * es) % 16 != 0 || (reinterpret_cast<uintptr_t>(y) & 15) != 0) return false;
+  return encode(map, kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, N, M, (uint64_t)N * es,
+                128 / es, 32, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE) == cudaSuccess;
+}
+
+template <int BN, int STAGES, bool kF32>
+cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, int N, int K, int* err,
+                        cudaStream_t st) {
+  CUtensorMap ta, tb, tsa, tsb, tc = {};
+  cudaError_t e;
+  if ((e = map_codes(&ta, a.codes, M, K, kBM)) != cudaSuccess) return e;
+  if ((e = map_codes(&tb, b.codes, N, K, BN / 2)) != cudaSuccess) return e;
+  if ((e = map_scales(&tsa, a.scales, M, K, 1)) != cudaSuccess) return e;
+  if ((e = map_scales(&tsb, b.scales, N, K, 2)) != cudaSuccess) return e;
+  const int tma_store = map_out<kF32>(&tc, y, M, N) ? 1 : 0;
+  const size_t smem = 1024 + (size_t)STAGES * ((kBM + BN / 2) * kRowBytes + 6 * kSfTile) + kEpiBytes + sizeof(Ctl);
+  auto k = k_mx_pair<BN, STAGES, kF32>;
+  if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  // clusters that fit on the device at once, found once per device
+  static std::mutex mu;
+  static std::map<int, int> by_device;
+  int dev = 0, cap = 0;
+  cudaGetDevice(&dev);
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = by_device.find(dev);
+    if (it == by_device.end()) {
+      cfg.gridDim = dim3(2 * device_sm_count());
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&cap, k, &cfg) != cudaSuccess || cap < 1) cap = device_sm_count() / 2;
+      by_device[dev] = cap;
+    } else {
+      cap = it->second;
+    }
+  }
+  const long long tiles = (long long)((M + 2 * kBM - 1) / (2 * kBM)) * ((N + BN - 1) / BN);
+  cfg.gridDim = dim3(2 * (unsigned)(tiles < cap ? tiles : cap));
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, ta, tb, tsa, tsb, tc, tma_store, static_cast<typename Out<kF32>::T*>(y), M, N, K,
+                            err);
+}
+
+// Cluster size of the few-row kernel: as many K splits as keep every CTA
+// resident in one wave, at most 8, at least two stages of K per CTA.
+int fewrow_splits(int N, int kblocks, size_t smem) {
+  const int nb = (N + kBM - 1) / kBM;
+  int per_sm = (int)((228 * 1024) / (smem + 1024));
+  if (per_sm < 1) per_sm = 1;
+  int s = (int)(0.9 * per_sm * device_sm_count() / nb);
+  if (s > 8) s = 8;
+  if (s > kblocks / 2) s = kblocks / 2;
+  return s < 1 ? 1 : s;
+}
+
+template <int BNT, int STAGES, bool kF32>
+cudaError_t launch_fewrow(const MxOperand& x, const MxOperand& w, void* y, int Mtok, int N, int K, bool w_early, int* err,
+                          cudaStream_t st) {
+  CUtensorMap tw, tx, tsw, tsx;
+  cudaError_t e;
+  if ((e = map_codes(&tw, w.codes, N, K, kBM)) != cudaSuccess) return e;
+  if ((e = map_codes(&tx, x.codes, Mtok, K, BNT)) != cudaSuccess) return e;
+  if ((e = map_scales(&tsw, w.scales, N, K, 1)) != cudaSuccess) return e;
+  if ((e = map_scales(&tsx, x.scales, Mtok, K, 1)) != cudaSuccess) return e;
+  const size_t smem = 1024 + (size_t)STAGES * ((kBM + BNT) * kRowBytes + 4 * kSfTile) + sizeof(Ctl);
+  auto k = k_mx_fewrow<BNT, STAGES, kF32>;
+  if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
+  const int S = fewrow_splits(N, (K + kBK - 1) / kBK, smem);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)S * (unsigned)((N + kBM - 1) / kBM));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, tw, tx, tsw, tsx, static_cast<typename Out<kF32>::T*>(y), Mtok, N, K, S,
+                            (int)w_early, err);
+}
+
+template <bool kF32>
+cudaError_t gemm_t(const MxOperand& a, const MxOperand& w, void* y, int M, int N, int K, bool w_early, int* err,
+                   cudaStream_t st) {
+  if (M <= 16) return launch_fewrow<16, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
+  if (M <= 32) return launch_fewrow<32, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
+  if (M <= 64) return launch_fewrow<64, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
+  if (M <= 128) return launch_fewrow<128, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
+  return launch_pair<192, 6, kF32>(a, w, y, M, N, K, err, st);
+}
+
+}  // namespace
+
+cudaError_t gemm_mx(const MxOperand& a, const MxOperand& w, void* y, bool f32, int M, int N, int K, bool w_early, int* err,
+                    cudaStream_t st) {
+  if (M <= 0) return cudaSuccess;
+  return f32 ? gemm_t<true>(a, w, y, M, N, K, w_early, err, st) : gemm_t<false>(a, w, y, M, N, K, w_early, err, st);
+}
+
+}  // namespace m2

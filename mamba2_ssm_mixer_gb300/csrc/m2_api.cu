@@ -310,6 +310,7 @@ static m2_status error_word_status(int v, const char* who) {
   if (v & kErrDupSlot)
     return fail(M2_EINVAL, "%s: two decode rows named the same slot (the later rows were skipped)", who);
   if (v & kErrAdapter) return fail(M2_EINVAL, "%s: a row named an adapter outside [-1, n_adapters)", who);
+  if (v & kErrToken) return fail(M2_EINVAL, "%s: a row named a token outside [-1, vocab)", who);
   if (v & kErrBeam)
     return fail(M2_EINVAL, "%s: a row's parent names no beam with a slot, or a request has more rows than slots", who);
   return M2_OK;
@@ -1421,5 +1422,191 @@ extern "C" m2_status m2_state_reorder(uint16_t* const* conv_pools, void* const* 
   if ((s = standalone_error_word(&err))) return s;
   M2_CUDA(launch_state_reorder(conv_pools, ssm_pools, layers, ssm_dtype == M2_DTYPE_BF16, n_slots, slot_idx, parents,
                                new_slot_idx, batch, beams, err, static_cast<cudaStream_t>(stream)));
+  return M2_OK;
+}
+
+// ---------------------------------------------------------------- the head: 4-bit operands, log probabilities
+
+static m2_status check_mx_shape(int rows, int K, const char* who) {
+  if (rows < 0 || rows > (1 << 24) || K < 32 || K > (1 << 24) || K % 32)
+    return fail(M2_ESHAPE, "%s: %d rows, K %d (rows up to 2^24, K a multiple of 32 in [32, 2^24])", who, rows, K);
+  return M2_OK;
+}
+
+// Bytes from a matrix's first to its last element.
+static size_t extent(int rows, size_t stride, int cols, size_t es) {
+  return rows > 0 ? ((size_t)(rows - 1) * stride + (size_t)cols) * es : 0;
+}
+
+static size_t code_bytes(int rows, int K) { return (size_t)rows * (size_t)K / 2; }
+
+static m2_status check_mx_rows(const uint16_t* x, size_t row_stride, int K, const char* who) {
+  if (row_stride < (size_t)K || row_stride % 8 || row_stride > ((size_t)1 << 40))
+    return fail(M2_ESHAPE, "%s: row_stride %zu must be a multiple of 8 in [K = %d, 2^40]", who, row_stride, K);
+  if ((uintptr_t)x % 16) return fail(M2_EINVAL, "%s: x must be 16-byte aligned", who);
+  return M2_OK;
+}
+
+extern "C" m2_status mxfp4_scale_bytes(int rows, int K, size_t* bytes) {
+  if (!bytes) return fail(M2_EINVAL, "mxfp4_scale_bytes: null argument");
+  m2_status s = check_mx_shape(rows, K, "mxfp4_scale_bytes");
+  if (s) return s;
+  *bytes = mx_scale_bytes(rows, K);
+  return M2_OK;
+}
+
+extern "C" m2_status mxfp4_pack_scales(const uint8_t* scales, int rows, int K, uint8_t* tiles, void* stream) {
+  g_err.clear();
+  m2_status s = check_mx_shape(rows, K, "mxfp4_pack_scales");
+  if (s) return s;
+  if (rows && (!scales || !tiles)) return fail(M2_EINVAL, "mxfp4_pack_scales: null pointer");
+  if ((uintptr_t)tiles % 16) return fail(M2_EINVAL, "mxfp4_pack_scales: tiles must be 16-byte aligned");
+  if (overlap(scales, (size_t)rows * (K / 32), tiles, mx_scale_bytes(rows, K)))
+    return fail(M2_EINVAL, "mxfp4_pack_scales: tiles overlap the scales");
+  if ((s = check_device())) return s;
+  M2_CUDA(launch_mx_pack(scales, rows, K, tiles, static_cast<cudaStream_t>(stream)));
+  return M2_OK;
+}
+
+extern "C" m2_status mxfp4_quant(const uint16_t* x, size_t row_stride, int rows, int K, uint8_t* codes, uint8_t* scales,
+                                 void* stream) {
+  g_err.clear();
+  m2_status s = check_mx_shape(rows, K, "mxfp4_quant");
+  if (s || (s = check_mx_rows(x, row_stride, K, "mxfp4_quant"))) return s;
+  if (rows && (!x || !codes || !scales)) return fail(M2_EINVAL, "mxfp4_quant: null pointer");
+  if ((uintptr_t)codes % 16 || (uintptr_t)scales % 16)
+    return fail(M2_EINVAL, "mxfp4_quant: codes and scales must be 16-byte aligned");
+  const size_t xb = extent(rows, row_stride, K, 2), cb = code_bytes(rows, K), sb = mx_scale_bytes(rows, K);
+  if (overlap(codes, cb, x, xb) || overlap(scales, sb, x, xb) || overlap(codes, cb, scales, sb))
+    return fail(M2_EINVAL, "mxfp4_quant: x, codes and scales overlap");
+  if ((s = check_device())) return s;
+  M2_CUDA(launch_mx_quant(x, row_stride, rows, K, codes, scales, static_cast<cudaStream_t>(stream)));
+  return M2_OK;
+}
+
+extern "C" m2_status mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int rows, int K, uint16_t* out,
+                                   void* stream) {
+  g_err.clear();
+  m2_status s = check_mx_shape(rows, K, "mxfp4_dequant");
+  if (s) return s;
+  if (rows && (!codes || !scales || !out)) return fail(M2_EINVAL, "mxfp4_dequant: null pointer");
+  if ((uintptr_t)codes % 16 || (uintptr_t)scales % 16 || (uintptr_t)out % 16)
+    return fail(M2_EINVAL, "mxfp4_dequant: pointers must be 16-byte aligned");
+  const size_t ob = (size_t)rows * K * 2;
+  if (overlap(out, ob, codes, code_bytes(rows, K)) || overlap(out, ob, scales, mx_scale_bytes(rows, K)))
+    return fail(M2_EINVAL, "mxfp4_dequant: out overlaps an input");
+  if ((s = check_device())) return s;
+  M2_CUDA(launch_mx_dequant(codes, scales, rows, K, out, static_cast<cudaStream_t>(stream)));
+  return M2_OK;
+}
+
+static m2_status check_mx_linear(const uint8_t* w_codes, const uint8_t* w_scales, const void* y, int out_dtype, int M,
+                                 int N, int K, const char* who) {
+  m2_status s = check_mx_shape(M, K, who);
+  if (s) return s;
+  if (N < 1 || N > (1 << 24) || (long long)M * N > (1ll << 40))
+    return fail(M2_ESHAPE, "%s: M %d, N %d (N in [1, 2^24], M * N up to 2^40)", who, M, N);
+  if (out_dtype != M2_DTYPE_F32 && out_dtype != M2_DTYPE_BF16)
+    return fail(M2_EINVAL, "%s: out_dtype must be M2_DTYPE_F32 or M2_DTYPE_BF16", who);
+  if (M && (!w_codes || !w_scales || !y)) return fail(M2_EINVAL, "%s: null pointer", who);
+  if ((uintptr_t)w_codes % 16 || (uintptr_t)w_scales % 16)
+    return fail(M2_EINVAL, "%s: codes and scales must be 16-byte aligned", who);
+  const size_t es = out_dtype == M2_DTYPE_F32 ? 4 : 2, yb = (size_t)M * N * es;
+  if ((uintptr_t)y % es) return fail(M2_EINVAL, "%s: y is not aligned to its element", who);
+  if (overlap(y, yb, w_codes, code_bytes(N, K)) || overlap(y, yb, w_scales, mx_scale_bytes(N, K)))
+    return fail(M2_EINVAL, "%s: y overlaps an input", who);
+  return M2_OK;
+}
+
+extern "C" m2_status mxfp4_linear(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                                  const uint8_t* w_scales, void* y, int out_dtype, int M, int N, int K, void* stream) {
+  g_err.clear();
+  m2_status s = check_mx_linear(w_codes, w_scales, y, out_dtype, M, N, K, "mxfp4_linear");
+  if (s) return s;
+  if (M && (!a_codes || !a_scales)) return fail(M2_EINVAL, "mxfp4_linear: null pointer");
+  if ((uintptr_t)a_codes % 16 || (uintptr_t)a_scales % 16)
+    return fail(M2_EINVAL, "mxfp4_linear: codes and scales must be 16-byte aligned");
+  const size_t yb = (size_t)M * N * (out_dtype == M2_DTYPE_F32 ? 4 : 2);
+  if (overlap(y, yb, a_codes, code_bytes(M, K)) || overlap(y, yb, a_scales, mx_scale_bytes(M, K)))
+    return fail(M2_EINVAL, "mxfp4_linear: y overlaps an input");
+  if ((s = check_device())) return s;
+  int* err = nullptr;
+  if ((s = standalone_error_word(&err))) return s;
+  M2_CUDA(gemm_mx({a_codes, a_scales}, {w_codes, w_scales}, y, out_dtype == M2_DTYPE_F32, M, N, K, false, err,
+                  static_cast<cudaStream_t>(stream)));
+  return M2_OK;
+}
+
+extern "C" m2_status mxfp4_linear_bf16_workspace_size(int M, int N, int K, size_t* bytes) {
+  if (!bytes) return fail(M2_EINVAL, "mxfp4_linear_bf16_workspace_size: null argument");
+  m2_status s = check_mx_shape(M, K, "mxfp4_linear_bf16_workspace_size");
+  if (s) return s;
+  if (N < 1 || N > (1 << 24)) return fail(M2_ESHAPE, "mxfp4_linear_bf16_workspace_size: N %d not in [1, 2^24]", N);
+  *bytes = align256(code_bytes(M, K)) + mx_scale_bytes(M, K);
+  return M2_OK;
+}
+
+extern "C" m2_status mxfp4_linear_bf16(const uint16_t* x, size_t row_stride, const uint8_t* w_codes,
+                                       const uint8_t* w_scales, void* y, int out_dtype, int M, int N, int K,
+                                       void* workspace, size_t ws_bytes, void* stream) {
+  g_err.clear();
+  m2_status s = check_mx_linear(w_codes, w_scales, y, out_dtype, M, N, K, "mxfp4_linear_bf16");
+  if (s || (s = check_mx_rows(x, row_stride, K, "mxfp4_linear_bf16"))) return s;
+  if (M && !x) return fail(M2_EINVAL, "mxfp4_linear_bf16: null pointer");
+  const size_t yb = (size_t)M * N * (out_dtype == M2_DTYPE_F32 ? 4 : 2), xb = extent(M, row_stride, K, 2);
+  if (overlap(y, yb, x, xb)) return fail(M2_EINVAL, "mxfp4_linear_bf16: y overlaps an input");
+  const size_t cb = align256(code_bytes(M, K)), need = cb + mx_scale_bytes(M, K);
+  if (ws_bytes < need || (need && !workspace))
+    return fail(M2_ENOMEM, "mxfp4_linear_bf16: workspace %zu bytes < %zu needed", ws_bytes, need);
+  if ((uintptr_t)workspace % 256) return fail(M2_EINVAL, "mxfp4_linear_bf16: workspace must be 256-byte aligned");
+  if (overlap(workspace, need, x, xb) || overlap(workspace, need, y, yb) ||
+      overlap(workspace, need, w_codes, code_bytes(N, K)) || overlap(workspace, need, w_scales, mx_scale_bytes(N, K)))
+    return fail(M2_EINVAL, "mxfp4_linear_bf16: the workspace overlaps an argument");
+  if ((s = check_device())) return s;
+  int* err = nullptr;
+  if ((s = standalone_error_word(&err))) return s;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  M2_CUDA(launch_mx_quant(x, row_stride, M, K, codes, codes + cb, st));
+  M2_CUDA(gemm_mx({codes, codes + cb}, {w_codes, w_scales}, y, out_dtype == M2_DTYPE_F32, M, N, K, true, err, st));
+  return M2_OK;
+}
+
+extern "C" m2_status m2_token_logprobs(const void* logits, int dtype, size_t row_stride, int rows, int vocab,
+                                       const int32_t* tokens, int top, float* logprobs, int32_t* ranks, float* entropy,
+                                       int32_t* top_tokens, float* top_logprobs, void* stream) {
+  g_err.clear();
+  if (rows < 0 || rows > (1 << 24)) return fail(M2_ESHAPE, "m2_token_logprobs: rows %d not in [0, 2^24]", rows);
+  if (vocab < 1 || vocab > (1 << 24)) return fail(M2_ESHAPE, "m2_token_logprobs: vocab %d not in [1, 2^24]", vocab);
+  if (top < 0 || top > kLpMaxTop) return fail(M2_ESHAPE, "m2_token_logprobs: top %d not in [0, %d]", top, kLpMaxTop);
+  if (dtype != M2_DTYPE_F32 && dtype != M2_DTYPE_BF16)
+    return fail(M2_EINVAL, "m2_token_logprobs: dtype must be M2_DTYPE_F32 or M2_DTYPE_BF16");
+  if (row_stride < (size_t)vocab || row_stride > ((size_t)1 << 40))
+    return fail(M2_ESHAPE, "m2_token_logprobs: row_stride %zu is below vocab %d or above 2^40", row_stride, vocab);
+  const size_t es = dtype == M2_DTYPE_BF16 ? 2 : 4, rb = (size_t)rows * 4, tb = rb * top;
+  if (rows && !logits) return fail(M2_EINVAL, "m2_token_logprobs: null pointer");
+  if (rows && ((tokens != nullptr) != (logprobs != nullptr) || (tokens != nullptr) != (ranks != nullptr)))
+    return fail(M2_EINVAL, "m2_token_logprobs: tokens, logprobs and ranks go together");
+  if (rows && top && (!top_tokens || !top_logprobs)) return fail(M2_EINVAL, "m2_token_logprobs: null pointer");
+  if (rows && !tokens && !entropy && !top) return fail(M2_EINVAL, "m2_token_logprobs: nothing to compute");
+  const void* o[5] = {logprobs, ranks, entropy, top_tokens, top_logprobs};
+  const size_t ob[5] = {rb, rb, rb, tb, tb};
+  if ((uintptr_t)logits % es || (uintptr_t)tokens % 4)
+    return fail(M2_EINVAL, "m2_token_logprobs: a pointer is not aligned to its element");
+  for (int i = 0; i < 5; ++i) {
+    if ((uintptr_t)o[i] % 4) return fail(M2_EINVAL, "m2_token_logprobs: a pointer is not aligned to its element");
+    if (overlap(o[i], ob[i], logits, extent(rows, row_stride, vocab, es)) || overlap(o[i], ob[i], tokens, rb))
+      return fail(M2_EINVAL, "m2_token_logprobs: an output overlaps an input");
+    for (int j = i + 1; j < 5; ++j)
+      if (overlap(o[i], ob[i], o[j], ob[j])) return fail(M2_EINVAL, "m2_token_logprobs: two outputs overlap");
+  }
+  m2_status s = check_device();
+  if (s) return s;
+  if (!rows) return M2_OK;
+  int* err = nullptr;
+  if ((s = standalone_error_word(&err))) return s;
+  const LpOut out{logprobs, ranks, entropy, top_tokens, top_logprobs};
+  M2_CUDA(launch_token_logprobs(logits, dtype == M2_DTYPE_BF16, row_stride, rows, vocab, tokens, top, out, err,
+                                static_cast<cudaStream_t>(stream)));
   return M2_OK;
 }

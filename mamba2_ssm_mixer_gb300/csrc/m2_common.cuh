@@ -34,6 +34,7 @@ constexpr int kErrSlot = 1;      // a decode row named a slot outside [0, n_slot
 constexpr int kErrTimeout = 2;   // a bounded wait ran out
 constexpr int kErrDupSlot = 4;   // two decode rows of one call named the same slot
 constexpr int kErrAdapter = 8;   // a row named an adapter outside [-1, n_adapters)
+constexpr int kErrToken = 32;    // a row named a token outside [-1, vocab)
 constexpr int kErrBeam = 16;     // a row's parent names no beam with a slot, or its request has too few slots
 
 __device__ __forceinline__ float bf2f(__nv_bfloat16 v) { return __bfloat162float(v); }

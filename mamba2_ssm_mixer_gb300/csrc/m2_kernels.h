@@ -122,6 +122,27 @@ cudaError_t launch_beam_select(const void* logits, bool bf16, size_t stride, int
                                const float* scores, const uint8_t* done, int eos, int k, int32_t* tokens,
                                int32_t* parents, float* out_scores, uint8_t* out_done, void* ws, cudaStream_t st);
 
+// mxfp4.cu: the microscaled 4-bit format.  x rows `stride` elements apart.
+size_t mx_scale_bytes(int rows, int K);
+cudaError_t launch_mx_quant(const uint16_t* x, size_t stride, int rows, int K, uint8_t* codes, uint8_t* scales,
+                            cudaStream_t st);
+cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int rows, int K, uint16_t* out,
+                              cudaStream_t st);
+cudaError_t launch_mx_pack(const uint8_t* scales, int rows, int K, uint8_t* tiles, cudaStream_t st);
+
+// token_logprobs.cu: log probabilities of given tokens (tokens may be null),
+// their ranks, the rows' entropy and the `top` largest tokens.
+constexpr int kLpMaxTop = 64;
+struct LpOut {
+  float* logprobs;      // [rows] (not written without tokens)
+  int32_t* ranks;       // [rows] (likewise)
+  float* entropy;       // [rows] or null
+  int32_t* top_tokens;  // [rows, top]
+  float* top_logprobs;  // [rows, top]
+};
+cudaError_t launch_token_logprobs(const void* logits, bool bf16, size_t stride, int rows, int vocab,
+                                  const int32_t* tokens, int top, const LpOut& out, int* err, cudaStream_t st);
+
 // reorder.cu: the paged states after a beam selection (slots renamed, the
 // rows of a beam's further children copied, in every layer's pools).
 constexpr int kReorderMaxLayers = 64;

@@ -231,6 +231,54 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// ---------------------------------------------------------------- tcgen05, block-scaled 4-bit operands
+// D[tmem] (+)= (A x 2^sa) x (B x 2^sb)^T: e2m1 operands, 64 of K per MMA, one
+// ue8m0 scale per 32 of them, read from TMEM: `sfa` holds 128 rows in four
+// columns (lane = row % 32 of each 32-lane quarter, column = row / 32, byte =
+// K block; the descriptor's id picks bytes 0-1 or 2-3), `sfb` four columns per
+// 128 columns of D likewise.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+}
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate));
+}
+// 512 bytes of shared memory (32 rows of 16) into four TMEM columns, the same
+// in each quarter of the lanes.  MMAs issued after it by the same thread see
+// it, MMAs issued before it have read the columns' old contents.
+__device__ __forceinline__ void tmem_cp_32x128b(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+// The same in both CTAs of the pair, each from its own shared memory.
+__device__ __forceinline__ void tmem_cp_32x128b_pair(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+// Descriptor of such a 512-byte tile: unswizzled, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t desc_scale_tile(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);   // start address
+  d |= (uint64_t)(128 >> 4) << 32;            // stride byte offset: next 8 rows
+  d |= (uint64_t)1 << 46;                     // descriptor version (sm_100 family)
+  return d;
+}
+// Instruction descriptor of kind::mxf4 (e2m1 x e2m1, ue8m0 scales, K-major):
+//   bits 4-5 scale B id, 7-9 A format (1), 10-12 B format (1), 17-22 N >> 3,
+//   23 scale format (1: ue8m0), 24-28 M >> 4, 29-30 scale A id.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
+         (sf_id << 29);
+}
+
 // Instruction descriptor: f32 accumulate, A/B K-major, dense.
 //   bits 4-5 D format (1 = f32), 7-9 A format, 10-12 B format,
 //   17-22 N >> 3, 24-28 M >> 4.
@@ -334,6 +382,17 @@ __device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t caddr) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(caddr)
                : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint64_t ld_dsmem_u64(uint32_t caddr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(caddr) : "memory");
+  return v;
+}
+__device__ __forceinline__ int ld_dsmem_s32(uint32_t caddr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
   return v;
 }
 
