@@ -206,23 +206,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer (both CTAs)
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t issued_phase[STAGES];
-      bool issued[STAGES];
-      for (int s = 0; s < STAGES; ++s) issued[s] = false, issued_phase[s] = 0;
-      bool ok = true;
-      for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-        const int m0 = (tile % tiles_m) * kPM + (int)rank * kBM;
-        const int nt = (tile / tiles_m) * BN, n0 = nt + (int)rank * (BN / 2);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort)) {
-            raise_abort(ctl, err);
-            ok = false;
-            break;
-          }
+    // ---------------- TMA producer (both CTAs): the warp loops, one lane issues
+    const bool lead = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;   // stages requested
+    bool ok = true;
+    for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+      const int m0 = (tile % tiles_m) * kPM + (int)rank * kBM;
+      const int nt = (tile / tiles_m) * BN, n0 = nt + (int)rank * (BN / 2);
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->empty[stage], phase ^ 1u, abort))) {
+          if (lead) raise_abort(ctl, err);
+          ok = false;
+          break;
+        }
+        if (lead) {
           uint8_t* sA = smem + stage * STAGE_BYTES;
           const uint32_t full0 = cluster_map(smem_u32(&ctl->full[stage]), 0);
           if (rank == 0) mbar_expect_tx(&ctl->full[stage], 2 * STAGE_BYTES);
@@ -231,44 +230,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (the maps of the scales are in 4-byte words: 256 words = two tiles)
           tma_load_2d_pair(sA + A_BYTES + B_BYTES, &tmSA, full0, kb * 256, m0 / 128);
           tma_load_2d_pair(sA + A_BYTES + B_BYTES + SA_BYTES, &tmSB, full0, kb * 256, nt / 128);
-          issued[stage] = true;
-          issued_phase[stage] = phase;
-          if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
-      }
-      if (*abort) {
-        // the even CTA's full barriers count both CTAs' copies: let those in
-        // flight land before the pair exits
-        if (rank == 0)
-          for (int s = 0; s < STAGES; ++s)
-            if (issued[s]) mbar_wait(&ctl->full[s], issued_phase[s], nullptr, 100000000ull);
-      } else {
-        for (int s = 0; s < STAGES; ++s)
-          if (issued[s] && !mbar_wait(&ctl->empty[s], issued_phase[s], abort)) {
-            raise_abort(ctl, err);
-            break;
-          }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
       }
     }
+    // before the CTA may exit: every stage's last MMA commit has arrived on
+    // its empty barrier; after an abort, the copies in flight have landed (the
+    // even CTA's full barriers count both CTAs')
+    for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i) {
+      const int s = i % STAGES;
+      const uint32_t ph = (uint32_t)(i / STAGES) & 1u;
+      if (!*abort) {
+        if (!mbar_wait(&ctl->empty[s], ph, abort) && lead) raise_abort(ctl, err);
+      } else if (rank == 0) {
+        mbar_wait(&ctl->full[s], ph, nullptr, 100000000ull);
+      }
+    }
+    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // ---------------- MMA issuer (even CTA only)
+    if (rank == 0) {
+      // ---------------- MMA issuer (even CTA only): the warp loops, one lane issues
+      const bool lead = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
       for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-        if (!mbar_wait_cluster(&ctl->tempty[acc], acc_phase ^ 1u, abort)) {
-          raise_abort(ctl, err);
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&ctl->tempty[acc], acc_phase ^ 1u, abort))) {
+          if (lead) raise_abort(ctl, err);
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
         const uint32_t sfb0 = tmem_base + SFB_COL + (((tile / tiles_m) * BN) % 128) / 32;
         for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(&ctl->full[stage], phase, abort)) {
-            raise_abort(ctl, err);
+          if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[stage], phase, abort))) {
+            if (lead) raise_abort(ctl, err);
             ok = false;
             break;
           }
@@ -278,31 +278,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t adesc = desc_kmajor_sw128(a_addr);
           const uint64_t bdesc = desc_kmajor_sw128(a_addr + A_BYTES);
           const int left = K - kb * kBK;
+          if (lead) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {   // 128 values: their scales, then two MMAs
-            if (t * 128 < left) {
-              tmem_cp_32x128b_pair(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
-              tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t, desc_scale_tile(sf_addr + SA_BYTES + t * kSfTile));
-              tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t + 4,
-                                   desc_scale_tile(sf_addr + SA_BYTES + (2 + t) * kSfTile));
+            for (int t = 0; t < 2; ++t) {   // 128 values: their scales, then two MMAs
+              if (t * 128 < left) {
+                tmem_cp_32x128b_pair(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
+                tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t, desc_scale_tile(sf_addr + SA_BYTES + t * kSfTile));
+                tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t + 4,
+                                     desc_scale_tile(sf_addr + SA_BYTES + (2 + t) * kSfTile));
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (t * 128 + h * 64 < left)
-                  mma_mxf4_pair(d_tmem, adesc + 2 * (2 * t + h), bdesc + 2 * (2 * t + h), idesc_mxf4(kPM, BN, 2 * h),
-                                tmem_base + SFA_COL + 4 * t, sfb0 + 8 * t, (kb | t | h) != 0);
+                for (int h = 0; h < 2; ++h)
+                  if (t * 128 + h * 64 < left)
+                    mma_mxf4_pair(d_tmem, adesc + 2 * (2 * t + h), bdesc + 2 * (2 * t + h), idesc_mxf4(kPM, BN, 2 * h),
+                                  tmem_base + SFA_COL + 4 * t, sfb0 + 8 * t, (kb | t | h) != 0);
+              }
             }
+            mma_commit_pair(&ctl->empty[stage], kPair);
           }
-          mma_commit_pair(&ctl->empty[stage], kPair);
+          __syncwarp();
           if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
         if (!ok) break;
-        mma_commit_pair(&ctl->tfull[acc], kPair);
+        if (lead) mma_commit_pair(&ctl->tfull[acc], kPair);
+        __syncwarp();
         if (++acc == 2) acc = 0, acc_phase ^= 1u;
       }
-      if (*abort) {
+      if (*abort && lead) {
         mma_commit_pair(&ctl->drain, kPair);
         mbar_wait(&ctl->drain, 0, nullptr, 100000000ull);
       }
+      __syncwarp();
     }
   } else {
     // ---------------- epilogue (both CTAs): warps 2..5 own TMEM lane quarters (warp % 4)
@@ -441,22 +446,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_trigger();
     if (warp == 1) {
-      if (lane == 0) {
-        // ---------------- MMA issuer
-        bool ok = true;
-        for (int i = 0; i < nk; ++i) {
-          const int stg = i % STAGES;
-          if (!mbar_wait(&ctl->full[stg], (uint32_t)(i / STAGES) & 1u, abort)) {
-            raise_abort(ctl, err);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + stg * STAGE_BYTES);
-          const uint32_t sf_addr = a_addr + A_BYTES + B_BYTES;
-          const uint64_t adesc = desc_kmajor_sw128(a_addr);
-          const uint64_t bdesc = desc_kmajor_sw128(a_addr + A_BYTES);
-          const int left = K - (kb0 + i) * kBK;
+      // ---------------- MMA issuer: the warp loops, one lane issues
+      const bool lead = elect_one();
+      bool ok = true;
+      int stg = 0;
+      uint32_t phase = 0;
+      for (int i = 0; i < nk; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[stg], phase, abort))) {
+          if (lead) raise_abort(ctl, err);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a_addr = smem_u32(smem + stg * STAGE_BYTES);
+        const uint32_t sf_addr = a_addr + A_BYTES + B_BYTES;
+        const uint64_t adesc = desc_kmajor_sw128(a_addr);
+        const uint64_t bdesc = desc_kmajor_sw128(a_addr + A_BYTES);
+        const int left = K - (kb0 + i) * kBK;
+        if (lead) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t * 128 < left) {
@@ -471,6 +478,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(&ctl->empty[stg]);
         }
+        __syncwarp();
+        if (++stg == STAGES) stg = 0, phase ^= 1u;
+      }
+      if (lead) {
         if (ok && nk > 0) {
           mma_commit(&ctl->tfull[0]);
         } else {
@@ -478,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait(&ctl->drain, 0, nullptr, 100000000ull);
         }
       }
+      __syncwarp();
     } else {
       // ---------------- epilogue warps 2..5: accumulator rows -> own exchange buffer
       const int quarter = warp & 3;

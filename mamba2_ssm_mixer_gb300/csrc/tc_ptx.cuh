@@ -231,6 +231,21 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// One lane of a converged warp, the same every time.  A warp that loops as a
+// whole and issues tcgen05 and TMA instructions under this predicate keeps
+// their operands in uniform registers; a loop of one lane moves each operand
+// there first (an MMA then takes 56 clocks to issue, more than N = 64 takes
+// to run).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- tcgen05, block-scaled 4-bit operands
 // D[tmem] (+)= (A x 2^sa) x (B x 2^sb)^T: e2m1 operands, 64 of K per MMA, one
 // ue8m0 scale per 32 of them, read from TMEM: `sfa` holds 128 rows in four
