@@ -603,8 +603,8 @@ m2_status m2_state_reorder(uint16_t* const* conv_pools, void* const* ssm_pools, 
  * [ceil(rows / 128)][ceil(K / 128)]; row r and block b of a tile at byte
  * (r % 32) * 16 + (r / 32) * 4 + b, zero past the rows and past K
  * (mxfp4_scale_bytes; mxfp4_pack_scales makes them from row-major codes).
- * K: a multiple of 32 in [32, 2^24]; rows up to 2^24; codes and scales 16-byte
- * aligned.
+ * K: a multiple of 32 in [32, 2^24]; rows up to 2^24; rows * K up to 2^38;
+ * codes and scales 16-byte aligned.
  * ------------------------------------------------------------------------ */
 
 /* Bytes of the scale tiles of a [rows, K] operand. */

@@ -19,6 +19,7 @@
 
 #include <map>
 #include <mutex>
+#include <type_traits>
 
 #include "gemm.h"
 #include "launch_util.h"
@@ -50,6 +51,22 @@ struct __align__(8) Ctl {
 __device__ __forceinline__ void raise_abort(Ctl* ctl, int* err) {
   *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
   if (err) atomicOr(err, kErrTimeout);
+}
+
+// go(steps) with as many 64-value steps (at most 4) as `left` values of K take.
+// The choice is made outside the issuing lane's code: conditions in there keep
+// its operands out of uniform registers (4 MMAs of N = 192: 474 clocks
+// instead of 384).
+template <class Go>
+__device__ __forceinline__ void by_steps(int left, Go& go) {
+  if (left > 192)
+    go(std::integral_constant<int, 4>());
+  else if (left > 128)
+    go(std::integral_constant<int, 3>());
+  else if (left > 64)
+    go(std::integral_constant<int, 2>());
+  else
+    go(std::integral_constant<int, 1>());
 }
 
 // Output staging: two buffers per epilogue warp, 32 rows of 128 bytes each in
@@ -277,24 +294,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sf_addr = a_addr + A_BYTES + B_BYTES;
           const uint64_t adesc = desc_kmajor_sw128(a_addr);
           const uint64_t bdesc = desc_kmajor_sw128(a_addr + A_BYTES);
-          const int left = K - kb * kBK;
-          if (lead) {
+          // the stage's first n MMAs and their scales
+          auto issue = [&](auto n) {
+            if (lead) {
+              constexpr int kN = decltype(n)::value;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {   // 128 values: their scales, then two MMAs
-              if (t * 128 < left) {
+              for (int t = 0; t < (kN + 1) / 2; ++t) {   // the scales of 128 values each
                 tmem_cp_32x128b_pair(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
                 tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t, desc_scale_tile(sf_addr + SA_BYTES + t * kSfTile));
                 tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t + 4,
                                      desc_scale_tile(sf_addr + SA_BYTES + (2 + t) * kSfTile));
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if (t * 128 + h * 64 < left)
-                    mma_mxf4_pair(d_tmem, adesc + 2 * (2 * t + h), bdesc + 2 * (2 * t + h), idesc_mxf4(kPM, BN, 2 * h),
-                                  tmem_base + SFA_COL + 4 * t, sfb0 + 8 * t, (kb | t | h) != 0);
               }
+#pragma unroll
+              for (int i = 0; i < kN; ++i)
+                mma_mxf4_pair(d_tmem, adesc + 2 * i, bdesc + 2 * i, idesc_mxf4(kPM, BN, 2 * (i % 2)),
+                              tmem_base + SFA_COL + 4 * (i / 2), sfb0 + 8 * (i / 2), (kb | i) != 0);
+              mma_commit_pair(&ctl->empty[stage], kPair);
             }
-            mma_commit_pair(&ctl->empty[stage], kPair);
-          }
+          };
+          by_steps(K - kb * kBK, issue);
           __syncwarp();
           if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
@@ -462,22 +480,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sf_addr = a_addr + A_BYTES + B_BYTES;
         const uint64_t adesc = desc_kmajor_sw128(a_addr);
         const uint64_t bdesc = desc_kmajor_sw128(a_addr + A_BYTES);
-        const int left = K - (kb0 + i) * kBK;
-        if (lead) {
+        auto issue = [&](auto n) {
+          if (lead) {
+            constexpr int kN = decltype(n)::value;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t * 128 < left) {
+            for (int t = 0; t < (kN + 1) / 2; ++t) {
               tmem_cp_32x128b(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
               tmem_cp_32x128b(tmem_base + SFB_COL + 4 * t, desc_scale_tile(sf_addr + SF_BYTES + t * kSfTile));
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (t * 128 + h * 64 < left)
-                  mma_mxf4(tmem_base, adesc + 2 * (2 * t + h), bdesc + 2 * (2 * t + h), idesc_mxf4(kBM, BNT, 2 * h),
-                           tmem_base + SFA_COL + 4 * t, tmem_base + SFB_COL + 4 * t, (i | t | h) != 0);
             }
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+              mma_mxf4(tmem_base, adesc + 2 * j, bdesc + 2 * j, idesc_mxf4(kBM, BNT, 2 * (j % 2)),
+                       tmem_base + SFA_COL + 4 * (j / 2), tmem_base + SFB_COL + 4 * (j / 2), (i | j) != 0);
+            mma_commit(&ctl->empty[stg]);
           }
-          mma_commit(&ctl->empty[stg]);
-        }
+        };
+        by_steps(K - (kb0 + i) * kBK, issue);
         __syncwarp();
         if (++stg == STAGES) stg = 0, phase ^= 1u;
       }

@@ -1430,6 +1430,7 @@ extern "C" m2_status m2_state_reorder(uint16_t* const* conv_pools, void* const* 
 static m2_status check_mx_shape(int rows, int K, const char* who) {
   if (rows < 0 || rows > (1 << 24) || K < 32 || K > (1 << 24) || K % 32)
     return fail(M2_ESHAPE, "%s: %d rows, K %d (rows up to 2^24, K a multiple of 32 in [32, 2^24])", who, rows, K);
+  if ((long long)rows * K > (1ll << 38)) return fail(M2_ESHAPE, "%s: %d rows x K %d is above 2^38", who, rows, K);
   return M2_OK;
 }
 

@@ -73,15 +73,15 @@ __global__ void __launch_bounds__(kMxThreads) k_mx_quant(const uint16_t* __restr
   pdl_wait();
   pdl_trigger();
   const int KB = mx_kb(K), lane16 = threadIdx.x & 15;
-  const size_t units = (size_t)rows_pad * KB;
-  const size_t u0 = ((size_t)blockIdx.x * kMxUnroll * kMxThreads + threadIdx.x) / 16;
+  const uint32_t units = (uint32_t)rows_pad * (uint32_t)KB;   // (below 2^32: rows K <= 2^38)
+  const uint32_t u0 = blockIdx.x * (kMxUnroll * kMxThreads / 16) + threadIdx.x / 16;
   uint4 v[kMxUnroll];
   int row[kMxUnroll], kb[kMxUnroll];
 #pragma unroll
   for (int i = 0; i < kMxUnroll; ++i) {
-    const size_t u = u0 + (size_t)i * (kMxThreads / 16);
-    row[i] = u < units ? (int)(u / KB) : rows_pad;
-    kb[i] = (int)(u % KB);
+    const uint32_t u = u0 + i * (kMxThreads / 16);
+    row[i] = u < units ? (int)(u / (uint32_t)KB) : rows_pad;
+    kb[i] = (int)(u % (uint32_t)KB);
     v[i] = make_uint4(0u, 0u, 0u, 0u);
     if (row[i] < rows && kb[i] * 128 + lane16 * 8 < K)
       v[i] = *reinterpret_cast<const uint4*>(x + (size_t)row[i] * stride + kb[i] * 128 + lane16 * 8);
@@ -113,14 +113,14 @@ __global__ void __launch_bounds__(kMxThreads) k_mx_dequant(const uint8_t* __rest
   pdl_wait();
   pdl_trigger();
   const int KB = mx_kb(K), lane16 = threadIdx.x & 15;
-  const size_t units = (size_t)rows * KB;
-  const size_t u0 = ((size_t)blockIdx.x * kMxUnroll * kMxThreads + threadIdx.x) / 16;
+  const uint32_t units = (uint32_t)rows * (uint32_t)KB;
+  const uint32_t u0 = blockIdx.x * (kMxUnroll * kMxThreads / 16) + threadIdx.x / 16;
   uint32_t q[kMxUnroll], s[kMxUnroll];
   size_t at[kMxUnroll];
 #pragma unroll
   for (int i = 0; i < kMxUnroll; ++i) {
-    const size_t u = u0 + (size_t)i * (kMxThreads / 16);
-    const int row = (int)(u / KB), kb = (int)(u % KB), k = kb * 128 + lane16 * 8;
+    const uint32_t u = u0 + i * (kMxThreads / 16);
+    const int row = (int)(u / (uint32_t)KB), kb = (int)(u % (uint32_t)KB), k = kb * 128 + lane16 * 8;
     const bool in = u < units && k < K;
     at[i] = in ? (size_t)row * K + k : ~(size_t)0;
     q[i] = in ? *reinterpret_cast<const uint32_t*>(codes + at[i] / 2) : 0u;
