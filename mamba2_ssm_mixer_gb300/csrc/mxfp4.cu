@@ -12,7 +12,7 @@
 // memory: tiles of 128 rows x 4 blocks (128 values of K), 512 bytes, byte
 // (r % 32) 16 + (r / 32) 4 + b of a tile for row r and block b; tiles
 // [ceil(rows / 128)][ceil(K / 128)], zero past the rows and past K.
-#include <cuda_fp4.h>
+#include <cuda_bf16.h>
 
 #include "launch_util.h"
 #include "m2_kernels.h"
@@ -22,7 +22,7 @@ namespace m2 {
 namespace {
 
 constexpr int kMxThreads = 256;
-constexpr int kMxUnroll = 4;
+constexpr int kMxUnroll = 2;
 
 __host__ __device__ inline int mx_kb(int K) { return (K + 127) / 128; }
 // Bytes offset of the four scale codes of row r's 128-value group kb.
@@ -30,78 +30,129 @@ __device__ __forceinline__ size_t scale_word(int r, int kb, int KB) {
   return ((size_t)(r >> 7) * KB + kb) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
-// Scale code of a block from the largest |x| bits (bf16): exponent field less
-// 2, 0 at least (subnormals and zeros included), 255 for infinities and NaN.
+// Scale code of a block from its largest |x| (bf16 bits): exponent field less 2,
+// 0 at least (subnormals and zeros included), 255 for infinities and NaN.
 __device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
   const uint32_t e = amax >> 7;
   return amax >= 0x7F80u ? 255u : e > 2u ? e - 2u : 0u;
 }
 
-// e2m1 codes of two floats, a in the low half of the byte.
-__device__ __forceinline__ uint32_t e2m1x2(float a, float b) {
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest);
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
+// The larger magnitudes of two pairs, NaN if there is one.
+__device__ __forceinline__ __nv_bfloat162 max_abs(__nv_bfloat162 a, __nv_bfloat162 b) {
+  return __hmax2_nan(__habs2(a), __habs2(b));
+}
+__device__ __forceinline__ __nv_bfloat162 max_abs(const uint4& v) {
+  return max_abs(max_abs(as_bf16x2(v.x), as_bf16x2(v.y)), max_abs(as_bf16x2(v.z), as_bf16x2(v.w)));
 }
 
-// 2^(127 - code) for code <= 254: the exact factor of x / 2^(code - 127).
-__device__ __forceinline__ float inverse_scale(uint32_t code) { return __uint_as_float((254u - code) << 23); }
-// 2^(code - 127), NaN for 255.
-__device__ __forceinline__ float scale_value(uint32_t code) {
-  return __uint_as_float(code == 255u ? 0x7FC00000u : code ? code << 23 : 0x00400000u);
-}
-
-__device__ __forceinline__ uint32_t quant8(const uint4& v, uint32_t code) {
-  if (code == 255u) return 0u;
-  const float f = inverse_scale(code);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t q = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q |= e2m1x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f) << (8 * i);
+// e2m1 codes of eight bf16 times f (a power of two: exact, but for products
+// below bf16's range, whose code is 0 either way).
+__device__ __forceinline__ uint32_t quant8(const uint4& v, __nv_bfloat162 f) {
+  const uint32_t w[4] = {bits_of(__hmul2(as_bf16x2(v.x), f)), bits_of(__hmul2(as_bf16x2(v.y), f)),
+                         bits_of(__hmul2(as_bf16x2(v.z), f)), bits_of(__hmul2(as_bf16x2(v.w), f))};
+  uint32_t q;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}\n"
+      : "=r"(q)
+      : "r"(w[0] << 16), "r"(w[0] & 0xFFFF0000u), "r"(w[1] << 16), "r"(w[1] & 0xFFFF0000u), "r"(w[2] << 16),
+        "r"(w[2] & 0xFFFF0000u), "r"(w[3] << 16), "r"(w[3] & 0xFFFF0000u));
   return q;
 }
 
+// bf16 values of eight e2m1 codes times f.  A magnitude's two bytes come from
+// tables of eight, picked by the code's nibble.
+__device__ __forceinline__ uint4 dequant8(uint32_t q, __nv_bfloat162 f) {
+  uint32_t o[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t c = q >> (16 * h), sel = c & 0x7777u;
+    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel);   // 0, 0.5, 1, 1.5 | 2, 3, 4, 6
+    const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+    const uint32_t s0 = ((c << 12) & 0x8000u) | ((c << 24) & 0x80000000u);
+    const uint32_t s1 = ((c << 4) & 0x8000u) | ((c << 16) & 0x80000000u);
+    o[2 * h] = bits_of(__hmul2(as_bf16x2(__byte_perm(lo, hi, 0x5140) | s0), f));
+    o[2 * h + 1] = bits_of(__hmul2(as_bf16x2(__byte_perm(lo, hi, 0x7362) | s1), f));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// 2^(127 - code) twice, for code <= 252: the exact factor of x / 2^(code - 127).
+__device__ __forceinline__ __nv_bfloat162 inverse_scale(uint32_t code) {
+  return as_bf16x2(((254u - code) << 7) * 0x10001u);
+}
+// 2^(code - 127) twice, NaN for 255.
+__device__ __forceinline__ __nv_bfloat162 scale_value(uint32_t code) {
+  return as_bf16x2((code == 255u ? 0x7FC0u : code ? code << 7 : 0x0040u) * 0x10001u);
+}
+
+// A unit is 128 values of one row, taken by 8 lanes of 16 values; a thread has
+// kMxUnroll of them, kMxThreads / 8 units apart, under way together.  The
+// first one's place takes a division, the others steps.
+struct Units {
+  int row, kb, KB, dr, dk;
+  __device__ Units(int K) : KB(mx_kb(K)) {
+    const uint32_t u = blockIdx.x * (kMxUnroll * kMxThreads / 8) + threadIdx.x / 8;   // (below 2^32: rows K <= 2^38)
+    row = (int)(u / (uint32_t)KB);
+    kb = (int)(u % (uint32_t)KB);
+    dr = (kMxThreads / 8) / KB;
+    dk = (kMxThreads / 8) % KB;
+  }
+  __device__ void step() {
+    row += dr;
+    kb += dk;
+    if (kb >= KB) kb -= KB, ++row;
+  }
+};
+
 }  // namespace
 
-// A half-warp takes 128 values of one row (16 lanes x 8 values: 256 bytes in,
-// 64 bytes of codes and one word of four scale codes out), kMxUnroll of them
-// with their loads under way together.
+// 16 values of a thread are 32 bytes in and 8 bytes of codes out; a block's
+// largest magnitude takes one exchange, a unit's word of scale codes two.
+// Bound by the instructions: with 8 values a thread, an index division per 8
+// and f32 products 8192 x 2688 took 15.3 us.
 __global__ void __launch_bounds__(kMxThreads) k_mx_quant(const uint16_t* __restrict__ x, size_t stride, int rows, int K,
                                                          int rows_pad, uint8_t* __restrict__ codes,
                                                          uint8_t* __restrict__ scales) {
   pdl_wait();
   pdl_trigger();
-  const int KB = mx_kb(K), lane16 = threadIdx.x & 15;
-  const uint32_t units = (uint32_t)rows_pad * (uint32_t)KB;   // (below 2^32: rows K <= 2^38)
-  const uint32_t u0 = blockIdx.x * (kMxUnroll * kMxThreads / 16) + threadIdx.x / 16;
-  uint4 v[kMxUnroll];
-  int row[kMxUnroll], kb[kMxUnroll];
+  const int lane8 = threadIdx.x & 7;
+  uint4 v[kMxUnroll][2];
+  Units at(K);
 #pragma unroll
-  for (int i = 0; i < kMxUnroll; ++i) {
-    const uint32_t u = u0 + i * (kMxThreads / 16);
-    row[i] = u < units ? (int)(u / (uint32_t)KB) : rows_pad;
-    kb[i] = (int)(u % (uint32_t)KB);
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (row[i] < rows && kb[i] * 128 + lane16 * 8 < K)
-      v[i] = *reinterpret_cast<const uint4*>(x + (size_t)row[i] * stride + kb[i] * 128 + lane16 * 8);
+  for (int i = 0; i < kMxUnroll; ++i, at.step()) {
+    const int k = at.kb * 128 + lane8 * 16;
+    const bool in = at.row < rows && k < K;
+    const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)at.row * stride + k);
+    v[i][0] = in ? __ldg(p) : make_uint4(0u, 0u, 0u, 0u);
+    v[i][1] = in ? __ldg(p + 1) : make_uint4(0u, 0u, 0u, 0u);
   }
+  at = Units(K);
 #pragma unroll
-  for (int i = 0; i < kMxUnroll; ++i) {
-    // the block's largest |x| as bf16 bits, over four lanes
-    uint32_t m = max_u16x2(max_u16x2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
-                           max_u16x2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
-    m = max(m & 0xFFFFu, m >> 16);
+  for (int i = 0; i < kMxUnroll; ++i, at.step()) {
+    const uint32_t two = bits_of(max_abs(max_abs(v[i][0]), max_abs(v[i][1])));
+    uint32_t m = max(two & 0xFFFFu, two >> 16);   // (no sign: magnitudes order like their bits)
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t code = scale_code(m);
-    uint32_t word = code << (8 * (lane16 >> 2));
+    uint32_t word = code << (8 * (lane8 >> 1));
+    word |= __shfl_xor_sync(0xffffffffu, word, 2);
     word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    if (row[i] >= rows_pad) continue;
-    if (lane16 == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(row[i], kb[i], KB)) = word;
-    if (row[i] < rows && kb[i] * 128 + lane16 * 8 < K)
-      *reinterpret_cast<uint32_t*>(codes + ((size_t)row[i] * K + kb[i] * 128 + lane16 * 8) / 2) = quant8(v[i], code);
+    if (lane8 == 0 && at.row < rows_pad)
+      *reinterpret_cast<uint32_t*>(scales + scale_word(at.row, at.kb, at.KB)) = word;
+    const int k = at.kb * 128 + lane8 * 16;
+    if (at.row < rows && k < K) {
+      uint2 q = make_uint2(0u, 0u);
+      if (code != 255u) {
+        const __nv_bfloat162 f = inverse_scale(code);
+        q = make_uint2(quant8(v[i][0], f), quant8(v[i][1], f));
+      }
+      *reinterpret_cast<uint2*>(codes + ((size_t)at.row * K + k) / 2) = q;
+    }
   }
 }
 
@@ -112,39 +163,27 @@ __global__ void __launch_bounds__(kMxThreads) k_mx_dequant(const uint8_t* __rest
                                                            uint16_t* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  const int KB = mx_kb(K), lane16 = threadIdx.x & 15;
-  const uint32_t units = (uint32_t)rows * (uint32_t)KB;
-  const uint32_t u0 = blockIdx.x * (kMxUnroll * kMxThreads / 16) + threadIdx.x / 16;
-  uint32_t q[kMxUnroll], s[kMxUnroll];
-  size_t at[kMxUnroll];
+  const int lane8 = threadIdx.x & 7;
+  uint2 q[kMxUnroll];
+  uint32_t s[kMxUnroll];
+  Units at(K);
 #pragma unroll
-  for (int i = 0; i < kMxUnroll; ++i) {
-    const uint32_t u = u0 + i * (kMxThreads / 16);
-    const int row = (int)(u / (uint32_t)KB), kb = (int)(u % (uint32_t)KB), k = kb * 128 + lane16 * 8;
-    const bool in = u < units && k < K;
-    at[i] = in ? (size_t)row * K + k : ~(size_t)0;
-    q[i] = in ? *reinterpret_cast<const uint32_t*>(codes + at[i] / 2) : 0u;
-    s[i] = in ? scales[scale_word(row, kb, KB) + (lane16 >> 2)] : 0u;
+  for (int i = 0; i < kMxUnroll; ++i, at.step()) {
+    const int k = at.kb * 128 + lane8 * 16;
+    const bool in = at.row < rows && k < K;
+    q[i] = in ? __ldg(reinterpret_cast<const uint2*>(codes + ((size_t)at.row * K + k) / 2)) : make_uint2(0u, 0u);
+    s[i] = in ? __ldg(scales + scale_word(at.row, at.kb, at.KB) + (lane8 >> 1)) : 0u;
   }
+  at = Units(K);
 #pragma unroll
-  for (int i = 0; i < kMxUnroll; ++i) {
-    if (at[i] == ~(size_t)0) continue;
-    const float f = scale_value(s[i]);
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float e[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t c = q[i] >> (8 * j + 4 * h);
-        // exponent field 0 is 0 or 0.5; else (1 + m / 2) 2^(field - 1)
-        const uint32_t mag = c & 7u;
-        const float v = mag < 2u ? 0.5f * (float)mag : __uint_as_float((126u + (mag >> 1)) << 23 | (mag & 1u) << 22);
-        e[h] = __uint_as_float(__float_as_uint(v) | (c & 8u) << 28) * f;
-      }
-      o[j] = pack_bf16x2(e[0], e[1]);
+  for (int i = 0; i < kMxUnroll; ++i, at.step()) {
+    const int k = at.kb * 128 + lane8 * 16;
+    if (at.row < rows && k < K) {
+      const __nv_bfloat162 f = scale_value(s[i]);
+      uint4* o = reinterpret_cast<uint4*>(out + (size_t)at.row * K + k);
+      o[0] = dequant8(q[i].x, f);
+      o[1] = dequant8(q[i].y, f);
     }
-    *reinterpret_cast<uint4*>(out + at[i]) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -175,7 +214,7 @@ cudaError_t launch_mx_quant(const uint16_t* x, size_t stride, int rows, int K, u
                             cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   const int rows_pad = (rows + 127) / 128 * 128;
-  const size_t units = (size_t)rows_pad * mx_kb(K), per = (size_t)kMxUnroll * kMxThreads / 16;
+  const size_t units = (size_t)rows_pad * mx_kb(K), per = (size_t)kMxUnroll * kMxThreads / 8;
   return launch_pdl(k_mx_quant, dim3((unsigned)((units + per - 1) / per)), dim3(kMxThreads), 0, st, x, stride, rows, K,
                     rows_pad, codes, scales);
 }
@@ -183,7 +222,7 @@ cudaError_t launch_mx_quant(const uint16_t* x, size_t stride, int rows, int K, u
 cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int rows, int K, uint16_t* out,
                               cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  const size_t units = (size_t)rows * mx_kb(K), per = (size_t)kMxUnroll * kMxThreads / 16;
+  const size_t units = (size_t)rows * mx_kb(K), per = (size_t)kMxUnroll * kMxThreads / 8;
   return launch_pdl(k_mx_dequant, dim3((unsigned)((units + per - 1) / per)), dim3(kMxThreads), 0, st, codes, scales, rows,
                     K, out);
 }
