@@ -42,7 +42,7 @@ struct __align__(8) Ctl {
   uint64_t full[8];
   uint64_t empty[8];
   uint64_t tfull[2];
-  uint64_t tempty[2];
+  uint64_t tempty[1];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -90,24 +90,34 @@ struct Out<true> {
 };
 
 // One epilogue warp: 32 accumulator lanes (output rows row0 ..) over the
-// tile's BN columns from TMEM column `tcol`, output column n0.  With a store
-// map, 128-byte slices go through shared memory and TMA stores; else every
-// thread writes its own row.
-template <int BN, bool kF32>
+// tile's BN columns from TMEM column `tcol`, output column n0, in slices from
+// the last to the first (`down`) or up; `first_read` is called when the first
+// slice has been read from TMEM.  With a store map, 128-byte slices go through
+// shared memory and TMA stores; else 32 x 32 pieces do, transposed, so that a
+// warp writes a row's consecutive elements.
+template <int BN, bool kF32, class FirstRead>
 __device__ __forceinline__ void epilogue_rows(uint32_t tcol, uint8_t* bufs, int& buf, const CUtensorMap* tmC,
                                               bool tma_store, typename Out<kF32>::T* __restrict__ C, int M, int N,
-                                              int row0, int n0, int lane) {
+                                              int row0, int n0, int lane, bool down, FirstRead first_read) {
   using O = Out<kF32>;
   if (tma_store) {
+    constexpr int kSlices = BN / O::kCols;
 #pragma unroll 1
-    for (int c = 0; c < BN; c += O::kCols) {
-      // slices outside the output are neither staged nor stored (warp-uniform)
-      if (row0 >= M || n0 + c >= N) break;
+    for (int i = 0; i < kSlices; ++i) {
+      const int c = (down ? kSlices - 1 - i : i) * O::kCols;
+      // slices outside the output are neither staged nor stored: each staged
+      // buffer is followed by its store, which the read wait below counts on
+      // (warp-uniform)
+      const bool in = row0 < M && n0 + c < N;
       uint32_t r[O::kCols];
+      if (in) {
 #pragma unroll
-      for (int h = 0; h < O::kCols; h += 32)
-        tmem_ld_32x32b_x32(tcol + (uint32_t)(c + h), *reinterpret_cast<uint32_t(*)[32]>(&r[h]));
-      tmem_ld_wait();
+        for (int h = 0; h < O::kCols; h += 32)
+          tmem_ld_32x32b_x32(tcol + (uint32_t)(c + h), *reinterpret_cast<uint32_t(*)[32]>(&r[h]));
+        tmem_ld_wait();
+      }
+      if (i == 0) first_read();
+      if (!in) continue;
       uint8_t* b = bufs + buf * kEpiBuf;
       if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
@@ -135,40 +145,49 @@ __device__ __forceinline__ void epilogue_rows(uint32_t tcol, uint8_t* bufs, int&
     }
     return;
   }
-  const int row = row0 + lane;
-  typename O::T* crow = C + (size_t)row * N;
+  constexpr int kPieces = BN / 32;
+  uint32_t* piece = reinterpret_cast<uint32_t*>(bufs);   // word (row, column) at row 32 + (column ^ row)
 #pragma unroll 1
-  for (int c = 0; c < BN; c += 32) {
+  for (int i = 0; i < kPieces; ++i) {
+    const int c = (down ? kPieces - 1 - i : i) * 32;
+    const bool in = row0 < M && n0 + c < N;
     uint32_t r[32];
-    tmem_ld_32x32b_x32(tcol + (uint32_t)c, r);
-    tmem_ld_wait();
-    const int n = n0 + c;
-    if (row < M) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (n + j < N) crow[n + j] = O::one(r[j]);
+    if (in) {
+      tmem_ld_32x32b_x32(tcol + (uint32_t)c, r);
+      tmem_ld_wait();
     }
+    if (i == 0) first_read();
+    if (!in) continue;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) piece[lane * 32 + (j ^ lane)] = r[j];
+    __syncwarp();
+    const int n = n0 + c + lane, rows = min(32, M - row0);
+    if (n < N) {
+      typename O::T* col = C + (size_t)row0 * N + n;
+#pragma unroll 8
+      for (int j = 0; j < rows; ++j) col[(size_t)j * N] = O::one(piece[j * 32 + (lane ^ j)]);
+    }
+    __syncwarp();
   }
 }
 
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// 256 x BN tiles on CTA pairs.  CTA r of a pair stages rows [128 r, ..) of A
-// with their scales, columns [r BN / 2, ..) of B and the scales of all of the
-// tile's columns (two 128-row tiles of them: a tile of B starts on a multiple
-// of 64 rows, in the middle of a scale tile for odd ones, and the MMA then
-// reads from the third of the tile's columns on).  The rest as k_gemm_pair.
+// 256 x 256 tiles on CTA pairs.  CTA r of a pair stages rows [128 r, ..) of A
+// with their scales, columns [128 r, ..) of B and the scales of all of the
+// tile's columns.  TMEM holds two accumulators and the scales in 512 columns:
+// the accumulators share 24, which the epilogue of a tile reads first; the
+// next tile's MMAs start after that.
 // ---------------------------------------------------------------------------
-template <int BN, int STAGES, bool kF32>
+template <int STAGES, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
     k_mx_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
               const __grid_constant__ CUtensorMap tmC, int tma_store, typename Out<kF32>::T* __restrict__ C, int M, int N,
               int K, int* err) {
-  static_assert(BN % 64 == 0 && BN >= 64 && BN <= 192, "BN");
   static_assert(STAGES <= 8, "STAGES");
-  constexpr int kPM = 2 * kBM;
+  constexpr int BN = 256, kPM = 2 * kBM;
   constexpr uint32_t A_BYTES = kBM * kRowBytes;
   constexpr uint32_t B_BYTES = (BN / 2) * kRowBytes;
   constexpr uint32_t SA_BYTES = 2 * kSfTile;          // 128 rows x 256 values
@@ -176,8 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
   static_assert(STAGE_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
   constexpr uint32_t TMEM_COLS = 512;
-  constexpr uint32_t SFA_COL = 2 * BN, SFB_COL = SFA_COL + 8;   // 2 x 4 and 2 x 8 columns
-  static_assert(SFB_COL + 16 <= TMEM_COLS, "scale columns");
+  constexpr uint32_t SFA_COL = TMEM_COLS - 24, SFB_COL = SFA_COL + 8;   // 2 x 4 and 2 x 8 columns
+  constexpr uint32_t ACC1_COL = SFA_COL - BN;
+  static_assert(BN - ACC1_COL <= 32, "the shared columns lie in the slices read first");
   constexpr uint16_t kPair = 0x3;
 
   extern __shared__ uint8_t smem_raw[];
@@ -198,10 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->tfull[i], 1);
-      mbar_init(&ctl->tempty[i], 2 * 4);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl->tfull[i], 1);
+    mbar_init(&ctl->tempty[0], 2 * 4);                // one arrival per epilogue warp of both CTAs
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -273,16 +291,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
-      uint32_t acc_phase = 0;
+      uint32_t free_phase = 1;   // (the first tile waits for nothing)
       bool ok = true;
       for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&ctl->tempty[acc], acc_phase ^ 1u, abort))) {
+        // the tile before has been read as far as this one's columns (and the
+        // one before that, by the same warps, as a whole)
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&ctl->tempty[0], free_phase, abort))) {
           if (lead) raise_abort(ctl, err);
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-        const uint32_t sfb0 = tmem_base + SFB_COL + (((tile / tiles_m) * BN) % 128) / 32;
+        free_phase ^= 1u;
+        const uint32_t d_tmem = tmem_base + (uint32_t)acc * ACC1_COL;
         for (int kb = 0; kb < kblocks; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[stage], phase, abort))) {
             if (lead) raise_abort(ctl, err);
@@ -308,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < kN; ++i)
                 mma_mxf4_pair(d_tmem, adesc + 2 * i, bdesc + 2 * i, idesc_mxf4(kPM, BN, 2 * (i % 2)),
-                              tmem_base + SFA_COL + 4 * (i / 2), sfb0 + 8 * (i / 2), (kb | i) != 0);
+                              tmem_base + SFA_COL + 4 * (i / 2), tmem_base + SFB_COL + 8 * (i / 2), (kb | i) != 0);
               mma_commit_pair(&ctl->empty[stage], kPair);
             }
           };
@@ -319,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (lead) mma_commit_pair(&ctl->tfull[acc], kPair);
         __syncwarp();
-        if (++acc == 2) acc = 0, acc_phase ^= 1u;
+        acc ^= 1;
       }
       if (*abort && lead) {
         mma_commit_pair(&ctl->drain, kPair);
@@ -330,8 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- epilogue (both CTAs): warps 2..5 own TMEM lane quarters (warp % 4)
     const int quarter = warp & 3;
-    const uint32_t tempty0[2] = {cluster_map(smem_u32(&ctl->tempty[0]), 0),
-                                 cluster_map(smem_u32(&ctl->tempty[1]), 0)};
+    const uint32_t free0 = cluster_map(smem_u32(&ctl->tempty[0]), 0);
     uint8_t* bufs = epi + quarter * 2 * kEpiBuf;
     int buf = 0;
     int acc = 0;
@@ -343,11 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      epilogue_rows<BN, kF32>(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN), bufs, buf, &tmC,
-                              tma_store != 0, C, M, N, m0 + quarter * 32, n0, lane);
+      epilogue_rows<BN, kF32>(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)acc * ACC1_COL, bufs, buf, &tmC,
+                              tma_store != 0, C, M, N, m0 + quarter * 32, n0, lane, acc == 0, [&] {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive_remote(free0);
+                              });
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty0[acc]);
       if (++acc == 2) acc = 0, acc_phase ^= 1u;
     }
     if (lane == 0) bulk_wait<0>();
@@ -620,9 +641,10 @@ bool map_out(CUtensorMap* map, void* y, int M, int N) {
                 128 / es, 32, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE) == cudaSuccess;
 }
 
-template <int BN, int STAGES, bool kF32>
+template <int STAGES, bool kF32>
 cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, int N, int K, int* err,
                         cudaStream_t st) {
+  constexpr int BN = 256;
   CUtensorMap ta, tb, tsa, tsb, tc = {};
   cudaError_t e;
   if ((e = map_codes(&ta, a.codes, M, K, kBM)) != cudaSuccess) return e;
@@ -631,7 +653,7 @@ cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, 
   if ((e = map_scales(&tsb, b.scales, N, K, 2)) != cudaSuccess) return e;
   const int tma_store = map_out<kF32>(&tc, y, M, N) ? 1 : 0;
   const size_t smem = 1024 + (size_t)STAGES * ((kBM + BN / 2) * kRowBytes + 6 * kSfTile) + kEpiBytes + sizeof(Ctl);
-  auto k = k_mx_pair<BN, STAGES, kF32>;
+  auto k = k_mx_pair<STAGES, kF32>;
   if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
@@ -719,7 +741,7 @@ cudaError_t gemm_t(const MxOperand& a, const MxOperand& w, void* y, int M, int N
   if (M <= 32) return launch_fewrow<32, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
   if (M <= 64) return launch_fewrow<64, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
   if (M <= 128) return launch_fewrow<128, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
-  return launch_pair<192, 6, kF32>(a, w, y, M, N, K, err, st);
+  return launch_pair<5, kF32>(a, w, y, M, N, K, err, st);
 }
 
 }  // namespace
