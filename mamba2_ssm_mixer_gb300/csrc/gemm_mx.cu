@@ -14,6 +14,8 @@
 // k_mx_fewrow (up to 128 rows): the weights are the MMA's 128-row operand, K
 //   is split over the CTAs of a cluster and the partial sums meet in
 //   distributed shared memory.
+// k_mx_stream (up to 128 rows, many columns): the same tiles, unsplit, on
+//   persistent CTAs.
 // Waits are bounded as in gemm_tc.cu.
 #include <cudaTypedefs.h>
 
@@ -42,7 +44,7 @@ struct __align__(8) Ctl {
   uint64_t full[8];
   uint64_t empty[8];
   uint64_t tfull[2];
-  uint64_t tempty[1];
+  uint64_t tempty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -90,34 +92,27 @@ struct Out<true> {
 };
 
 // One epilogue warp: 32 accumulator lanes (output rows row0 ..) over the
-// tile's BN columns from TMEM column `tcol`, output column n0, in slices from
-// the last to the first (`down`) or up; `first_read` is called when the first
-// slice has been read from TMEM.  With a store map, 128-byte slices go through
-// shared memory and TMA stores; else 32 x 32 pieces do, transposed, so that a
-// warp writes a row's consecutive elements.
-template <int BN, bool kF32, class FirstRead>
+// tile's BN columns from TMEM column `tcol`, output column n0.  With a store
+// map, 128-byte slices go through shared memory and TMA stores; else 32 x 32
+// pieces do, transposed, so that a warp writes a row's consecutive elements
+// (517 x 5003 x 1056 f32: 11.5 us, rows written by a thread each 35.5).
+template <int BN, bool kF32>
 __device__ __forceinline__ void epilogue_rows(uint32_t tcol, uint8_t* bufs, int& buf, const CUtensorMap* tmC,
                                               bool tma_store, typename Out<kF32>::T* __restrict__ C, int M, int N,
-                                              int row0, int n0, int lane, bool down, FirstRead first_read) {
+                                              int row0, int n0, int lane) {
   using O = Out<kF32>;
   if (tma_store) {
-    constexpr int kSlices = BN / O::kCols;
 #pragma unroll 1
-    for (int i = 0; i < kSlices; ++i) {
-      const int c = (down ? kSlices - 1 - i : i) * O::kCols;
+    for (int c = 0; c < BN; c += O::kCols) {
       // slices outside the output are neither staged nor stored: each staged
       // buffer is followed by its store, which the read wait below counts on
       // (warp-uniform)
-      const bool in = row0 < M && n0 + c < N;
+      if (row0 >= M || n0 + c >= N) break;
       uint32_t r[O::kCols];
-      if (in) {
 #pragma unroll
-        for (int h = 0; h < O::kCols; h += 32)
-          tmem_ld_32x32b_x32(tcol + (uint32_t)(c + h), *reinterpret_cast<uint32_t(*)[32]>(&r[h]));
-        tmem_ld_wait();
-      }
-      if (i == 0) first_read();
-      if (!in) continue;
+      for (int h = 0; h < O::kCols; h += 32)
+        tmem_ld_32x32b_x32(tcol + (uint32_t)(c + h), *reinterpret_cast<uint32_t(*)[32]>(&r[h]));
+      tmem_ld_wait();
       uint8_t* b = bufs + buf * kEpiBuf;
       if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
@@ -145,19 +140,13 @@ __device__ __forceinline__ void epilogue_rows(uint32_t tcol, uint8_t* bufs, int&
     }
     return;
   }
-  constexpr int kPieces = BN / 32;
   uint32_t* piece = reinterpret_cast<uint32_t*>(bufs);   // word (row, column) at row 32 + (column ^ row)
 #pragma unroll 1
-  for (int i = 0; i < kPieces; ++i) {
-    const int c = (down ? kPieces - 1 - i : i) * 32;
-    const bool in = row0 < M && n0 + c < N;
+  for (int c = 0; c < BN; c += 32) {
+    if (row0 >= M || n0 + c >= N) break;
     uint32_t r[32];
-    if (in) {
-      tmem_ld_32x32b_x32(tcol + (uint32_t)c, r);
-      tmem_ld_wait();
-    }
-    if (i == 0) first_read();
-    if (!in) continue;
+    tmem_ld_32x32b_x32(tcol + (uint32_t)c, r);
+    tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; ++j) piece[lane * 32 + (j ^ lane)] = r[j];
     __syncwarp();
@@ -174,20 +163,29 @@ __device__ __forceinline__ void epilogue_rows(uint32_t tcol, uint8_t* bufs, int&
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// 256 x 256 tiles on CTA pairs.  CTA r of a pair stages rows [128 r, ..) of A
-// with their scales, columns [128 r, ..) of B and the scales of all of the
-// tile's columns.  TMEM holds two accumulators and the scales in 512 columns:
-// the accumulators share 24, which the epilogue of a tile reads first; the
-// next tile's MMAs start after that.
+// 256 x BN tiles on CTA pairs.  CTA r of a pair stages rows [128 r, ..) of A
+// with their scales, columns [r BN / 2, ..) of B and the scales of all of the
+// tile's columns (two 128-row tiles of them: a tile of B starts on a multiple
+// of 64 rows, in the middle of a scale tile for odd ones, and the MMA then
+// reads from the third of the tile's columns on).  The rest as k_gemm_pair.
+// 8192 x 10304 x 2688 in 84 us (5.4 PFLOP/s).  The MMAs alone take 48 at their
+// 96 clocks, with their scales' copies and the loads 62 to 64: the loads then
+// run at 18 TB/s out of L2, and the stores take the rest in its way (to the
+// same few lines 81, none at all 67).  256 columns a tile need both
+// accumulators to share columns with each other: 88, a bubble of 2000 clocks
+// a tile; clusters of two pairs sharing A or B by multicast 85 (their loads
+// are fewer, but only 36 such clusters fit); 256-bit stores from the registers
+// instead of staged ones 85.
 // ---------------------------------------------------------------------------
-template <int STAGES, bool kF32>
+template <int BN, int STAGES, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
     k_mx_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
               const __grid_constant__ CUtensorMap tmC, int tma_store, typename Out<kF32>::T* __restrict__ C, int M, int N,
               int K, int* err) {
+  static_assert(BN % 64 == 0 && BN >= 64 && BN <= 192, "BN");
   static_assert(STAGES <= 8, "STAGES");
-  constexpr int BN = 256, kPM = 2 * kBM;
+  constexpr int kPM = 2 * kBM;
   constexpr uint32_t A_BYTES = kBM * kRowBytes;
   constexpr uint32_t B_BYTES = (BN / 2) * kRowBytes;
   constexpr uint32_t SA_BYTES = 2 * kSfTile;          // 128 rows x 256 values
@@ -195,9 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
   static_assert(STAGE_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
   constexpr uint32_t TMEM_COLS = 512;
-  constexpr uint32_t SFA_COL = TMEM_COLS - 24, SFB_COL = SFA_COL + 8;   // 2 x 4 and 2 x 8 columns
-  constexpr uint32_t ACC1_COL = SFA_COL - BN;
-  static_assert(BN - ACC1_COL <= 32, "the shared columns lie in the slices read first");
+  constexpr uint32_t SFA_COL = 2 * BN, SFB_COL = SFA_COL + 8;   // 2 x 4 and 2 x 8 columns
+  static_assert(SFB_COL + 16 <= TMEM_COLS, "scale columns");
   constexpr uint16_t kPair = 0x3;
 
   extern __shared__ uint8_t smem_raw[];
@@ -218,8 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&ctl->tfull[i], 1);
-    mbar_init(&ctl->tempty[0], 2 * 4);                // one arrival per epilogue warp of both CTAs
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->tfull[i], 1);
+      mbar_init(&ctl->tempty[i], 2 * 4);
+    }
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -291,18 +290,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
-      uint32_t free_phase = 1;   // (the first tile waits for nothing)
+      uint32_t acc_phase = 0;
       bool ok = true;
       for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-        // the tile before has been read as far as this one's columns (and the
-        // one before that, by the same warps, as a whole)
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&ctl->tempty[0], free_phase, abort))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&ctl->tempty[acc], acc_phase ^ 1u, abort))) {
           if (lead) raise_abort(ctl, err);
           break;
         }
         tc_fence_after();
-        free_phase ^= 1u;
-        const uint32_t d_tmem = tmem_base + (uint32_t)acc * ACC1_COL;
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+        const uint32_t sfb0 = tmem_base + SFB_COL + (((tile / tiles_m) * BN) % 128) / 32;
         for (int kb = 0; kb < kblocks; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[stage], phase, abort))) {
             if (lead) raise_abort(ctl, err);
@@ -328,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < kN; ++i)
                 mma_mxf4_pair(d_tmem, adesc + 2 * i, bdesc + 2 * i, idesc_mxf4(kPM, BN, 2 * (i % 2)),
-                              tmem_base + SFA_COL + 4 * (i / 2), tmem_base + SFB_COL + 8 * (i / 2), (kb | i) != 0);
+                              tmem_base + SFA_COL + 4 * (i / 2), sfb0 + 8 * (i / 2), (kb | i) != 0);
               mma_commit_pair(&ctl->empty[stage], kPair);
             }
           };
@@ -339,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (lead) mma_commit_pair(&ctl->tfull[acc], kPair);
         __syncwarp();
-        acc ^= 1;
+        if (++acc == 2) acc = 0, acc_phase ^= 1u;
       }
       if (*abort && lead) {
         mma_commit_pair(&ctl->drain, kPair);
@@ -350,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- epilogue (both CTAs): warps 2..5 own TMEM lane quarters (warp % 4)
     const int quarter = warp & 3;
-    const uint32_t free0 = cluster_map(smem_u32(&ctl->tempty[0]), 0);
+    const uint32_t tempty0[2] = {cluster_map(smem_u32(&ctl->tempty[0]), 0),
+                                 cluster_map(smem_u32(&ctl->tempty[1]), 0)};
     uint8_t* bufs = epi + quarter * 2 * kEpiBuf;
     int buf = 0;
     int acc = 0;
@@ -362,13 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      epilogue_rows<BN, kF32>(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)acc * ACC1_COL, bufs, buf, &tmC,
-                              tma_store != 0, C, M, N, m0 + quarter * 32, n0, lane, acc == 0, [&] {
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive_remote(free0);
-                              });
+      epilogue_rows<BN, kF32>(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN), bufs, buf, &tmC,
+                              tma_store != 0, C, M, N, m0 + quarter * 32, n0, lane);
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(tempty0[acc]);
       if (++acc == 2) acc = 0, acc_phase ^= 1u;
     }
     if (lane == 0) bulk_wait<0>();
@@ -588,6 +584,211 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// Few rows against many weights (a head): persistent CTAs walk the 128-row
+// blocks of W, D^T = W X^T as above with all of K, the ring running on from
+// block to block and two accumulators, so that W streams without a pause.  A
+// thread of the epilogue holds one column n of y: a warp writes 32 consecutive
+// elements of a row.
+// ---------------------------------------------------------------------------
+template <int BNT, int STAGES, bool kF32>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_mx_stream(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
+                typename Out<kF32>::T* __restrict__ y, int Mtok, int N, int K, int w_early, int* err) {
+  static_assert(BNT % 16 == 0 && BNT >= 16 && BNT <= 128 && STAGES <= 8, "BNT, STAGES");
+  using O = Out<kF32>;
+  constexpr uint32_t A_BYTES = kBM * kRowBytes;
+  constexpr uint32_t B_BYTES = BNT * kRowBytes;
+  constexpr uint32_t SF_BYTES = 2 * kSfTile;
+  constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
+  static_assert(STAGE_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
+  constexpr uint32_t ACC_COLS = BNT < 32 ? 32 : BNT;
+  constexpr uint32_t SFA_COL = 2 * ACC_COLS, SFB_COL = SFA_COL + 8;
+  constexpr uint32_t TMEM_COLS = BNT <= 32 ? 128 : (BNT <= 64 ? 256 : 512);
+  static_assert(SFB_COL + 8 <= TMEM_COLS, "scale columns");
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_align<1024>(smem_raw);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * STAGE_BYTES);
+  volatile int* abort = &ctl->abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blocks = (N + kBM - 1) / kBM;
+  const int kblocks = (K + kBK - 1) / kBK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->tfull[i], 1);
+      mbar_init(&ctl->tempty[i], 4);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+    tma_prefetch(&tmW);
+    tma_prefetch(&tmX);
+    tma_prefetch(&tmSW);
+    tma_prefetch(&tmSX);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, TMEM_COLS);
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+
+  if (warp == 0) {
+    // ---------------- TMA producer: the warp loops, one lane issues
+    const bool lead = elect_one();
+    auto load_w = [&](int stg, int kb, int n0) {
+      uint8_t* s = smem + stg * STAGE_BYTES;
+      mbar_expect_tx(&ctl->full[stg], STAGE_BYTES);
+      tma_load_2d(s, &tmW, &ctl->full[stg], kb * kRowBytes, n0);
+      tma_load_2d(s + A_BYTES + B_BYTES, &tmSW, &ctl->full[stg], kb * 256, n0 / 128);
+    };
+    auto load_x = [&](int stg, int kb) {
+      uint8_t* s = smem + stg * STAGE_BYTES;
+      tma_load_2d(s + A_BYTES, &tmX, &ctl->full[stg], kb * kRowBytes, 0);
+      tma_load_2d(s + A_BYTES + B_BYTES + SF_BYTES, &tmSX, &ctl->full[stg], kb * 256, 0);
+    };
+    // the first block's first stages of W, before the wait
+    const int npre = w_early ? (kblocks < STAGES ? kblocks : STAGES) : 0;
+    if (lead)
+      for (int i = 0; i < npre; ++i) load_w(i, i, (int)blockIdx.x * kBM);
+    __syncwarp();
+    pdl_wait();
+    pdl_trigger();
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int blk = blockIdx.x; blk < blocks && ok; blk += gridDim.x)
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->empty[stage], phase ^ 1u, abort))) {
+          if (lead) raise_abort(ctl, err);
+          ok = false;
+          break;
+        }
+        if (lead) {
+          if (issued >= npre) load_w(stage, kb, blk * kBM);
+          load_x(stage, kb);
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+      }
+    // after an abort, the copies in flight land before the CTA can exit
+    if (*abort && lead) {
+      for (int i = issued; i < npre; ++i) load_x(i, i);   // (stages whose W went out alone)
+      const int last = issued > npre ? issued : npre;
+      for (int i = last > STAGES ? last - STAGES : 0; i < last; ++i)
+        mbar_wait(&ctl->full[i % STAGES], (uint32_t)(i / STAGES) & 1u, nullptr, 100000000ull);
+    }
+    __syncwarp();
+  } else {
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 1) {
+      // ---------------- MMA issuer: the warp loops, one lane issues
+      const bool lead = elect_one();
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int blk = blockIdx.x; blk < blocks && ok; blk += gridDim.x) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->tempty[acc], acc_phase ^ 1u, abort))) {
+          if (lead) raise_abort(ctl, err);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)acc * ACC_COLS;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[stage], phase, abort))) {
+            if (lead) raise_abort(ctl, err);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + stage * STAGE_BYTES);
+          const uint32_t sf_addr = a_addr + A_BYTES + B_BYTES;
+          const uint64_t adesc = desc_kmajor_sw128(a_addr);
+          const uint64_t bdesc = desc_kmajor_sw128(a_addr + A_BYTES);
+          auto issue = [&](auto n) {
+            if (lead) {
+              constexpr int kN = decltype(n)::value;
+#pragma unroll
+              for (int t = 0; t < (kN + 1) / 2; ++t) {
+                tmem_cp_32x128b(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
+                tmem_cp_32x128b(tmem_base + SFB_COL + 4 * t, desc_scale_tile(sf_addr + SF_BYTES + t * kSfTile));
+              }
+#pragma unroll
+              for (int j = 0; j < kN; ++j)
+                mma_mxf4(d_tmem, adesc + 2 * j, bdesc + 2 * j, idesc_mxf4(kBM, BNT, 2 * (j % 2)),
+                         tmem_base + SFA_COL + 4 * (j / 2), tmem_base + SFB_COL + 4 * (j / 2), (kb | j) != 0);
+              mma_commit(&ctl->empty[stage]);
+            }
+          };
+          by_steps(K - kb * kBK, issue);
+          __syncwarp();
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
+        if (!ok) break;
+        if (lead) mma_commit(&ctl->tfull[acc]);
+        __syncwarp();
+        if (++acc == 2) acc = 0, acc_phase ^= 1u;
+      }
+      if (*abort && lead) {
+        mma_commit(&ctl->drain);
+        mbar_wait(&ctl->drain, 0, nullptr, 100000000ull);
+      }
+      __syncwarp();
+    } else {
+      // ---------------- epilogue warps 2..5
+      const int quarter = warp & 3;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      for (int blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->tfull[acc], acc_phase, abort))) {
+          if (lane == 0) raise_abort(ctl, err);
+          break;
+        }
+        tc_fence_after();
+        constexpr int kStep = BNT < 32 ? 16 : 32;
+        const int n = blk * kBM + quarter * 32 + lane;
+        const uint32_t col = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)acc * ACC_COLS;
+#pragma unroll 1
+        for (int c = 0; c < Mtok; c += kStep) {
+          uint32_t r[kStep];
+          if constexpr (kStep == 16)
+            tmem_ld_32x32b_x16(col + (uint32_t)c, r);
+          else
+            tmem_ld_32x32b_x32(col + (uint32_t)c, r);
+          tmem_ld_wait();
+          if (n < N) {
+            typename O::T* yc = y + (size_t)c * N + n;
+#pragma unroll
+            for (int j = 0; j < kStep; ++j)
+              if (c + j < Mtok) yc[(size_t)j * N] = O::one(r[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->tempty[acc]);
+        if (++acc == 2) acc = 0, acc_phase ^= 1u;
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 namespace {
@@ -641,10 +842,9 @@ bool map_out(CUtensorMap* map, void* y, int M, int N) {
                 128 / es, 32, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE) == cudaSuccess;
 }
 
-template <int STAGES, bool kF32>
+template <int BN, int STAGES, bool kF32>
 cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, int N, int K, int* err,
                         cudaStream_t st) {
-  constexpr int BN = 256;
   CUtensorMap ta, tb, tsa, tsb, tc = {};
   cudaError_t e;
   if ((e = map_codes(&ta, a.codes, M, K, kBM)) != cudaSuccess) return e;
@@ -653,7 +853,7 @@ cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, 
   if ((e = map_scales(&tsb, b.scales, N, K, 2)) != cudaSuccess) return e;
   const int tma_store = map_out<kF32>(&tc, y, M, N) ? 1 : 0;
   const size_t smem = 1024 + (size_t)STAGES * ((kBM + BN / 2) * kRowBytes + 6 * kSfTile) + kEpiBytes + sizeof(Ctl);
-  auto k = k_mx_pair<STAGES, kF32>;
+  auto k = k_mx_pair<BN, STAGES, kF32>;
   if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
@@ -703,7 +903,7 @@ int fewrow_splits(int N, int kblocks, size_t smem) {
   return s < 1 ? 1 : s;
 }
 
-template <int BNT, int STAGES, bool kF32>
+template <int BNT, int STAGES, int STREAM_STAGES, bool kF32>
 cudaError_t launch_fewrow(const MxOperand& x, const MxOperand& w, void* y, int Mtok, int N, int K, bool w_early, int* err,
                           cudaStream_t st) {
   CUtensorMap tw, tx, tsw, tsx;
@@ -712,6 +912,14 @@ cudaError_t launch_fewrow(const MxOperand& x, const MxOperand& w, void* y, int M
   if ((e = map_codes(&tx, x.codes, Mtok, K, BNT)) != cudaSuccess) return e;
   if ((e = map_scales(&tsw, w.scales, N, K, 1)) != cudaSuccess) return e;
   if ((e = map_scales(&tsx, x.scales, Mtok, K, 1)) != cudaSuccess) return e;
+  // at least a block of W for every SM: no split of K, persistent CTAs
+  if ((N + kBM - 1) / kBM >= device_sm_count()) {
+    const size_t smem = 1024 + (size_t)STREAM_STAGES * ((kBM + BNT) * kRowBytes + 4 * kSfTile) + sizeof(Ctl);
+    auto k = k_mx_stream<BNT, STREAM_STAGES, kF32>;
+    if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
+    return launch_pdl(k, dim3(device_sm_count()), dim3(kThreads), smem, st, tw, tx, tsw, tsx,
+                      static_cast<typename Out<kF32>::T*>(y), Mtok, N, K, (int)w_early, err);
+  }
   const size_t smem = 1024 + (size_t)STAGES * ((kBM + BNT) * kRowBytes + 4 * kSfTile) + sizeof(Ctl);
   auto k = k_mx_fewrow<BNT, STAGES, kF32>;
   if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
@@ -737,11 +945,11 @@ cudaError_t launch_fewrow(const MxOperand& x, const MxOperand& w, void* y, int M
 template <bool kF32>
 cudaError_t gemm_t(const MxOperand& a, const MxOperand& w, void* y, int M, int N, int K, bool w_early, int* err,
                    cudaStream_t st) {
-  if (M <= 16) return launch_fewrow<16, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
-  if (M <= 32) return launch_fewrow<32, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
-  if (M <= 64) return launch_fewrow<64, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
-  if (M <= 128) return launch_fewrow<128, 4, kF32>(a, w, y, M, N, K, w_early, err, st);
-  return launch_pair<5, kF32>(a, w, y, M, N, K, err, st);
+  if (M <= 16) return launch_fewrow<16, 4, 8, kF32>(a, w, y, M, N, K, w_early, err, st);
+  if (M <= 32) return launch_fewrow<32, 4, 8, kF32>(a, w, y, M, N, K, w_early, err, st);
+  if (M <= 64) return launch_fewrow<64, 4, 8, kF32>(a, w, y, M, N, K, w_early, err, st);
+  if (M <= 128) return launch_fewrow<128, 4, 6, kF32>(a, w, y, M, N, K, w_early, err, st);
+  return launch_pair<192, 6, kF32>(a, w, y, M, N, K, err, st);
 }
 
 }  // namespace
