@@ -8,19 +8,20 @@
 // thread run in the order issued, so one set of scale columns serves every
 // stage.
 //
-// k_mx_pair (more than 128 rows): persistent two-CTA clusters on 256 x BN
+// k_mx_pair (more than 64 rows): persistent two-CTA clusters on 256 x BN
 //   output tiles, as the e4m3 kernel of gemm_tc.cu; each CTA keeps the scales
 //   of its own 128 rows of A and of all BN columns.
-// k_mx_fewrow (up to 128 rows): the weights are the MMA's 128-row operand, K
+// k_mx_fewrow (up to 64 rows): the weights are the MMA's 128-row operand, K
 //   is split over the CTAs of a cluster and the partial sums meet in
 //   distributed shared memory.
-// k_mx_stream (up to 128 rows, many columns): the same tiles, unsplit, on
+// k_mx_stream (up to 64 rows, many columns): the same tiles, unsplit, on
 //   persistent CTAs.
 // Waits are bounded as in gemm_tc.cu.
 #include <cudaTypedefs.h>
 
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <type_traits>
 
 #include "gemm.h"
@@ -183,14 +184,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
               const __grid_constant__ CUtensorMap tmC, int tma_store, typename Out<kF32>::T* __restrict__ C, int M, int N,
               int K, int* err) {
-  static_assert(BN % 64 == 0 && BN >= 64 && BN <= 192, "BN");
   static_assert(STAGES <= 8, "STAGES");
   constexpr int kPM = 2 * kBM;
   constexpr uint32_t A_BYTES = kBM * kRowBytes;
   constexpr uint32_t B_BYTES = (BN / 2) * kRowBytes;
   constexpr uint32_t SA_BYTES = 2 * kSfTile;          // 128 rows x 256 values
-  constexpr uint32_t SB_BYTES = 4 * kSfTile;          // 256 rows x 256 values
+  constexpr int kSbTiles = BN > 128 ? 2 : 1;          // tiles of 128 rows of B that a tile's columns lie in
+  constexpr uint32_t SB_BYTES = kSbTiles * 2 * kSfTile;
   constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+  static_assert(BN == 64 || BN == 128 || BN == 192, "a tile's columns start on half a scale tile and lie in kSbTiles");
   static_assert(STAGE_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
   constexpr uint32_t TMEM_COLS = 512;
   constexpr uint32_t SFA_COL = 2 * BN, SFB_COL = SFA_COL + 8;   // 2 x 4 and 2 x 8 columns
@@ -319,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int t = 0; t < (kN + 1) / 2; ++t) {   // the scales of 128 values each
                 tmem_cp_32x128b_pair(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
                 tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t, desc_scale_tile(sf_addr + SA_BYTES + t * kSfTile));
-                tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t + 4,
-                                     desc_scale_tile(sf_addr + SA_BYTES + (2 + t) * kSfTile));
+                if constexpr (kSbTiles == 2)
+                  tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t + 4,
+                                       desc_scale_tile(sf_addr + SA_BYTES + (2 + t) * kSfTile));
               }
 #pragma unroll
               for (int i = 0; i < kN; ++i)
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_mx_fewrow(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
                 typename Out<kF32>::T* __restrict__ y, int Mtok, int N, int K, int S, int w_early, int* err) {
-  static_assert(BNT % 16 == 0 && BNT >= 16 && BNT <= 128, "BNT");
+  static_assert(BNT % 16 == 0 && BNT >= 16 && BNT <= 64, "BNT");
   using O = Out<kF32>;
   constexpr uint32_t A_BYTES = kBM * kRowBytes;
   constexpr uint32_t B_BYTES = BNT * kRowBytes;
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(STAGE_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
   constexpr uint32_t ACC_COLS = BNT < 32 ? 32 : BNT;
   constexpr uint32_t SFA_COL = ACC_COLS, SFB_COL = ACC_COLS + 8;
-  constexpr uint32_t TMEM_COLS = BNT <= 32 ? 64 : (BNT <= 64 ? 128 : 256);
+  constexpr uint32_t TMEM_COLS = BNT <= 32 ? 64 : 128;
   static_assert(SFB_COL + 8 <= TMEM_COLS, "scale columns");
   constexpr int RED_LD = BNT + 4;
   static_assert(kBM * RED_LD * 4 <= (int)(STAGES * STAGE_BYTES), "the exchange buffer fits in the ring");
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_mx_stream(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
                 typename Out<kF32>::T* __restrict__ y, int Mtok, int N, int K, int w_early, int* err) {
-  static_assert(BNT % 16 == 0 && BNT >= 16 && BNT <= 128 && STAGES <= 8, "BNT, STAGES");
+  static_assert(BNT % 16 == 0 && BNT >= 16 && BNT <= 64 && STAGES <= 8, "BNT, STAGES");
   using O = Out<kF32>;
   constexpr uint32_t A_BYTES = kBM * kRowBytes;
   constexpr uint32_t B_BYTES = BNT * kRowBytes;
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(STAGE_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
   constexpr uint32_t ACC_COLS = BNT < 32 ? 32 : BNT;
   constexpr uint32_t SFA_COL = 2 * ACC_COLS, SFB_COL = SFA_COL + 8;
-  constexpr uint32_t TMEM_COLS = BNT <= 32 ? 128 : (BNT <= 64 ? 256 : 512);
+  constexpr uint32_t TMEM_COLS = BNT <= 32 ? 128 : 256;
   static_assert(SFB_COL + 8 <= TMEM_COLS, "scale columns");
 
   extern __shared__ uint8_t smem_raw[];
@@ -842,6 +845,36 @@ bool map_out(CUtensorMap* map, void* y, int M, int N) {
                 128 / es, 32, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE) == cudaSuccess;
 }
 
+// Clusters of `size` CTAs of a kernel that fit on the device at once (found
+// once per device, kernel and size).
+int max_clusters(const void* kernel, int size, size_t smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, const void*, int>, int> known;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = known.find({dev, kernel, size});
+  if (it != known.end()) return it->second;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(size * device_sm_count()));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = device_sm_count() / size > 1 ? device_sm_count() / size : 1;
+  }
+  known[{dev, kernel, size}] = n;
+  return n;
+}
+
 template <int BN, int STAGES, bool kF32>
 cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, int N, int K, int* err,
                         cudaStream_t st) {
@@ -850,9 +883,10 @@ cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, 
   if ((e = map_codes(&ta, a.codes, M, K, kBM)) != cudaSuccess) return e;
   if ((e = map_codes(&tb, b.codes, N, K, BN / 2)) != cudaSuccess) return e;
   if ((e = map_scales(&tsa, a.scales, M, K, 1)) != cudaSuccess) return e;
-  if ((e = map_scales(&tsb, b.scales, N, K, 2)) != cudaSuccess) return e;
+  if ((e = map_scales(&tsb, b.scales, N, K, BN > 128 ? 2 : 1)) != cudaSuccess) return e;
   const int tma_store = map_out<kF32>(&tc, y, M, N) ? 1 : 0;
-  const size_t smem = 1024 + (size_t)STAGES * ((kBM + BN / 2) * kRowBytes + 6 * kSfTile) + kEpiBytes + sizeof(Ctl);
+  const size_t smem =
+      1024 + (size_t)STAGES * ((kBM + BN / 2) * kRowBytes + (BN > 128 ? 6 : 4) * kSfTile) + kEpiBytes + sizeof(Ctl);
   auto k = k_mx_pair<BN, STAGES, kF32>;
   if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -867,23 +901,7 @@ cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, 
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  // clusters that fit on the device at once, found once per device
-  static std::mutex mu;
-  static std::map<int, int> by_device;
-  int dev = 0, cap = 0;
-  cudaGetDevice(&dev);
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    auto it = by_device.find(dev);
-    if (it == by_device.end()) {
-      cfg.gridDim = dim3(2 * device_sm_count());
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&cap, k, &cfg) != cudaSuccess || cap < 1) cap = device_sm_count() / 2;
-      by_device[dev] = cap;
-    } else {
-      cap = it->second;
-    }
-  }
+  const int cap = max_clusters(reinterpret_cast<const void*>(k), 2, smem);
   const long long tiles = (long long)((M + 2 * kBM - 1) / (2 * kBM)) * ((N + BN - 1) / BN);
   cfg.gridDim = dim3(2 * (unsigned)(tiles < cap ? tiles : cap));
   cfg.numAttrs = 2;
@@ -891,15 +909,20 @@ cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, 
                             err);
 }
 
-// Cluster size of the few-row kernel: as many K splits as keep every CTA
-// resident in one wave, at most 8, at least two stages of K per CTA.
-int fewrow_splits(int N, int kblocks, size_t smem) {
-  const int nb = (N + kBM - 1) / kBM;
-  int per_sm = (int)((228 * 1024) / (smem + 1024));
-  if (per_sm < 1) per_sm = 1;
-  int s = (int)(0.9 * per_sm * device_sm_count() / nb);
+// Over how many CTAs K is split for few rows: as many as let the clusters of
+// all nb blocks of W run at once with a CTA on an SM, at most 8, with two
+// stages of K each at least.  (64 rows, 4096 -> 2688, 21 blocks: 6 splits 6.0
+// us, 8 splits 8.7, since 16 clusters of 8 fit.  2688 -> 10304, 81 blocks: 1
+// split 7.6, 2 splits 7.9.)  Up to 16 rows a second CTA fits beside the first
+// and costs nothing more: 2 splits at least (1 row, 2688 -> 10304: 4.65 us,
+// unsplit 5.35).
+int fewrow_splits(const void* kernel, size_t smem, int nb, int kblocks, int bnt) {
+  const int sms = device_sm_count();
+  int s = sms / nb;
   if (s > 8) s = 8;
   if (s > kblocks / 2) s = kblocks / 2;
+  while (s > 1 && max_clusters(kernel, s, smem) < nb) --s;
+  if (s < 2 && bnt <= 16 && nb < sms && kblocks >= 4) s = 2;
   return s < 1 ? 1 : s;
 }
 
@@ -912,20 +935,21 @@ cudaError_t launch_fewrow(const MxOperand& x, const MxOperand& w, void* y, int M
   if ((e = map_codes(&tx, x.codes, Mtok, K, BNT)) != cudaSuccess) return e;
   if ((e = map_scales(&tsw, w.scales, N, K, 1)) != cudaSuccess) return e;
   if ((e = map_scales(&tsx, x.scales, Mtok, K, 1)) != cudaSuccess) return e;
-  // at least a block of W for every SM: no split of K, persistent CTAs
-  if ((N + kBM - 1) / kBM >= device_sm_count()) {
-    const size_t smem = 1024 + (size_t)STREAM_STAGES * ((kBM + BNT) * kRowBytes + 4 * kSfTile) + sizeof(Ctl);
-    auto k = k_mx_stream<BNT, STREAM_STAGES, kF32>;
-    if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
-    return launch_pdl(k, dim3(device_sm_count()), dim3(kThreads), smem, st, tw, tx, tsw, tsx,
-                      static_cast<typename Out<kF32>::T*>(y), Mtok, N, K, (int)w_early, err);
-  }
   const size_t smem = 1024 + (size_t)STAGES * ((kBM + BNT) * kRowBytes + 4 * kSfTile) + sizeof(Ctl);
   auto k = k_mx_fewrow<BNT, STAGES, kF32>;
   if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
-  const int S = fewrow_splits(N, (K + kBK - 1) / kBK, smem);
+  const int nb = (N + kBM - 1) / kBM;
+  const int S = fewrow_splits(reinterpret_cast<const void*>(k), smem, nb, (K + kBK - 1) / kBK, BNT);
+  if (S == 1) {
+    const size_t bytes = 1024 + (size_t)STREAM_STAGES * ((kBM + BNT) * kRowBytes + 4 * kSfTile) + sizeof(Ctl);
+    auto stream = k_mx_stream<BNT, STREAM_STAGES, kF32>;
+    if ((e = ensure_smem_optin(reinterpret_cast<const void*>(stream), (int)bytes)) != cudaSuccess) return e;
+    const int sms = device_sm_count();
+    return launch_pdl(stream, dim3(nb < sms ? nb : sms), dim3(kThreads), bytes, st, tw, tx, tsw, tsx,
+                      static_cast<typename Out<kF32>::T*>(y), Mtok, N, K, (int)w_early, err);
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)S * (unsigned)((N + kBM - 1) / kBM));
+  cfg.gridDim = dim3((unsigned)(S * nb));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -948,7 +972,15 @@ cudaError_t gemm_t(const MxOperand& a, const MxOperand& w, void* y, int M, int N
   if (M <= 16) return launch_fewrow<16, 4, 8, kF32>(a, w, y, M, N, K, w_early, err, st);
   if (M <= 32) return launch_fewrow<32, 4, 8, kF32>(a, w, y, M, N, K, w_early, err, st);
   if (M <= 64) return launch_fewrow<64, 4, 8, kF32>(a, w, y, M, N, K, w_early, err, st);
-  if (M <= 128) return launch_fewrow<128, 4, 6, kF32>(a, w, y, M, N, K, w_early, err, st);
+  // (from 65 rows on, with the weights as N operand: 128 rows 2688 -> 10304 in 6.7 us, as few rows 9.1)
+  // The tile width with the shortest waves of tiles: a stage of a tile takes as
+  // long as its bytes into an SM (31, 26 and 22 KB).  517 x 5003 x 1056 f32: 81
+  // tiles of 192 columns, two waves of 76 pairs.
+  const long long tiles_m = (M + 2 * kBM - 1) / (2 * kBM), pairs = device_sm_count() / 2;
+  auto cost = [&](int bn, int kb) { return ((tiles_m * ((N + bn - 1) / bn) + pairs - 1) / pairs) * kb; };
+  const long long c192 = cost(192, 31), c128 = cost(128, 26), c64 = cost(64, 22);
+  if (c64 < c192 && c64 < c128) return launch_pair<64, 8, kF32>(a, w, y, M, N, K, err, st);
+  if (c128 < c192) return launch_pair<128, 7, kF32>(a, w, y, M, N, K, err, st);
   return launch_pair<192, 6, kF32>(a, w, y, M, N, K, err, st);
 }
 
