@@ -43,6 +43,7 @@ constexpr int kChunkBytes = kChunkVecs * 16;
 constexpr int kStages = 4;
 constexpr int kGroups = 16;                         // groups of vectors per thread
 constexpr int kLpCap = 2048;                        // survivors ranked by counting
+constexpr int kLpHits = 1024;                       // groups they may lie in
 constexpr int kStep = kLpCap / 2 / kLpThreads;      // tokens a thread takes per step of top_again
 constexpr float kL = 1.4426950408889634f;           // log2 e, rounded to f32
 constexpr double kLn2 = 0.6931471805599453094;
@@ -65,7 +66,8 @@ struct __align__(16) LpShared {
   uint32_t tau[kLpWarps];
   double z;                          // log S of the whole row (relative to its maximum m)
   float m;
-  int n_cand, abort;
+  int n_cand, n_hit, abort;
+  uint16_t hits[kLpHits];            // groups whose maximum reaches the threshold
 };
 
 // Order-preserving map of floats to unsigned (no NaN).
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
         a = join(a, b);
       }
       if (lane == 0) sh->warp[warp] = a;
-      if (tid == 0) sh->n_cand = 0;
+      if (tid == 0) sh->n_cand = 0, sh->n_hit = 0;
       if (top) {
         // this warp's ceil(k / w)-th largest thread maximum, w the warps whose
         // threads all have a vector (none: every token is a candidate)
@@ -497,7 +499,36 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
         if (lane == 0) sh->tau[warp] = warp < full ? t : 0xffffffffu;
       }
       consumers_sync();
-      if (tid < 32) {
+      // what the given token and the entropy get from a row's whole part
+      auto finish = [&](const LpPart& b, float2 again, bool odd) {
+        double z = again.x, h = again.y;
+        if (!odd && b.m > -INFINITY) {
+          // S = 2^e f with f near 1: its logarithm without a double's
+          const int e = (int)((__float_as_uint(b.s) + 0x4AFB0Du) >> 23) - 127;
+          const double ln = kLn2 * (double)e + (double)logf(__uint_as_float(__float_as_uint(b.s) - ((uint32_t)e << 23)));
+          const double shift = kLn2 * ((double)b.c + (double)b.m * kLRest);
+          const float q = b.u / b.s;
+          const double mean = (double)q + (double)(fmaf(-q, b.s, b.u) / b.s);   // u / s past f32
+          z = ln + (shift - (double)b.m);
+          h = ln + (shift - (mean + (double)b.c) * (1.0 / (double)kL));
+        }
+        sh->z = z;
+        sh->m = b.m;
+        if (!(b.m > -INFINITY)) h = 0.0;
+        if (out.entropy) out.entropy[row] = fmaxf((float)h, 0.f);
+        float lp = 0.f;
+        int rank = 0;
+        if (valid(token)) {
+          lp = masked ? -INFINITY : b.m == INFINITY ? (xt == INFINITY ? (float)-z : -INFINITY)
+                                                     : (float)((double)xt - (double)b.m - z);
+          rank = 1 + b.greater;
+        } else if (token != -1 && err) {
+          atomicOr(err, kErrToken);
+        }
+        if (tokens) out.logprobs[row] = lp, out.ranks[row] = rank;
+      };
+      auto is_odd = [](float m) { return m > -INFINITY && !(fabsf(m) <= kPlain); };
+      if (warp == 0) {
         LpPart b = sh->warp[lane & (kLpWarps - 1)];
 #pragma unroll
         for (int o = kLpWarps / 2; o; o >>= 1) {
@@ -509,7 +540,11 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
           d.greater = __shfl_xor_sync(0xffffffffu, b.greater, o);
           b = join(b, d);
         }
-        if (lane == 0) sh->part = b;
+        if (lane == 0) {
+          sh->part = b;
+          if (S == 1 && !is_odd(b.m)) finish(b, make_float2(0.f, 0.f), false);
+        }
+        __syncwarp();
       }
       // ---------------- the slice's largest tokens
       if (top) {
@@ -517,29 +552,36 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
         for (int w = 0; w < kLpWarps; ++w) tau = min(tau, sh->tau[w]);
         if (tau == 0xffffffffu || (v1 - v0) / 32 * 32 < top) tau = 0;
         tau = max(tau, kOrdNegInf + 1);
+        // the groups with a token that reaches tau, then their vectors, one per
+        // thread: read where they are found, a warp takes its groups' loads one
+        // after another (4096 x 131072: 519 us)
         const int groups = chunks ? (chunks + per_group - 1) / per_group : 0;
-        for (int g = 0; g < groups; ++g) {
-          if (sh->gmax[g][tid] < tau) continue;
-          const int last = min(chunks, (g + 1) * per_group);
-          for (int ch = g * per_group; ch < last; ++ch)
-            for (int j = 0; j < kVpt; ++j) {
-              const int v = v0 + ch * kChunkVecs + j * kLpThreads + tid;
-              if (v >= v1) continue;
-              uint4 q = __ldg(r.vec + v);
-              if (r.edge(v)) r.edges(q, v);
+        for (int g = 0; g < groups; ++g)
+          if (sh->gmax[g][tid] >= tau) {
+            const int at = atomicAdd(&sh->n_hit, 1);
+            if (at < kLpHits) sh->hits[at] = (uint16_t)(g * kLpThreads + tid);
+          }
+        consumers_sync();
+        const int hits = sh->n_hit, per_hit = per_group * kVpt;
+        if (hits <= kLpHits)
+          for (int i = tid; i < hits * per_hit; i += kLpThreads) {
+            const int hit = sh->hits[i / per_hit], j = i % per_hit;
+            const int v = v0 + (hit / kLpThreads * per_hit + j) * kLpThreads + hit % kLpThreads;
+            if (v >= v1) continue;
+            uint4 q = __ldg(r.vec + v);
+            if (r.edge(v)) r.edges(q, v);
 #pragma unroll
-              for (int e = 0; e < V::kN; ++e) {
-                const float x = V::at(q, e);
-                if (x > -INFINITY && ord32(x + 0.f) >= tau) {
-                  const int at = atomicAdd(&sh->n_cand, 1);
-                  if (at < kLpCap) sh->cand[at] = key_of(x, v * V::kN + e - r.off);
-                }
+            for (int e = 0; e < V::kN; ++e) {
+              const float x = V::at(q, e);
+              if (x > -INFINITY && ord32(x + 0.f) >= tau) {
+                const int at = atomicAdd(&sh->n_cand, 1);
+                if (at < kLpCap) sh->cand[at] = key_of(x, v * V::kN + e - r.off);
               }
             }
-        }
+          }
         consumers_sync();
         const int n = sh->n_cand;
-        if (n <= kLpCap)
+        if (hits <= kLpHits && n <= kLpCap)
           rank_candidates(sh->cand, n, top, sh->best);
         else
           top_again(sh, r.base, max(0, v0 * V::kN - r.off), min(vocab, v1 * V::kN - r.off), top);
@@ -558,7 +600,10 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
             b = join(b, p);
           }
           consumers_sync();
-          if (tid == 0) sh->part = b;
+          if (tid == 0) {
+            sh->part = b;
+            if (!is_odd(b.m)) finish(b, make_float2(0.f, 0.f), false);
+          }
           if (top) {
             for (int i = tid; i < S * top; i += kLpThreads)
               sh->cand[i] = ld_dsmem_u64(cluster_map(smem_u32(&sh->best[i % top]), (uint32_t)(i / top)));
@@ -576,46 +621,18 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
       }
       if (slice == 0) {
         const LpPart b = sh->part;
-        float2 again = make_float2(0.f, 0.f);
-        const bool odd = b.m > -INFINITY && !(fabsf(b.m) <= kPlain);
-        if (odd) again = row_again(sh, r.base, vocab, b.m);
-        if (tid == 0) {
-          double z = again.x, h = again.y;
-          if (!odd && b.m > -INFINITY) {
-            // S = 2^e f with f near 1: its logarithm without a double's
-            const int e = (int)((__float_as_uint(b.s) + 0x4AFB0Du) >> 23) - 127;
-            const double ln = kLn2 * (double)e + (double)logf(__uint_as_float(__float_as_uint(b.s) - ((uint32_t)e << 23)));
-            const double shift = kLn2 * ((double)b.c + (double)b.m * kLRest);
-            const float q = b.u / b.s;
-            const double mean = (double)q + (double)(fmaf(-q, b.s, b.u) / b.s);   // u / s past f32
-            z = ln + (shift - (double)b.m);
-            h = ln + (shift - (mean + (double)b.c) * (1.0 / (double)kL));
-          }
-          sh->z = z;
-          sh->m = b.m;
-          if (!(b.m > -INFINITY)) h = 0.0;
-          if (out.entropy) out.entropy[row] = fmaxf((float)h, 0.f);
-          float lp = 0.f;
-          int rank = 0;
-          if (valid(token)) {
-            lp = masked ? -INFINITY : b.m == INFINITY ? (xt == INFINITY ? (float)-z : -INFINITY)
-                                                       : (float)((double)xt - (double)b.m - z);
-            rank = 1 + b.greater;
-          } else if (token != -1 && err) {
-            atomicOr(err, kErrToken);
-          }
-          if (tokens) out.logprobs[row] = lp, out.ranks[row] = rank;
-        }
-        if (top) {
+        if (is_odd(b.m)) {   // (the same for all)
+          const float2 again = row_again(sh, r.base, vocab, b.m);
+          if (tid == 0) finish(b, again, true);
           consumers_sync();
-          for (int i = tid; i < top; i += kLpThreads) {
-            const uint64_t key = sh->best[i];
-            const float x = key_logit(key);
-            const bool any = key != 0 && (sh->m < INFINITY || x == INFINITY);
-            out.top_tokens[(size_t)row * top + i] = any ? key_token(key) : -1;
-            out.top_logprobs[(size_t)row * top + i] =
-                !any ? -INFINITY : sh->m == INFINITY ? (float)-sh->z : (float)((double)x - (double)sh->m - sh->z);
-          }
+        }
+        for (int i = tid; i < top; i += kLpThreads) {
+          const uint64_t key = sh->best[i];
+          const float x = key_logit(key);
+          const bool any = key != 0 && (sh->m < INFINITY || x == INFINITY);
+          out.top_tokens[(size_t)row * top + i] = any ? key_token(key) : -1;
+          out.top_logprobs[(size_t)row * top + i] =
+              !any ? -INFINITY : sh->m == INFINITY ? (float)-sh->z : (float)((double)x - (double)sh->m - sh->z);
         }
       }
       consumers_sync();   // the shared parts are free for the next row
