@@ -405,9 +405,9 @@ __device__ __forceinline__ uint64_t ld_dsmem_u64(uint32_t caddr) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(caddr) : "memory");
   return v;
 }
-__device__ __forceinline__ int ld_dsmem_s32(uint32_t caddr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t caddr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
   return v;
 }
 

@@ -6,9 +6,9 @@
 //
 // k_token_logprobs: a CTA takes a row, or a slice of one where rows are few (the
 // slices' CTAs form a cluster and the first of them joins the parts through
-// distributed shared memory).  Warp 8 streams 16 KB chunks into a ring with
-// bulk copies, across rows, so that the stream does not wait for a row's
-// end; warps 0 to 7 keep per thread
+// distributed shared memory).  One warp streams 16 KB chunks into a ring with
+// bulk copies, from row to row without a pause.  Eight warps (the readers) keep
+// per thread
 //  - sums in base 2 with a whole number c as reference: u = fma(x, L, -c) with
 //    L = f32(log2 e) is rounded once, S += 2^u, U += 2^u u.  c moves only when
 //    a chunk's maximum passes it by 16 (no rescaling in most chunks), and what
@@ -22,7 +22,8 @@
 // tau; only groups whose maximum reaches tau are read again (a few KB of the
 // row, from L2), and the survivors are ranked by counting.  Where equal values
 // leave more survivors than fit, the row is read once more against a running
-// k-th best (top_again).
+// k-th best (top_again).  Three warps (the selectors) do that and write a row's
+// results while the readers are at the next row.
 #include <cuda_bf16.h>
 
 #include "launch_util.h"
@@ -35,16 +36,16 @@ using namespace tc;
 
 namespace {
 
-constexpr int kLpWarps = 8;
-constexpr int kLpThreads = kLpWarps * 32;           // consumers
-constexpr int kVpt = 4;                             // 16-byte vectors per thread and chunk
-constexpr int kChunkVecs = kLpThreads * kVpt;
+constexpr int kReaders = 256;                       // threads of warps 0 .. 7
+constexpr int kSelectors = 96;                      // of warps 8 .. 10; warp 11 copies
+constexpr int kReadWarps = kReaders / 32, kSelWarps = kSelectors / 32;
+constexpr int kLpThreads = kReaders + kSelectors + 32;
+constexpr int kVpt = 4;                             // 16-byte vectors per reader and chunk
+constexpr int kChunkVecs = kReaders * kVpt;
 constexpr int kChunkBytes = kChunkVecs * 16;
-constexpr int kStages = 4;
-constexpr int kGroups = 16;                         // groups of vectors per thread
-constexpr int kLpCap = 2048;                        // survivors ranked by counting
-constexpr int kLpHits = 1024;                       // groups they may lie in
-constexpr int kStep = kLpCap / 2 / kLpThreads;      // tokens a thread takes per step of top_again
+constexpr int kStages = 3;                          // with two CTAs per SM
+constexpr int kGroups = 16;                         // groups of vectors per reader
+constexpr int kLpCap = 1024;                        // survivors ranked by counting
 constexpr float kL = 1.4426950408889634f;           // log2 e, rounded to f32
 constexpr double kLn2 = 0.6931471805599453094;
 constexpr double kLRest = 1.4426950408889634074 - (double)1.4426950408889634f;   // log2 e - L
@@ -53,21 +54,29 @@ constexpr float kPlain = 0x1p16f;                   // |m| up to which c is exac
 
 struct __align__(16) LpPart {
   float c, s, u, m;   // reference, sums, maximum
-  int greater;        // logits before the given token's
+  float greater;      // logits before the given token's (below 2^24: exact)
+};
+
+// What the readers hand over of a row.
+struct __align__(16) LpRow {
+  uint32_t gmax[kGroups][kReaders];
+  LpPart warp[kReadWarps];
+  uint32_t tau[kReadWarps];
 };
 
 struct __align__(16) LpShared {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kStages], empty[kStages];   // the ring's
+  uint64_t read[2], taken[2];               // the two LpRow's
   uint64_t cand[kLpCap];
-  uint64_t best[kLpMaxTop];          // the slice's largest keys, in order
-  uint32_t gmax[kGroups][kLpThreads];
-  LpPart warp[kLpWarps];
-  LpPart part;                       // the slice's
-  uint32_t tau[kLpWarps];
-  double z;                          // log S of the whole row (relative to its maximum m)
+  uint64_t best[kLpMaxTop];                 // the slice's largest keys, in order
+  LpRow row[2];
+  LpPart part;                              // the slice's
+  double z;                                 // log S of the whole row (relative to its maximum m)
   float m;
   int n_cand, n_hit, abort;
-  uint16_t hits[kLpHits];            // groups whose maximum reaches the threshold
+  float sum[kSelWarps][2];
+  uint32_t step_tau[kSelWarps];
+  uint16_t hits[kGroups * kReaders];        // groups whose maximum reaches the threshold
 };
 
 // Order-preserving map of floats to unsigned (no NaN).
@@ -124,7 +133,20 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kLpThreads) : "memory"); }
+// Barrier of the selectors; sel_any: whether `p` holds for one of them.
+__device__ __forceinline__ void sel_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSelectors) : "memory"); }
+__device__ __forceinline__ bool sel_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)p), "n"(kSelectors)
+      : "memory");
+  return r != 0;
+}
 
 // 16-byte vectors of logits.  Maxima ignore NaN.
 template <typename T>
@@ -143,21 +165,33 @@ struct Vec<uint16_t> {
     *w = e & 1 ? (*w & 0xFFFFu) | 0xFF800000u : (*w & 0xFFFF0000u) | 0xFF80u;
   }
   __device__ static float max(const uint4 (&q)[kVpt]) {
-    uint32_t m = max_bf16x2(max_bf16x2(q[0].x, q[0].y), max_bf16x2(q[0].z, q[0].w));
+    uint32_t m[kVpt];
 #pragma unroll
-    for (int j = 1; j < kVpt; ++j)
-      m = max_bf16x2(m, max_bf16x2(max_bf16x2(q[j].x, q[j].y), max_bf16x2(q[j].z, q[j].w)));
-    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
-  }
-  // logits greater than the bf16 value thr
-  __device__ static int greater(const uint4& q, float thr) {
-    const __nv_bfloat162 t = __float2bfloat162_rn(thr);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    __nv_bfloat162 n = __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]), t);
+    for (int j = 0; j < kVpt; ++j) m[j] = max_bf16x2(max_bf16x2(q[j].x, q[j].y), max_bf16x2(q[j].z, q[j].w));
 #pragma unroll
-    for (int i = 1; i < 4; ++i) n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), t));
-    return (int)(__low2float(n) + __high2float(n));
+    for (int o = kVpt / 2; o; o /= 2)
+#pragma unroll
+      for (int j = 0; j < o; ++j) m[j] = max_bf16x2(m[j], m[j + o]);
+    return fmaxf(__uint_as_float(m[0] << 16), __uint_as_float(m[0] & 0xFFFF0000u));
   }
+  // Counts of logits greater than a bf16 value, in bf16 pairs: exact up to 256
+  // a half, of which a chunk's vectors give 32.
+  struct Thr {
+    __nv_bfloat162 v;
+    __device__ explicit Thr(float thr) : v(__float2bfloat162_rn(thr)) {}
+  };
+  struct Count {
+    __nv_bfloat162 n = __float2bfloat162_rn(0.f);
+    __device__ void add(const uint4& q, const Thr& t) {
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), t.v));
+    }
+    __device__ float total() const {
+      const uint32_t b = *reinterpret_cast<const uint32_t*>(&n);
+      return __uint_as_float(b << 16) + __uint_as_float(b & 0xFFFF0000u);
+    }
+  };
   __device__ static float below(float x) { return next_below(x, 0x10000u); }
   struct Low {
     uint32_t v;
@@ -192,12 +226,18 @@ struct Vec<float> {
       m = fmaxf(m, fmaxf(fmaxf(at(q[j], 0), at(q[j], 1)), fmaxf(at(q[j], 2), at(q[j], 3))));
     return m;
   }
-  __device__ static int greater(const uint4& q, float thr) {
+  struct Thr {
+    float v;
+    __device__ explicit Thr(float thr) : v(thr) {}
+  };
+  struct Count {
     int n = 0;
+    __device__ void add(const uint4& q, const Thr& t) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) n += at(q, e) > thr;
-    return n;
-  }
+      for (int e = 0; e < 4; ++e) n += at(q, e) > t.v;
+    }
+    __device__ float total() const { return (float)n; }
+  };
   __device__ static float below(float x) { return next_below(x, 1u); }
   struct Low {
     float v;
@@ -250,74 +290,135 @@ __device__ __forceinline__ LpPart join(const LpPart& a, const LpPart& b) {
 }
 
 // The k largest of cand[0, n) by counting, in order, to best[0, k) (n < k: the
-// rest are 0).
-__device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int k, uint64_t* best) {
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
+// rest are 0).  All selectors, `sel` their index.
+__device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int k, uint64_t* best, int sel) {
+  for (int i = sel; i < n; i += kSelectors) {
     const uint64_t mine = cand[i];
     int r = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) r += cand[j] > mine;
     if (r < k) best[r] = mine;
   }
-  for (int i = n + (int)threadIdx.x; i < k; i += kLpThreads) best[i] = 0;
+  for (int i = n + sel; i < k; i += kSelectors) best[i] = 0;
 }
 
-// The k largest keys of tokens [t0, t1) of a row, by a pass in order against
-// the k-th best so far: equal logits never pass it later.  All consumers.
+// A warp's n-th largest key (n <= 32).
+__device__ __forceinline__ uint32_t nth_largest(uint32_t mine, int n, int lane) {
+  uint32_t t = 0;
+  for (int i = 0; i < n; ++i) {
+    t = __reduce_max_sync(0xffffffffu, mine);
+    if (__ffs(__ballot_sync(0xffffffffu, mine == t)) - 1 == lane) mine = 0;
+  }
+  return t;
+}
+
+// The k largest keys of vectors [v0, v1) of a row, by a pass in order against
+// the k-th best so far: once k are held, equal logits (of later tokens) never
+// pass, so that a step whose maximum is not greater is done with.  In a step
+// the selectors' maxima bound what has to be looked at, as for a row; where
+// equal values leave more than fits, its vectors are taken one by one.  All
+// selectors.
 template <typename T>
-__device__ __noinline__ void top_again(LpShared* sh, const T* base, int t0, int t1, int k) {
-  uint64_t floor = 0;
-  consumers_sync();
-  if (threadIdx.x == 0) sh->n_cand = 0;
-  consumers_sync();
+__device__ __noinline__ void top_again(LpShared* sh, const RowAt<T>& r, int v0, int v1, int k, int sel) {
+  using V = Vec<T>;
+  static_assert(kSelectors * V::kN + kLpMaxTop <= kLpCap, "a vector of each selector fits beside the best");
+  float floor = -INFINITY;
   int held = 0;
-  for (int t = t0; t < t1; t += kStep * kLpThreads) {
-    for (int e = 0; e < kStep; ++e) {
-      const int i = t + e * kLpThreads + (int)threadIdx.x;
-      if (i < t1) {
-        const float x = Vec<T>::load(base + i);
-        const uint64_t key = key_of(x, i);
-        if (x > -INFINITY && key > floor) sh->cand[atomicAdd(&sh->n_cand, 1)] = key;
-      }
-    }
-    consumers_sync();
-    const int n = sh->n_cand;
-    consumers_sync();   // all have read it before any appends again
-    if (n == held) continue;
-    rank_candidates(sh->cand, n, k, sh->best);
-    consumers_sync();
+  sel_sync();
+  if (sel == 0) sh->n_cand = 0;
+  sel_sync();
+  // what has been appended joins the best
+  auto join_best = [&](int n) {
+    rank_candidates(sh->cand, n, k, sh->best, sel);
+    sel_sync();
     held = n < k ? n : k;
-    if ((int)threadIdx.x < held) sh->cand[threadIdx.x] = sh->best[threadIdx.x];
-    if (n >= k) floor = sh->best[k - 1];
-    if (threadIdx.x == 0) sh->n_cand = held;
-    consumers_sync();
+    for (int i = sel; i < held; i += kSelectors) sh->cand[i] = sh->best[i];
+    if (n >= k) floor = key_logit(sh->best[k - 1]);
+    if (sel == 0) sh->n_cand = held;
+    sel_sync();
+  };
+  for (int v = v0; v < v1; v += kVpt * kSelectors) {
+    uint4 q[kVpt];
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j) {
+      const int at = v + j * kSelectors + sel;
+      q[j] = at < v1 ? __ldg(r.vec + at) : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+      if (at < v1 && r.edge(at)) r.edges(q[j], at);
+    }
+    const float mx = V::max(q);
+    if (!sel_any(mx > floor)) continue;
+    const uint32_t w = nth_largest(ord32(fmaxf(mx, -INFINITY) + 0.f), (k + kSelWarps - 1) / kSelWarps, sel & 31);
+    if ((sel & 31) == 0) sh->step_tau[sel >> 5] = w;
+    sel_sync();
+    uint32_t tau = sh->step_tau[0];
+    for (int i = 1; i < kSelWarps; ++i) tau = min(tau, sh->step_tau[i]);
+    auto append = [&](const uint4& vec, int j) {
+#pragma unroll
+      for (int e = 0; e < V::kN; ++e) {
+        const float x = V::at(vec, e);
+        if (x > floor && ord32(x + 0.f) >= tau) {
+          const int at = atomicAdd(&sh->n_cand, 1);
+          if (at < kLpCap) sh->cand[at] = key_of(x, (v + j * kSelectors + sel) * V::kN + e - r.off);
+        }
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < kVpt; ++j) append(q[j], j);
+    sel_sync();
+    const int n = sh->n_cand;
+    sel_sync();   // all have read it before any appends again
+    if (n <= kLpCap) {
+      if (n != held) join_best(n);
+      continue;
+    }
+    if (sel == 0) sh->n_cand = held;   // (the best are still in the first places)
+    sel_sync();
+#pragma unroll 1
+    for (int j = 0; j < kVpt; ++j) {
+      uint4 mine = q[0];   // (q[j] without an index into registers)
+#pragma unroll
+      for (int i = 1; i < kVpt; ++i)
+        if (i == j) mine = q[i];
+      append(mine, j);
+      sel_sync();
+      const int some = sh->n_cand;
+      sel_sync();
+      if (some != held) join_best(some);
+    }
   }
   if (held == 0)
-    for (int i = threadIdx.x; i < k; i += kLpThreads) sh->best[i] = 0;
-  consumers_sync();
+    for (int i = sel; i < k; i += kSelectors) sh->best[i] = 0;
+  sel_sync();
 }
 
 // log S and the entropy of a row whose maximum m is finite and large, or +inf
-// (then the +inf tokens share the probability).  All consumers.
+// (then the +inf tokens share the probability).  All selectors.
 template <typename T>
-__device__ __noinline__ float2 row_again(LpShared* sh, const T* base, int vocab, float m) {
+__device__ __noinline__ float2 row_again(LpShared* sh, const RowAt<T>& r, float m, int sel) {
+  using V = Vec<T>;
   float s = 0.f, u = 0.f;
-  for (int i = threadIdx.x; i < vocab; i += kLpThreads) {
-    const float x = Vec<T>::load(base + i);
-    if (m == INFINITY) {
-      s += x == INFINITY ? 1.f : 0.f;
-    } else {
-      const float d = x - m, p = expf(d);
-      if (p > 0.f) s += p, u = fmaf(p, d, u);
+#pragma unroll 4
+  for (int v = sel; v < r.nv; v += kSelectors) {
+    uint4 q = __ldg(r.vec + v);
+    if (r.edge(v)) r.edges(q, v);
+#pragma unroll
+    for (int e = 0; e < V::kN; ++e) {
+      const float x = V::at(q, e);
+      if (m == INFINITY) {
+        s += x == INFINITY ? 1.f : 0.f;
+      } else {
+        const float d = x - m, p = expf(d);
+        if (p > 0.f) s += p, u = fmaf(p, d, u);
+      }
     }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o), u += __shfl_xor_sync(0xffffffffu, u, o);
-  consumers_sync();
-  if ((threadIdx.x & 31) == 0) sh->warp[threadIdx.x >> 5].s = s, sh->warp[threadIdx.x >> 5].u = u;
-  consumers_sync();
+  sel_sync();
+  if ((sel & 31) == 0) sh->sum[sel >> 5][0] = s, sh->sum[sel >> 5][1] = u;
+  sel_sync();
   s = u = 0.f;
-  for (int w = 0; w < kLpWarps; ++w) s += sh->warp[w].s, u += sh->warp[w].u;
-  consumers_sync();
+  for (int w = 0; w < kSelWarps; ++w) s += sh->sum[w][0], u += sh->sum[w][1];
   const float z = logf(s);
   return make_float2(z, z - u / s);
 }
@@ -325,7 +426,7 @@ __device__ __noinline__ float2 row_again(LpShared* sh, const T* base, int vocab,
 }  // namespace
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads + 32, 2)
+__global__ void __launch_bounds__(kLpThreads, 2)
     k_token_logprobs(const T* __restrict__ logits, size_t stride, int rows, int vocab, const int32_t* __restrict__ tokens,
                      int top, LpOut out, int* err) {
   using V = Vec<T>;
@@ -341,7 +442,11 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], kLpWarps);
+      mbar_init(&sh->empty[s], kReadWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->read[i], kReadWarps);
+      mbar_init(&sh->taken[i], kSelWarps);
     }
     sh->abort = 0;
     fence_mbar_init();
@@ -354,10 +459,23 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
     v0 = (int)((long long)r.nv * slice / S);
     v1 = (int)((long long)r.nv * (slice + 1) / S);
   };
+  // a warp's wait; after one that ran out the rows left go through without data
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool there = *abort ? false : mbar_wait(bar, parity, abort);
+    if (!__all_sync(0xffffffffu, there)) {
+      *abort = 1;
+      if (err && lane == 0) atomicOr(err, kErrTimeout);
+    }
+  };
+  auto token_of = [&](int row) { return tokens && row < rows ? tokens[row] : -1; };
+  auto valid = [&](int t) { return t >= 0 && t < vocab; };
+  auto logit_of = [&](int row, int t) { return valid(t) ? V::load(logits + (size_t)row * stride + t) : 0.f; };
+  // chunks of a group of vectors
+  auto group_of = [](int chunks) { return (chunks + kGroups - 1) / kGroups; };
 
-  if (warp == kLpWarps) {
+  if (warp == kReadWarps + kSelWarps) {
     if (lane == 0) {
-      // ---------------- producer
+      // ---------------- copies
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       for (int row = row0; row < rows && !*abort; row += row_step) {
@@ -382,47 +500,42 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
           mbar_wait(&sh->full[i % kStages], (uint32_t)(i / kStages) & 1u, nullptr, 100000000ull);
     }
     __syncwarp();
-  } else {
-    // ---------------- consumers
-    int stage = 0;
+  } else if (warp < kReadWarps) {
+    // ---------------- readers
+    int stage = 0, it = 0;
     uint32_t phase = 0;
-    auto token_of = [&](int row) { return tokens && row < rows ? tokens[row] : -1; };
-    auto valid = [&](int t) { return t >= 0 && t < vocab; };
-    auto logit_of = [&](int row, int t) { return valid(t) ? V::load(logits + (size_t)row * stride + t) : 0.f; };
     int token = token_of(row0);
     float xt = logit_of(row0, token);
-    for (int row = row0; row < rows; row += row_step) {
+    for (int row = row0; row < rows; row += row_step, ++it) {
       const RowAt<T> r(logits, stride, row, vocab);
       int v0, v1;
       slice_of(r, v0, v1);
       const int chunks = (v1 - v0 + kChunkVecs - 1) / kChunkVecs;
-      const int per_group = (chunks + kGroups - 1) / kGroups;   // chunks of a group
+      const int per_group = group_of(chunks);
       const int next_token = token_of(row + row_step);
       const bool masked = !(xt > -INFINITY);                    // (NaN too)
       // before the given token's vector equal logits count as greater
       const int vt = valid(token) && !masked ? (token + r.off) / V::kN : -1;
-      const float thr = masked ? -INFINITY : xt, thr_eq = masked ? -INFINITY : V::below(xt);
+      const typename V::Thr above(masked ? -INFINITY : xt), from(masked ? -INFINITY : V::below(xt));
+      LpRow& hand = sh->row[it & 1];
+      wait(&sh->taken[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u);
 
-      float c = kNone, m = -INFINITY, gm = -INFINITY;
-      uint64_t s2 = pair(0.f, 0.f), u2 = pair(0.f, 0.f);
-      int greater = 0;
+      float c = kNone, m = -INFINITY, gm = -INFINITY, greater = 0.f;
+      uint64_t s2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)}, u2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+      int group = 0, left = per_group;
       for (int ch = 0; ch < chunks; ++ch) {
-        const bool there = *abort ? false : mbar_wait(&sh->full[stage], phase, abort);
-        if (!__all_sync(0xffffffffu, there)) {   // (the rows left go through without data)
-          *abort = 1;
-          if (err && lane == 0) atomicOr(err, kErrTimeout);
-        }
-        const int va = v0 + ch * kChunkVecs + tid;
+        wait(&sh->full[stage], phase);
+        const int vc = v0 + ch * kChunkVecs;
         const uint4* p = reinterpret_cast<const uint4*>(ring + stage * kChunkBytes) + tid;
         uint4 q[kVpt];
         if (ch > 0 && ch + 1 < chunks) {
 #pragma unroll
-          for (int j = 0; j < kVpt; ++j) q[j] = p[j * kLpThreads];
+          for (int j = 0; j < kVpt; ++j) q[j] = p[j * kReaders];
         } else {
 #pragma unroll
           for (int j = 0; j < kVpt; ++j) {
-            const int v = va + j * kLpThreads;
-            q[j] = v < v1 ? p[j * kLpThreads] : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+            const int v = vc + j * kReaders + tid;
+            q[j] = v < v1 ? p[j * kReaders] : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
             if (v < v1 && r.edge(v)) r.edges(q[j], v);
           }
         }
@@ -432,46 +545,57 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
 
         const float mx = V::max(q);
         gm = fmaxf(gm, mx);
-        if (top && ((ch + 1) % per_group == 0 || ch + 1 == chunks)) {
-          sh->gmax[ch / per_group][tid] = ord32(gm + 0.f);
+        if (--left == 0 || ch + 1 == chunks) {
+          if (top) hand.gmax[group][tid] = ord32(gm + 0.f);
           m = fmaxf(m, gm);
           gm = -INFINITY;
+          ++group;
+          left = per_group;
         }
         if (mx * kL > c + 16.f) {
           const float cn = rintf(mx * kL), d = fmaxf(c - cn, -1e30f), f = exp2_fast(d);
-          u2 = fma_pair(s2, pair(d, d), u2);
-          s2 = fma_pair(s2, pair(f, f), pair(0.f, 0.f));
-          u2 = fma_pair(u2, pair(f, f), pair(0.f, 0.f));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            u2[i] = fma_pair(s2[i], pair(d, d), u2[i]);
+            s2[i] = fma_pair(s2[i], pair(f, f), pair(0.f, 0.f));
+            u2[i] = fma_pair(u2[i], pair(f, f), pair(0.f, 0.f));
+          }
           c = cn;
         }
         if (c > kNone) {
           // masked logits and NaN take a value whose exponential is 0 (-160 in base 2 at least, finite)
-          float low = (c - 160.f) / kL;
-          low -= fabsf(low) * 0.01f;
-          const typename V::Low lo(low);
+          const float low = (c - 160.f) * 0.6931472f;
+          const typename V::Low lo(fmaf(fabsf(low), -0.01f, low));
           const uint64_t cc = pair(-c, -c);
 #pragma unroll
-          for (int j = 0; j < kVpt; ++j) V::sums(q[j], lo, cc, s2, u2);
+          for (int j = 0; j < kVpt; ++j) V::sums(q[j], lo, cc, s2[j & 1], u2[j & 1]);
         }
+        typename V::Count count;
+        if (vt < vc || vt >= vc + kChunkVecs) {   // (the same for all)
+          const typename V::Thr t = vt < vc ? above : from;
 #pragma unroll
-        for (int j = 0; j < kVpt; ++j) {
-          const int v = va + j * kLpThreads;
-          if (v != vt) {
-            greater += V::greater(q[j], v < vt ? thr_eq : thr);
-          } else {
+          for (int j = 0; j < kVpt; ++j) count.add(q[j], t);
+        } else {
 #pragma unroll
-            for (int e = 0; e < V::kN; ++e) {
-              const float x = V::at(q[j], e);
-              greater += x > xt || (x == xt && v * V::kN + e - r.off < token);
+          for (int j = 0; j < kVpt; ++j) {
+            const int v = vc + j * kReaders + tid;
+            if (v != vt) {
+              count.add(q[j], v < vt ? from : above);
+            } else {
+#pragma unroll
+              for (int e = 0; e < V::kN; ++e) {
+                const float x = V::at(q[j], e);
+                greater += x > xt || (x == xt && v * V::kN + e - r.off < token) ? 1.f : 0.f;
+              }
             }
           }
         }
+        greater += count.total();
       }
       const float next_xt = logit_of(row + row_step, next_token);
-      m = fmaxf(m, gm);
 
-      // ---------------- the slice's sums
-      const float2 ss = unpair(s2), uu = unpair(u2);
+      // ---------------- the warp's part to the selectors
+      const float2 ss = unpair(add_pair(s2[0], s2[1])), uu = unpair(add_pair(u2[0], u2[1]));
       LpPart a{c, ss.x + ss.y, uu.x + uu.y, m, greater};
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
@@ -483,22 +607,38 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
         b.greater = __shfl_xor_sync(0xffffffffu, a.greater, o);
         a = join(a, b);
       }
-      if (lane == 0) sh->warp[warp] = a;
-      if (tid == 0) sh->n_cand = 0, sh->n_hit = 0;
+      if (lane == 0) hand.warp[warp] = a;
       if (top) {
         // this warp's ceil(k / w)-th largest thread maximum, w the warps whose
-        // threads all have a vector (none: every token is a candidate)
-        const int full = min(kLpWarps, (v1 - v0) / 32);
+        // threads all have a vector (none, or too few threads: every token is a
+        // candidate)
+        const int full = min(kReadWarps, (v1 - v0) / 32);
         const int need = full ? (top + full - 1) / full : 33;
-        uint32_t mine = ord32(m + 0.f), t = 0;
-        if (need <= 32)
-          for (int i = 0; i < need; ++i) {
-            t = __reduce_max_sync(0xffffffffu, mine);
-            if (__ffs(__ballot_sync(0xffffffffu, mine == t)) - 1 == lane) mine = 0;
-          }
-        if (lane == 0) sh->tau[warp] = warp < full ? t : 0xffffffffu;
+        const uint32_t t = need <= 32 ? nth_largest(ord32(m + 0.f), need, lane) : 0u;
+        if (lane == 0) hand.tau[warp] = warp < full ? t : full ? 0xffffffffu : 0u;
       }
-      consumers_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->read[it & 1]);
+      token = next_token;
+      xt = next_xt;
+    }
+  } else {
+    // ---------------- selectors
+    const int sel = tid - kReaders;
+    int it = 0;
+    for (int row = row0; row < rows; row += row_step, ++it) {
+      const RowAt<T> r(logits, stride, row, vocab);
+      int v0, v1;
+      slice_of(r, v0, v1);
+      const int chunks = (v1 - v0 + kChunkVecs - 1) / kChunkVecs;
+      const int per_group = group_of(chunks);
+      const int token = token_of(row);
+      const float xt = logit_of(row, token);
+      if (sel == 0) sh->n_cand = 0, sh->n_hit = 0;
+      sel_sync();
+      wait(&sh->read[it & 1], (uint32_t)(it >> 1) & 1u);
+      const LpRow& hand = sh->row[it & 1];
+
       // what the given token and the entropy get from a row's whole part
       auto finish = [&](const LpPart& b, float2 again, bool odd) {
         double z = again.x, h = again.y;
@@ -516,117 +656,125 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
         sh->m = b.m;
         if (!(b.m > -INFINITY)) h = 0.0;
         if (out.entropy) out.entropy[row] = fmaxf((float)h, 0.f);
+        const bool masked = !(xt > -INFINITY);
         float lp = 0.f;
         int rank = 0;
         if (valid(token)) {
           lp = masked ? -INFINITY : b.m == INFINITY ? (xt == INFINITY ? (float)-z : -INFINITY)
                                                      : (float)((double)xt - (double)b.m - z);
-          rank = 1 + b.greater;
+          rank = 1 + (int)b.greater;
         } else if (token != -1 && err) {
           atomicOr(err, kErrToken);
         }
         if (tokens) out.logprobs[row] = lp, out.ranks[row] = rank;
       };
       auto is_odd = [](float m) { return m > -INFINITY && !(fabsf(m) <= kPlain); };
-      if (warp == 0) {
-        LpPart b = sh->warp[lane & (kLpWarps - 1)];
-#pragma unroll
-        for (int o = kLpWarps / 2; o; o >>= 1) {
-          LpPart d;
-          d.c = __shfl_xor_sync(0xffffffffu, b.c, o);
-          d.s = __shfl_xor_sync(0xffffffffu, b.s, o);
-          d.u = __shfl_xor_sync(0xffffffffu, b.u, o);
-          d.m = __shfl_xor_sync(0xffffffffu, b.m, o);
-          d.greater = __shfl_xor_sync(0xffffffffu, b.greater, o);
-          b = join(b, d);
-        }
-        if (lane == 0) {
-          sh->part = b;
-          if (S == 1 && !is_odd(b.m)) finish(b, make_float2(0.f, 0.f), false);
-        }
-        __syncwarp();
+      if (sel == 0) {
+        LpPart b = hand.warp[0];
+        for (int w = 1; w < kReadWarps; ++w) b = join(b, hand.warp[w]);
+        sh->part = b;
+        if (S == 1 && !is_odd(b.m)) finish(b, make_float2(0.f, 0.f), false);
       }
+      __syncwarp();
       // ---------------- the slice's largest tokens
       if (top) {
         uint32_t tau = 0xffffffffu;
-        for (int w = 0; w < kLpWarps; ++w) tau = min(tau, sh->tau[w]);
-        if (tau == 0xffffffffu || (v1 - v0) / 32 * 32 < top) tau = 0;
+        for (int w = 0; w < kReadWarps; ++w) tau = min(tau, hand.tau[w]);
         tau = max(tau, kOrdNegInf + 1);
         // the groups with a token that reaches tau, then their vectors, one per
         // thread: read where they are found, a warp takes its groups' loads one
-        // after another (4096 x 131072: 519 us)
+        // after another
         const int groups = chunks ? (chunks + per_group - 1) / per_group : 0;
-        for (int g = 0; g < groups; ++g)
-          if (sh->gmax[g][tid] >= tau) {
-            const int at = atomicAdd(&sh->n_hit, 1);
-            if (at < kLpHits) sh->hits[at] = (uint16_t)(g * kLpThreads + tid);
-          }
-        consumers_sync();
-        const int hits = sh->n_hit, per_hit = per_group * kVpt;
-        if (hits <= kLpHits)
-          for (int i = tid; i < hits * per_hit; i += kLpThreads) {
-            const int hit = sh->hits[i / per_hit], j = i % per_hit;
-            const int v = v0 + (hit / kLpThreads * per_hit + j) * kLpThreads + hit % kLpThreads;
-            if (v >= v1) continue;
-            uint4 q = __ldg(r.vec + v);
-            if (r.edge(v)) r.edges(q, v);
+        const uint4* gmax = reinterpret_cast<const uint4*>(hand.gmax);
+        for (int i = sel; i < groups * (kReaders / 4); i += kSelectors) {
+          const uint4 g = gmax[i];
+          const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-            for (int e = 0; e < V::kN; ++e) {
-              const float x = V::at(q, e);
-              if (x > -INFINITY && ord32(x + 0.f) >= tau) {
-                const int at = atomicAdd(&sh->n_cand, 1);
-                if (at < kLpCap) sh->cand[at] = key_of(x, v * V::kN + e - r.off);
-              }
+          for (int e = 0; e < 4; ++e)
+            if (w[e] >= tau) sh->hits[atomicAdd(&sh->n_hit, 1)] = (uint16_t)(4 * i + e);
+        }
+        sel_sync();
+        const int hits = sh->n_hit, per_hit = per_group * kVpt;
+        for (int i = sel; i < hits * per_hit; i += kSelectors) {
+          const int hit = sh->hits[i / per_hit], j = i % per_hit;
+          const int v = v0 + (hit / kReaders * per_hit + j) * kReaders + hit % kReaders;
+          if (v >= v1) continue;
+          uint4 q = __ldg(r.vec + v);
+          if (r.edge(v)) r.edges(q, v);
+#pragma unroll
+          for (int e = 0; e < V::kN; ++e) {
+            const float x = V::at(q, e);
+            if (x > -INFINITY && ord32(x + 0.f) >= tau) {
+              const int at = atomicAdd(&sh->n_cand, 1);
+              if (at < kLpCap) sh->cand[at] = key_of(x, v * V::kN + e - r.off);
             }
           }
-        consumers_sync();
-        const int n = sh->n_cand;
-        if (hits <= kLpHits && n <= kLpCap)
-          rank_candidates(sh->cand, n, top, sh->best);
-        else
-          top_again(sh, r.base, max(0, v0 * V::kN - r.off), min(vocab, v1 * V::kN - r.off), top);
+        }
       }
-      consumers_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->taken[it & 1]);   // (the parts and tau are read; the hits are this side's)
+      sel_sync();
+      if (top) {
+        const int n = sh->n_cand;
+        if (n <= kLpCap)
+          rank_candidates(sh->cand, n, top, sh->best, sel);
+        else
+          top_again<T>(sh, r, v0, v1, top, sel);
+        sel_sync();
+      }
 
       // ---------------- the row's results, from its slices' parts
       if (S > 1) {
-        cluster_sync();   // (the producer's warp arrives too, below)
+        cluster_sync();   // (the other warps arrive too, below)
         if (slice == 0) {
           LpPart b = sh->part;
           for (int o = 1; o < S; ++o) {
             const uint32_t at = cluster_map(smem_u32(&sh->part), (uint32_t)o);
             const float4 d = ld_dsmem_f32x4(at);
-            LpPart p{d.x, d.y, d.z, d.w, ld_dsmem_s32(at + 16)};
+            const LpPart p{d.x, d.y, d.z, d.w, ld_dsmem_f32(at + 16)};
             b = join(b, p);
           }
-          consumers_sync();
-          if (tid == 0) {
+          sel_sync();
+          if (sel == 0) {
             sh->part = b;
             if (!is_odd(b.m)) finish(b, make_float2(0.f, 0.f), false);
           }
           if (top) {
-            for (int i = tid; i < S * top; i += kLpThreads)
+            for (int i = sel; i < S * top; i += kSelectors)
               sh->cand[i] = ld_dsmem_u64(cluster_map(smem_u32(&sh->best[i % top]), (uint32_t)(i / top)));
-            consumers_sync();
-            // (empty places hold 0 and may be many: they stay behind every key)
-            for (int i = tid; i < S * top; i += kLpThreads) {
+            sel_sync();
+            // a key's place: its own slice's keys before it, and those of the
+            // other slices that are greater (each list is in order, empty
+            // places hold 0)
+            for (int i = sel; i < top; i += kSelectors) sh->best[i] = 0;
+            sel_sync();
+            for (int i = sel; i < S * top; i += kSelectors) {
               const uint64_t mine = sh->cand[i];
-              int n = 0;
-              for (int j = 0; j < S * top; ++j) n += sh->cand[j] > mine || (sh->cand[j] == mine && j < i);
+              if (mine == 0) continue;
+              int n = i % top;
+              for (int o = 0; o < S && n < top; ++o) {
+                if (o == i / top) continue;
+                int lo = 0, hi = top;   // the first that is not greater lies in [lo, hi]
+                while (lo < hi) {
+                  const int mid = (lo + hi) / 2;
+                  if (sh->cand[o * top + mid] > mine) lo = mid + 1; else hi = mid;
+                }
+                n += lo;
+              }
               if (n < top) sh->best[n] = mine;
             }
           }
-          consumers_sync();
+          sel_sync();
         }
       }
       if (slice == 0) {
         const LpPart b = sh->part;
         if (is_odd(b.m)) {   // (the same for all)
-          const float2 again = row_again(sh, r.base, vocab, b.m);
-          if (tid == 0) finish(b, again, true);
-          consumers_sync();
+          const float2 again = row_again<T>(sh, r, b.m, sel);
+          if (sel == 0) finish(b, again, true);
+          sel_sync();
         }
-        for (int i = tid; i < top; i += kLpThreads) {
+        for (int i = sel; i < top; i += kSelectors) {
           const uint64_t key = sh->best[i];
           const float x = key_logit(key);
           const bool any = key != 0 && (sh->m < INFINITY || x == INFINITY);
@@ -635,13 +783,11 @@ __global__ void __launch_bounds__(kLpThreads + 32, 2)
               !any ? -INFINITY : sh->m == INFINITY ? (float)-sh->z : (float)((double)x - (double)sh->m - sh->z);
         }
       }
-      consumers_sync();   // the shared parts are free for the next row
-      token = next_token;
-      xt = next_xt;
+      sel_sync();   // the shared results are free for the next row
     }
   }
   if (S > 1) {
-    if (warp == kLpWarps) cluster_sync();   // (the consumers' first one)
+    if (warp < kReadWarps || warp == kReadWarps + kSelWarps) cluster_sync();   // (the selectors' first one)
     cluster_sync();                         // no CTA leaves while another reads its parts
   }
 }
@@ -662,7 +808,7 @@ static cudaError_t launch_t(const T* logits, size_t stride, int rows, int vocab,
   while (S < 8 && (long long)2 * S * rows <= resident && 2 * S <= chunks) S *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(S, S > 1 ? rows : (rows < resident ? rows : resident));
-  cfg.blockDim = dim3(kLpThreads + 32);
+  cfg.blockDim = dim3(kLpThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
