@@ -3,26 +3,26 @@
 //   m = max x, S = sum exp(x - m), E = sum exp(x - m) x / S
 //   logprob(t) = (x_t - m) - log S, entropy = m + log S - E,
 //   rank(t) = 1 + the tokens before t in the order (greater logit, lower token).
-//
-// k_token_logprobs: a CTA takes a row, or a slice of one where rows are few (the
-// slices' CTAs form a cluster and the first of them joins the parts through
-// distributed shared memory).  One warp streams 16 KB chunks into a ring with
-// bulk copies, from row to row without a pause.  Eight warps (the readers) keep
-// per thread
+// Threads keep
 //  - sums in base 2 with a whole number c as reference: u = fma(x, L, -c) with
-//    L = f32(log2 e) is rounded once, S += 2^u, U += 2^u u.  c moves only when
-//    a chunk's maximum passes it by 16 (no rescaling in most chunks), and what
-//    L lacks of log2 e is put back at the end: lse = ln 2 (c + m (log2 e - L)) +
-//    log S.  Rows whose maximum is beyond +-2^16 (or +inf) are summed again
-//    as x - m (row_again);
+//    L = f32(log2 e) is rounded once, S += 2^u, U += 2^u u.  What L lacks of
+//    log2 e is put back at the end: lse = ln 2 (c + m (log2 e - L)) + log S.
+//    Rows whose maximum is beyond +-2^16 (or +inf) are summed again as x - m
+//    (row_again);
 //  - the number of logits greater than the given token's;
-//  - the maxima of up to kGroups groups of its vectors.
-// The k largest need no sort and no list while streaming: if each of w warps has
+//  - maxima of groups of their vectors.
+// The k largest need no sort and no list on the way: if each of w warps has
 // ceil(k / w) threads whose maximum is at least tau, at least k tokens are >=
-// tau; only groups whose maximum reaches tau are read again (a few KB of the
-// row, from L2), and the survivors are ranked by counting.  Where equal values
-// leave more survivors than fit, the row is read once more against a running
-// k-th best (top_again).  Three warps (the selectors) do that and write a row's
+// tau; only groups whose maximum reaches tau are looked at again, and the
+// survivors are ranked by counting.  Where equal values leave more survivors
+// than fit, the row is read once more against a running k-th best (top_again).
+//
+// k_lp_held (few rows, or short ones): a CTA, or each of a cluster's, holds its
+// slice of one row in registers; the first CTA joins the slices' parts through
+// distributed shared memory.  A row's latency is what counts.
+// k_lp_stream (many long rows): two persistent CTAs per SM.  One warp copies
+// chunks into a ring, from row to row without a pause; eight warps (the readers)
+// sum; three warps (the selectors) find a row's largest tokens and write its
 // results while the readers are at the next row.
 #include <cuda_bf16.h>
 
@@ -36,47 +36,29 @@ using namespace tc;
 
 namespace {
 
-constexpr int kReaders = 256;                       // threads of warps 0 .. 7
+constexpr int kReaders = 256;                       // threads of k_lp_stream's warps 0 .. 7
 constexpr int kSelectors = 96;                      // of warps 8 .. 10; warp 11 copies
 constexpr int kReadWarps = kReaders / 32, kSelWarps = kSelectors / 32;
-constexpr int kLpThreads = kReaders + kSelectors + 32;
-constexpr int kVpt = 4;                             // 16-byte vectors per reader and chunk
+constexpr int kStreamThreads = kReaders + kSelectors + 32;
+constexpr int kVpt = 4;                             // 16-byte vectors per reader and chunk, at most
 constexpr int kChunkVecs = kReaders * kVpt;
 constexpr int kChunkBytes = kChunkVecs * 16;
-constexpr int kStages = 3;                          // with two CTAs per SM
+constexpr int kStages = 3;
 constexpr int kGroups = 16;                         // groups of vectors per reader
-constexpr int kLpCap = 1024;                        // survivors ranked by counting
+constexpr int kHeldThreads = 256;                   // of k_lp_held
+constexpr int kHeldWarps = kHeldThreads / 32;
+constexpr int kHeldVecs = 8;                        // vectors per thread, at most
+constexpr int kLpMaxSlices = 8;
 constexpr float kL = 1.4426950408889634f;           // log2 e, rounded to f32
-constexpr double kLn2 = 0.6931471805599453094;
-constexpr double kLRest = 1.4426950408889634074 - (double)1.4426950408889634f;   // log2 e - L
+constexpr float kLn2 = 0.693147180559945309f, kLn2Lo = (float)(0.693147180559945309 - (double)kLn2);   // ln 2
+constexpr double kLRest = 1.4426950408889634074 - (double)1.4426950408889634f;                         // log2 e - L
+constexpr double kInvL = 1.0 / (double)1.4426950408889634f;
 constexpr float kNone = -0x1p18f;                   // reference c before any unmasked logit
 constexpr float kPlain = 0x1p16f;                   // |m| up to which c is exact enough
 
 struct __align__(16) LpPart {
   float c, s, u, m;   // reference, sums, maximum
-  float greater;      // logits before the given token's (below 2^24: exact)
-};
-
-// What the readers hand over of a row.
-struct __align__(16) LpRow {
-  uint32_t gmax[kGroups][kReaders];
-  LpPart warp[kReadWarps];
-  uint32_t tau[kReadWarps];
-};
-
-struct __align__(16) LpShared {
-  uint64_t full[kStages], empty[kStages];   // the ring's
-  uint64_t read[2], taken[2];               // the two LpRow's
-  uint64_t cand[kLpCap];
-  uint64_t best[kLpMaxTop];                 // the slice's largest keys, in order
-  LpRow row[2];
-  LpPart part;                              // the slice's
-  double z;                                 // log S of the whole row (relative to its maximum m)
-  float m;
-  int n_cand, n_hit, abort;
-  float sum[kSelWarps][2];
-  uint32_t step_tau[kSelWarps];
-  uint16_t hits[kGroups * kReaders];        // groups whose maximum reaches the threshold
+  int greater;        // logits before the given token's
 };
 
 // Order-preserving map of floats to unsigned (no NaN).
@@ -133,21 +115,6 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Barrier of the selectors; sel_any: whether `p` holds for one of them.
-__device__ __forceinline__ void sel_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSelectors) : "memory"); }
-__device__ __forceinline__ bool sel_any(bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.red.or.pred q, 1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(r)
-      : "r"((uint32_t)p), "n"(kSelectors)
-      : "memory");
-  return r != 0;
-}
-
 // 16-byte vectors of logits.  Maxima ignore NaN.
 template <typename T>
 struct Vec;
@@ -164,32 +131,29 @@ struct Vec<uint16_t> {
     uint32_t* w = reinterpret_cast<uint32_t*>(&q) + e / 2;
     *w = e & 1 ? (*w & 0xFFFFu) | 0xFF800000u : (*w & 0xFFFF0000u) | 0xFF80u;
   }
-  __device__ static float max(const uint4 (&q)[kVpt]) {
-    uint32_t m[kVpt];
-#pragma unroll
-    for (int j = 0; j < kVpt; ++j) m[j] = max_bf16x2(max_bf16x2(q[j].x, q[j].y), max_bf16x2(q[j].z, q[j].w));
-#pragma unroll
-    for (int o = kVpt / 2; o; o /= 2)
-#pragma unroll
-      for (int j = 0; j < o; ++j) m[j] = max_bf16x2(m[j], m[j + o]);
-    return fmaxf(__uint_as_float(m[0] << 16), __uint_as_float(m[0] & 0xFFFF0000u));
+  using Max = uint32_t;   // of the even and of the odd elements
+  __device__ static Max max(const uint4& q) { return max_bf16x2(max_bf16x2(q.x, q.y), max_bf16x2(q.z, q.w)); }
+  __device__ static Max max(Max a, Max b) { return max_bf16x2(a, b); }
+  __device__ static float whole(Max m) {
+    return fmaxf(fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)), -INFINITY);   // (NaN: -inf)
   }
-  // Counts of logits greater than a bf16 value, in bf16 pairs: exact up to 256
-  // a half, of which a chunk's vectors give 32.
+  // Counts of logits greater than a bf16 value: the comparisons' masks (0xFFFF
+  // a half) are summed as whole words, two per addition.  H and L of them:
+  // sum = 65536 (L - H) - L modulo 2^32.
   struct Thr {
     __nv_bfloat162 v;
     __device__ explicit Thr(float thr) : v(__float2bfloat162_rn(thr)) {}
   };
   struct Count {
-    __nv_bfloat162 n = __float2bfloat162_rn(0.f);
+    uint32_t n = 0;
     __device__ void add(const uint4& q, const Thr& t) {
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), t.v));
+      for (int i = 0; i < 4; ++i) n += __hgt2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), t.v);
     }
-    __device__ float total() const {
-      const uint32_t b = *reinterpret_cast<const uint32_t*>(&n);
-      return __uint_as_float(b << 16) + __uint_as_float(b & 0xFFFF0000u);
+    __device__ int total() const {
+      const uint32_t l = (0u - n) & 0xFFFFu, d = (n + l) >> 16;   // d = L - H modulo 2^16
+      return (int)(2 * l - (uint32_t)(int)(int16_t)d);
     }
   };
   __device__ static float below(float x) { return next_below(x, 0x10000u); }
@@ -197,11 +161,12 @@ struct Vec<uint16_t> {
     uint32_t v;
     __device__ explicit Low(float low) { v = pack_bf16x2(low, low); }
   };
+  template <bool kLow>
   __device__ static void sums(const uint4& q, const Low& low, uint64_t cc, uint64_t& s, uint64_t& u) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t x = max_bf16x2(w[i], low.v);
+      const uint32_t x = kLow ? max_bf16x2(w[i], low.v) : w[i];
       const uint64_t d = fma_pair(pair(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u)), pair(kL, kL), cc);
       const float2 t = unpair(d);
       const uint64_t p = pair(exp2_fast(t.x), exp2_fast(t.y));
@@ -219,13 +184,10 @@ struct Vec<float> {
     return __uint_as_float(e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w);
   }
   __device__ static void mask(uint4& q, int e) { reinterpret_cast<uint32_t*>(&q)[e] = kNegInf; }
-  __device__ static float max(const uint4 (&q)[kVpt]) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kVpt; ++j)
-      m = fmaxf(m, fmaxf(fmaxf(at(q[j], 0), at(q[j], 1)), fmaxf(at(q[j], 2), at(q[j], 3))));
-    return m;
-  }
+  using Max = float;
+  __device__ static Max max(const uint4& q) { return fmaxf(fmaxf(at(q, 0), at(q, 1)), fmaxf(at(q, 2), at(q, 3))); }
+  __device__ static Max max(Max a, Max b) { return fmaxf(a, b); }
+  __device__ static float whole(Max m) { return fmaxf(m, -INFINITY); }
   struct Thr {
     float v;
     __device__ explicit Thr(float thr) : v(thr) {}
@@ -236,17 +198,19 @@ struct Vec<float> {
 #pragma unroll
       for (int e = 0; e < 4; ++e) n += at(q, e) > t.v;
     }
-    __device__ float total() const { return (float)n; }
+    __device__ int total() const { return n; }
   };
   __device__ static float below(float x) { return next_below(x, 1u); }
   struct Low {
     float v;
     __device__ explicit Low(float low) : v(low) {}
   };
+  template <bool kLow>
   __device__ static void sums(const uint4& q, const Low& low, uint64_t cc, uint64_t& s, uint64_t& u) {
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-      const uint64_t d = fma_pair(pair(fmaxf(at(q, i), low.v), fmaxf(at(q, i + 1), low.v)), pair(kL, kL), cc);
+      const float a = at(q, i), b = at(q, i + 1);
+      const uint64_t d = fma_pair(kLow ? pair(fmaxf(a, low.v), fmaxf(b, low.v)) : pair(a, b), pair(kL, kL), cc);
       const float2 t = unpair(d);
       const uint64_t p = pair(exp2_fast(t.x), exp2_fast(t.y));
       s = add_pair(s, p);
@@ -254,6 +218,20 @@ struct Vec<float> {
     }
   }
 };
+
+// Maximum of a thread's vectors.
+template <typename T, int N>
+__device__ __forceinline__ float max_of(const uint4 (&q)[N]) {
+  using V = Vec<T>;
+  typename V::Max m[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) m[j] = V::max(q[j]);
+#pragma unroll
+  for (int o = N / 2; o; o /= 2)
+#pragma unroll
+    for (int j = 0; j < o; ++j) m[j] = V::max(m[j], m[j + o]);
+  return V::whole(m[0]);
+}
 
 // Where a row's vectors lie: token i is element (i + off) % kN of vector
 // (i + off) / kN, counted from the 16-byte boundary at or below the row.
@@ -288,19 +266,21 @@ __device__ __forceinline__ LpPart join(const LpPart& a, const LpPart& b) {
   return {c, a.s * fa + b.s * fb, fmaf(a.s, da, a.u) * fa + fmaf(b.s, db, b.u) * fb, fmaxf(a.m, b.m),
           a.greater + b.greater};
 }
-
-// The k largest of cand[0, n) by counting, in order, to best[0, k) (n < k: the
-// rest are 0).  All selectors, `sel` their index.
-__device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int k, uint64_t* best, int sel) {
-  for (int i = sel; i < n; i += kSelectors) {
-    const uint64_t mine = cand[i];
-    int r = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) r += cand[j] > mine;
-    if (r < k) best[r] = mine;
+// The parts of `n` neighbouring lanes (a power of two) as one.
+__device__ __forceinline__ LpPart join_lanes(LpPart a, int n) {
+  for (int o = n / 2; o; o >>= 1) {
+    LpPart b;
+    b.c = __shfl_xor_sync(0xffffffffu, a.c, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    b.u = __shfl_xor_sync(0xffffffffu, a.u, o);
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.greater = __shfl_xor_sync(0xffffffffu, a.greater, o);
+    a = join(a, b);
   }
-  for (int i = n + sel; i < k; i += kSelectors) best[i] = 0;
+  return a;
 }
+// A row that is summed again as x - m.
+__device__ __forceinline__ bool is_odd(float m) { return m > -INFINITY && !(fabsf(m) <= kPlain); }
 
 // A warp's n-th largest key (n <= 32).
 __device__ __forceinline__ uint32_t nth_largest(uint32_t mine, int n, int lane) {
@@ -311,94 +291,158 @@ __device__ __forceinline__ uint32_t nth_largest(uint32_t mine, int n, int lane) 
   }
   return t;
 }
+// What one of `full` warps whose threads all have a vector gives to the bound
+// that k tokens reach: its ceil(k / full)-th largest thread maximum; 0 (every
+// token is looked at) where there are too few threads, all ones from a warp
+// that does not count.
+__device__ __forceinline__ uint32_t warp_tau(float thread_max, int k, int full, int warp, int lane) {
+  const int need = full ? (k + full - 1) / full : 33;
+  if (need > 32) return 0u;
+  const uint32_t t = nth_largest(ord32(thread_max + 0.f), need, lane);
+  return warp < full ? t : 0xffffffffu;
+}
+
+// The threads that select for a row.
+struct SelectorGroup {
+  static constexpr int kSize = kSelectors;
+  int at;
+  __device__ void sync() const { asm volatile("bar.sync 1, %0;" ::"n"(kSelectors) : "memory"); }
+  __device__ bool any(bool p) const {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"((uint32_t)p), "n"(kSelectors)
+        : "memory");
+    return r != 0;
+  }
+};
+struct BlockGroup {
+  static constexpr int kSize = kHeldThreads;
+  int at;
+  __device__ void sync() const { __syncthreads(); }
+  __device__ bool any(bool p) const { return __syncthreads_or(p) != 0; }
+};
+
+// Their shared state.
+template <class G>
+struct __align__(16) LpSelect {
+  static constexpr int kCap = G::kSize == kSelectors ? 1024 : 2048 + kLpMaxTop;   // survivors ranked by counting
+  uint64_t cand[kCap];
+  uint64_t best[kLpMaxTop];            // the slice's largest keys, in order
+  LpPart part, whole;                  // the slice's, the row's
+  float z, z_lo, m;                    // log S of the row, relative to its maximum m, in two parts
+  int n_cand, n_hit;
+  float sum[G::kSize / 32][2];
+  uint32_t step_tau[G::kSize / 32];
+};
+
+// The k largest of cand[0, n) by counting, in order, to best[0, k) (n < k: the
+// rest are 0).
+template <class G>
+__device__ __forceinline__ void rank_candidates(LpSelect<G>* sh, const G& g, int n, int k) {
+  for (int i = g.at; i < n; i += G::kSize) {
+    const uint64_t mine = sh->cand[i];
+    int r = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) r += sh->cand[j] > mine;
+    if (r < k) sh->best[r] = mine;
+  }
+  for (int i = n + g.at; i < k; i += G::kSize) sh->best[i] = 0;
+  g.sync();
+}
 
 // The k largest keys of vectors [v0, v1) of a row, by a pass in order against
 // the k-th best so far: once k are held, equal logits (of later tokens) never
 // pass, so that a step whose maximum is not greater is done with.  In a step
-// the selectors' maxima bound what has to be looked at, as for a row; where
-// equal values leave more than fits, its vectors are taken one by one.  All
-// selectors.
-template <typename T>
-__device__ __noinline__ void top_again(LpShared* sh, const RowAt<T>& r, int v0, int v1, int k, int sel) {
+// the threads' maxima bound what has to be looked at, as for a row; where equal
+// values leave more than fits, its vectors are taken one by one.
+template <typename T, class G>
+__device__ __noinline__ void top_again(LpSelect<G>* sh, const G g, const RowAt<T> r, int v0, int v1, int k) {
   using V = Vec<T>;
-  static_assert(kSelectors * V::kN + kLpMaxTop <= kLpCap, "a vector of each selector fits beside the best");
+  constexpr int kN = 4, kWarps = G::kSize / 32, kCap = LpSelect<G>::kCap;
+  static_assert(G::kSize * V::kN + kLpMaxTop <= kCap, "a vector of each thread fits beside the best");
   float floor = -INFINITY;
   int held = 0;
-  sel_sync();
-  if (sel == 0) sh->n_cand = 0;
-  sel_sync();
+  g.sync();
+  if (g.at == 0) sh->n_cand = 0;
+  g.sync();
   // what has been appended joins the best
   auto join_best = [&](int n) {
-    rank_candidates(sh->cand, n, k, sh->best, sel);
-    sel_sync();
+    rank_candidates(sh, g, n, k);
     held = n < k ? n : k;
-    for (int i = sel; i < held; i += kSelectors) sh->cand[i] = sh->best[i];
+    for (int i = g.at; i < held; i += G::kSize) sh->cand[i] = sh->best[i];
     if (n >= k) floor = key_logit(sh->best[k - 1]);
-    if (sel == 0) sh->n_cand = held;
-    sel_sync();
+    if (g.at == 0) sh->n_cand = held;
+    g.sync();
   };
-  for (int v = v0; v < v1; v += kVpt * kSelectors) {
-    uint4 q[kVpt];
+  for (int v = v0; v < v1; v += kN * G::kSize) {
+    uint4 q[kN];
 #pragma unroll
-    for (int j = 0; j < kVpt; ++j) {
-      const int at = v + j * kSelectors + sel;
+    for (int j = 0; j < kN; ++j) {
+      const int at = v + j * G::kSize + g.at;
       q[j] = at < v1 ? __ldg(r.vec + at) : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
       if (at < v1 && r.edge(at)) r.edges(q[j], at);
     }
-    const float mx = V::max(q);
-    if (!sel_any(mx > floor)) continue;
-    const uint32_t w = nth_largest(ord32(fmaxf(mx, -INFINITY) + 0.f), (k + kSelWarps - 1) / kSelWarps, sel & 31);
-    if ((sel & 31) == 0) sh->step_tau[sel >> 5] = w;
-    sel_sync();
+    const float mx = max_of<T>(q);
+    if (!g.any(mx > floor)) continue;
+    const int need = (k + kWarps - 1) / kWarps;   // (more than 32: no bound)
+    const uint32_t w = need <= 32 ? nth_largest(ord32(mx + 0.f), need, g.at & 31) : 0u;
+    if ((g.at & 31) == 0) sh->step_tau[g.at >> 5] = w;
+    g.sync();
     uint32_t tau = sh->step_tau[0];
-    for (int i = 1; i < kSelWarps; ++i) tau = min(tau, sh->step_tau[i]);
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) tau = min(tau, sh->step_tau[i]);
     auto append = [&](const uint4& vec, int j) {
 #pragma unroll
       for (int e = 0; e < V::kN; ++e) {
         const float x = V::at(vec, e);
         if (x > floor && ord32(x + 0.f) >= tau) {
           const int at = atomicAdd(&sh->n_cand, 1);
-          if (at < kLpCap) sh->cand[at] = key_of(x, (v + j * kSelectors + sel) * V::kN + e - r.off);
+          if (at < kCap) sh->cand[at] = key_of(x, (v + j * G::kSize + g.at) * V::kN + e - r.off);
         }
       }
     };
-#pragma unroll
-    for (int j = 0; j < kVpt; ++j) append(q[j], j);
-    sel_sync();
-    const int n = sh->n_cand;
-    sel_sync();   // all have read it before any appends again
-    if (n <= kLpCap) {
-      if (n != held) join_best(n);
-      continue;
-    }
-    if (sel == 0) sh->n_cand = held;   // (the best are still in the first places)
-    sel_sync();
+    // vectors [j0, j1) of the step; false if they hold more than fits
+    auto take = [&](int j0, int j1) {
 #pragma unroll 1
-    for (int j = 0; j < kVpt; ++j) {
-      uint4 mine = q[0];   // (q[j] without an index into registers)
+      for (int j = j0; j < j1; ++j) {
+        uint4 mine = q[0];   // (q[j] without an index into registers)
 #pragma unroll
-      for (int i = 1; i < kVpt; ++i)
-        if (i == j) mine = q[i];
-      append(mine, j);
-      sel_sync();
-      const int some = sh->n_cand;
-      sel_sync();
-      if (some != held) join_best(some);
-    }
+        for (int i = 1; i < kN; ++i)
+          if (i == j) mine = q[i];
+        append(mine, j);
+      }
+      g.sync();
+      const int n = sh->n_cand;
+      g.sync();   // all have read it before any appends again
+      if (n > kCap) {
+        if (g.at == 0) sh->n_cand = held;   // (the best are still in the first places)
+        g.sync();
+        return false;
+      }
+      if (n != held) join_best(n);
+      return true;
+    };
+    if (!take(0, kN))
+      for (int j = 0; j < kN; ++j) take(j, j + 1);
   }
   if (held == 0)
-    for (int i = sel; i < k; i += kSelectors) sh->best[i] = 0;
-  sel_sync();
+    for (int i = g.at; i < k; i += G::kSize) sh->best[i] = 0;
+  g.sync();
 }
 
 // log S and the entropy of a row whose maximum m is finite and large, or +inf
-// (then the +inf tokens share the probability).  All selectors.
-template <typename T>
-__device__ __noinline__ float2 row_again(LpShared* sh, const RowAt<T>& r, float m, int sel) {
+// (then the +inf tokens share the probability).
+template <typename T, class G>
+__device__ __noinline__ float2 row_again(LpSelect<G>* sh, const G g, const RowAt<T> r, float m) {
   using V = Vec<T>;
   float s = 0.f, u = 0.f;
 #pragma unroll 4
-  for (int v = sel; v < r.nv; v += kSelectors) {
+  for (int v = g.at; v < r.nv; v += G::kSize) {
     uint4 q = __ldg(r.vec + v);
     if (r.edge(v)) r.edges(q, v);
 #pragma unroll
@@ -414,21 +458,340 @@ __device__ __noinline__ float2 row_again(LpShared* sh, const RowAt<T>& r, float 
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o), u += __shfl_xor_sync(0xffffffffu, u, o);
-  sel_sync();
-  if ((sel & 31) == 0) sh->sum[sel >> 5][0] = s, sh->sum[sel >> 5][1] = u;
-  sel_sync();
+  g.sync();
+  if ((g.at & 31) == 0) sh->sum[g.at >> 5][0] = s, sh->sum[g.at >> 5][1] = u;
+  g.sync();
   s = u = 0.f;
-  for (int w = 0; w < kSelWarps; ++w) s += sh->sum[w][0], u += sh->sum[w][1];
+#pragma unroll
+  for (int w = 0; w < G::kSize / 32; ++w) s += sh->sum[w][0], u += sh->sum[w][1];
   const float z = logf(s);
   return make_float2(z, z - u / s);
 }
 
+// A row and the token to score in it.
+template <typename T>
+struct LpJob {
+  RowAt<T> r;
+  int row, vocab, token;
+  float xt;   // its logit
+  __device__ bool valid() const { return token >= 0 && token < vocab; }
+};
+
+// a + b exactly, as a rounded sum and its error.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+// a + b for a in two parts.
+__device__ __forceinline__ Two add(const Two& a, float b) {
+  const Two s = two_sum(a.hi, b);
+  return {s.hi, s.lo + a.lo};
+}
+// x - m - z, rounded once but for the errors' errors.
+__device__ __forceinline__ float minus_z(float x, float m, float z, float z_lo) {
+  const Two d = two_sum(x, -m);
+  if (!(fabsf(d.hi) < 0x1p100f)) return d.hi;   // (past what z can change, or infinite)
+  const Two e = two_sum(d.hi, -z);
+  return e.hi + (e.lo + (d.lo - z_lo));
+}
+
+// What the given token and the entropy get from the whole row's part b (one
+// thread); `again`: log S and the entropy of an odd row.  In pairs of f32
+// values: a double's operations take this one thread longer than the rest of a
+// short row's.
+template <typename T, class G>
+__device__ __forceinline__ void finish(LpSelect<G>* sh, const LpJob<T>& job, const LpPart& b, float2 again,
+                                       const LpOut& out, bool scored, int* err) {
+  float z = again.x, z_lo = 0.f, h = again.y;
+  if (!is_odd(b.m) && b.m > -INFINITY) {
+    // S = 2^e f with f near 1: log S = e ln 2 + log f
+    const int e = (int)((__float_as_uint(b.s) + 0x4AFB0Du) >> 23) - 127;
+    const float lf = logf(__uint_as_float(__float_as_uint(b.s) - ((uint32_t)e << 23))), ef = (float)e;
+    const float el = ef * kLn2;
+    const Two ln = add(add({el, fmaf(ef, kLn2, -el) + ef * kLn2Lo}, lf), 0.f);
+    // z = log S + (c ln 2 - m) + m (log2 e - L) ln 2
+    const float rest = b.m * (float)(kLRest * 0.693147180559945309), cl = b.c * kLn2;
+    const Two dc = two_sum(cl, -b.m);
+    Two t = add(ln, dc.hi);
+    t.lo += dc.lo + (fmaf(b.c, kLn2, -cl) + b.c * kLn2Lo) + rest;
+    z = t.hi + t.lo;
+    z_lo = t.lo - (z - t.hi);
+    // h = log S - (U / S) / L + c (ln 2 - 1 / L) + m (log2 e - L) ln 2
+    const float q = b.u / b.s, ql = fmaf(-q, b.s, b.u) / b.s, qi = q * (float)kInvL;
+    const Two g = add(ln, -qi);
+    h = g.hi + (g.lo - (fmaf(q, (float)kInvL, -qi) + q * (float)(kInvL - (double)(float)kInvL) + ql * (float)kInvL) +
+                (b.c * (float)(0.693147180559945309 - kInvL) + rest));
+  }
+  sh->z = z;
+  sh->z_lo = z_lo;
+  sh->m = b.m;
+  if (!(b.m > -INFINITY)) h = 0.f;
+  if (out.entropy) out.entropy[job.row] = fmaxf(h, 0.f);
+  if (!scored) return;
+  float lp = 0.f;
+  int rank = 0;
+  if (job.valid()) {
+    lp = !(job.xt > -INFINITY) ? -INFINITY
+         : b.m == INFINITY     ? (job.xt == INFINITY ? -z : -INFINITY)
+                               : minus_z(job.xt, b.m, z, z_lo);
+    rank = 1 + b.greater;
+  } else if (job.token != -1 && err) {
+    atomicOr(err, kErrToken);
+  }
+  out.logprobs[job.row] = lp;
+  out.ranks[job.row] = rank;
+}
+
+// From the slice's part and largest keys (sh->part, sh->best; S = 1: the whole
+// row's, finished unless it is odd) to the row's results.  S > 1: after a
+// cluster barrier, by the first slice's CTA.
+template <typename T, class G>
+__device__ __forceinline__ void row_results(LpSelect<G>* sh, const G& g, const LpJob<T>& job, int S, int top,
+                                            const LpOut& out, bool scored, int* err) {
+  if (S > 1) {
+    if (g.at < 32) {   // a lane per slice
+      const uint32_t at = cluster_map(smem_u32(&sh->part), (uint32_t)(g.at & (S - 1)));
+      const float4 d = ld_dsmem_f32x4(at);
+      const LpPart b = join_lanes({d.x, d.y, d.z, d.w, __float_as_int(ld_dsmem_f32(at + 16))}, S);
+      if (g.at == 0) {
+        sh->whole = b;
+        if (!is_odd(b.m)) finish(sh, job, b, make_float2(0.f, 0.f), out, scored, err);
+      }
+      __syncwarp();
+    }
+    if (top) {
+      for (int i = g.at; i < S * top; i += G::kSize)
+        sh->cand[i] = ld_dsmem_u64(cluster_map(smem_u32(&sh->best[i % top]), (uint32_t)(i / top)));
+      g.sync();
+      for (int i = g.at; i < top; i += G::kSize) sh->best[i] = 0;
+      g.sync();
+      // a key's place: its own slice's keys before it, and those of the other
+      // slices that are greater (each list is in order, empty places hold 0)
+      for (int i = g.at; i < S * top; i += G::kSize) {
+        const uint64_t mine = sh->cand[i];
+        if (mine == 0) continue;
+        int lo[kLpMaxSlices], hi[kLpMaxSlices];   // the first that is not greater lies in [lo, hi]
+#pragma unroll
+        for (int o = 0; o < kLpMaxSlices; ++o) lo[o] = 0, hi[o] = o < S && o != i / top ? top : 0;
+        for (int width = top; width; width >>= 1)
+#pragma unroll
+          for (int o = 0; o < kLpMaxSlices; ++o)
+            if (lo[o] < hi[o]) {
+              const int mid = (lo[o] + hi[o]) >> 1;
+              if (sh->cand[o * top + mid] > mine) lo[o] = mid + 1; else hi[o] = mid;
+            }
+        int n = i % top;
+#pragma unroll
+        for (int o = 0; o < kLpMaxSlices; ++o) n += lo[o];
+        if (n < top) sh->best[n] = mine;
+      }
+    }
+    g.sync();
+  }
+  const LpPart b = S > 1 ? sh->whole : sh->part;
+  if (is_odd(b.m)) {   // (the same for all)
+    const float2 again = row_again<T, G>(sh, g, job.r, b.m);
+    if (g.at == 0) finish(sh, job, b, again, out, scored, err);
+    g.sync();
+  }
+  for (int i = g.at; i < top; i += G::kSize) {
+    const uint64_t key = sh->best[i];
+    const float x = key_logit(key);
+    const bool any = key != 0 && (sh->m < INFINITY || x == INFINITY);
+    out.top_tokens[(size_t)job.row * top + i] = any ? key_token(key) : -1;
+    out.top_logprobs[(size_t)job.row * top + i] =
+        !any ? -INFINITY : sh->m == INFINITY ? -sh->z : minus_z(x, sh->m, sh->z, sh->z_lo);
+  }
+}
+
+// Sums of a thread's vectors.
+template <typename T>
+struct Sums {
+  using V = Vec<T>;
+  float c = kNone;
+  uint64_t s[2] = {pair(0.f, 0.f), pair(0.f, 0.f)}, u[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+
+  // The reference moves where a maximum passes it by 16.
+  __device__ void reach(float mx) {
+    if (mx * kL > c + 16.f) {
+      const float cn = rintf(mx * kL), d = fmaxf(c - cn, -1e30f), f = exp2_fast(d);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        u[i] = fma_pair(s[i], pair(d, d), u[i]);
+        s[i] = fma_pair(s[i], pair(f, f), pair(0.f, 0.f));
+        u[i] = fma_pair(u[i], pair(f, f), pair(0.f, 0.f));
+      }
+      c = cn;
+    }
+  }
+  // Masked logits and NaN take a value whose exponential is 0 (-160 in base 2
+  // at least, finite: 0 times it is 0).
+  __device__ typename V::Low low() const {
+    const float l = (c - 160.f) * 0.6931472f;
+    return typename V::Low(fmaf(fabsf(l), -0.01f, l));
+  }
+  __device__ LpPart part(float m, int greater) const {
+    const float2 a = unpair(add_pair(s[0], s[1])), b = unpair(add_pair(u[0], u[1]));
+    return {c, a.x + a.y, b.x + b.y, m, greater};
+  }
+};
+
+}  // namespace
+
+template <typename T, int VPT>
+__global__ void __launch_bounds__(kHeldThreads, VPT == 8 ? 3 : 5)
+    k_lp_held(const T* __restrict__ logits, size_t stride, int vocab, const int32_t* __restrict__ tokens, int top,
+              LpOut out, int S, int* err) {
+  using V = Vec<T>;
+  constexpr int kLists = 512;   // vectors with a token that reaches the bound
+  __shared__ LpSelect<BlockGroup> sel;
+  __shared__ uint4 vecs[kLists];
+  __shared__ int vec_at[kLists];
+  __shared__ LpPart parts[kHeldWarps];
+  __shared__ uint32_t taus[kHeldWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = (int)(blockIdx.x / (unsigned)S), slice = (int)(blockIdx.x % (unsigned)S);
+  const RowAt<T> r(logits, stride, row, vocab);
+  const BlockGroup g{tid};
+  const int v0 = (int)((long long)r.nv * slice / S), v1 = (int)((long long)r.nv * (slice + 1) / S);
+  if (tid == 0) sel.n_cand = 0, sel.n_hit = 0;
+  pdl_wait();
+  pdl_trigger();
+
+  uint4 q[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = v0 + j * kHeldThreads + tid;
+    q[j] = v < v1 ? __ldg(r.vec + v) : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+  }
+  LpJob<T> job{r, row, vocab, tokens ? tokens[row] : -1, 0.f};
+  if (job.valid()) job.xt = V::load(r.base + job.token);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = v0 + j * kHeldThreads + tid;
+    if (v < v1 && r.edge(v)) r.edges(q[j], v);
+  }
+  const float mx = max_of<T>(q);
+  Sums<T> sums;
+  sums.reach(mx);
+  if (sums.c > kNone) {
+    const typename V::Low low = sums.low();
+    const uint64_t cc = pair(-sums.c, -sums.c);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) V::template sums<true>(q[j], low, cc, sums.s[j & 1], sums.u[j & 1]);
+  }
+  int greater = 0;
+  if (job.valid()) {   // before the given token's vector equal logits count as greater
+    const bool masked = !(job.xt > -INFINITY);
+    const int vt = masked ? -1 : (job.token + r.off) / V::kN;
+    const typename V::Thr above(masked ? -INFINITY : job.xt), from(masked ? -INFINITY : V::below(job.xt));
+    typename V::Count count;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = v0 + j * kHeldThreads + tid;
+      if (v != vt) {
+        count.add(q[j], v < vt ? from : above);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V::kN; ++e) {
+          const float x = V::at(q[j], e);
+          greater += x > job.xt || (x == job.xt && v * V::kN + e - r.off < job.token);
+        }
+      }
+    }
+    greater += count.total();
+  }
+  const LpPart a = join_lanes(sums.part(mx, greater), 32);
+  if (lane == 0) parts[warp] = a;
+  if (top) {
+    const uint32_t t = warp_tau(mx, top, min(kHeldWarps, (v1 - v0) / 32), warp, lane);
+    if (lane == 0) taus[warp] = t;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const LpPart b = join_lanes(parts[lane & (kHeldWarps - 1)], kHeldWarps);
+    if (lane == 0) sel.part = b;
+  }
+  if (top) {
+    uint32_t tau = kOrdNegInf + 1, t = taus[0];
+#pragma unroll
+    for (int w = 1; w < kHeldWarps; ++w) t = min(t, taus[w]);
+    tau = max(tau, t);
+    const float bound = unord32(tau);
+    // vectors that reach the bound, then their tokens, one per thread
+    if (mx >= bound) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (V::whole(V::max(q[j])) >= bound) {
+          const int at = atomicAdd(&sel.n_hit, 1);
+          if (at < kLists) vecs[at] = q[j], vec_at[at] = v0 + j * kHeldThreads + tid;
+        }
+    }
+    __syncthreads();
+    const int hits = sel.n_hit;
+    if (hits <= kLists)
+      for (int i = tid; i < hits * V::kN; i += kHeldThreads) {
+        const float x = V::load(reinterpret_cast<const T*>(vecs) + i);
+        if (x >= bound) {
+          const int at = atomicAdd(&sel.n_cand, 1);
+          if (at < sel.kCap) sel.cand[at] = key_of(x, vec_at[i / V::kN] * V::kN + i % V::kN - r.off);
+        }
+      }
+    if (S == 1 && tid == 32 * (kHeldWarps - 1) && !is_odd(sel.part.m))   // (beside the others' search)
+      finish(&sel, job, sel.part, make_float2(0.f, 0.f), out, tokens != nullptr, err);
+    __syncthreads();
+    const int n = sel.n_cand;
+    if (hits <= kLists && n <= sel.kCap)
+      rank_candidates(&sel, g, n, top);
+    else
+      top_again<T>(&sel, g, r, v0, v1, top);
+  } else {
+    __syncthreads();
+    if (S == 1 && tid == 0 && !is_odd(sel.part.m))
+      finish(&sel, job, sel.part, make_float2(0.f, 0.f), out, tokens != nullptr, err);
+  }
+  if (S > 1) {
+    cluster_sync();
+    if (slice == 0) row_results(&sel, g, job, S, top, out, tokens != nullptr, err);
+    cluster_sync();   // no CTA leaves while another reads its parts
+  } else {
+    row_results(&sel, g, job, 1, top, out, tokens != nullptr, err);
+  }
+}
+
+namespace {
+
+// What the readers hand over of a row.
+struct __align__(16) LpRow {
+  uint32_t gmax[kGroups][kReaders];
+  LpPart warp[kReadWarps];
+  uint32_t tau[kReadWarps];
+};
+
+struct __align__(16) LpShared {
+  uint64_t full[kStages], empty[kStages];        // the ring's
+  uint64_t read[2], taken[2];                    // the two rows'
+  LpRow row[2];
+  LpSelect<SelectorGroup> sel;
+  uint16_t hits[kGroups * kReaders];             // groups whose maximum reaches the bound
+  int abort;
+};
+
+// How a slice of nv vectors is cut: chunks, and chunks of a group.
+struct Cut {
+  int chunks, group;
+  __device__ explicit Cut(int nv) : chunks((nv + kChunkVecs - 1) / kChunkVecs), group((chunks + kGroups - 1) / kGroups) {}
+};
+
 }  // namespace
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 2)
-    k_token_logprobs(const T* __restrict__ logits, size_t stride, int rows, int vocab, const int32_t* __restrict__ tokens,
-                     int top, LpOut out, int* err) {
+__global__ void __launch_bounds__(kStreamThreads, 2)
+    k_lp_stream(const T* __restrict__ logits, size_t stride, int rows, int vocab, const int32_t* __restrict__ tokens,
+                int top, LpOut out, int* err) {
   using V = Vec<T>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_align<128>(smem_raw);
@@ -459,9 +822,10 @@ __global__ void __launch_bounds__(kLpThreads, 2)
     v0 = (int)((long long)r.nv * slice / S);
     v1 = (int)((long long)r.nv * (slice + 1) / S);
   };
-  // a warp's wait; after one that ran out the rows left go through without data
+  // a warp's wait (asleep: polling warps would take issue slots from the
+  // others); after one that ran out the rows left go through without data
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool there = *abort ? false : mbar_wait(bar, parity, abort);
+    const bool there = *abort ? false : mbar_wait_sleep(bar, parity, abort);
     if (!__all_sync(0xffffffffu, there)) {
       *abort = 1;
       if (err && lane == 0) atomicOr(err, kErrTimeout);
@@ -470,8 +834,6 @@ __global__ void __launch_bounds__(kLpThreads, 2)
   auto token_of = [&](int row) { return tokens && row < rows ? tokens[row] : -1; };
   auto valid = [&](int t) { return t >= 0 && t < vocab; };
   auto logit_of = [&](int row, int t) { return valid(t) ? V::load(logits + (size_t)row * stride + t) : 0.f; };
-  // chunks of a group of vectors
-  auto group_of = [](int chunks) { return (chunks + kGroups - 1) / kGroups; };
 
   if (warp == kReadWarps + kSelWarps) {
     if (lane == 0) {
@@ -482,6 +844,7 @@ __global__ void __launch_bounds__(kLpThreads, 2)
         const RowAt<T> r(logits, stride, row, vocab);
         int v0, v1;
         slice_of(r, v0, v1);
+        const Cut cut(v1 - v0);
         for (int v = v0; v < v1; v += kChunkVecs) {
           if (!mbar_wait_sleep(&sh->empty[stage], phase ^ 1u, abort)) {
             *abort = 1;
@@ -502,33 +865,33 @@ __global__ void __launch_bounds__(kLpThreads, 2)
     __syncwarp();
   } else if (warp < kReadWarps) {
     // ---------------- readers
-    int stage = 0, it = 0;
-    uint32_t phase = 0;
+    int stage = 0, turn = 0;
+    uint32_t phase = 0, turn_phase = 0;
     int token = token_of(row0);
     float xt = logit_of(row0, token);
-    for (int row = row0; row < rows; row += row_step, ++it) {
+    for (int row = row0; row < rows; row += row_step) {
       const RowAt<T> r(logits, stride, row, vocab);
       int v0, v1;
       slice_of(r, v0, v1);
-      const int chunks = (v1 - v0 + kChunkVecs - 1) / kChunkVecs;
-      const int per_group = group_of(chunks);
+      const Cut cut(v1 - v0);
       const int next_token = token_of(row + row_step);
       const bool masked = !(xt > -INFINITY);                    // (NaN too)
       // before the given token's vector equal logits count as greater
       const int vt = valid(token) && !masked ? (token + r.off) / V::kN : -1;
       const typename V::Thr above(masked ? -INFINITY : xt), from(masked ? -INFINITY : V::below(xt));
-      LpRow& hand = sh->row[it & 1];
-      wait(&sh->taken[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u);
+      LpRow& hand = sh->row[turn];
+      wait(&sh->taken[turn], turn_phase ^ 1u);
 
-      float c = kNone, m = -INFINITY, gm = -INFINITY, greater = 0.f;
-      uint64_t s2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)}, u2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-      int group = 0, left = per_group;
-      for (int ch = 0; ch < chunks; ++ch) {
+      Sums<T> sums;
+      float m = -INFINITY, gm = -INFINITY;
+      bool clamp = false;   // the row has had masked logits
+      int greater = 0, group = 0, left = cut.group;
+      for (int ch = 0; ch < cut.chunks; ++ch) {
         wait(&sh->full[stage], phase);
         const int vc = v0 + ch * kChunkVecs;
         const uint4* p = reinterpret_cast<const uint4*>(ring + stage * kChunkBytes) + tid;
         uint4 q[kVpt];
-        if (ch > 0 && ch + 1 < chunks) {
+        if (ch > 0 && ch + 1 < cut.chunks) {
 #pragma unroll
           for (int j = 0; j < kVpt; ++j) q[j] = p[j * kReaders];
         } else {
@@ -543,38 +906,44 @@ __global__ void __launch_bounds__(kLpThreads, 2)
         if (lane == 0) mbar_arrive(&sh->empty[stage]);
         if (++stage == kStages) stage = 0, phase ^= 1u;
 
-        const float mx = V::max(q);
+        const float mx = max_of<T>(q);
         gm = fmaxf(gm, mx);
-        if (--left == 0 || ch + 1 == chunks) {
+        if (--left == 0 || ch + 1 == cut.chunks) {
           if (top) hand.gmax[group][tid] = ord32(gm + 0.f);
           m = fmaxf(m, gm);
           gm = -INFINITY;
           ++group;
-          left = per_group;
+          left = cut.group;
         }
-        if (mx * kL > c + 16.f) {
-          const float cn = rintf(mx * kL), d = fmaxf(c - cn, -1e30f), f = exp2_fast(d);
+        sums.reach(mx);
+        if (sums.c > kNone) {
+          const uint64_t cc = pair(-sums.c, -sums.c);
+          bool summed = false;
+          if (!clamp) {
+            Sums<T> t = sums;
+            const typename V::Low none(0.f);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            u2[i] = fma_pair(s2[i], pair(d, d), u2[i]);
-            s2[i] = fma_pair(s2[i], pair(f, f), pair(0.f, 0.f));
-            u2[i] = fma_pair(u2[i], pair(f, f), pair(0.f, 0.f));
+            for (int j = 0; j < kVpt; ++j)
+              V::template sums<false>(q[j], none, cc, t.s[j & 1], t.u[j & 1]);
+            // masked logits and NaN make U a NaN (0 times -inf): from here on they are looked for in this row
+            const float2 n = unpair(add_pair(t.u[0], t.u[1]));
+            summed = !isnan(n.x + n.y);
+            clamp = !summed;
+            if (summed) sums = t;
           }
-          c = cn;
-        }
-        if (c > kNone) {
-          // masked logits and NaN take a value whose exponential is 0 (-160 in base 2 at least, finite)
-          const float low = (c - 160.f) * 0.6931472f;
-          const typename V::Low lo(fmaf(fabsf(low), -0.01f, low));
-          const uint64_t cc = pair(-c, -c);
+          if (!summed) {
+            const typename V::Low low = sums.low();
 #pragma unroll
-          for (int j = 0; j < kVpt; ++j) V::sums(q[j], lo, cc, s2[j & 1], u2[j & 1]);
+            for (int j = 0; j < kVpt; ++j)
+              V::template sums<true>(q[j], low, cc, sums.s[j & 1], sums.u[j & 1]);
+          }
         }
         typename V::Count count;
         if (vt < vc || vt >= vc + kChunkVecs) {   // (the same for all)
           const typename V::Thr t = vt < vc ? above : from;
 #pragma unroll
-          for (int j = 0; j < kVpt; ++j) count.add(q[j], t);
+          for (int j = 0; j < kVpt; ++j)
+            count.add(q[j], t);
         } else {
 #pragma unroll
           for (int j = 0; j < kVpt; ++j) {
@@ -585,7 +954,7 @@ __global__ void __launch_bounds__(kLpThreads, 2)
 #pragma unroll
               for (int e = 0; e < V::kN; ++e) {
                 const float x = V::at(q[j], e);
-                greater += x > xt || (x == xt && v * V::kN + e - r.off < token) ? 1.f : 0.f;
+                greater += x > xt || (x == xt && v * V::kN + e - r.off < token);
               }
             }
           }
@@ -595,233 +964,170 @@ __global__ void __launch_bounds__(kLpThreads, 2)
       const float next_xt = logit_of(row + row_step, next_token);
 
       // ---------------- the warp's part to the selectors
-      const float2 ss = unpair(add_pair(s2[0], s2[1])), uu = unpair(add_pair(u2[0], u2[1]));
-      LpPart a{c, ss.x + ss.y, uu.x + uu.y, m, greater};
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        LpPart b;
-        b.c = __shfl_xor_sync(0xffffffffu, a.c, o);
-        b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-        b.u = __shfl_xor_sync(0xffffffffu, a.u, o);
-        b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-        b.greater = __shfl_xor_sync(0xffffffffu, a.greater, o);
-        a = join(a, b);
-      }
+      const LpPart a = join_lanes(sums.part(m, greater), 32);
       if (lane == 0) hand.warp[warp] = a;
       if (top) {
-        // this warp's ceil(k / w)-th largest thread maximum, w the warps whose
-        // threads all have a vector (none, or too few threads: every token is a
-        // candidate)
-        const int full = min(kReadWarps, (v1 - v0) / 32);
-        const int need = full ? (top + full - 1) / full : 33;
-        const uint32_t t = need <= 32 ? nth_largest(ord32(m + 0.f), need, lane) : 0u;
-        if (lane == 0) hand.tau[warp] = warp < full ? t : full ? 0xffffffffu : 0u;
+        const uint32_t t = warp_tau(m, top, min(kReadWarps, (v1 - v0) / 32), warp, lane);
+        if (lane == 0) hand.tau[warp] = t;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->read[it & 1]);
+      if (lane == 0) mbar_arrive(&sh->read[turn]);
+      if (++turn == 2) turn = 0, turn_phase ^= 1u;
       token = next_token;
       xt = next_xt;
     }
   } else {
     // ---------------- selectors
-    const int sel = tid - kReaders;
-    int it = 0;
-    for (int row = row0; row < rows; row += row_step, ++it) {
-      const RowAt<T> r(logits, stride, row, vocab);
+    LpSelect<SelectorGroup>* sel = &sh->sel;
+    const SelectorGroup g{tid - kReaders};
+    int turn = 0;
+    uint32_t turn_phase = 0;
+    for (int row = row0; row < rows; row += row_step) {
+      LpJob<T> job{RowAt<T>(logits, stride, row, vocab), row, vocab, token_of(row), 0.f};
+      const RowAt<T>& r = job.r;
       int v0, v1;
       slice_of(r, v0, v1);
-      const int chunks = (v1 - v0 + kChunkVecs - 1) / kChunkVecs;
-      const int per_group = group_of(chunks);
-      const int token = token_of(row);
-      const float xt = logit_of(row, token);
-      if (sel == 0) sh->n_cand = 0, sh->n_hit = 0;
-      sel_sync();
-      wait(&sh->read[it & 1], (uint32_t)(it >> 1) & 1u);
-      const LpRow& hand = sh->row[it & 1];
-
-      // what the given token and the entropy get from a row's whole part
-      auto finish = [&](const LpPart& b, float2 again, bool odd) {
-        double z = again.x, h = again.y;
-        if (!odd && b.m > -INFINITY) {
-          // S = 2^e f with f near 1: its logarithm without a double's
-          const int e = (int)((__float_as_uint(b.s) + 0x4AFB0Du) >> 23) - 127;
-          const double ln = kLn2 * (double)e + (double)logf(__uint_as_float(__float_as_uint(b.s) - ((uint32_t)e << 23)));
-          const double shift = kLn2 * ((double)b.c + (double)b.m * kLRest);
-          const float q = b.u / b.s;
-          const double mean = (double)q + (double)(fmaf(-q, b.s, b.u) / b.s);   // u / s past f32
-          z = ln + (shift - (double)b.m);
-          h = ln + (shift - (mean + (double)b.c) * (1.0 / (double)kL));
+      const Cut cut(v1 - v0);
+      job.xt = logit_of(row, job.token);
+      if (g.at == 0) sel->n_cand = 0, sel->n_hit = 0;
+      g.sync();
+      wait(&sh->read[turn], turn_phase);
+      const LpRow& hand = sh->row[turn];
+      if (warp == kReadWarps + kSelWarps - 1) {   // (beside the others' search)
+        const LpPart b = join_lanes(hand.warp[lane & (kReadWarps - 1)], kReadWarps);
+        if (lane == 0) {
+          sel->part = b;
+          if (S == 1 && !is_odd(b.m)) finish(sel, job, b, make_float2(0.f, 0.f), out, tokens != nullptr, err);
         }
-        sh->z = z;
-        sh->m = b.m;
-        if (!(b.m > -INFINITY)) h = 0.0;
-        if (out.entropy) out.entropy[row] = fmaxf((float)h, 0.f);
-        const bool masked = !(xt > -INFINITY);
-        float lp = 0.f;
-        int rank = 0;
-        if (valid(token)) {
-          lp = masked ? -INFINITY : b.m == INFINITY ? (xt == INFINITY ? (float)-z : -INFINITY)
-                                                     : (float)((double)xt - (double)b.m - z);
-          rank = 1 + (int)b.greater;
-        } else if (token != -1 && err) {
-          atomicOr(err, kErrToken);
-        }
-        if (tokens) out.logprobs[row] = lp, out.ranks[row] = rank;
-      };
-      auto is_odd = [](float m) { return m > -INFINITY && !(fabsf(m) <= kPlain); };
-      if (sel == 0) {
-        LpPart b = hand.warp[0];
-        for (int w = 1; w < kReadWarps; ++w) b = join(b, hand.warp[w]);
-        sh->part = b;
-        if (S == 1 && !is_odd(b.m)) finish(b, make_float2(0.f, 0.f), false);
+        __syncwarp();
       }
-      __syncwarp();
-      // ---------------- the slice's largest tokens
       if (top) {
-        uint32_t tau = 0xffffffffu;
-        for (int w = 0; w < kReadWarps; ++w) tau = min(tau, hand.tau[w]);
-        tau = max(tau, kOrdNegInf + 1);
-        // the groups with a token that reaches tau, then their vectors, one per
-        // thread: read where they are found, a warp takes its groups' loads one
-        // after another
-        const int groups = chunks ? (chunks + per_group - 1) / per_group : 0;
+        const uint32_t tau = max(kOrdNegInf + 1, __reduce_min_sync(0xffffffffu, hand.tau[lane & (kReadWarps - 1)]));
+        const float bound = unord32(tau);
+        // the groups with a token that reaches the bound, then their vectors,
+        // one per thread, a few loads under way
+        const int groups = cut.chunks ? (cut.chunks + cut.group - 1) / cut.group : 0;
         const uint4* gmax = reinterpret_cast<const uint4*>(hand.gmax);
-        for (int i = sel; i < groups * (kReaders / 4); i += kSelectors) {
-          const uint4 g = gmax[i];
-          const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+        for (int i = g.at; i < groups * (kReaders / 4); i += kSelectors) {
+          const uint4 x = gmax[i];
+          if (max(max(x.x, x.y), max(x.z, x.w)) >= tau) {
+            const uint32_t e4[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (w[e] >= tau) sh->hits[atomicAdd(&sh->n_hit, 1)] = (uint16_t)(4 * i + e);
+            for (int e = 0; e < 4; ++e)
+              if (e4[e] >= tau) sh->hits[atomicAdd(&sel->n_hit, 1)] = (uint16_t)(4 * i + e);
+          }
         }
-        sel_sync();
-        const int hits = sh->n_hit, per_hit = per_group * kVpt;
-        for (int i = sel; i < hits * per_hit; i += kSelectors) {
-          const int hit = sh->hits[i / per_hit], j = i % per_hit;
-          const int v = v0 + (hit / kReaders * per_hit + j) * kReaders + hit % kReaders;
-          if (v >= v1) continue;
-          uint4 q = __ldg(r.vec + v);
-          if (r.edge(v)) r.edges(q, v);
+        g.sync();
+        const int per_hit = cut.group * kVpt, total = sel->n_hit * per_hit;
+        constexpr int kAhead = 4;
+#pragma unroll 1
+        for (int i0 = g.at; i0 < total; i0 += kSelectors * kAhead) {
+          uint4 q[kAhead];
+          int v[kAhead];
 #pragma unroll
-          for (int e = 0; e < V::kN; ++e) {
-            const float x = V::at(q, e);
-            if (x > -INFINITY && ord32(x + 0.f) >= tau) {
-              const int at = atomicAdd(&sh->n_cand, 1);
-              if (at < kLpCap) sh->cand[at] = key_of(x, v * V::kN + e - r.off);
+          for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + kSelectors * k;
+            v[k] = v1;
+            if (i < total) {
+              const int hit = sh->hits[i / per_hit], j = i % per_hit;
+              v[k] = v0 + (hit / kReaders * per_hit + j) * kReaders + hit % kReaders;
+            }
+            if (v[k] < v1) q[k] = __ldg(r.vec + v[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            if (v[k] >= v1) continue;
+            if (r.edge(v[k])) r.edges(q[k], v[k]);
+            if (V::whole(V::max(q[k])) < bound) continue;
+#pragma unroll
+            for (int e = 0; e < V::kN; ++e) {
+              const float x = V::at(q[k], e);
+              if (x >= bound) {
+                const int n = atomicAdd(&sel->n_cand, 1);
+                if (n < sel->kCap) sel->cand[n] = key_of(x, v[k] * V::kN + e - r.off);
+              }
             }
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->taken[it & 1]);   // (the parts and tau are read; the hits are this side's)
-      sel_sync();
+      if (lane == 0) mbar_arrive(&sh->taken[turn]);   // what the readers handed over is read
+      if (++turn == 2) turn = 0, turn_phase ^= 1u;
+      g.sync();
       if (top) {
-        const int n = sh->n_cand;
-        if (n <= kLpCap)
-          rank_candidates(sh->cand, n, top, sh->best, sel);
+        const int n = sel->n_cand;
+        if (n <= sel->kCap)
+          rank_candidates(sel, g, n, top);
         else
-          top_again<T>(sh, r, v0, v1, top, sel);
-        sel_sync();
+          top_again<T>(sel, g, r, v0, v1, top);
       }
-
-      // ---------------- the row's results, from its slices' parts
-      if (S > 1) {
-        cluster_sync();   // (the other warps arrive too, below)
-        if (slice == 0) {
-          LpPart b = sh->part;
-          for (int o = 1; o < S; ++o) {
-            const uint32_t at = cluster_map(smem_u32(&sh->part), (uint32_t)o);
-            const float4 d = ld_dsmem_f32x4(at);
-            const LpPart p{d.x, d.y, d.z, d.w, ld_dsmem_f32(at + 16)};
-            b = join(b, p);
-          }
-          sel_sync();
-          if (sel == 0) {
-            sh->part = b;
-            if (!is_odd(b.m)) finish(b, make_float2(0.f, 0.f), false);
-          }
-          if (top) {
-            for (int i = sel; i < S * top; i += kSelectors)
-              sh->cand[i] = ld_dsmem_u64(cluster_map(smem_u32(&sh->best[i % top]), (uint32_t)(i / top)));
-            sel_sync();
-            // a key's place: its own slice's keys before it, and those of the
-            // other slices that are greater (each list is in order, empty
-            // places hold 0)
-            for (int i = sel; i < top; i += kSelectors) sh->best[i] = 0;
-            sel_sync();
-            for (int i = sel; i < S * top; i += kSelectors) {
-              const uint64_t mine = sh->cand[i];
-              if (mine == 0) continue;
-              int n = i % top;
-              for (int o = 0; o < S && n < top; ++o) {
-                if (o == i / top) continue;
-                int lo = 0, hi = top;   // the first that is not greater lies in [lo, hi]
-                while (lo < hi) {
-                  const int mid = (lo + hi) / 2;
-                  if (sh->cand[o * top + mid] > mine) lo = mid + 1; else hi = mid;
-                }
-                n += lo;
-              }
-              if (n < top) sh->best[n] = mine;
-            }
-          }
-          sel_sync();
-        }
-      }
-      if (slice == 0) {
-        const LpPart b = sh->part;
-        if (is_odd(b.m)) {   // (the same for all)
-          const float2 again = row_again<T>(sh, r, b.m, sel);
-          if (sel == 0) finish(b, again, true);
-          sel_sync();
-        }
-        for (int i = sel; i < top; i += kSelectors) {
-          const uint64_t key = sh->best[i];
-          const float x = key_logit(key);
-          const bool any = key != 0 && (sh->m < INFINITY || x == INFINITY);
-          out.top_tokens[(size_t)row * top + i] = any ? key_token(key) : -1;
-          out.top_logprobs[(size_t)row * top + i] =
-              !any ? -INFINITY : sh->m == INFINITY ? (float)-sh->z : (float)((double)x - (double)sh->m - sh->z);
-        }
-      }
-      sel_sync();   // the shared results are free for the next row
+      if (S > 1) cluster_sync();   // (the other warps arrive too, below)
+      if (slice == 0) row_results(sel, g, job, S, top, out, tokens != nullptr, err);
+      g.sync();   // the shared results are free for the next row
     }
   }
-  if (S > 1) {
+  if (S > 1) {   // one row
     if (warp < kReadWarps || warp == kReadWarps + kSelWarps) cluster_sync();   // (the selectors' first one)
-    cluster_sync();                         // no CTA leaves while another reads its parts
+    cluster_sync();                                                            // no CTA leaves while another reads its parts
   }
 }
 
-size_t lp_smem_bytes() { return 128 + (size_t)kStages * kChunkBytes + sizeof(LpShared); }
+namespace {
 
-template <typename T>
-static cudaError_t launch_t(const T* logits, size_t stride, int rows, int vocab, const int32_t* tokens, int top,
-                            const LpOut& out, int* err, cudaStream_t st) {
-  auto k = k_token_logprobs<T>;
-  const size_t smem = lp_smem_bytes();
-  cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem);
-  if (e != cudaSuccess) return e;
-  // few rows: slices of at least one chunk, as many as CTAs fit beside one another
-  const int resident = 2 * device_sm_count();
-  const long long chunks = ((long long)vocab * (long long)sizeof(T) + kChunkBytes - 1) / kChunkBytes;
-  int S = 1;
-  while (S < 8 && (long long)2 * S * rows <= resident && 2 * S <= chunks) S *= 2;
+template <typename K, typename... A>
+cudaError_t launch_cluster(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(S, S > 1 ? rows : (rows < resident ? rows : resident));
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k, logits, stride, rows, vocab, tokens, top, out, err);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+template <typename T>
+cudaError_t launch_t(const T* logits, size_t stride, int rows, int vocab, const int32_t* tokens, int top,
+                     const LpOut& out, int* err, cudaStream_t st) {
+  const int sms = device_sm_count();
+  // vectors of a row (one more where rows start on different places of theirs)
+  const bool aligned = (uintptr_t)logits % 16 == 0 && (rows == 1 || stride * sizeof(T) % 16 == 0);
+  const int nv = (int)(((long long)vocab + (aligned ? 1 : 2) * (Vec<T>::kN - 1)) / Vec<T>::kN);
+  // the fewest slices that registers hold, then more while CTAs fit beside one
+  // another and have a vector per thread
+  int S = 1;
+  while (S < kLpMaxSlices && (nv + S - 1) / S > kHeldThreads * kHeldVecs) S *= 2;
+  const bool fits = (nv + S - 1) / S <= kHeldThreads * kHeldVecs;
+  if (fits && (S == 1 || rows <= 16)) {
+    while (S < kLpMaxSlices && (long long)2 * S * rows <= 2 * sms && nv / (2 * S) >= kHeldThreads) S *= 2;
+    const int per = ((nv + S - 1) / S + kHeldThreads - 1) / kHeldThreads;
+    auto go = [&](auto k) {
+      return launch_cluster(k, dim3((unsigned)S * (unsigned)rows), kHeldThreads, 0, S, st, logits, stride, vocab, tokens,
+                            top, out, S, err);
+    };
+    if (per <= 1) return go(k_lp_held<T, 1>);
+    if (per <= 2) return go(k_lp_held<T, 2>);
+    if (per <= 4) return go(k_lp_held<T, 4>);
+    return go(k_lp_held<T, 8>);
+  }
+  const size_t smem = 128 + (size_t)kStages * kChunkBytes + sizeof(LpShared);
+  auto k = k_lp_stream<T>;
+  cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem);
+  if (e != cudaSuccess) return e;
+  S = 1;
+  while (S < kLpMaxSlices && (long long)2 * S * rows <= 2 * sms && 2ll * S * kChunkVecs <= nv) S *= 2;
+  return launch_cluster(k, dim3(S, S > 1 ? rows : (rows < 2 * sms ? rows : 2 * sms)), kStreamThreads, smem, S, st, logits,
+                        stride, rows, vocab, tokens, top, out, err);
+}
+
+}  // namespace
 
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, size_t stride, int rows, int vocab,
                                   const int32_t* tokens, int top, const LpOut& out, int* err, cudaStream_t st) {
