@@ -333,9 +333,10 @@ struct __align__(16) LpSelect {
   static constexpr int kCap = G::kSize == kSelectors ? 1024 : 2048 + kLpMaxTop;   // survivors ranked by counting
   uint64_t cand[kCap];
   uint64_t best[kLpMaxTop];            // the slice's largest keys, in order
+  uint64_t merged[kLpMaxTop];          // the row's, from several slices'
   LpPart part, whole;                  // the slice's, the row's
   float z, z_lo, m;                    // log S of the row, relative to its maximum m, in two parts
-  int n_cand, n_hit;
+  int n_cand, n_hit, n_over;
   float sum[G::kSize / 32][2];
   uint32_t step_tau[G::kSize / 32];
 };
@@ -520,7 +521,7 @@ __device__ __forceinline__ void finish(LpSelect<G>* sh, const LpJob<T>& job, con
     z = t.hi + t.lo;
     z_lo = t.lo - (z - t.hi);
     // h = log S - (U / S) / L + c (ln 2 - 1 / L) + m (log2 e - L) ln 2
-    const float q = b.u / b.s, ql = fmaf(-q, b.s, b.u) / b.s, qi = q * (float)kInvL;
+    const float q = __fdividef(b.u, b.s), ql = __fdividef(fmaf(-q, b.s, b.u), b.s), qi = q * (float)kInvL;   // U / S in two parts
     const Two g = add(ln, -qi);
     h = g.hi + (g.lo - (fmaf(q, (float)kInvL, -qi) + q * (float)(kInvL - (double)(float)kInvL) + ql * (float)kInvL) +
                 (b.c * (float)(0.693147180559945309 - kInvL) + rest));
@@ -546,50 +547,56 @@ __device__ __forceinline__ void finish(LpSelect<G>* sh, const LpJob<T>& job, con
 }
 
 // From the slice's part and largest keys (sh->part, sh->best; S = 1: the whole
-// row's, finished unless it is odd) to the row's results.  S > 1: after a
-// cluster barrier, by the first slice's CTA.
+// row's, finished unless it is odd) to the row's results.  S > 1: by the first
+// slice's CTA, between the cluster's two barriers, the second of which it
+// passes itself when it has read the others' parts; sh->merged is 0.
 template <typename T, class G>
 __device__ __forceinline__ void row_results(LpSelect<G>* sh, const G& g, const LpJob<T>& job, int S, int top,
                                             const LpOut& out, bool scored, int* err) {
+  const uint64_t* best = sh->best;
   if (S > 1) {
-    if (g.at < 32) {   // a lane per slice
+    const bool last = g.at >= G::kSize - 32;   // (a warp whose keys, if any, are few)
+    LpPart mine;
+    if (last) {   // a lane per slice
       const uint32_t at = cluster_map(smem_u32(&sh->part), (uint32_t)(g.at & (S - 1)));
       const float4 d = ld_dsmem_f32x4(at);
-      const LpPart b = join_lanes({d.x, d.y, d.z, d.w, __float_as_int(ld_dsmem_f32(at + 16))}, S);
-      if (g.at == 0) {
+      mine = {d.x, d.y, d.z, d.w, __float_as_int(ld_dsmem_f32(at + 16))};
+    }
+    for (int i = g.at; i < S * top; i += G::kSize)
+      sh->cand[i] = ld_dsmem_u64(cluster_map(smem_u32(&sh->best[i % top]), (uint32_t)(i / top)));
+    g.sync();
+    cluster_sync();
+    // a key's place: its own slice's keys before it, and those of the other
+    // slices that are greater (each list is in order, empty places hold 0)
+    for (int i = g.at; i < S * top; i += G::kSize) {
+      const uint64_t key = sh->cand[i];
+      if (key == 0) continue;
+      int lo[kLpMaxSlices], hi[kLpMaxSlices];   // the first that is not greater lies in [lo, hi]
+#pragma unroll
+      for (int o = 0; o < kLpMaxSlices; ++o) lo[o] = 0, hi[o] = o < S && o != i / top ? top : 0;
+      for (int width = top; width; width >>= 1)
+#pragma unroll
+        for (int o = 0; o < kLpMaxSlices; ++o)
+          if (lo[o] < hi[o]) {
+            const int mid = (lo[o] + hi[o]) >> 1;
+            if (sh->cand[o * top + mid] > key) lo[o] = mid + 1; else hi[o] = mid;
+          }
+      int n = i % top;
+#pragma unroll
+      for (int o = 0; o < kLpMaxSlices; ++o) n += lo[o];
+      if (n < top) sh->merged[n] = key;
+    }
+    __syncwarp();
+    if (last) {
+      const LpPart b = join_lanes(mine, S);
+      if (g.at == G::kSize - 32) {
         sh->whole = b;
         if (!is_odd(b.m)) finish(sh, job, b, make_float2(0.f, 0.f), out, scored, err);
       }
       __syncwarp();
     }
-    if (top) {
-      for (int i = g.at; i < S * top; i += G::kSize)
-        sh->cand[i] = ld_dsmem_u64(cluster_map(smem_u32(&sh->best[i % top]), (uint32_t)(i / top)));
-      g.sync();
-      for (int i = g.at; i < top; i += G::kSize) sh->best[i] = 0;
-      g.sync();
-      // a key's place: its own slice's keys before it, and those of the other
-      // slices that are greater (each list is in order, empty places hold 0)
-      for (int i = g.at; i < S * top; i += G::kSize) {
-        const uint64_t mine = sh->cand[i];
-        if (mine == 0) continue;
-        int lo[kLpMaxSlices], hi[kLpMaxSlices];   // the first that is not greater lies in [lo, hi]
-#pragma unroll
-        for (int o = 0; o < kLpMaxSlices; ++o) lo[o] = 0, hi[o] = o < S && o != i / top ? top : 0;
-        for (int width = top; width; width >>= 1)
-#pragma unroll
-          for (int o = 0; o < kLpMaxSlices; ++o)
-            if (lo[o] < hi[o]) {
-              const int mid = (lo[o] + hi[o]) >> 1;
-              if (sh->cand[o * top + mid] > mine) lo[o] = mid + 1; else hi[o] = mid;
-            }
-        int n = i % top;
-#pragma unroll
-        for (int o = 0; o < kLpMaxSlices; ++o) n += lo[o];
-        if (n < top) sh->best[n] = mine;
-      }
-    }
     g.sync();
+    best = sh->merged;
   }
   const LpPart b = S > 1 ? sh->whole : sh->part;
   if (is_odd(b.m)) {   // (the same for all)
@@ -598,7 +605,7 @@ __device__ __forceinline__ void row_results(LpSelect<G>* sh, const G& g, const L
     g.sync();
   }
   for (int i = g.at; i < top; i += G::kSize) {
-    const uint64_t key = sh->best[i];
+    const uint64_t key = best[i];
     const float x = key_logit(key);
     const bool any = key != 0 && (sh->m < INFINITY || x == INFINITY);
     out.top_tokens[(size_t)job.row * top + i] = any ? key_token(key) : -1;
@@ -658,6 +665,7 @@ __global__ void __launch_bounds__(kHeldThreads, VPT == 8 ? 3 : 5)
   const BlockGroup g{tid};
   const int v0 = (int)((long long)r.nv * slice / S), v1 = (int)((long long)r.nv * (slice + 1) / S);
   if (tid == 0) sel.n_cand = 0, sel.n_hit = 0;
+  if (tid < kLpMaxTop) sel.merged[tid] = 0;
   pdl_wait();
   pdl_trigger();
 
@@ -755,18 +763,20 @@ __global__ void __launch_bounds__(kHeldThreads, VPT == 8 ? 3 : 5)
   }
   if (S > 1) {
     cluster_sync();
-    if (slice == 0) row_results(&sel, g, job, S, top, out, tokens != nullptr, err);
-    cluster_sync();   // no CTA leaves while another reads its parts
-  } else {
-    row_results(&sel, g, job, 1, top, out, tokens != nullptr, err);
+    if (slice != 0) {
+      cluster_sync();   // (no CTA leaves while another reads its parts)
+      return;
+    }
   }
+  row_results(&sel, g, job, S, top, out, tokens != nullptr, err);
 }
 
 namespace {
 
 // What the readers hand over of a row.
 struct __align__(16) LpRow {
-  uint32_t gmax[kGroups][kReaders];
+  uint32_t gmax[kGroups][kReaders];   // maxima of a reader's groups
+  uint32_t tmax[kReaders];            // and of all of them
   LpPart warp[kReadWarps];
   uint32_t tau[kReadWarps];
 };
@@ -776,7 +786,8 @@ struct __align__(16) LpShared {
   uint64_t read[2], taken[2];                    // the two rows'
   LpRow row[2];
   LpSelect<SelectorGroup> sel;
-  uint16_t hits[kGroups * kReaders];             // groups whose maximum reaches the bound
+  uint16_t over[kReaders];                       // readers whose maximum reaches the bound
+  uint16_t hits[kGroups * kReaders];             // and their groups
   int abort;
 };
 
@@ -825,6 +836,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   // a warp's wait (asleep: polling warps would take issue slots from the
   // others); after one that ran out the rows left go through without data
   auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
     const bool there = *abort ? false : mbar_wait_sleep(bar, parity, abort);
     if (!__all_sync(0xffffffffu, there)) {
       *abort = 1;
@@ -967,6 +979,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       const LpPart a = join_lanes(sums.part(m, greater), 32);
       if (lane == 0) hand.warp[warp] = a;
       if (top) {
+        hand.tmax[tid] = ord32(m + 0.f);
         const uint32_t t = warp_tau(m, top, min(kReadWarps, (v1 - v0) / 32), warp, lane);
         if (lane == 0) hand.tau[warp] = t;
       }
@@ -989,12 +1002,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       slice_of(r, v0, v1);
       const Cut cut(v1 - v0);
       job.xt = logit_of(row, job.token);
-      if (g.at == 0) sel->n_cand = 0, sel->n_hit = 0;
+      if (g.at == 0) sel->n_cand = 0, sel->n_hit = 0, sel->n_over = 0;
       g.sync();
       wait(&sh->read[turn], turn_phase);
       const LpRow& hand = sh->row[turn];
       if (warp == kReadWarps + kSelWarps - 1) {   // (beside the others' search)
-        const LpPart b = join_lanes(hand.warp[lane & (kReadWarps - 1)], kReadWarps);
+        const LpPart b = join_lanes(lane < kReadWarps ? hand.warp[lane] : LpPart{kNone, 0.f, 0.f, -INFINITY, 0}, 16);
         if (lane == 0) {
           sel->part = b;
           if (S == 1 && !is_odd(b.m)) finish(sel, job, b, make_float2(0.f, 0.f), out, tokens != nullptr, err);
@@ -1002,20 +1015,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         __syncwarp();
       }
       if (top) {
-        const uint32_t tau = max(kOrdNegInf + 1, __reduce_min_sync(0xffffffffu, hand.tau[lane & (kReadWarps - 1)]));
+        const uint32_t tau = max(kOrdNegInf + 1, __reduce_min_sync(0xffffffffu, lane < kReadWarps ? hand.tau[lane] : 0xffffffffu));
         const float bound = unord32(tau);
-        // the groups with a token that reaches the bound, then their vectors,
-        // one per thread, a few loads under way
+        // the readers and their groups with a token that reaches the bound, then
+        // the groups' vectors, one per thread, a few loads under way
         const int groups = cut.chunks ? (cut.chunks + cut.group - 1) / cut.group : 0;
-        const uint4* gmax = reinterpret_cast<const uint4*>(hand.gmax);
-        for (int i = g.at; i < groups * (kReaders / 4); i += kSelectors) {
-          const uint4 x = gmax[i];
-          if (max(max(x.x, x.y), max(x.z, x.w)) >= tau) {
-            const uint32_t e4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (e4[e] >= tau) sh->hits[atomicAdd(&sel->n_hit, 1)] = (uint16_t)(4 * i + e);
-          }
+        for (int i = g.at; i < kReaders; i += kSelectors)
+          if (hand.tmax[i] >= tau) sh->over[atomicAdd(&sel->n_over, 1)] = (uint16_t)i;
+        g.sync();
+        const int pairs = sel->n_over * groups;
+        for (int i = g.at; i < pairs; i += kSelectors) {
+          const int j = i % groups, who = sh->over[i / groups];
+          if (hand.gmax[j][who] >= tau) sh->hits[atomicAdd(&sel->n_hit, 1)] = (uint16_t)(j * kReaders + who);
         }
         g.sync();
         const int per_hit = cut.group * kVpt, total = sel->n_hit * per_hit;
@@ -1061,14 +1072,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         else
           top_again<T>(sel, g, r, v0, v1, top);
       }
-      if (S > 1) cluster_sync();   // (the other warps arrive too, below)
+      if (S > 1) {   // (the other warps arrive too, below)
+        for (int i = g.at; i < kLpMaxTop; i += kSelectors) sel->merged[i] = 0;
+        cluster_sync();
+        if (slice != 0) cluster_sync();
+      }
       if (slice == 0) row_results(sel, g, job, S, top, out, tokens != nullptr, err);
       g.sync();   // the shared results are free for the next row
     }
   }
-  if (S > 1) {   // one row
-    if (warp < kReadWarps || warp == kReadWarps + kSelWarps) cluster_sync();   // (the selectors' first one)
-    cluster_sync();                                                            // no CTA leaves while another reads its parts
+  if (S > 1 && (warp < kReadWarps || warp == kReadWarps + kSelWarps)) {
+    // one row: the selectors' two, between which another CTA reads this one's parts
+    cluster_sync();
+    cluster_sync();
   }
 }
 
