@@ -647,8 +647,10 @@ m2_status mxfp4_linear(const uint8_t* a_codes, const uint8_t* a_scales, const ui
 
 /*
  * The quantise-inside form: x bf16 [M, K] (rows row_stride elements apart, as
- * mxfp4_quant) is quantised into the workspace, then as mxfp4_linear: the same
- * bits.  workspace: device, 256-byte aligned, >= the size call's bytes.
+ * mxfp4_quant) is quantised, then as mxfp4_linear: the values that mxfp4_quant
+ * gives, their sum in an order that may differ.  workspace: device, 256-byte
+ * aligned, >= the bytes that the size call gives on the same device (0 for
+ * small sizes up to 64 rows, which one kernel serves; then it may be NULL).
  */
 m2_status mxfp4_linear_bf16_workspace_size(int M, int N, int K, size_t* bytes);
 m2_status mxfp4_linear_bf16(const uint16_t* x, size_t row_stride, const uint8_t* w_codes, const uint8_t* w_scales, void* y,

@@ -47,6 +47,11 @@ struct MxOperand {
 };
 cudaError_t gemm_mx(const MxOperand& a, const MxOperand& w, void* y, bool f32, int M, int N, int K, bool w_early, int* err,
                     cudaStream_t st);
+// The same of bf16 rows that one kernel quantises itself: over how many CTAs it
+// splits K on the current device (0: not for this shape), and the product.
+int mx_inside_splits(int M, int N, int K);
+cudaError_t gemm_mx_inside(const uint16_t* x, size_t x_stride, const MxOperand& w, void* y, bool f32, int M, int N, int K,
+                           int splits, int* err, cudaStream_t st);
 
 // Failure-detection self-test: one CTA allocates TMEM, waits with the GEMMs'
 // bounded mbarrier wait (limit_ns) on a barrier nothing arrives at, takes

@@ -27,6 +27,7 @@
 #include "gemm.h"
 #include "launch_util.h"
 #include "m2_common.cuh"
+#include "mxfp4.cuh"
 #include "tc_ptx.cuh"
 
 namespace m2 {
@@ -40,6 +41,7 @@ constexpr int kRowBytes = 128;   // bytes of K per stage and row
 constexpr int kBK = 256;         // values of K per stage
 constexpr int kThreads = 192;    // 6 warps: producer, MMA, 4 x epilogue
 constexpr uint32_t kSfTile = 512;
+constexpr int kInsideStages = 12, kInsideThreads = kThreads + 128;   // (the form that quantises X itself)
 
 struct __align__(8) Ctl {
   uint64_t full[8];
@@ -47,6 +49,7 @@ struct __align__(8) Ctl {
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
+  uint64_t xfull[kInsideStages];   // the stages of X that the kernel quantises itself
   uint32_t tmem_base;
   int abort;
 };
@@ -385,19 +388,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Few rows: D^T[n, m] = W X^T for one 128-row block of W per cluster, K split
 // over its CTAs, as k_gemm_fewrow.  w_early: W and its scales are not written
 // by the kernel before this one in the stream, so the first stages of them are
-// requested before waiting for it.
+// requested before waiting for it.  kInside: X is bf16 and the epilogue's warps
+// quantise the CTA's part of it into shared memory first, while W arrives (one
+// launch and no workspace).  2688 -> 10304, 1 row: 5.25 us, the quantisation by
+// itself before it 5.7; 4096 -> 2688, 64 rows: 9.1 and 7.8, but an eager call's
+// host time is 10 us instead of 18, and the calls are the host's.
 // ---------------------------------------------------------------------------
-template <int BNT, int STAGES, bool kF32>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int BNT, int STAGES, bool kF32, bool kInside>
+__global__ void __launch_bounds__(kInside ? kInsideThreads : kThreads, 1)
     k_mx_fewrow(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
-                typename Out<kF32>::T* __restrict__ y, int Mtok, int N, int K, int S, int w_early, int* err) {
+                const uint16_t* __restrict__ x, size_t x_stride, typename Out<kF32>::T* __restrict__ y, int Mtok, int N,
+                int K, int S, int w_early, int* err) {
   static_assert(BNT % 16 == 0 && BNT >= 16 && BNT <= 64, "BNT");
   using O = Out<kF32>;
   constexpr uint32_t A_BYTES = kBM * kRowBytes;
   constexpr uint32_t B_BYTES = BNT * kRowBytes;
   constexpr uint32_t SF_BYTES = 2 * kSfTile;
-  constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
+  constexpr uint32_t X_BYTES = B_BYTES + SF_BYTES;                   // a stage of X with its scales
+  constexpr uint32_t STAGE_BYTES = A_BYTES + SF_BYTES + (kInside ? 0u : X_BYTES);   // W, its scales, X, its scales
   static_assert(STAGE_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
   constexpr uint32_t ACC_COLS = BNT < 32 ? 32 : BNT;
   constexpr uint32_t SFA_COL = ACC_COLS, SFB_COL = ACC_COLS + 8;
@@ -408,14 +417,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align<1024>(smem_raw);
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * STAGE_BYTES);
+  const int kblocks = (K + kBK - 1) / kBK;
+  uint8_t* xs = smem + STAGES * STAGE_BYTES;          // kInside: this CTA's stages of X
+  Ctl* ctl = reinterpret_cast<Ctl*>(xs + (kInside ? (kblocks + S - 1) / S : 0) * X_BYTES);
   float* red = reinterpret_cast<float*>(smem);
   volatile int* abort = &ctl->abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();            // of the S CTAs of a weight block
   const int n0 = (int)(blockIdx.x / (unsigned)S) * kBM;
-  const int kblocks = (K + kBK - 1) / kBK;
   const int kb0 = rank * kblocks / S;
   const int nk = (rank + 1) * kblocks / S - kb0;
 
@@ -426,12 +436,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&ctl->tfull[0], 1);
     mbar_init(&ctl->drain, 1);
+    if (kInside)
+      for (int i = 0; i < kInsideStages; ++i) mbar_init(&ctl->xfull[i], (kInsideThreads - 64) / 32);
     ctl->abort = 0;
     fence_mbar_init();
     tma_prefetch(&tmW);
-    tma_prefetch(&tmX);
     tma_prefetch(&tmSW);
-    tma_prefetch(&tmSX);
+    if (!kInside) {
+      tma_prefetch(&tmX);
+      tma_prefetch(&tmSX);
+    }
   }
   if (warp == 1) {
     tmem_alloc(&ctl->tmem_base, TMEM_COLS);
@@ -450,13 +464,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* bar = &ctl->full[i % STAGES];
         mbar_expect_tx(bar, STAGE_BYTES);
         tma_load_2d(s, &tmW, bar, (kb0 + i) * kRowBytes, n0);
-        tma_load_2d(s + A_BYTES + B_BYTES, &tmSW, bar, (kb0 + i) * 256, n0 / 128);
+        tma_load_2d(s + A_BYTES, &tmSW, bar, (kb0 + i) * 256, n0 / 128);
       };
       auto load_x = [&](int i) {
+        if (kInside) return;
         uint8_t* s = smem + (i % STAGES) * STAGE_BYTES;
         uint64_t* bar = &ctl->full[i % STAGES];
-        tma_load_2d(s + A_BYTES, &tmX, bar, (kb0 + i) * kRowBytes, 0);
-        tma_load_2d(s + A_BYTES + B_BYTES + SF_BYTES, &tmSX, bar, (kb0 + i) * 256, 0);
+        tma_load_2d(s + A_BYTES + SF_BYTES, &tmX, bar, (kb0 + i) * kRowBytes, 0);
+        tma_load_2d(s + A_BYTES + SF_BYTES + B_BYTES, &tmSX, bar, (kb0 + i) * 256, 0);
       };
       if (w_early)
         for (int i = 0; i < npre; ++i) load_w(i);
@@ -490,23 +505,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stg = 0;
       uint32_t phase = 0;
       for (int i = 0; i < nk; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[stg], phase, abort))) {
+        if (!__all_sync(0xffffffffu, (!kInside || mbar_wait(&ctl->xfull[i], 0, abort)) &&
+                                         mbar_wait(&ctl->full[stg], phase, abort))) {
           if (lead) raise_abort(ctl, err);
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t a_addr = smem_u32(smem + stg * STAGE_BYTES);
-        const uint32_t sf_addr = a_addr + A_BYTES + B_BYTES;
+        const uint32_t sf_addr = a_addr + A_BYTES;
+        const uint32_t x_addr = kInside ? smem_u32(xs + i * X_BYTES) : sf_addr + SF_BYTES;
         const uint64_t adesc = desc_kmajor_sw128(a_addr);
-        const uint64_t bdesc = desc_kmajor_sw128(a_addr + A_BYTES);
+        const uint64_t bdesc = desc_kmajor_sw128(x_addr);
         auto issue = [&](auto n) {
           if (lead) {
             constexpr int kN = decltype(n)::value;
 #pragma unroll
             for (int t = 0; t < (kN + 1) / 2; ++t) {
               tmem_cp_32x128b(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
-              tmem_cp_32x128b(tmem_base + SFB_COL + 4 * t, desc_scale_tile(sf_addr + SF_BYTES + t * kSfTile));
+              tmem_cp_32x128b(tmem_base + SFB_COL + 4 * t, desc_scale_tile(x_addr + B_BYTES + t * kSfTile));
             }
 #pragma unroll
             for (int j = 0; j < kN; ++j)
@@ -529,26 +546,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else {
-      // ---------------- epilogue warps 2..5: accumulator rows -> own exchange buffer
-      const int quarter = warp & 3;
-      float* dst = red + (quarter * 32 + lane) * RED_LD;
-      if (__all_sync(0xffffffffu, nk > 0 && mbar_wait(&ctl->tfull[0], 0, abort))) {
-        tc_fence_after();
+      if constexpr (kInside) {
+        // ---------------- warps 2..9 quantise: 16 values a thread, 16 rows of a stage at a time
+        constexpr int kRows = (kInsideThreads - 64) / 16, kSub = BNT / kRows, kBatch = 8;   // (a batch's loads under way together)
+        const int t = threadIdx.x - 64, c = t & 15;
+        for (int j0 = 0; j0 < nk * kSub; j0 += kBatch) {
+          uint4 v[kBatch][2];
 #pragma unroll
-        for (int c = 0; c < BNT; c += 16) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, r);
-          tmem_ld_wait();
+          for (int b = 0; b < kBatch; ++b) {
+            const int j = j0 + b, row = j % kSub * kRows + (t >> 4), k = (kb0 + j / kSub) * kBK + c * 16;
+            v[b][0] = v[b][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (j < nk * kSub && row < Mtok && k < K) {
+              const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)row * x_stride + k);
+              v[b][0] = __ldg(p);
+              v[b][1] = __ldg(p + 1);
+            }
+          }
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4*>(dst + c + 4 * q) =
-                make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
-                            __uint_as_float(r[4 * q + 3]));
+          for (int b = 0; b < kBatch; ++b) {
+            const int j = j0 + b, row = j % kSub * kRows + (t >> 4);
+            if (j >= nk * kSub) break;
+            uint32_t code;
+            const uint2 q = quant16(v[b], &code);
+            uint8_t* st = xs + j / kSub * X_BYTES;
+            // as TMA writes 128-byte rows in the 128-byte swizzle
+            *reinterpret_cast<uint2*>(st + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8) = q;
+            if (!(c & 1)) st[B_BYTES + (c >> 3) * kSfTile + (row & 31) * 16 + (row >> 5) * 4 + ((c & 7) >> 1)] = (uint8_t)code;
+            if ((j + 1) % kSub == 0) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl->xfull[j / kSub]);
+            }
+          }
         }
-        tc_fence_before();
-      } else {
-        if (nk > 0) raise_abort(ctl, err);
-        for (int c = 0; c < BNT; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      // ---------------- epilogue warps 2..5: accumulator rows -> own exchange buffer
+      if (!kInside || warp < 6) {
+        const int quarter = warp & 3;
+        float* dst = red + (quarter * 32 + lane) * RED_LD;
+        if (__all_sync(0xffffffffu, nk > 0 && mbar_wait(&ctl->tfull[0], 0, abort))) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < BNT; c += 16) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<float4*>(dst + c + 4 * q) =
+                  make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
+                              __uint_as_float(r[4 * q + 3]));
+          }
+          tc_fence_before();
+        } else {
+          if (nk > 0) raise_abort(ctl, err);
+          for (int c = 0; c < BNT; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       }
     }
   }
@@ -558,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r0 = rank * kBM / S, rows = (rank + 1) * kBM / S - r0;
     const int quads = (Mtok + 3) >> 2;
     const uint32_t red_s = smem_u32(red);
-    for (int idx = threadIdx.x; idx < rows * quads; idx += kThreads) {
+    for (int idx = threadIdx.x; idx < rows * quads; idx += kInside ? kInsideThreads : kThreads) {
       const int nl = r0 + idx % rows, m = 4 * (idx / rows);
       const uint32_t off = red_s + (uint32_t)((nl * RED_LD + m) * 4);
       float4 v[8];
@@ -847,17 +900,17 @@ bool map_out(CUtensorMap* map, void* y, int M, int N) {
 
 // Clusters of `size` CTAs of a kernel that fit on the device at once (found
 // once per device, kernel and size).
-int max_clusters(const void* kernel, int size, size_t smem) {
+int max_clusters(const void* kernel, int size, size_t smem, int threads = kThreads) {
   static std::mutex mu;
-  static std::map<std::tuple<int, const void*, int>, int> known;
+  static std::map<std::tuple<int, const void*, int, size_t>, int> known;
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(mu);
-  auto it = known.find({dev, kernel, size});
+  auto it = known.find({dev, kernel, size, smem});
   if (it != known.end()) return it->second;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(size * device_sm_count()));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -871,7 +924,7 @@ int max_clusters(const void* kernel, int size, size_t smem) {
     cudaGetLastError();
     n = device_sm_count() / size > 1 ? device_sm_count() / size : 1;
   }
-  known[{dev, kernel, size}] = n;
+  known[{dev, kernel, size, smem}] = n;
   return n;
 }
 
@@ -936,7 +989,7 @@ cudaError_t launch_fewrow(const MxOperand& x, const MxOperand& w, void* y, int M
   if ((e = map_scales(&tsw, w.scales, N, K, 1)) != cudaSuccess) return e;
   if ((e = map_scales(&tsx, x.scales, Mtok, K, 1)) != cudaSuccess) return e;
   const size_t smem = 1024 + (size_t)STAGES * ((kBM + BNT) * kRowBytes + 4 * kSfTile) + sizeof(Ctl);
-  auto k = k_mx_fewrow<BNT, STAGES, kF32>;
+  auto k = k_mx_fewrow<BNT, STAGES, kF32, false>;
   if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
   const int nb = (N + kBM - 1) / kBM;
   const int S = fewrow_splits(reinterpret_cast<const void*>(k), smem, nb, (K + kBK - 1) / kBK, BNT);
@@ -962,8 +1015,69 @@ cudaError_t launch_fewrow(const MxOperand& x, const MxOperand& w, void* y, int M
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k, tw, tx, tsw, tsx, static_cast<typename Out<kF32>::T*>(y), Mtok, N, K, S,
-                            (int)w_early, err);
+  return cudaLaunchKernelEx(&cfg, k, tw, tx, tsw, tsx, (const uint16_t*)nullptr, (size_t)0,
+                            static_cast<typename Out<kF32>::T*>(y), Mtok, N, K, S, (int)w_early, err);
+}
+
+// The few-row kernel that quantises X itself: over how many CTAs K is split, 0
+// where that form is not for the shape.  A CTA's quantising warps take up to 12
+// pieces of 16 values a thread (beyond that the quantisation by itself, spread
+// over the GPU, is faster); the clusters of all blocks of W run at once.
+constexpr int kInsideRing = 4;
+constexpr int inside_stages(int bnt) { return 12 * 16 / bnt < kInsideStages ? 12 * 16 / bnt : kInsideStages; }
+size_t inside_smem(int bnt, int stages) {
+  return 1024 + (size_t)kInsideRing * (kBM * kRowBytes + 2 * kSfTile) +
+         (size_t)stages * (bnt * kRowBytes + 2 * kSfTile) + sizeof(Ctl);
+}
+template <int BNT>
+int inside_splits(int N, int K) {
+  const void* k = reinterpret_cast<const void*>(k_mx_fewrow<BNT, kInsideRing, false, true>);   // (f32's takes as much)
+  const int kblocks = (K + kBK - 1) / kBK, nb = (N + kBM - 1) / kBM, sms = device_sm_count();
+  if (nb >= sms) return 0;
+  int s = sms / nb;
+  if (s < 2 && BNT <= 16) s = 2;
+  if (s > 8) s = 8;
+  if (s > kblocks / 2) s = kblocks / 2 > 1 ? kblocks / 2 : 1;
+  for (; s >= 1; --s) {
+    const int stages = (kblocks + s - 1) / s;
+    if (stages > inside_stages(BNT)) return 0;   // (fewer splits only mean more)
+    const size_t smem = inside_smem(BNT, stages);
+    if (ensure_smem_optin(k, (int)inside_smem(BNT, inside_stages(BNT))) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    if (s == 1 || (s == 2 && sms / nb < 2) || max_clusters(k, s, smem, kInsideThreads) >= nb)
+      return s;
+  }
+  return 0;
+}
+
+template <int BNT, bool kF32>
+cudaError_t launch_inside(const uint16_t* x, size_t x_stride, const MxOperand& w, void* y, int Mtok, int N, int K, int S,
+                          int* err, cudaStream_t st) {
+  CUtensorMap tw, tsw;
+  cudaError_t e;
+  if ((e = map_codes(&tw, w.codes, N, K, kBM)) != cudaSuccess) return e;
+  if ((e = map_scales(&tsw, w.scales, N, K, 1)) != cudaSuccess) return e;
+  auto k = k_mx_fewrow<BNT, kInsideRing, kF32, true>;
+  if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)inside_smem(BNT, inside_stages(BNT)))) != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(S * ((N + kBM - 1) / kBM)));
+  cfg.blockDim = dim3(kInsideThreads);
+  cfg.dynamicSmemBytes = inside_smem(BNT, ((K + kBK - 1) / kBK + S - 1) / S);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, tw, tw, tsw, tsw, x, x_stride,
+                            static_cast<typename Out<kF32>::T*>(y), Mtok, N, K, S, 0, err);
 }
 
 template <bool kF32>
@@ -990,6 +1104,23 @@ cudaError_t gemm_mx(const MxOperand& a, const MxOperand& w, void* y, bool f32, i
                     cudaStream_t st) {
   if (M <= 0) return cudaSuccess;
   return f32 ? gemm_t<true>(a, w, y, M, N, K, w_early, err, st) : gemm_t<false>(a, w, y, M, N, K, w_early, err, st);
+}
+
+int mx_inside_splits(int M, int N, int K) {
+  if (M < 1 || M > 64) return 0;
+  return M <= 16 ? inside_splits<16>(N, K) : M <= 32 ? inside_splits<32>(N, K) : inside_splits<64>(N, K);
+}
+
+cudaError_t gemm_mx_inside(const uint16_t* x, size_t x_stride, const MxOperand& w, void* y, bool f32, int M, int N, int K,
+                           int splits, int* err, cudaStream_t st) {
+  auto go = [&](auto bnt) {
+    constexpr int kB = decltype(bnt)::value;
+    return f32 ? launch_inside<kB, true>(x, x_stride, w, y, M, N, K, splits, err, st)
+               : launch_inside<kB, false>(x, x_stride, w, y, M, N, K, splits, err, st);
+  };
+  if (M <= 16) return go(std::integral_constant<int, 16>());
+  if (M <= 32) return go(std::integral_constant<int, 32>());
+  return go(std::integral_constant<int, 64>());
 }
 
 }  // namespace m2

@@ -1543,7 +1543,7 @@ extern "C" m2_status mxfp4_linear_bf16_workspace_size(int M, int N, int K, size_
   m2_status s = check_mx_shape(M, K, "mxfp4_linear_bf16_workspace_size");
   if (s) return s;
   if (N < 1 || N > (1 << 24)) return fail(M2_ESHAPE, "mxfp4_linear_bf16_workspace_size: N %d not in [1, 2^24]", N);
-  *bytes = align256(code_bytes(M, K)) + mx_scale_bytes(M, K);
+  *bytes = mx_inside_splits(M, N, K) ? 0 : align256(code_bytes(M, K)) + mx_scale_bytes(M, K);
   return M2_OK;
 }
 
@@ -1556,10 +1556,11 @@ extern "C" m2_status mxfp4_linear_bf16(const uint16_t* x, size_t row_stride, con
   if (M && !x) return fail(M2_EINVAL, "mxfp4_linear_bf16: null pointer");
   const size_t yb = (size_t)M * N * (out_dtype == M2_DTYPE_F32 ? 4 : 2), xb = extent(M, row_stride, K, 2);
   if (overlap(y, yb, x, xb)) return fail(M2_EINVAL, "mxfp4_linear_bf16: y overlaps an input");
-  const size_t cb = align256(code_bytes(M, K)), need = cb + mx_scale_bytes(M, K);
+  const int splits = mx_inside_splits(M, N, K);
+  const size_t cb = align256(code_bytes(M, K)), need = splits ? 0 : cb + mx_scale_bytes(M, K);
   if (ws_bytes < need || (need && !workspace))
     return fail(M2_ENOMEM, "mxfp4_linear_bf16: workspace %zu bytes < %zu needed", ws_bytes, need);
-  if ((uintptr_t)workspace % 256) return fail(M2_EINVAL, "mxfp4_linear_bf16: workspace must be 256-byte aligned");
+  if (need && (uintptr_t)workspace % 256) return fail(M2_EINVAL, "mxfp4_linear_bf16: workspace must be 256-byte aligned");
   if (overlap(workspace, need, x, xb) || overlap(workspace, need, y, yb) ||
       overlap(workspace, need, w_codes, code_bytes(N, K)) || overlap(workspace, need, w_scales, mx_scale_bytes(N, K)))
     return fail(M2_EINVAL, "mxfp4_linear_bf16: the workspace overlaps an argument");
@@ -1568,6 +1569,10 @@ extern "C" m2_status mxfp4_linear_bf16(const uint16_t* x, size_t row_stride, con
   if ((s = standalone_error_word(&err))) return s;
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (splits) {
+    M2_CUDA(gemm_mx_inside(x, row_stride, {w_codes, w_scales}, y, out_dtype == M2_DTYPE_F32, M, N, K, splits, err, st));
+    return M2_OK;
+  }
   M2_CUDA(launch_mx_quant(x, row_stride, M, K, codes, codes + cb, st));
   M2_CUDA(gemm_mx({codes, codes + cb}, {w_codes, w_scales}, y, out_dtype == M2_DTYPE_F32, M, N, K, true, err, st));
   return M2_OK;

@@ -12,10 +12,9 @@
 // memory: tiles of 128 rows x 4 blocks (128 values of K), 512 bytes, byte
 // (r % 32) 16 + (r / 32) 4 + b of a tile for row r and block b; tiles
 // [ceil(rows / 128)][ceil(K / 128)], zero past the rows and past K.
-#include <cuda_bf16.h>
-
 #include "launch_util.h"
 #include "m2_kernels.h"
+#include "mxfp4.cuh"
 
 namespace m2 {
 
@@ -24,45 +23,9 @@ namespace {
 constexpr int kMxThreads = 256;
 constexpr int kMxUnroll = 2;
 
-__host__ __device__ inline int mx_kb(int K) { return (K + 127) / 128; }
 // Bytes offset of the four scale codes of row r's 128-value group kb.
 __device__ __forceinline__ size_t scale_word(int r, int kb, int KB) {
   return ((size_t)(r >> 7) * KB + kb) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
-}
-
-// Scale code of a block from its largest |x| (bf16 bits): exponent field less 2,
-// 0 at least (subnormals and zeros included), 255 for infinities and NaN.
-__device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
-  const uint32_t e = amax >> 7;
-  return amax >= 0x7F80u ? 255u : e > 2u ? e - 2u : 0u;
-}
-
-__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
-__device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
-// The larger magnitudes of two pairs, NaN if there is one.
-__device__ __forceinline__ __nv_bfloat162 max_abs(__nv_bfloat162 a, __nv_bfloat162 b) {
-  return __hmax2_nan(__habs2(a), __habs2(b));
-}
-__device__ __forceinline__ __nv_bfloat162 max_abs(const uint4& v) {
-  return max_abs(max_abs(as_bf16x2(v.x), as_bf16x2(v.y)), max_abs(as_bf16x2(v.z), as_bf16x2(v.w)));
-}
-
-// e2m1 codes of eight bf16 times f (a power of two: exact, but for products
-// below bf16's range, whose code is 0 either way).
-__device__ __forceinline__ uint32_t quant8(const uint4& v, __nv_bfloat162 f) {
-  const uint32_t w[4] = {bits_of(__hmul2(as_bf16x2(v.x), f)), bits_of(__hmul2(as_bf16x2(v.y), f)),
-                         bits_of(__hmul2(as_bf16x2(v.z), f)), bits_of(__hmul2(as_bf16x2(v.w), f))};
-  uint32_t q;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}\n"
-      : "=r"(q)
-      : "r"(w[0] << 16), "r"(w[0] & 0xFFFF0000u), "r"(w[1] << 16), "r"(w[1] & 0xFFFF0000u), "r"(w[2] << 16),
-        "r"(w[2] & 0xFFFF0000u), "r"(w[3] << 16), "r"(w[3] & 0xFFFF0000u));
-  return q;
 }
 
 // bf16 values of eight e2m1 codes times f.  A magnitude's two bytes come from
@@ -82,10 +45,6 @@ __device__ __forceinline__ uint4 dequant8(uint32_t q, __nv_bfloat162 f) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 2^(127 - code) twice, for code <= 252: the exact factor of x / 2^(code - 127).
-__device__ __forceinline__ __nv_bfloat162 inverse_scale(uint32_t code) {
-  return as_bf16x2(((254u - code) << 7) * 0x10001u);
-}
 // 2^(code - 127) twice, NaN for 255.
 __device__ __forceinline__ __nv_bfloat162 scale_value(uint32_t code) {
   return as_bf16x2((code == 255u ? 0x7FC0u : code ? code << 7 : 0x0040u) * 0x10001u);
@@ -135,24 +94,15 @@ __global__ void __launch_bounds__(kMxThreads) k_mx_quant(const uint16_t* __restr
   at = Units(K);
 #pragma unroll
   for (int i = 0; i < kMxUnroll; ++i, at.step()) {
-    const uint32_t two = bits_of(max_abs(max_abs(v[i][0]), max_abs(v[i][1])));
-    uint32_t m = max(two & 0xFFFFu, two >> 16);   // (no sign: magnitudes order like their bits)
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const uint32_t code = scale_code(m);
+    uint32_t code;
+    const uint2 q = quant16(v[i], &code);
     uint32_t word = code << (8 * (lane8 >> 1));
     word |= __shfl_xor_sync(0xffffffffu, word, 2);
     word |= __shfl_xor_sync(0xffffffffu, word, 4);
     if (lane8 == 0 && at.row < rows_pad)
       *reinterpret_cast<uint32_t*>(scales + scale_word(at.row, at.kb, at.KB)) = word;
     const int k = at.kb * 128 + lane8 * 16;
-    if (at.row < rows && k < K) {
-      uint2 q = make_uint2(0u, 0u);
-      if (code != 255u) {
-        const __nv_bfloat162 f = inverse_scale(code);
-        q = make_uint2(quant8(v[i][0], f), quant8(v[i][1], f));
-      }
-      *reinterpret_cast<uint2*>(codes + ((size_t)at.row * K + k) / 2) = q;
-    }
+    if (at.row < rows && k < K) *reinterpret_cast<uint2*>(codes + ((size_t)at.row * K + k) / 2) = q;
   }
 }
 

@@ -243,18 +243,49 @@ def test_scales_far_apart(M):
     check_product(m2.mxfp4_linear(qa, qw, dtype=F32), a, w)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 300, 2688), (64, 2688, 4096), (130, 333, 160), (500, 1000, 96)])
-def test_quantise_inside_gives_the_same_bits(M, N, K):
+@pytest.mark.parametrize("M,N,K", [(1, 300, 2688), (2, 10304, 2688), (16, 129, 160), (7, 2000, 5000 // 32 * 32), (17, 777, 1056),
+                                   (33, 2688, 32), (64, 2688, 4096), (50, 1000, 288), (64, 10304, 2688), (130, 333, 160),
+                                   (500, 1000, 96)])
+def test_quantise_inside(M, N, K):
+    """The values of mxfp4_quant, products within the bound, and where it takes
+    a workspace (the same kernels on the same operands) the same bits."""
     g = torch.Generator(device="cuda").manual_seed(M)
     wide = torch.randn(M, K + 40, generator=g, device="cuda").to(BF)
     qw, w = operand(np.random.default_rng(K), N, K)
     x = wide[:, 8:8 + K]
+    x[M // 2, 5] = 0.0
+    q = m2.mxfp4_quant(x)
+    a = values(*unpack(q)[:2])
+    need = m2.mxfp4_linear_bf16_workspace_size(M, N, K)
     for dtype in (BF, F32):
-        want = m2.mxfp4_linear(m2.mxfp4_quant(x), qw, dtype=dtype)
-        assert torch.equal(m2.mxfp4_linear_bf16(x, qw, dtype=dtype), want)
-        ws = torch.empty(m2.mxfp4_linear_bf16_workspace_size(M, N, K), dtype=torch.uint8, device="cuda").fill_(255)
-        y = torch.empty((M, N), dtype=dtype, device="cuda")
-        assert m2.mxfp4_linear_bf16(x, qw, y=y, workspace=ws) is y and torch.equal(y, want)
+        got = m2.mxfp4_linear_bf16(x, qw, dtype=dtype)
+        torch.cuda.synchronize()
+        m2.check_standalone()
+        check_product(got, a, w)
+        if need:
+            assert torch.equal(got, m2.mxfp4_linear(q, qw, dtype=dtype))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)
+        buf = torch.full((M * N + 8,), float("nan"), dtype=dtype, device="cuda")
+        y = buf[:M * N].view(M, N)
+        assert m2.mxfp4_linear_bf16(x, qw, y=y, workspace=ws) is y and torch.equal(y, got)
+        assert torch.isnan(buf[M * N:]).all()
+
+
+@pytest.mark.parametrize("M", [3, 20, 60])
+def test_quantise_inside_of_small_whole_numbers_is_exact(M):
+    """Sums within f32's 24 bits: the quantised values and places have to be
+    right to the bit, blocks that become NaN too."""
+    rng = np.random.default_rng(M)
+    (qa, a), (qw, w) = operand(rng, M, 800, 0), operand(rng, 640, 800, 0)
+    x = m2.mxfp4_dequant(qa)
+    x[:, 3::32] = 6.0                                          # every block's scale stays 1
+    y = m2.mxfp4_linear_bf16(x, qw, dtype=F32)
+    assert np.array_equal(y.double().cpu().numpy(), np64(x) @ w.T)
+    x[1, 70], x[2, 799] = float("nan"), float("inf")
+    z = m2.mxfp4_linear_bf16(x, qw, dtype=F32)
+    bad = torch.zeros(M, 640, dtype=torch.bool, device="cuda")
+    bad[1] = bad[2] = True
+    assert torch.equal(torch.isnan(z), bad) and torch.equal(z[~bad], y[~bad])
 
 
 @pytest.mark.parametrize("M", [12, 300])
@@ -328,6 +359,6 @@ def test_python_refuses_what_does_not_fit():
     with pytest.raises(ValueError):
         m2.mxfp4_pack(qw.codes, qw.scales)
     with pytest.raises(m2.M2Error) as e:
-        m2.mxfp4_linear_bf16(torch.zeros(2, 64, dtype=BF, device="cuda"), qw,
+        m2.mxfp4_linear_bf16(torch.zeros(100, 64, dtype=BF, device="cuda"), qw,
                              workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == m2.M2_ENOMEM

@@ -101,7 +101,7 @@ def test_linear_refuses_pointers(m2, kw):
 
 
 def _linear_bf16(m2, **kw):
-    a = dict(x=at(1), stride=128, wc=at(3), ws=at(4), y=at(5), dtype=1, M=4, N=64, K=128, work=at(6), n=BIG)
+    a = dict(x=at(1), stride=128, wc=at(3), ws=at(4), y=at(5), dtype=1, M=100, N=64, K=128, work=at(6), n=BIG)
     a.update(kw)
     return m2._lib.mxfp4_linear_bf16(a["x"], a["stride"], a["wc"], a["ws"], a["y"], a["dtype"], a["M"], a["N"], a["K"],
                                      a["work"], a["n"], None)
@@ -112,7 +112,7 @@ def test_linear_bf16_refuses(m2):
     assert m2._lib.mxfp4_linear_bf16_workspace_size(4, 64, 128, None) == m2.M2_EINVAL
     assert m2._lib.mxfp4_linear_bf16_workspace_size(4, 0, 128, ctypes.byref(n)) == m2.M2_ESHAPE
     assert m2._lib.mxfp4_linear_bf16_workspace_size(4, 64, 130, ctypes.byref(n)) == m2.M2_ESHAPE
-    assert m2._lib.mxfp4_linear_bf16_workspace_size(4, 64, 128, ctypes.byref(n)) == m2.M2_OK and n.value > 0
+    assert m2._lib.mxfp4_linear_bf16_workspace_size(100, 64, 128, ctypes.byref(n)) == m2.M2_OK and n.value > 0
     assert _linear_bf16(m2, n=n.value - 1) == m2.M2_ENOMEM
     assert _linear_bf16(m2, work=None) == m2.M2_ENOMEM
     for kw in (dict(work=at(6) + 128), dict(x=at(1) + 8), dict(x=None), dict(y=at(1) + 64), dict(work=at(1), n=n.value),
