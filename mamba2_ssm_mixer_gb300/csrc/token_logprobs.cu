@@ -879,14 +879,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     // ---------------- readers
     int stage = 0, turn = 0;
     uint32_t phase = 0, turn_phase = 0;
-    int token = token_of(row0);
+    // the tokens to score and their logits are asked for a row ahead of their use
+    int token = token_of(row0), token1 = token_of(row0 + row_step);
     float xt = logit_of(row0, token);
     for (int row = row0; row < rows; row += row_step) {
       const RowAt<T> r(logits, stride, row, vocab);
       int v0, v1;
       slice_of(r, v0, v1);
       const Cut cut(v1 - v0);
-      const int next_token = token_of(row + row_step);
+      const float xt1 = logit_of(row + row_step, token1);
+      const int token2 = token_of(row + 2 * row_step);
       const bool masked = !(xt > -INFINITY);                    // (NaN too)
       // before the given token's vector equal logits count as greater
       const int vt = valid(token) && !masked ? (token + r.off) / V::kN : -1;
@@ -896,7 +898,6 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 
       Sums<T> sums;
       float m = -INFINITY, gm = -INFINITY;
-      bool clamp = false;   // the row has had masked logits
       int greater = 0, group = 0, left = cut.group;
       for (int ch = 0; ch < cut.chunks; ++ch) {
         wait(&sh->full[stage], phase);
@@ -930,25 +931,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         sums.reach(mx);
         if (sums.c > kNone) {
           const uint64_t cc = pair(-sums.c, -sums.c);
-          bool summed = false;
-          if (!clamp) {
-            Sums<T> t = sums;
-            const typename V::Low none(0.f);
+          const typename V::Low low = sums.low();
 #pragma unroll
-            for (int j = 0; j < kVpt; ++j)
-              V::template sums<false>(q[j], none, cc, t.s[j & 1], t.u[j & 1]);
-            // masked logits and NaN make U a NaN (0 times -inf): from here on they are looked for in this row
-            const float2 n = unpair(add_pair(t.u[0], t.u[1]));
-            summed = !isnan(n.x + n.y);
-            clamp = !summed;
-            if (summed) sums = t;
-          }
-          if (!summed) {
-            const typename V::Low low = sums.low();
-#pragma unroll
-            for (int j = 0; j < kVpt; ++j)
-              V::template sums<true>(q[j], low, cc, sums.s[j & 1], sums.u[j & 1]);
-          }
+          for (int j = 0; j < kVpt; ++j) V::template sums<true>(q[j], low, cc, sums.s[j & 1], sums.u[j & 1]);
         }
         typename V::Count count;
         if (vt < vc || vt >= vc + kChunkVecs) {   // (the same for all)
@@ -973,8 +958,6 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         }
         greater += count.total();
       }
-      const float next_xt = logit_of(row + row_step, next_token);
-
       // ---------------- the warp's part to the selectors
       const LpPart a = join_lanes(sums.part(m, greater), 32);
       if (lane == 0) hand.warp[warp] = a;
@@ -986,8 +969,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->read[turn]);
       if (++turn == 2) turn = 0, turn_phase ^= 1u;
-      token = next_token;
-      xt = next_xt;
+      token = token1, token1 = token2;
+      xt = xt1;
     }
   } else {
     // ---------------- selectors
