@@ -8,9 +8,9 @@
 // thread run in the order issued, so one set of scale columns serves every
 // stage.
 //
-// k_mx_pair (more than 64 rows): persistent two-CTA clusters on 256 x BN
-//   output tiles, as the e4m3 kernel of gemm_tc.cu; each CTA keeps the scales
-//   of its own 128 rows of A and of all BN columns.
+// k_mx_pair (more than 64 rows): persistent two-CTA clusters on 256-row output
+//   tiles, as the e4m3 kernel of gemm_tc.cu; each CTA keeps the scales of its
+//   own 128 rows of A and of all of the tile's columns.
 // k_mx_fewrow (up to 64 rows): the weights are the MMA's 128-row operand, K
 //   is split over the CTAs of a cluster and the partial sums meet in
 //   distributed shared memory.
@@ -42,6 +42,10 @@ constexpr int kBK = 256;         // values of K per stage
 constexpr int kThreads = 192;    // 6 warps: producer, MMA, 4 x epilogue
 constexpr uint32_t kSfTile = 512;
 constexpr int kInsideStages = 12, kInsideThreads = kThreads + 128;   // (the form that quantises X itself)
+
+// Tiles of 128 rows of scales that a tile of `width` columns lies in: it starts
+// on a multiple of 64, tiles of 128 on their own width.
+__host__ __device__ constexpr int sb_tiles(int width) { return width == 128 ? 1 : (width + 64 + 127) / 128; }
 
 struct __align__(8) Ctl {
   uint64_t full[8];
@@ -100,8 +104,8 @@ struct Out<true> {
 // map, 128-byte slices go through shared memory and TMA stores; else 32 x 32
 // pieces do, transposed, so that a warp writes a row's consecutive elements
 // (517 x 5003 x 1056 f32: 11.5 us, rows written by a thread each 35.5).
-template <int BN, bool kF32>
-__device__ __forceinline__ void epilogue_rows(uint32_t tcol, uint8_t* bufs, int& buf, const CUtensorMap* tmC,
+template <bool kF32>
+__device__ __forceinline__ void epilogue_rows(int BN, uint32_t tcol, uint8_t* bufs, int& buf, const CUtensorMap* tmC,
                                               bool tma_store, typename Out<kF32>::T* __restrict__ C, int M, int N,
                                               int row0, int n0, int lane) {
   using O = Out<kF32>;
@@ -167,39 +171,42 @@ __device__ __forceinline__ void epilogue_rows(uint32_t tcol, uint8_t* bufs, int&
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// 256 x BN tiles on CTA pairs.  CTA r of a pair stages rows [128 r, ..) of A
-// with their scales, columns [r BN / 2, ..) of B and the scales of all of the
-// tile's columns (two 128-row tiles of them: a tile of B starts on a multiple
-// of 64 rows, in the middle of a scale tile for odd ones, and the MMA then
-// reads from the third of the tile's columns on).  The rest as k_gemm_pair.
-// 8192 x 10304 x 2688 in 84 us (5.4 PFLOP/s).  The MMAs alone take 48 at their
-// 96 clocks, with their scales' copies and the loads 62 to 64: the loads then
-// run at 18 TB/s out of L2, and the stores take the rest in its way (to the
-// same few lines 81, none at all 67).  256 columns a tile need both
-// accumulators to share columns with each other: 88, a bubble of 2000 clocks
-// a tile; clusters of two pairs sharing A or B by multicast 85 (their loads
-// are fewer, but only 36 such clusters fit); 256-bit stores from the registers
-// instead of staged ones 85.
+// Tiles of 256 rows on CTA pairs.  CTA r of a pair stages rows [128 r, ..) of A
+// with their scales, half of the tile's columns of B and the scales of all of
+// them (sb_tiles of 128 rows: a tile may start in the middle of one, and the MMA
+// then reads from its third column on).  The two accumulators may differ in
+// width (W0, W1): a pair's unit is then a tile of each, side by side; 256 + 192
+// columns and the scales are what TMEM holds.  The rest as k_gemm_pair.
+// Bound by the bytes into an SM: 8192 x 10304 x 2688 takes 82 us (5.5 PFLOP/s), at
+// 55 bytes a clock and SM for operands and output; the MMAs alone take 48 at
+// their 128 and 96 clocks, with the loads but no stores 68.  192 columns in both
+// accumulators: 84 (5669 x 2688 x 4096: 24.4 us, 22.3 with 256 + 192).  256 in
+// both, sharing 24 columns: 88, a bubble of 2000 clocks a tile.  Clusters of two
+// pairs that share A or B by multicast: 85 (fewer bytes out of L2, the same into
+// an SM, and only 36 such clusters fit).  256-bit stores from the registers
+// instead of staged ones: 85.
 // ---------------------------------------------------------------------------
-template <int BN, int STAGES, bool kF32>
+template <int W0, int W1, int STAGES, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_mx_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    k_mx_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
+              const __grid_constant__ CUtensorMap tmB1,
               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
               const __grid_constant__ CUtensorMap tmC, int tma_store, typename Out<kF32>::T* __restrict__ C, int M, int N,
               int K, int* err) {
   static_assert(STAGES <= 8, "STAGES");
   constexpr int kPM = 2 * kBM;
+  constexpr int kSub = W0 == W1 ? 1 : 2, kSpan = W0 == W1 ? W0 : W0 + W1;   // tiles and columns of a unit
   constexpr uint32_t A_BYTES = kBM * kRowBytes;
-  constexpr uint32_t B_BYTES = (BN / 2) * kRowBytes;
+  constexpr uint32_t B_BYTES = (W0 / 2) * kRowBytes;
   constexpr uint32_t SA_BYTES = 2 * kSfTile;          // 128 rows x 256 values
-  constexpr int kSbTiles = BN > 128 ? 2 : 1;          // tiles of 128 rows of B that a tile's columns lie in
+  constexpr int kSbTiles = sb_tiles(W0);
   constexpr uint32_t SB_BYTES = kSbTiles * 2 * kSfTile;
   constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-  static_assert(BN == 64 || BN == 128 || BN == 192, "a tile's columns start on half a scale tile and lie in kSbTiles");
+  static_assert(W0 >= W1 && kSpan % 64 == 0 && W0 % 64 == 0, "a tile's columns start on half a scale tile");
   static_assert(STAGE_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "operand tiles on 1024-byte boundaries");
   constexpr uint32_t TMEM_COLS = 512;
-  constexpr uint32_t SFA_COL = 2 * BN, SFB_COL = SFA_COL + 8;   // 2 x 4 and 2 x 8 columns
-  static_assert(SFB_COL + 16 <= TMEM_COLS, "scale columns");
+  constexpr uint32_t SFA_COL = W0 + W1, SFB_COL = SFA_COL + 8;   // 2 x 4 and 2 x 4 kSbTiles columns
+  static_assert(SFB_COL + 8 * kSbTiles <= TMEM_COLS, "scale columns");
   constexpr uint16_t kPair = 0x3;
 
   extern __shared__ uint8_t smem_raw[];
@@ -211,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int tiles_m = (M + kPM - 1) / kPM, tiles_n = (N + BN - 1) / BN;
-  const int num_tiles = tiles_m * tiles_n;
+  const int tiles_m = (M + kPM - 1) / kPM, tiles_n = (N + kSpan - 1) / kSpan;
+  const int num_units = tiles_m * tiles_n;
   const int kblocks = (K + kBK - 1) / kBK;
 
   if (threadIdx.x == 0) {
@@ -228,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl->abort = 0;
     fence_mbar_init();
     tma_prefetch(&tmA);
-    tma_prefetch(&tmB);
+    tma_prefetch(&tmB0);
+    if (kSub == 2) tma_prefetch(&tmB1);
     tma_prefetch(&tmSA);
     tma_prefetch(&tmSB);
     if (tma_store) tma_prefetch(&tmC);
@@ -251,28 +259,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     int issued = 0;   // stages requested
     bool ok = true;
-    for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-      const int m0 = (tile % tiles_m) * kPM + (int)rank * kBM;
-      const int nt = (tile / tiles_m) * BN, n0 = nt + (int)rank * (BN / 2);
-      for (int kb = 0; kb < kblocks; ++kb) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->empty[stage], phase ^ 1u, abort))) {
-          if (lead) raise_abort(ctl, err);
-          ok = false;
-          break;
+    for (int unit = pair; unit < num_units && ok; unit += npairs) {
+      const int m0 = (unit % tiles_m) * kPM + (int)rank * kBM;
+      for (int sub = 0; sub < kSub && ok; ++sub) {
+        const int width = sub ? W1 : W0;
+        const int nt = (unit / tiles_m) * kSpan + sub * W0, n0 = nt + (int)rank * (width / 2);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&ctl->empty[stage], phase ^ 1u, abort))) {
+            if (lead) raise_abort(ctl, err);
+            ok = false;
+            break;
+          }
+          if (lead) {
+            uint8_t* sA = smem + stage * STAGE_BYTES;
+            const uint32_t full0 = cluster_map(smem_u32(&ctl->full[stage]), 0);
+            if (rank == 0)
+              mbar_expect_tx(&ctl->full[stage], 2 * (STAGE_BYTES - (uint32_t)(W0 - width) / 2 * kRowBytes));
+            tma_load_2d_pair(sA, &tmA, full0, kb * kRowBytes, m0);
+            tma_load_2d_pair(sA + A_BYTES, sub ? &tmB1 : &tmB0, full0, kb * kRowBytes, n0);
+            // (the maps of the scales are in 4-byte words: 256 words = two tiles)
+            tma_load_2d_pair(sA + A_BYTES + B_BYTES, &tmSA, full0, kb * 256, m0 / 128);
+            tma_load_2d_pair(sA + A_BYTES + B_BYTES + SA_BYTES, &tmSB, full0, kb * 256, nt / 128);
+          }
+          __syncwarp();
+          ++issued;
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
-        if (lead) {
-          uint8_t* sA = smem + stage * STAGE_BYTES;
-          const uint32_t full0 = cluster_map(smem_u32(&ctl->full[stage]), 0);
-          if (rank == 0) mbar_expect_tx(&ctl->full[stage], 2 * STAGE_BYTES);
-          tma_load_2d_pair(sA, &tmA, full0, kb * kRowBytes, m0);
-          tma_load_2d_pair(sA + A_BYTES, &tmB, full0, kb * kRowBytes, n0);
-          // (the maps of the scales are in 4-byte words: 256 words = two tiles)
-          tma_load_2d_pair(sA + A_BYTES + B_BYTES, &tmSA, full0, kb * 256, m0 / 128);
-          tma_load_2d_pair(sA + A_BYTES + B_BYTES + SA_BYTES, &tmSB, full0, kb * 256, nt / 128);
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == STAGES) stage = 0, phase ^= 1u;
       }
     }
     // before the CTA may exit: every stage's last MMA commit has arrived on
@@ -296,20 +308,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true;
-      for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+      // one tile of `width` columns
+      auto tile = [&](auto width, int nt) {
+        constexpr int kW = decltype(width)::value;
         if (!__all_sync(0xffffffffu, mbar_wait_cluster(&ctl->tempty[acc], acc_phase ^ 1u, abort))) {
           if (lead) raise_abort(ctl, err);
-          break;
+          return false;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-        const uint32_t sfb0 = tmem_base + SFB_COL + (((tile / tiles_m) * BN) % 128) / 32;
+        const uint32_t d_tmem = tmem_base + (uint32_t)acc * W0;
+        const uint32_t sfb0 = tmem_base + SFB_COL + (uint32_t)(nt % 128) / 32;
         for (int kb = 0; kb < kblocks; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[stage], phase, abort))) {
             if (lead) raise_abort(ctl, err);
-            ok = false;
-            break;
+            return false;
           }
           tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + stage * STAGE_BYTES);
@@ -323,15 +335,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int t = 0; t < (kN + 1) / 2; ++t) {   // the scales of 128 values each
                 tmem_cp_32x128b_pair(tmem_base + SFA_COL + 4 * t, desc_scale_tile(sf_addr + t * kSfTile));
-                tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t, desc_scale_tile(sf_addr + SA_BYTES + t * kSfTile));
-                if constexpr (kSbTiles == 2)
-                  tmem_cp_32x128b_pair(tmem_base + SFB_COL + 8 * t + 4,
-                                       desc_scale_tile(sf_addr + SA_BYTES + (2 + t) * kSfTile));
+#pragma unroll
+                for (int q = 0; q < sb_tiles(kW); ++q)
+                  tmem_cp_32x128b_pair(tmem_base + SFB_COL + 4 * (kSbTiles * t + q),
+                                       desc_scale_tile(sf_addr + SA_BYTES + (2 * q + t) * kSfTile));
               }
 #pragma unroll
               for (int i = 0; i < kN; ++i)
-                mma_mxf4_pair(d_tmem, adesc + 2 * i, bdesc + 2 * i, idesc_mxf4(kPM, BN, 2 * (i % 2)),
-                              tmem_base + SFA_COL + 4 * (i / 2), sfb0 + 8 * (i / 2), (kb | i) != 0);
+                mma_mxf4_pair(d_tmem, adesc + 2 * i, bdesc + 2 * i, idesc_mxf4(kPM, kW, 2 * (i % 2)),
+                              tmem_base + SFA_COL + 4 * (i / 2), sfb0 + 4 * kSbTiles * (i / 2), (kb | i) != 0);
               mma_commit_pair(&ctl->empty[stage], kPair);
             }
           };
@@ -339,10 +351,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
-        if (!ok) break;
         if (lead) mma_commit_pair(&ctl->tfull[acc], kPair);
         __syncwarp();
         if (++acc == 2) acc = 0, acc_phase ^= 1u;
+        return true;
+      };
+      for (int unit = pair; unit < num_units; unit += npairs) {
+        const int nt = (unit / tiles_m) * kSpan;
+        if (!tile(std::integral_constant<int, W0>(), nt)) break;
+        if constexpr (kSub == 2)
+          if (!tile(std::integral_constant<int, W1>(), nt + W0)) break;
       }
       if (*abort && lead) {
         mma_commit_pair(&ctl->drain, kPair);
@@ -359,20 +377,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     int buf = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int tile = pair; tile < num_tiles; tile += npairs) {
-      const int m0 = (tile % tiles_m) * kPM + (int)rank * kBM, n0 = (tile / tiles_m) * BN;
-      if (!__all_sync(0xffffffffu, mbar_wait(&ctl->tfull[acc], acc_phase, abort))) {
-        raise_abort(ctl, err);
-        break;
+    bool ok = true;
+    for (int unit = pair; unit < num_units && ok; unit += npairs)
+      for (int sub = 0; sub < kSub; ++sub) {
+        const int m0 = (unit % tiles_m) * kPM + (int)rank * kBM, n0 = (unit / tiles_m) * kSpan + sub * W0;
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->tfull[acc], acc_phase, abort))) {
+          raise_abort(ctl, err);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        epilogue_rows<kF32>(sub ? W1 : W0, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)acc * W0, bufs, buf, &tmC,
+                            tma_store != 0, C, M, N, m0 + quarter * 32, n0, lane);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty0[acc]);
+        if (++acc == 2) acc = 0, acc_phase ^= 1u;
       }
-      tc_fence_after();
-      epilogue_rows<BN, kF32>(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN), bufs, buf, &tmC,
-                              tma_store != 0, C, M, N, m0 + quarter * 32, n0, lane);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty0[acc]);
-      if (++acc == 2) acc = 0, acc_phase ^= 1u;
-    }
     if (lane == 0) bulk_wait<0>();
   }
   __syncwarp();
@@ -928,19 +949,21 @@ int max_clusters(const void* kernel, int size, size_t smem, int threads = kThrea
   return n;
 }
 
-template <int BN, int STAGES, bool kF32>
+template <int W0, int W1, int STAGES, bool kF32>
 cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, int N, int K, int* err,
                         cudaStream_t st) {
-  CUtensorMap ta, tb, tsa, tsb, tc = {};
+  constexpr int kSpan = W0 == W1 ? W0 : W0 + W1;
+  CUtensorMap ta, tb0, tb1, tsa, tsb, tc = {};
   cudaError_t e;
   if ((e = map_codes(&ta, a.codes, M, K, kBM)) != cudaSuccess) return e;
-  if ((e = map_codes(&tb, b.codes, N, K, BN / 2)) != cudaSuccess) return e;
+  if ((e = map_codes(&tb0, b.codes, N, K, W0 / 2)) != cudaSuccess) return e;
+  if ((e = map_codes(&tb1, b.codes, N, K, W1 / 2)) != cudaSuccess) return e;
   if ((e = map_scales(&tsa, a.scales, M, K, 1)) != cudaSuccess) return e;
-  if ((e = map_scales(&tsb, b.scales, N, K, BN > 128 ? 2 : 1)) != cudaSuccess) return e;
+  if ((e = map_scales(&tsb, b.scales, N, K, sb_tiles(W0))) != cudaSuccess) return e;
   const int tma_store = map_out<kF32>(&tc, y, M, N) ? 1 : 0;
-  const size_t smem =
-      1024 + (size_t)STAGES * ((kBM + BN / 2) * kRowBytes + (BN > 128 ? 6 : 4) * kSfTile) + kEpiBytes + sizeof(Ctl);
-  auto k = k_mx_pair<BN, STAGES, kF32>;
+  const size_t smem = 1024 + (size_t)STAGES * ((kBM + W0 / 2) * kRowBytes + (2 + 2 * sb_tiles(W0)) * kSfTile) + kEpiBytes +
+                      sizeof(Ctl);
+  auto k = k_mx_pair<W0, W1, STAGES, kF32>;
   if ((e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
@@ -955,10 +978,10 @@ cudaError_t launch_pair(const MxOperand& a, const MxOperand& b, void* y, int M, 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   const int cap = max_clusters(reinterpret_cast<const void*>(k), 2, smem);
-  const long long tiles = (long long)((M + 2 * kBM - 1) / (2 * kBM)) * ((N + BN - 1) / BN);
-  cfg.gridDim = dim3(2 * (unsigned)(tiles < cap ? tiles : cap));
+  const long long units = (long long)((M + 2 * kBM - 1) / (2 * kBM)) * ((N + kSpan - 1) / kSpan);
+  cfg.gridDim = dim3(2 * (unsigned)(units < cap ? units : cap));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k, ta, tb, tsa, tsb, tc, tma_store, static_cast<typename Out<kF32>::T*>(y), M, N, K,
+  return cudaLaunchKernelEx(&cfg, k, ta, tb0, tb1, tsa, tsb, tc, tma_store, static_cast<typename Out<kF32>::T*>(y), M, N, K,
                             err);
 }
 
@@ -1087,15 +1110,16 @@ cudaError_t gemm_t(const MxOperand& a, const MxOperand& w, void* y, int M, int N
   if (M <= 32) return launch_fewrow<32, 4, 8, kF32>(a, w, y, M, N, K, w_early, err, st);
   if (M <= 64) return launch_fewrow<64, 4, 8, kF32>(a, w, y, M, N, K, w_early, err, st);
   // (from 65 rows on, with the weights as N operand: 128 rows 2688 -> 10304 in 6.7 us, as few rows 9.1)
-  // The tile width with the shortest waves of tiles: a stage of a tile takes as
-  // long as its bytes into an SM (31, 26 and 22 KB).  517 x 5003 x 1056 f32: 81
+  // The tile widths with the shortest waves: a stage of a tile takes as long as
+  // its bytes into an SM (36 + 32, 31, 26 and 22 KB).  517 x 5003 x 1056 f32: 81
   // tiles of 192 columns, two waves of 76 pairs.
   const long long tiles_m = (M + 2 * kBM - 1) / (2 * kBM), pairs = device_sm_count() / 2;
-  auto cost = [&](int bn, int kb) { return ((tiles_m * ((N + bn - 1) / bn) + pairs - 1) / pairs) * kb; };
-  const long long c192 = cost(192, 31), c128 = cost(128, 26), c64 = cost(64, 22);
-  if (c64 < c192 && c64 < c128) return launch_pair<64, 8, kF32>(a, w, y, M, N, K, err, st);
-  if (c128 < c192) return launch_pair<128, 7, kF32>(a, w, y, M, N, K, err, st);
-  return launch_pair<192, 6, kF32>(a, w, y, M, N, K, err, st);
+  auto cost = [&](int span, int kb) { return ((tiles_m * ((N + span - 1) / span) + pairs - 1) / pairs) * kb; };
+  const long long c448 = cost(448, 68), c192 = cost(192, 31), c128 = cost(128, 26), c64 = cost(64, 22);
+  if (c448 < c192 && c448 < c128 && c448 < c64) return launch_pair<256, 192, 5, kF32>(a, w, y, M, N, K, err, st);
+  if (c64 < c192 && c64 < c128) return launch_pair<64, 64, 8, kF32>(a, w, y, M, N, K, err, st);
+  if (c128 < c192) return launch_pair<128, 128, 7, kF32>(a, w, y, M, N, K, err, st);
+  return launch_pair<192, 192, 6, kF32>(a, w, y, M, N, K, err, st);
 }
 
 }  // namespace
