@@ -638,7 +638,7 @@ m2_status mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int rows, i
  *   y[m, n] = sum_k a[m, k] * w[n, k]
  * a [M, K], w [N, K] ([out, in]); f32 accumulation; y [M, N] bf16 or f32
  * (out_dtype), rounded once, aligned to its element; it overlaps no input.
- * M in [0, 2^24], N in [1, 2^24], M * N <= 2^40.
+ * M in [0, 2^24], N in [1, 2^24], M * N <= 2^40, N * K <= 2^38.
  * A bounded wait that runs out is reported by m2_check_standalone().
  * Errors: M2_EINVAL, M2_ESHAPE, M2_EDEVICE, M2_ECUDA.
  */

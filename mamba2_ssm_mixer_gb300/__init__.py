@@ -855,11 +855,12 @@ def _scales_shape(rows: int, K: int):
 
 
 def _need_mx(q: Mxfp4, name: str, shape=None):
+    """shape: (rows, K), either None for any."""
     if not isinstance(q, Mxfp4):
         raise ValueError(f"{name} must be an Mxfp4, got {type(q).__name__}")
     if q.codes.dim() != 2:
         raise ValueError(f"{name}.codes must be [rows, K / 2], got {tuple(q.codes.shape)}")
-    rows, K = q.shape if shape is None else shape
+    rows, K = (own if want is None else want for own, want in zip(q.shape, shape or (None, None)))
     if K < 32 or K % 32:
         raise ValueError(f"{name}: K must be a multiple of 32, got {K}")
     _need(q.codes, f"{name}.codes", torch.uint8, (rows, K // 2))
@@ -952,7 +953,7 @@ def mxfp4_linear(a: Mxfp4, w: Mxfp4, y: torch.Tensor | None = None, dtype=torch.
     `dtype` (bfloat16 or float32)."""
     _need_mx(a, "a")
     M, K = a.shape
-    _need_mx(w, "w", (w.codes.shape[0], K))
+    _need_mx(w, "w", (None, K))
     N = w.codes.shape[0]
     out_dtype = _mx_dtype(dtype if y is None else y.dtype)
     if y is not None:
@@ -980,7 +981,7 @@ def mxfp4_linear_bf16(x: torch.Tensor, w: Mxfp4, y: torch.Tensor | None = None, 
     [M, K], whose rows may be a slice of wider ones."""
     stride = _need_rows(x, "x", (torch.bfloat16,), 8)
     M, K = x.shape
-    _need_mx(w, "w", (w.codes.shape[0], K))
+    _need_mx(w, "w", (None, K))
     N = w.codes.shape[0]
     out_dtype = _mx_dtype(dtype if y is None else y.dtype)
     if y is not None:
@@ -1069,15 +1070,21 @@ class Mxfp4Head:
 
         return _on_device(h, stream, (self.norm_w, *self.weight, out), go)
 
+    @staticmethod
+    def _need_call(rows: int, tokens, top: int, max_rows: int):
+        if max_rows < 1:
+            raise ValueError(f"max_rows must be positive, got {max_rows}")
+        if not 0 <= top <= 64:
+            raise ValueError(f"top must be in [0, 64], got {top}")
+        if tokens is not None:
+            _need(tokens, "tokens", torch.int32, (rows,))
+
     def logprobs(self, h: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0, max_rows: int = 4096,
                  stream=None) -> TokenLogprobs:
         """m2_token_logprobs of h's logits, of which at most max_rows rows exist
         at a time."""
-        if max_rows < 1:
-            raise ValueError(f"max_rows must be positive, got {max_rows}")
         rows = h.shape[0]
-        if tokens is not None:
-            _need(tokens, "tokens", torch.int32, (rows,))
+        self._need_call(rows, tokens, top, max_rows)
 
         def go(_):
             if rows <= max_rows:
@@ -1173,12 +1180,17 @@ class Mamba2Stack:
               workspace=None, max_rows: int = 4096, stream=None):
         """Log probabilities along prompts: prefill, then the head's
         TokenLogprobs of every row.  tokens int32 [sum(T)]: the token that
-        follows each row, -1 for none (the last row of a sequence)."""
+        follows each row, -1 for none (the last row of a sequence).  What the
+        head refuses is refused before the prefill moves the states."""
+        head._need_call(hidden.shape[0], tokens, top, max_rows)
+        if head.weight.shape[1] != hidden.shape[1]:
+            raise ValueError(f"the head takes {head.weight.shape[1]} columns, the stack has {hidden.shape[1]}")
+
         def go(_):
             h = self.prefill(hidden, seqlens, conv_states, ssm_states, has_initial=has_initial, workspace=workspace)
             return head.logprobs(h, tokens, top, max_rows=max_rows)
 
-        return _on_device(hidden, stream, (tokens,), go)
+        return _on_device(hidden, stream, (tokens, head.norm_w, *head.weight), go)
 
     def decode(self, hidden, conv_pools, ssm_pools, slot_idx, workspace=None, stream=None):
         ws = workspace if workspace is not None else torch.empty(

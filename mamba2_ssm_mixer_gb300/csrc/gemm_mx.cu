@@ -945,7 +945,10 @@ int max_clusters(const void* kernel, int size, size_t smem, int threads = kThrea
     cudaGetLastError();
     n = device_sm_count() / size > 1 ? device_sm_count() / size : 1;
   }
-  known[{dev, kernel, size, smem}] = n;
+  try {
+    known[{dev, kernel, size, smem}] = n;
+  } catch (...) {   // (no memory: asked again the next time)
+  }
   return n;
 }
 

@@ -1505,8 +1505,8 @@ static m2_status check_mx_linear(const uint8_t* w_codes, const uint8_t* w_scales
                                  int N, int K, const char* who) {
   m2_status s = check_mx_shape(M, K, who);
   if (s) return s;
-  if (N < 1 || N > (1 << 24) || (long long)M * N > (1ll << 40))
-    return fail(M2_ESHAPE, "%s: M %d, N %d (N in [1, 2^24], M * N up to 2^40)", who, M, N);
+  if (N < 1 || N > (1 << 24) || (long long)M * N > (1ll << 40) || (long long)N * K > (1ll << 38))
+    return fail(M2_ESHAPE, "%s: M %d, N %d, K %d (N in [1, 2^24], M * N up to 2^40, N * K up to 2^38)", who, M, N, K);
   if (out_dtype != M2_DTYPE_F32 && out_dtype != M2_DTYPE_BF16)
     return fail(M2_EINVAL, "%s: out_dtype must be M2_DTYPE_F32 or M2_DTYPE_BF16", who);
   if (M && (!w_codes || !w_scales || !y)) return fail(M2_EINVAL, "%s: null pointer", who);
@@ -1542,7 +1542,9 @@ extern "C" m2_status mxfp4_linear_bf16_workspace_size(int M, int N, int K, size_
   if (!bytes) return fail(M2_EINVAL, "mxfp4_linear_bf16_workspace_size: null argument");
   m2_status s = check_mx_shape(M, K, "mxfp4_linear_bf16_workspace_size");
   if (s) return s;
-  if (N < 1 || N > (1 << 24)) return fail(M2_ESHAPE, "mxfp4_linear_bf16_workspace_size: N %d not in [1, 2^24]", N);
+  if (N < 1 || N > (1 << 24) || (long long)M * N > (1ll << 40) || (long long)N * K > (1ll << 38))
+    return fail(M2_ESHAPE, "mxfp4_linear_bf16_workspace_size: M %d, N %d, K %d (N in [1, 2^24], M * N up to 2^40, N * K up to 2^38)",
+                M, N, K);
   *bytes = mx_inside_splits(M, N, K) ? 0 : align256(code_bytes(M, K)) + mx_scale_bytes(M, K);
   return M2_OK;
 }

@@ -362,3 +362,59 @@ def test_python_refuses_what_does_not_fit():
         m2.mxfp4_linear_bf16(torch.zeros(100, 64, dtype=BF, device="cuda"), qw,
                              workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == m2.M2_ENOMEM
+
+
+def test_one_matrix_on_both_sides():
+    q, v = operand(np.random.default_rng(3), 130, 160)
+    exact = v @ v.T
+    y = np64(m2.mxfp4_linear(q, q, dtype=F32))
+    assert (np.abs(y - exact) <= 2.0 ** -24 * np.abs(exact) + (3 + 8) * 2.0 ** -22 * (np.abs(v) @ np.abs(v).T)).all()
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^32 values and outputs of more than 2^31: the rows
+    at the end are those of a small call."""
+    rows, K = (1 << 32) // 2688 + 200, 2688
+    x = torch.zeros(rows, K, dtype=BF, device="cuda")
+    x[-200:] = torch.randn(200, K, device="cuda").to(BF)
+    q = m2.mxfp4_quant(x)
+    small = m2.mxfp4_quant(x[-200:])
+    assert torch.equal(q.codes[-200:], small.codes) and not q.codes[:-200].any()
+    back = m2.mxfp4_dequant(q)
+    assert torch.equal(back[-200:], m2.mxfp4_dequant(small)) and not back[:-200].any()
+    # (a row block on its own: its tiles of scales start on a multiple of 128)
+    r0 = rows // 128 * 128 - 128
+    end = m2.Mxfp4(q.codes[r0:], q.scales[r0 // 128:])
+    qw, _ = operand(np.random.default_rng(0), 96, K)
+    assert torch.equal(m2.mxfp4_linear(q, qw)[r0:], m2.mxfp4_linear(end, qw))
+    far = x.view(-1).as_strided((3, 64), ((rows // 3) * K // 8 * 8, 1))
+    assert torch.equal(m2.mxfp4_quant(far).codes, m2.mxfp4_quant(far.contiguous()).codes)
+
+
+@pytest.mark.parametrize("N", [131072, 131071])
+def test_outputs_past_32_bits(N):
+    M, K = 16500, 32
+    (qa, _), (qw, _) = operand(np.random.default_rng(1), M, K), operand(np.random.default_rng(2), N, K)
+    y = m2.mxfp4_linear(qa, qw)
+    r0 = M // 256 * 256
+    end = m2.Mxfp4(qa.codes[r0:], qa.scales[r0 // 128:])
+    assert torch.equal(y[r0:], m2.mxfp4_linear(end, qw))
+    assert torch.equal(y[:100], m2.mxfp4_linear(m2.Mxfp4(qa.codes[:100], qa.scales[:1]), qw))
+
+
+def test_two_streams_at_once():
+    """Products of all kinds on two streams at the same time give what they give
+    one after another."""
+    rng = np.random.default_rng(4)
+    qw, _ = operand(rng, 4000, 1056)
+    xs = [torch.randn(M, 1056, device="cuda").to(BF) for M in (1, 20, 64, 70, 600)]
+    want = [m2.mxfp4_linear_bf16(x, qw) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for i in range(12):
+        for s, side in enumerate(streams):
+            got[s].append((m2.mxfp4_linear_bf16(xs[(i + 2 * s) % 5], qw, stream=side), (i + 2 * s) % 5))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[k]) for g in got for y, k in g)
+    m2.check_standalone()

@@ -246,3 +246,44 @@ def test_python_refuses_what_does_not_fit():
     with pytest.raises(m2.M2Error) as e:
         m2.m2_token_logprobs(L, t, 65)
     assert e.value.status == m2.M2_ESHAPE
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows,v", [(3, 700), (40, 140001)])
+def test_values_below_the_normal_range(rows, v, dtype):
+    """Logits whose differences only subnormal numbers and the signs of zeros
+    show: all equally likely, ordered by their values (-0 and +0 are equal)."""
+    rng = np.random.default_rng(v)
+    tiny = 2.0 ** (-149 if dtype == F32 else -133)
+    x = rng.integers(-3, 4, (rows, v)) * tiny
+    x = np.where(x == 0, np.where(rng.random((rows, v)) < 0.5, -0.0, 0.0), x)
+    logits = torch.from_numpy(x.astype(np.float32)).to(dtype).cuda()
+    check(logits, rng.integers(0, v, rows).astype(np.int32), 7)
+
+
+@pytest.mark.parametrize("rows,v", [(3, 1000), (20, 140000)])
+def test_offsets_past_32_bits(rows, v):
+    """Rows so far apart that the last lie past 2^32 elements."""
+    step = (1 << 32) // (rows - 1) + 17
+    wide = torch.empty(step * (rows - 1) + v, dtype=BF, device="cuda").as_strided((rows, v), (step, 1))
+    near, tokens = make(rows, v, BF, v)
+    wide.copy_(near)
+    t = torch.from_numpy(tokens).cuda()
+    for a, b in zip(m2.m2_token_logprobs(wide, t, 11), m2.m2_token_logprobs(near, t, 11)):
+        assert torch.equal(a, b) if a.dtype == torch.int32 else torch.allclose(a, b, rtol=0, atol=2 * LSE + 2.0 ** -20)
+
+
+def test_two_streams_at_once():
+    cases = [(make(r, v, d, r), k) for r, v, d, k in ((1, 131072, BF, 20), (64, 131072, BF, 5), (900, 9000, F32, 64),
+                                                      (20, 140001, F32, 9))]
+    cases = [(L, torch.from_numpy(t).cuda(), k) for (L, t), k in cases]
+    want = [m2.m2_token_logprobs(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(8):
+        for s, side in enumerate(streams):
+            got.append((m2.m2_token_logprobs(*cases[(i + 2 * s) % 4], stream=side), (i + 2 * s) % 4))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o, k in got for a, b in zip(o, want[k]))
+    m2.check_standalone()

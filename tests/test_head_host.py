@@ -158,3 +158,42 @@ def test_python_refuses_host_tensors_and_shapes(m2):
                  lambda: m2.Mxfp4Head(x[0], m2.Mxfp4(u8, u8))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_weights_past_the_largest_operand_are_refused(m2):
+    n = ctypes.c_size_t()
+    big = dict(M=100, N=1 << 24, K=1 << 15)
+    assert _linear(m2, **big) == m2.M2_ESHAPE
+    assert _linear_bf16(m2, stride=1 << 15, **big) == m2.M2_ESHAPE
+    assert m2._lib.mxfp4_linear_bf16_workspace_size(100, 1 << 24, 1 << 15, ctypes.byref(n)) == m2.M2_ESHAPE
+
+
+def test_products_ask_for_packed_weights(m2):
+    u8 = torch.zeros(4, 32, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="must be an Mxfp4"):
+        m2._need_mx((u8, u8), "w", (None, 64))
+
+
+def test_score_refuses_before_it_runs(m2, monkeypatch):
+    """A call that the head cannot serve leaves the stack's states alone."""
+    monkeypatch.setattr(m2, "_on_device", lambda ref, stream, others, call: call(None))
+    ran = []
+
+    class Stack(m2.Mamba2Stack):
+        def __init__(self):
+            pass
+
+        def prefill(self, *a, **kw):
+            ran.append(1)
+
+    head = object.__new__(m2.Mxfp4Head)
+    u8 = torch.zeros(4, 32, dtype=torch.uint8)
+    head.norm_w, head.weight = u8[0], m2.Mxfp4(u8, u8)
+    hidden = torch.zeros(3, 64, dtype=torch.bfloat16)
+    for kw in (dict(top=65), dict(top=-1), dict(max_rows=0), dict(tokens=torch.zeros(4, dtype=torch.int32)),
+               dict(hidden=torch.zeros(3, 96, dtype=torch.bfloat16))):
+        a = dict(hidden=hidden, tokens=None, top=1, max_rows=4)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            Stack().score(a["hidden"], [3], [], [], head, a["tokens"], top=a["top"], max_rows=a["max_rows"])
+    assert not ran
