@@ -14,8 +14,9 @@
 // The k largest need no sort and no list on the way: if each of w warps has
 // ceil(k / w) threads whose maximum is at least tau, at least k tokens are >=
 // tau; only groups whose maximum reaches tau are looked at again, and the
-// survivors are ranked by counting.  Where equal values leave more survivors
-// than fit, the row is read once more against a running k-th best (top_again).
+// survivors are ranked by counting.  Where they are many, a sample of them
+// gives the next tau; where many are equal, the first of those join the greater
+// ones (survivors).
 //
 // k_lp_held (few rows, or short ones): a CTA, or each of a cluster's, holds its
 // slice of one row in registers; the first CTA joins the slices' parts through
@@ -307,30 +308,17 @@ struct SelectorGroup {
   static constexpr int kSize = kSelectors;
   int at;
   __device__ void sync() const { asm volatile("bar.sync 1, %0;" ::"n"(kSelectors) : "memory"); }
-  __device__ bool any(bool p) const {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.red.or.pred q, 1, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}\n"
-        : "=r"(r)
-        : "r"((uint32_t)p), "n"(kSelectors)
-        : "memory");
-    return r != 0;
-  }
 };
 struct BlockGroup {
   static constexpr int kSize = kHeldThreads;
   int at;
   __device__ void sync() const { __syncthreads(); }
-  __device__ bool any(bool p) const { return __syncthreads_or(p) != 0; }
 };
 
 // Their shared state.
 template <class G>
 struct __align__(16) LpSelect {
-  static constexpr int kCap = G::kSize == kSelectors ? 1024 : 2048 + kLpMaxTop;   // survivors ranked by counting
+  static constexpr int kCap = 512;     // survivors ranked by counting, at most
   uint64_t cand[kCap];
   uint64_t best[kLpMaxTop];            // the slice's largest keys, in order
   uint64_t merged[kLpMaxTop];          // the row's, from several slices'
@@ -338,7 +326,7 @@ struct __align__(16) LpSelect {
   float z, z_lo, m;                    // log S of the row, relative to its maximum m, in two parts
   int n_cand, n_hit, n_over;
   float sum[G::kSize / 32][2];
-  uint32_t step_tau[G::kSize / 32];
+  int equal[G::kSize / 32];
 };
 
 // The k largest of cand[0, n) by counting, in order, to best[0, k) (n < k: the
@@ -356,84 +344,89 @@ __device__ __forceinline__ void rank_candidates(LpSelect<G>* sh, const G& g, int
   g.sync();
 }
 
-// The k largest keys of vectors [v0, v1) of a row, by a pass in order against
-// the k-th best so far: once k are held, equal logits (of later tokens) never
-// pass, so that a step whose maximum is not greater is done with.  In a step
-// the threads' maxima bound what has to be looked at, as for a row; where equal
-// values leave more than fits, its vectors are taken one by one.
+// The elements of a vector per thread that equal x join the n survivors, the
+// first ones in order of the threads until there are k; how many there are then.
 template <typename T, class G>
-__device__ __noinline__ void top_again(LpSelect<G>* sh, const G g, const RowAt<T> r, int v0, int v1, int k) {
+__device__ __forceinline__ int append_equal(LpSelect<G>* sh, const G& g, const uint4& q, float x, int token, int n, int k) {
   using V = Vec<T>;
-  constexpr int kN = 4, kWarps = G::kSize / 32, kCap = LpSelect<G>::kCap;
-  static_assert(G::kSize * V::kN + kLpMaxTop <= kCap, "a vector of each thread fits beside the best");
-  float floor = -INFINITY;
-  int held = 0;
-  g.sync();
-  if (g.at == 0) sh->n_cand = 0;
-  g.sync();
-  // what has been appended joins the best
-  auto join_best = [&](int n) {
-    rank_candidates(sh, g, n, k);
-    held = n < k ? n : k;
-    for (int i = g.at; i < held; i += G::kSize) sh->cand[i] = sh->best[i];
-    if (n >= k) floor = key_logit(sh->best[k - 1]);
-    if (g.at == 0) sh->n_cand = held;
-    g.sync();
-  };
-  for (int v = v0; v < v1; v += kN * G::kSize) {
-    uint4 q[kN];
+  const int lane = g.at & 31, warp = g.at >> 5;
+  int at = 0, all = 0;
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int at = v + j * G::kSize + g.at;
+  for (int e = 0; e < V::kN; ++e) {
+    const uint32_t who = __ballot_sync(0xffffffffu, V::at(q, e) == x);
+    at += __popc(who & ((1u << lane) - 1u));
+    all += __popc(who);
+  }
+  if (lane == 0) sh->equal[warp] = all;
+  g.sync();
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < G::kSize / 32; ++w) {
+    at += w < warp ? sh->equal[w] : 0;
+    all += sh->equal[w];
+  }
+  at += n;
+#pragma unroll
+  for (int e = 0; e < V::kN; ++e)
+    if (V::at(q, e) == x) {
+      if (at < k) sh->cand[at] = key_of(x, token + e);
+      ++at;
+    }
+  g.sync();
+  return min(n + all, k);
+}
+
+// Those of a row's vectors [v0, v1).
+template <typename T, class G>
+__device__ __noinline__ int first_equal(LpSelect<G>* sh, const G g, const RowAt<T> r, int v0, int v1, float x, int n, int k) {
+  using V = Vec<T>;
+  constexpr int kAhead = 4;
+  for (int v = v0; v < v1 && n < k; v += G::kSize * kAhead) {
+    uint4 q[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int at = v + G::kSize * j + g.at;
       q[j] = at < v1 ? __ldg(r.vec + at) : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
       if (at < v1 && r.edge(at)) r.edges(q[j], at);
     }
-    const float mx = max_of<T>(q);
-    if (!g.any(mx > floor)) continue;
-    const int need = (k + kWarps - 1) / kWarps;   // (more than 32: no bound)
-    const uint32_t w = need <= 32 ? nth_largest(ord32(mx + 0.f), need, g.at & 31) : 0u;
-    if ((g.at & 31) == 0) sh->step_tau[g.at >> 5] = w;
-    g.sync();
-    uint32_t tau = sh->step_tau[0];
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) tau = min(tau, sh->step_tau[i]);
-    auto append = [&](const uint4& vec, int j) {
-#pragma unroll
-      for (int e = 0; e < V::kN; ++e) {
-        const float x = V::at(vec, e);
-        if (x > floor && ord32(x + 0.f) >= tau) {
-          const int at = atomicAdd(&sh->n_cand, 1);
-          if (at < kCap) sh->cand[at] = key_of(x, (v + j * G::kSize + g.at) * V::kN + e - r.off);
-        }
-      }
-    };
-    // vectors [j0, j1) of the step; false if they hold more than fits
-    auto take = [&](int j0, int j1) {
-#pragma unroll 1
-      for (int j = j0; j < j1; ++j) {
-        uint4 mine = q[0];   // (q[j] without an index into registers)
-#pragma unroll
-        for (int i = 1; i < kN; ++i)
-          if (i == j) mine = q[i];
-        append(mine, j);
-      }
-      g.sync();
-      const int n = sh->n_cand;
-      g.sync();   // all have read it before any appends again
-      if (n > kCap) {
-        if (g.at == 0) sh->n_cand = held;   // (the best are still in the first places)
-        g.sync();
-        return false;
-      }
-      if (n != held) join_best(n);
-      return true;
-    };
-    if (!take(0, kN))
-      for (int j = 0; j < kN; ++j) take(j, j + 1);
+    for (int j = 0; j < kAhead; ++j) {
+      if (n >= k) break;   // (the same for all)
+      n = append_equal<T>(sh, g, q[j], x, (v + G::kSize * j + g.at) * V::kN - r.off, n, k);
+    }
   }
-  if (held == 0)
-    for (int i = g.at; i < k; i += G::kSize) sh->best[i] = 0;
-  g.sync();
+  return n;
+}
+
+// The k largest keys to best[0, k), given a bound that k tokens reach (or
+// every token above -inf does).  gather(lo) appends the tokens >= lo and
+// returns how many there are, at least that there are more than kCap; where
+// there are, the k-th largest of a sample of them is the next bound, and where
+// the sample shows nothing but the bound itself, only what is greater is
+// gathered and equal(x, n) adds the first tokens that equal it, in order, until
+// there are k.  (512 rows of 131072 bf16 logits, 10 of them above a finite
+// mask, 20 asked for: 78 us; another pass over the row
+// against a running k-th best 594.)
+template <typename T, class G, class Gather, class Equal>
+__device__ __forceinline__ int survivors(LpSelect<G>* sh, const G& g, int k, float lo, Gather gather, Equal equal) {
+  using V = Vec<T>;
+  constexpr int kSample = 256;
+  bool ties = false;   // tokens that equal `tie` are left out
+  float tie = lo;
+  int n;
+  for (;;) {
+    n = gather(lo);
+    if (n <= LpSelect<G>::kCap) break;
+    rank_candidates(sh, g, kSample, k);
+    const float x = key_logit(sh->best[k - 1]);
+    ties = x == lo;
+    tie = lo;
+    lo = ties ? -V::below(-lo) : x;
+    g.sync();   // (all have read it)
+    if (g.at == 0) sh->n_cand = 0, sh->n_hit = 0;
+    g.sync();
+  }
+  return ties && n < k ? equal(tie, n) : n;
 }
 
 // log S and the entropy of a row whose maximum m is finite and large, or +inf
@@ -730,32 +723,40 @@ __global__ void __launch_bounds__(kHeldThreads, VPT == 8 ? 3 : 5)
     tau = max(tau, t);
     const float bound = unord32(tau);
     // vectors that reach the bound, then their tokens, one per thread
-    if (mx >= bound) {
+    bool first = true;
+    auto gather = [&](float lo) {
+      if (mx >= lo) {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j)
-        if (V::whole(V::max(q[j])) >= bound) {
-          const int at = atomicAdd(&sel.n_hit, 1);
-          if (at < kLists) vecs[at] = q[j], vec_at[at] = v0 + j * kHeldThreads + tid;
-        }
-    }
-    __syncthreads();
-    const int hits = sel.n_hit;
-    if (hits <= kLists)
+        for (int j = 0; j < VPT; ++j)
+          if (V::whole(V::max(q[j])) >= lo) {
+            const int at = atomicAdd(&sel.n_hit, 1);
+            if (at < kLists) vecs[at] = q[j], vec_at[at] = v0 + j * kHeldThreads + tid;
+          }
+      }
+      __syncthreads();
+      const int hits = min(sel.n_hit, kLists);   // (each has a token: beyond kLists there are too many)
       for (int i = tid; i < hits * V::kN; i += kHeldThreads) {
         const float x = V::load(reinterpret_cast<const T*>(vecs) + i);
-        if (x >= bound) {
+        if (x >= lo) {
           const int at = atomicAdd(&sel.n_cand, 1);
           if (at < sel.kCap) sel.cand[at] = key_of(x, vec_at[i / V::kN] * V::kN + i % V::kN - r.off);
         }
       }
-    if (S == 1 && tid == 32 * (kHeldWarps - 1) && !is_odd(sel.part.m))   // (beside the others' search)
-      finish(&sel, job, sel.part, make_float2(0.f, 0.f), out, tokens != nullptr, err);
-    __syncthreads();
-    const int n = sel.n_cand;
-    if (hits <= kLists && n <= sel.kCap)
-      rank_candidates(&sel, g, n, top);
-    else
-      top_again<T>(&sel, g, r, v0, v1, top);
+      if (first && S == 1 && tid == 32 * (kHeldWarps - 1) && !is_odd(sel.part.m))   // (beside the others' search)
+        finish(&sel, job, sel.part, make_float2(0.f, 0.f), out, tokens != nullptr, err);
+      first = false;
+      __syncthreads();
+      return max(sel.n_cand, sel.n_hit);
+    };
+    auto equal = [&](float x, int n) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        if (n >= top) break;   // (the same for all)
+        n = append_equal<T>(&sel, g, q[j], x, (v0 + j * kHeldThreads + tid) * V::kN - r.off, n, top);
+      }
+      return n;
+    };
+    rank_candidates(&sel, g, survivors<T>(&sel, g, top, bound, gather, equal), top);
   } else {
     __syncthreads();
     if (S == 1 && tid == 0 && !is_odd(sel.part.m))
@@ -997,64 +998,70 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         }
         __syncwarp();
       }
+      int found = 0;
       if (top) {
         const uint32_t tau = max(kOrdNegInf + 1, __reduce_min_sync(0xffffffffu, lane < kReadWarps ? hand.tau[lane] : 0xffffffffu));
         const float bound = unord32(tau);
         // the readers and their groups with a token that reaches the bound, then
         // the groups' vectors, one per thread, a few loads under way
         const int groups = cut.chunks ? (cut.chunks + cut.group - 1) / cut.group : 0;
+        const int per_hit = cut.group * kVpt;
+        constexpr int kAhead = 4;
         for (int i = g.at; i < kReaders; i += kSelectors)
           if (hand.tmax[i] >= tau) sh->over[atomicAdd(&sel->n_over, 1)] = (uint16_t)i;
         g.sync();
         const int pairs = sel->n_over * groups;
-        for (int i = g.at; i < pairs; i += kSelectors) {
-          const int j = i % groups, who = sh->over[i / groups];
-          if (hand.gmax[j][who] >= tau) sh->hits[atomicAdd(&sel->n_hit, 1)] = (uint16_t)(j * kReaders + who);
-        }
-        g.sync();
-        const int per_hit = cut.group * kVpt, total = sel->n_hit * per_hit;
-        constexpr int kAhead = 4;
-#pragma unroll 1
-        for (int i0 = g.at; i0 < total; i0 += kSelectors * kAhead) {
-          uint4 q[kAhead];
-          int v[kAhead];
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            const int i = i0 + kSelectors * k;
-            v[k] = v1;
-            if (i < total) {
-              const int hit = sh->hits[i / per_hit], j = i % per_hit;
-              v[k] = v0 + (hit / kReaders * per_hit + j) * kReaders + hit % kReaders;
-            }
-            if (v[k] < v1) q[k] = __ldg(r.vec + v[k]);
+        auto gather = [&](float lo) {
+          const uint32_t key = ord32(lo);
+          for (int i = g.at; i < pairs; i += kSelectors) {
+            const int j = i % groups, who = sh->over[i / groups];
+            if (hand.gmax[j][who] >= key) sh->hits[atomicAdd(&sel->n_hit, 1)] = (uint16_t)(j * kReaders + who);
           }
+          g.sync();
+          const int total = sel->n_hit * per_hit;
+          volatile int* n_cand = &sel->n_cand;
+#pragma unroll 1
+          for (int i0 = g.at; i0 < total && *n_cand <= sel->kCap; i0 += kSelectors * kAhead) {
+            uint4 q[kAhead];
+            int v[kAhead];
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            if (v[k] >= v1) continue;
-            if (r.edge(v[k])) r.edges(q[k], v[k]);
-            if (V::whole(V::max(q[k])) < bound) continue;
+            for (int k = 0; k < kAhead; ++k) {
+              const int i = i0 + kSelectors * k;
+              v[k] = v1;
+              if (i < total) {
+                const int hit = sh->hits[i / per_hit], j = i % per_hit;
+                v[k] = v0 + (hit / kReaders * per_hit + j) * kReaders + hit % kReaders;
+              }
+              if (v[k] < v1) q[k] = __ldg(r.vec + v[k]);
+            }
 #pragma unroll
-            for (int e = 0; e < V::kN; ++e) {
-              const float x = V::at(q[k], e);
-              if (x >= bound) {
-                const int n = atomicAdd(&sel->n_cand, 1);
-                if (n < sel->kCap) sel->cand[n] = key_of(x, v[k] * V::kN + e - r.off);
+            for (int k = 0; k < kAhead; ++k) {
+              if (v[k] >= v1) continue;
+              if (r.edge(v[k])) r.edges(q[k], v[k]);
+              if (!(V::whole(V::max(q[k])) >= lo)) continue;
+#pragma unroll
+              for (int e = 0; e < V::kN; ++e) {
+                const float x = V::at(q[k], e);
+                if (x >= lo) {
+                  const int n = atomicAdd(&sel->n_cand, 1);
+                  if (n < sel->kCap) sel->cand[n] = key_of(x, v[k] * V::kN + e - r.off);
+                }
               }
             }
           }
-        }
+          g.sync();
+          return sel->n_cand;
+        };
+        auto equal = [&](float x, int n) { return first_equal<T>(sel, g, r, v0, v1, x, n, top); };
+        found = survivors<T>(sel, g, top, bound, gather, equal);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->taken[turn]);   // what the readers handed over is read
       if (++turn == 2) turn = 0, turn_phase ^= 1u;
-      g.sync();
-      if (top) {
-        const int n = sel->n_cand;
-        if (n <= sel->kCap)
-          rank_candidates(sel, g, n, top);
-        else
-          top_again<T>(sel, g, r, v0, v1, top);
-      }
+      if (top)
+        rank_candidates(sel, g, found, top);
+      else
+        g.sync();
       if (S > 1) {   // (the other warps arrive too, below)
         for (int i = g.at; i < kLpMaxTop; i += kSelectors) sel->merged[i] = 0;
         cluster_sync();

@@ -287,3 +287,22 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for o, k in got for a, b in zip(o, want[k]))
     m2.check_standalone()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows,v", [(20, 140001), (330, 17001)])
+def test_ties_in_many_long_rows(rows, v, dtype):
+    """Finite masks with fewer allowed tokens than asked for, equal and sorted
+    rows, few distinct values, ties that begin late in a row."""
+    rng = np.random.default_rng(v)
+    at = np.arange(v)
+    low = float(torch.finfo(dtype).min)
+    allowed = np.full(v, low)
+    allowed[rng.choice(v, 9, replace=False)] = rng.standard_normal(9)
+    kinds = [allowed, np.where(at < v - 50, -np.inf, low), np.zeros(v), at / 64.0, -at / 64.0,
+             rng.integers(-20, 20, v) / 8.0, np.where(at > v // 2, 2.0, np.where(at % 2, 1.0, -np.inf)),
+             np.where(rng.random(v) < 0.01, np.inf, 0.0)]
+    x = np.stack([kinds[i % len(kinds)] for i in range(rows)]).astype(np.float32)
+    logits = torch.from_numpy(x).to(dtype).cuda()
+    check(logits, rng.integers(0, v, rows).astype(np.int32), 20)
+    check(logits[:, 1:], rng.integers(0, v - 1, rows).astype(np.int32), 64)
