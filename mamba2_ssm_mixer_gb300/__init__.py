@@ -854,17 +854,22 @@ def _scales_shape(rows: int, K: int):
     return (rows + 127) // 128, (K + 127) // 128, 512
 
 
-def _need_mx(q: Mxfp4, name: str, shape=None):
-    """shape: (rows, K), either None for any."""
+def _need_mx(q: Mxfp4, name: str, rows=None, K=None):
+    """Its (rows, K); rows, K: None for any."""
     if not isinstance(q, Mxfp4):
         raise ValueError(f"{name} must be an Mxfp4, got {type(q).__name__}")
-    if q.codes.dim() != 2:
-        raise ValueError(f"{name}.codes must be [rows, K / 2], got {tuple(q.codes.shape)}")
-    rows, K = (own if want is None else want for own, want in zip(q.shape, shape or (None, None)))
-    if K < 32 or K % 32:
-        raise ValueError(f"{name}: K must be a multiple of 32, got {K}")
-    _need(q.codes, f"{name}.codes", torch.uint8, (rows, K // 2))
-    _need(q.scales, f"{name}.scales", torch.uint8, _scales_shape(rows, K))
+    codes, scales = q
+    if codes.dim() != 2:
+        raise ValueError(f"{name}.codes must be [rows, K / 2], got {tuple(codes.shape)}")
+    r, half = codes.shape
+    k = 2 * half
+    if rows is not None and r != rows or K is not None and k != K:
+        raise ValueError(f"{name} must be [{'any' if rows is None else rows}, {'any' if K is None else K}], got [{r}, {k}]")
+    if k < 32 or k % 32:
+        raise ValueError(f"{name}: K must be a multiple of 32, got {k}")
+    _need(codes, f"{name}.codes", torch.uint8)
+    _need(scales, f"{name}.scales", torch.uint8, _scales_shape(r, k))
+    return r, k
 
 
 def _need_rows(x: torch.Tensor, name: str, dtypes, multiple: int = 1) -> int:
@@ -922,7 +927,7 @@ def mxfp4_quant(x: torch.Tensor, out: Mxfp4 | None = None, stream=None) -> Mxfp4
     if K % 32:
         raise ValueError(f"K must be a multiple of 32, got {K}")
     if out is not None:
-        _need_mx(out, "out", (rows, K))
+        _need_mx(out, "out", rows, K)
 
     def call(handle):
         q = out if out is not None else Mxfp4(torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device),
@@ -935,8 +940,7 @@ def mxfp4_quant(x: torch.Tensor, out: Mxfp4 | None = None, stream=None) -> Mxfp4
 
 def mxfp4_dequant(q: Mxfp4, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values of an MXFP4 matrix, bf16 [rows, K]."""
-    _need_mx(q, "q")
-    rows, K = q.shape
+    rows, K = _need_mx(q, "q")
     if out is not None:
         _need(out, "out", torch.bfloat16, (rows, K))
 
@@ -951,10 +955,8 @@ def mxfp4_dequant(q: Mxfp4, out: torch.Tensor | None = None, stream=None) -> tor
 def mxfp4_linear(a: Mxfp4, w: Mxfp4, y: torch.Tensor | None = None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """y = a @ w^T of 4-bit operands on the tensor cores, f32 accumulation; y in
     `dtype` (bfloat16 or float32)."""
-    _need_mx(a, "a")
-    M, K = a.shape
-    _need_mx(w, "w", (None, K))
-    N = w.codes.shape[0]
+    M, K = _need_mx(a, "a")
+    N, _ = _need_mx(w, "w", K=K)
     out_dtype = _mx_dtype(dtype if y is None else y.dtype)
     if y is not None:
         _need(y, "y", y.dtype, (M, N))
@@ -981,8 +983,7 @@ def mxfp4_linear_bf16(x: torch.Tensor, w: Mxfp4, y: torch.Tensor | None = None, 
     [M, K], whose rows may be a slice of wider ones."""
     stride = _need_rows(x, "x", (torch.bfloat16,), 8)
     M, K = x.shape
-    _need_mx(w, "w", (None, K))
-    N = w.codes.shape[0]
+    N, _ = _need_mx(w, "w", K=K)
     out_dtype = _mx_dtype(dtype if y is None else y.dtype)
     if y is not None:
         _need(y, "y", y.dtype, (M, N))
@@ -1021,15 +1022,18 @@ def m2_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
     if tokens is not None:
         _need(tokens, "tokens", torch.int32, (rows,))
     if out is not None:
-        for t, name, dtype, shape, wanted in ((out.logprobs, "out.logprobs", torch.float32, (rows,), tokens is not None),
-                                              (out.ranks, "out.ranks", torch.int32, (rows,), tokens is not None),
-                                              (out.entropy, "out.entropy", torch.float32, (rows,), True),
-                                              (out.top_tokens, "out.top_tokens", torch.int32, (rows, top), top > 0),
-                                              (out.top_logprobs, "out.top_logprobs", torch.float32, (rows, top), top > 0)):
-            if wanted or (t is not None and t.numel()):
-                if not wanted:
-                    raise ValueError(f"{name} is not asked for")
-                _need(t, name, dtype, shape)
+        lp, rk, en, tt, tl = out
+        if tokens is not None:
+            _need(lp, "out.logprobs", torch.float32, (rows,))
+            _need(rk, "out.ranks", torch.int32, (rows,))
+        elif lp is not None and lp.numel() or rk is not None and rk.numel():
+            raise ValueError("out.logprobs and out.ranks are not asked for without tokens")
+        _need(en, "out.entropy", torch.float32, (rows,))
+        if top:
+            _need(tt, "out.top_tokens", torch.int32, (rows, top))
+            _need(tl, "out.top_logprobs", torch.float32, (rows, top))
+        elif tt is not None and tt.numel() or tl is not None and tl.numel():
+            raise ValueError("out.top_tokens and out.top_logprobs are not asked for")
 
     def call(handle):
         dev, o = logits.device, out

@@ -243,6 +243,12 @@ def test_python_refuses_what_does_not_fit():
                  lambda: m2.m2_token_logprobs(L.expand(3, 4, 100)[:, 0], None, 1)):
         with pytest.raises(ValueError):
             call()
+    full = m2.m2_token_logprobs(L, t, 5)
+    for call in (lambda: m2.m2_token_logprobs(L, None, 5, out=full), lambda: m2.m2_token_logprobs(L, t, 0, out=full),
+                 lambda: m2.m2_token_logprobs(L, t, 6, out=full), lambda: m2.m2_token_logprobs(L[:3], t[:3], 5, out=full),
+                 lambda: m2.m2_token_logprobs(L, t, 5, out=full._replace(ranks=None))):
+        with pytest.raises(ValueError):
+            call()
     with pytest.raises(m2.M2Error) as e:
         m2.m2_token_logprobs(L, t, 65)
     assert e.value.status == m2.M2_ESHAPE

@@ -171,7 +171,7 @@ def test_weights_past_the_largest_operand_are_refused(m2):
 def test_products_ask_for_packed_weights(m2):
     u8 = torch.zeros(4, 32, dtype=torch.uint8)
     with pytest.raises(ValueError, match="must be an Mxfp4"):
-        m2._need_mx((u8, u8), "w", (None, 64))
+        m2._need_mx((u8, u8), "w", K=64)
 
 
 def test_score_refuses_before_it_runs(m2, monkeypatch):
