@@ -224,6 +224,10 @@ class LoraAdapters:
     def ref(self):
         return ctypes.byref(self._c)
 
+    def get_device(self) -> int:
+        """The device's number, as a tensor's."""
+        return self.device.index
+
 
 class Mamba2Mixer:
     """One mixer block.  ``weights`` maps names to CPU or CUDA tensors:
@@ -660,14 +664,15 @@ def _on_device(ref: torch.Tensor, stream, others, call):
     """call(stream handle) with ref's device current and the call's stream
     current for what it allocates, so that the allocator frees that in the
     stream's order.  All tensors of the call have to be on ref's device."""
-    dev = ref.device
-    if dev.type != "cuda":
+    index = ref.get_device()   # (numbers: comparing torch.device objects is a fair part of a short call)
+    if index < 0:
         raise ValueError("the tensors of the call must be CUDA tensors")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors of one call are on {dev} and {t.device}")
-    if stream is None and dev.index == _current_device():
-        return call(_raw_stream(dev.index))
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors of one call are on {ref.device} and {t.device}")
+    if stream is None and index == _current_device():
+        return call(_raw_stream(index))
+    dev = ref.device
     with torch.cuda.device(dev):
         if stream is None:
             return call(_raw_stream(dev.index))
@@ -863,12 +868,15 @@ def _need_mx(q: Mxfp4, name: str, rows=None, K=None):
         raise ValueError(f"{name}.codes must be [rows, K / 2], got {tuple(codes.shape)}")
     r, half = codes.shape
     k = 2 * half
-    if rows is not None and r != rows or K is not None and k != K:
+    if (rows is not None and r != rows) or (K is not None and k != K):
         raise ValueError(f"{name} must be [{'any' if rows is None else rows}, {'any' if K is None else K}], got [{r}, {k}]")
     if k < 32 or k % 32:
         raise ValueError(f"{name}: K must be a multiple of 32, got {k}")
-    _need(codes, f"{name}.codes", torch.uint8)
-    _need(scales, f"{name}.scales", torch.uint8, _scales_shape(r, k))
+    tiles = _scales_shape(r, k)
+    if not (codes.dtype == scales.dtype == torch.uint8 and scales.shape == tiles and codes.is_cuda and scales.is_cuda and
+            codes.is_contiguous() and scales.is_contiguous()):
+        _need(codes, f"{name}.codes", torch.uint8)
+        _need(scales, f"{name}.scales", torch.uint8, tiles)
     return r, k
 
 
