@@ -26,10 +26,10 @@
 // chunks into a ring, from row to row without a pause; eight warps (the readers)
 // sum; three warps (the selectors) find a row's largest tokens and write its
 // results while the readers are at the next row.  2048 x 131072 f32 with 20
-// tokens: 172 us (0.93 of the copy rate); 4096 x 131072 bf16: 207 (0.78), where
-// the readers' latency counts (as many elements for half the bytes; without
-// tokens to select 1024 rows take 57 us, with 20 69); rows of 50000 f32 and
-// less are bound by the selection of a row, 6 to 9 us.
+// tokens: 172 us (0.93 of the copy rate); 4096 x 131072 bf16: 203 (0.79), where
+// the readers' latency counts (as many elements for half the bytes).  Shorter
+// rows are bound by the selection of one, 12000 clocks beside the readers: 4096
+// x 32000 bf16 takes 65 us without tokens to select, with 20 107.
 #include <cuda_bf16.h>
 
 #include "launch_util.h"
@@ -132,6 +132,13 @@ struct Vec<uint16_t> {
     const uint32_t w = e < 2 ? q.x : e < 4 ? q.y : e < 6 ? q.z : q.w;
     return __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
   }
+  // The elements that are at least lo, a bit each.
+  __device__ static uint32_t reach(const uint4& q, float lo) {
+    uint32_t which = 0;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) which |= at(q, e) >= lo ? 1u << e : 0u;
+    return which;
+  }
   __device__ static void mask(uint4& q, int e) {
     uint32_t* w = reinterpret_cast<uint32_t*>(&q) + e / 2;
     *w = e & 1 ? (*w & 0xFFFFu) | 0xFF800000u : (*w & 0xFFFF0000u) | 0xFF80u;
@@ -187,6 +194,13 @@ struct Vec<float> {
   __device__ static float load(const float* p) { return *p; }
   __device__ static float at(const uint4& q, int e) {
     return __uint_as_float(e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w);
+  }
+  // The elements that are at least lo, a bit each.
+  __device__ static uint32_t reach(const uint4& q, float lo) {
+    uint32_t which = 0;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) which |= at(q, e) >= lo ? 1u << e : 0u;
+    return which;
   }
   __device__ static void mask(uint4& q, int e) { reinterpret_cast<uint32_t*>(&q)[e] = kNegInf; }
   using Max = float;
@@ -337,12 +351,27 @@ struct __align__(16) LpSelect {
 // rest are 0).
 template <class G>
 __device__ __forceinline__ void rank_candidates(LpSelect<G>* sh, const G& g, int n, int k) {
-  for (int i = g.at; i < n; i += G::kSize) {
-    const uint64_t mine = sh->cand[i];
-    int r = 0;
+  if (n <= 48) {
+    if (g.at < n) {
+      const uint64_t mine = sh->cand[g.at];
+      int r = 0;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) r += sh->cand[j] > mine;
-    if (r < k) sh->best[r] = mine;
+      for (int j = 0; j < n; ++j) r += sh->cand[j] > mine;
+      if (r < k) sh->best[r] = mine;
+    }
+  } else {
+    // two threads for each, on every other one (64 x 131072 bf16, 20 tokens: 11.7
+    // us, by one thread each 12.1; with few survivors the exchange costs more than
+    // it saves: 4096 x 1000 bf16, 20 tokens: 29.7, by two 31.4)
+    for (int i0 = 0; i0 < n; i0 += G::kSize / 2) {
+      const int i = i0 + g.at / 2;
+      const uint64_t mine = sh->cand[min(i, n - 1)];
+      int r = 0;
+#pragma unroll 8
+      for (int j = g.at & 1; j < n; j += 2) r += sh->cand[j] > mine;
+      r += __shfl_xor_sync(0xffffffffu, r, 1);
+      if (i < n && r < k) sh->best[r] = mine;
+    }
   }
   for (int i = n + g.at; i < k; i += G::kSize) sh->best[i] = 0;
   g.sync();
@@ -1042,14 +1071,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             for (int k = 0; k < kAhead; ++k) {
               if (v[k] >= v1) continue;
               if (r.edge(v[k])) r.edges(q[k], v[k]);
-              if (!(V::whole(V::max(q[k])) >= lo)) continue;
-#pragma unroll
-              for (int e = 0; e < V::kN; ++e) {
-                const float x = V::at(q[k], e);
-                if (x >= lo) {
-                  const int n = atomicAdd(&sel->n_cand, 1);
-                  if (n < sel->kCap) sel->cand[n] = key_of(x, v[k] * V::kN + e - r.off);
-                }
+              for (uint32_t which = V::reach(q[k], lo); which; which &= which - 1) {
+                const int e = __ffs(which) - 1, n = atomicAdd(&sel->n_cand, 1);
+                if (n < sel->kCap) sel->cand[n] = key_of(V::at(q[k], e), v[k] * V::kN + e - r.off);
               }
             }
           }
