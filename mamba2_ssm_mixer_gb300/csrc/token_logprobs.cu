@@ -26,7 +26,7 @@
 // chunks into a ring, from row to row without a pause; eight warps (the readers)
 // sum; three warps (the selectors) find a row's largest tokens and write its
 // results while the readers are at the next row.  2048 x 131072 f32 with 20
-// tokens: 172 us (0.93 of the copy rate); 4096 x 131072 bf16: 203 (0.79), where
+// tokens: 172 us (0.93 of the copy rate); 4096 x 131072 bf16: 201 (0.80), where
 // the readers' latency counts (as many elements for half the bytes).  Shorter
 // rows are bound by the selection of one, 12000 clocks beside the readers: 4096
 // x 32000 bf16 takes 65 us without tokens to select, with 20 107.
@@ -963,12 +963,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           left = cut.group;
         }
         sums.reach(mx);
-        if (sums.c > kNone) {
-          const uint64_t cc = pair(-sums.c, -sums.c);
-          const typename V::Low low = sums.low();
+        // (while everything is masked the reference is kNone and what is added 0)
+        const uint64_t cc = pair(-sums.c, -sums.c);
+        const typename V::Low low = sums.low();
 #pragma unroll
-          for (int j = 0; j < kVpt; ++j) V::template sums<true>(q[j], low, cc, sums.s[j & 1], sums.u[j & 1]);
-        }
+        for (int j = 0; j < kVpt; ++j) V::template sums<true>(q[j], low, cc, sums.s[j & 1], sums.u[j & 1]);
         typename V::Count count;
         if (vt < vc || vt >= vc + kChunkVecs) {   // (the same for all)
           const typename V::Thr t = vt < vc ? above : from;

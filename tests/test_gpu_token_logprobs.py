@@ -312,3 +312,17 @@ def test_ties_in_many_long_rows(rows, v, dtype):
     logits = torch.from_numpy(x).to(dtype).cuda()
     check(logits, rng.integers(0, v, rows).astype(np.int32), 20)
     check(logits[:, 1:], rng.integers(0, v - 1, rows).astype(np.int32), 64)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows,v", [(3, 5000), (400, 20001)])
+def test_masks_in_front(rows, v, dtype):
+    """Long masked stretches before a row's first logits, below and above the
+    size from which rows are summed as differences."""
+    rng = np.random.default_rng(v)
+    x = rng.standard_normal((rows, v)) * 2
+    for r in range(rows):
+        x[r] += (0.0, 60000.0, -60000.0, -70000.0, -200000.0, 300.0)[r % 6]
+        x[r, :(0, v // 2, v - 3, v - 1)[r % 4]] = (-np.inf, np.nan)[r % 2]
+    logits = torch.from_numpy(x.astype(np.float32)).to(dtype).cuda()
+    check(logits, rng.integers(0, v, rows).astype(np.int32), 6)
