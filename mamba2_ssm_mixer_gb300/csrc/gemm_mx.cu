@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // quantise the CTA's part of it into shared memory first, while W arrives (one
 // launch and no workspace).  2688 -> 10304, 1 row: 5.25 us, the quantisation by
 // itself before it 5.7; 4096 -> 2688, 64 rows: 9.1 and 7.8, but an eager call
-// takes 10 us instead of 16, and the calls are the host's.
+// takes 9 us instead of 16, and the calls are the host's.
 // ---------------------------------------------------------------------------
 template <int BNT, int STAGES, bool kF32, bool kInside>
 __global__ void __launch_bounds__(kInside ? kInsideThreads : kThreads, 1)
