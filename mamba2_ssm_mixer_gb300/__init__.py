@@ -979,10 +979,16 @@ def mxfp4_linear(a: Mxfp4, w: Mxfp4, y: torch.Tensor | None = None, dtype=torch.
 
 
 @functools.lru_cache(maxsize=1024)
-def mxfp4_linear_bf16_workspace_size(M: int, N: int, K: int) -> int:
+def _mx_workspace_size(device: int, M: int, N: int, K: int) -> int:   # (device: the current one)
     n = _sz()
     _check(_lib.mxfp4_linear_bf16_workspace_size(M, N, K, ctypes.byref(n)))
     return n.value
+
+
+def mxfp4_linear_bf16_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes for mxfp4_linear_bf16 on the current device (they depend on its
+    SMs and on the clusters that fit)."""
+    return _mx_workspace_size(_current_device() if torch.cuda.is_initialized() else -1, M, N, K)
 
 
 def mxfp4_linear_bf16(x: torch.Tensor, w: Mxfp4, y: torch.Tensor | None = None, dtype=torch.bfloat16, workspace=None,
