@@ -1071,12 +1071,23 @@ def m2_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
 class Mxfp4Head:
     """The head of a stack with its output matrix in 4 bits: final RMSNorm, then
     logits = mxfp4(rmsnorm(h) * norm_w) @ weight^T.  norm_w bf16 [n], weight an
-    Mxfp4 [vocab, n]; dtype: of the logits (float32 or bfloat16)."""
+    Mxfp4 [vocab, n] (vocab up to 2^24, vocab * n up to 2^38), both 16-byte
+    aligned; dtype: of the logits (float32 or bfloat16)."""
 
     def __init__(self, norm_w: torch.Tensor, weight: Mxfp4, eps: float = 1e-5, dtype=torch.float32):
         _need_mx(weight, "weight")
-        _need(norm_w, "norm_w", torch.bfloat16, (weight.shape[1],))
+        vocab, n = weight.shape
+        _need(norm_w, "norm_w", torch.bfloat16, (n,))
         _mx_dtype(dtype)
+        # (what the kernels would refuse of every call: here, before a stack's
+        # states have moved)
+        if not ctypes.c_float(eps).value > 0:
+            raise ValueError(f"eps must be positive, got {eps}")
+        if not 1 <= vocab <= 1 << 24 or vocab * n > 1 << 38:
+            raise ValueError(f"weight must have a vocab in [1, 2^24] and up to 2^38 values, got [{vocab}, {n}]")
+        for t, name in ((norm_w, "norm_w"), (weight.codes, "weight.codes"), (weight.scales, "weight.scales")):
+            if t.data_ptr() % 16:
+                raise ValueError(f"{name} must be 16-byte aligned")
         self.norm_w, self.weight, self.eps, self.dtype = norm_w, weight, eps, dtype
         self.vocab = weight.shape[0]
 
