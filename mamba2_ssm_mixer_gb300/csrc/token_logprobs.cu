@@ -109,6 +109,11 @@ __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -173,17 +178,17 @@ struct Vec<uint16_t> {
     uint32_t v;
     __device__ explicit Low(float low) { v = pack_bf16x2(low, low); }
   };
-  template <bool kLow>
+  template <bool kFirst>   // (s and u begin here)
   __device__ static void sums(const uint4& q, const Low& low, uint64_t cc, uint64_t& s, uint64_t& u) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t x = kLow ? max_bf16x2(w[i], low.v) : w[i];
+      const uint32_t x = max_bf16x2(w[i], low.v);
       const uint64_t d = fma_pair(pair(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u)), pair(kL, kL), cc);
       const float2 t = unpair(d);
       const uint64_t p = pair(exp2_fast(t.x), exp2_fast(t.y));
-      s = add_pair(s, p);
-      u = fma_pair(p, d, u);
+      s = kFirst && i == 0 ? p : add_pair(s, p);
+      u = kFirst && i == 0 ? mul_pair(p, d) : fma_pair(p, d, u);
     }
   }
 };
@@ -224,16 +229,16 @@ struct Vec<float> {
     float v;
     __device__ explicit Low(float low) : v(low) {}
   };
-  template <bool kLow>
+  template <bool kFirst>   // (s and u begin here)
   __device__ static void sums(const uint4& q, const Low& low, uint64_t cc, uint64_t& s, uint64_t& u) {
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
       const float a = at(q, i), b = at(q, i + 1);
-      const uint64_t d = fma_pair(kLow ? pair(fmaxf(a, low.v), fmaxf(b, low.v)) : pair(a, b), pair(kL, kL), cc);
+      const uint64_t d = fma_pair(pair(fmaxf(a, low.v), fmaxf(b, low.v)), pair(kL, kL), cc);
       const float2 t = unpair(d);
       const uint64_t p = pair(exp2_fast(t.x), exp2_fast(t.y));
-      s = add_pair(s, p);
-      u = fma_pair(p, d, u);
+      s = kFirst && i == 0 ? p : add_pair(s, p);
+      u = kFirst && i == 0 ? mul_pair(p, d) : fma_pair(p, d, u);
     }
   }
 };
@@ -640,23 +645,20 @@ __device__ __forceinline__ void row_results(LpSelect<G>* sh, const G& g, const L
   }
 }
 
-// Sums of a thread's vectors.
+// A thread's sums s and u relative to its reference c, in pairs.
 template <typename T>
 struct Sums {
   using V = Vec<T>;
   float c = kNone;
-  uint64_t s[2] = {pair(0.f, 0.f), pair(0.f, 0.f)}, u[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+  uint64_t s = pair(0.f, 0.f), u = pair(0.f, 0.f);
 
   // The reference moves where a maximum passes it by 16.
+  __device__ bool passes(float mx) const { return mx * kL > c + 16.f; }
   __device__ void reach(float mx) {
-    if (mx * kL > c + 16.f) {
+    if (passes(mx)) {
       const float cn = rintf(mx * kL), d = fmaxf(c - cn, -1e30f), f = exp2_fast(d);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        u[i] = fma_pair(s[i], pair(d, d), u[i]);
-        s[i] = fma_pair(s[i], pair(f, f), pair(0.f, 0.f));
-        u[i] = fma_pair(u[i], pair(f, f), pair(0.f, 0.f));
-      }
+      u = fma_pair(fma_pair(s, pair(d, d), u), pair(f, f), pair(0.f, 0.f));
+      s = fma_pair(s, pair(f, f), pair(0.f, 0.f));
       c = cn;
     }
   }
@@ -667,10 +669,35 @@ struct Sums {
     return typename V::Low(fmaf(fabsf(l), -0.01f, l));
   }
   __device__ LpPart part(float m, int greater) const {
-    const float2 a = unpair(add_pair(s[0], s[1])), b = unpair(add_pair(u[0], u[1]));
+    const float2 a = unpair(s), b = unpair(u);
     return {c, a.x + a.y, b.x + b.y, m, greater};
   }
 };
+
+// What a reader of a long row has put by of its sums (in shared memory: it has
+// no registers left).  Among equal logits each addition errs to the same side, and
+// n terms one after another by up to n / 2 of the last place (in a row of 2^24
+// tokens 2^-13 of S).  So a chunk is summed by itself, its sum joins the thread's,
+// and after kCarry chunks that is put by: what this addition rounds off stays
+// behind as the next sum's first term.
+constexpr int kCarry = 16;
+struct LpCarried {
+  float c, s, u;
+};
+template <typename T>
+__device__ __forceinline__ void carry(LpCarried& to, Sums<T>& sums, bool first) {
+  const float2 a = unpair(sums.s), b = unpair(sums.u);
+  const float x = a.x + a.y, y = b.x + b.y;
+  float s0 = 0.f, u0 = 0.f;
+  if (!first) {
+    const float d = to.c - sums.c, f = exp2_fast(d);   // (a reference only grows)
+    s0 = to.s * f, u0 = fmaf(to.s, d, to.u) * f;
+  }
+  const float s = s0 + x, u = u0 + y;
+  to = {sums.c, s, u};
+  sums.s = pair(x - (s - s0), 0.f);
+  sums.u = pair(y - (u - u0), 0.f);
+}
 
 }  // namespace
 
@@ -710,12 +737,20 @@ __global__ void __launch_bounds__(kHeldThreads, VPT == 16 ? 2 : VPT == 8 ? 3 : 5
   }
   const float mx = max_of<T>(q);
   Sums<T> sums;
-  sums.reach(mx);
-  if (sums.c > kNone) {
+  if (sums.passes(mx)) {
+    sums.c = rintf(mx * kL);
     const typename V::Low low = sums.low();
     const uint64_t cc = pair(-sums.c, -sums.c);
+    uint64_t s[2], u[2];   // (of every other vector: up to 32 terms one after another)
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) V::template sums<true>(q[j], low, cc, sums.s[j & 1], sums.u[j & 1]);
+    for (int j = 0; j < VPT; ++j) {
+      if (j < 2)
+        V::template sums<true>(q[j], low, cc, s[j], u[j]);
+      else
+        V::template sums<false>(q[j], low, cc, s[j & 1], u[j & 1]);
+    }
+    sums.s = VPT > 1 ? add_pair(s[0], s[VPT > 1]) : s[0];
+    sums.u = VPT > 1 ? add_pair(u[0], u[VPT > 1]) : u[0];
   }
   int greater = 0;
   if (job.valid()) {   // before the given token's vector equal logits count as greater
@@ -819,6 +854,7 @@ struct __align__(16) LpShared {
   uint64_t full[kStages], empty[kStages];        // the ring's
   uint64_t read[2], taken[2];                    // the two rows'
   LpRow row[2];
+  LpCarried carried[kReaders];
   LpSelect<SelectorGroup> sel;
   uint16_t over[kReaders];                       // readers whose maximum reaches the bound
   uint16_t hits[kGroups * kReaders];             // and their groups
@@ -833,7 +869,11 @@ struct Cut {
 
 }  // namespace
 
-template <typename T>
+// kLong: slices of more than 2^17 tokens, whose sums are put by on the way.  Up to
+// there a thread's sums are 32 chunks' of 8 terms (bf16: 16 of 16) one after
+// another.  2000 x 151937 bf16: 129 us, without it 126; 4096 x 131072 with it
+// 204, without it 201.
+template <typename T, bool kLong>
 __global__ void __launch_bounds__(kStreamThreads, 2)
     k_lp_stream(const T* __restrict__ logits, size_t stride, int rows, int vocab, const int32_t* __restrict__ tokens,
                 int top, LpOut out, int* err) {
@@ -933,66 +973,86 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       Sums<T> sums;
       float m = -INFINITY, gm = -INFINITY;
       int greater = 0, group = 0, left = cut.group;
-      for (int ch = 0; ch < cut.chunks; ++ch) {
-        wait(&sh->full[stage], phase);
-        const int vc = v0 + ch * kChunkVecs;
-        const uint4* p = reinterpret_cast<const uint4*>(ring + stage * kChunkBytes) + tid;
-        uint4 q[kVpt];
-        if (ch > 0 && ch + 1 < cut.chunks) {
+      auto chunks = [&](int ch, int to) {
+        for (; ch < to; ++ch) {
+          wait(&sh->full[stage], phase);
+          const int vc = v0 + ch * kChunkVecs;
+          const uint4* p = reinterpret_cast<const uint4*>(ring + stage * kChunkBytes) + tid;
+          uint4 q[kVpt];
+          if (ch > 0 && ch + 1 < cut.chunks) {
 #pragma unroll
-          for (int j = 0; j < kVpt; ++j) q[j] = p[j * kReaders];
-        } else {
+            for (int j = 0; j < kVpt; ++j) q[j] = p[j * kReaders];
+          } else {
 #pragma unroll
-          for (int j = 0; j < kVpt; ++j) {
-            const int v = vc + j * kReaders + tid;
-            q[j] = v < v1 ? p[j * kReaders] : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
-            if (v < v1 && r.edge(v)) r.edges(q[j], v);
+            for (int j = 0; j < kVpt; ++j) {
+              const int v = vc + j * kReaders + tid;
+              q[j] = v < v1 ? p[j * kReaders] : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+              if (v < v1 && r.edge(v)) r.edges(q[j], v);
+            }
           }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->empty[stage]);
-        if (++stage == kStages) stage = 0, phase ^= 1u;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->empty[stage]);
+          if (++stage == kStages) stage = 0, phase ^= 1u;
 
-        const float mx = max_of<T>(q);
-        gm = fmaxf(gm, mx);
-        if (--left == 0 || ch + 1 == cut.chunks) {
-          if (top) hand.gmax[group][tid] = ord32(gm + 0.f);
-          m = fmaxf(m, gm);
-          gm = -INFINITY;
-          ++group;
-          left = cut.group;
-        }
-        sums.reach(mx);
-        // (while everything is masked the reference is kNone and what is added 0)
-        const uint64_t cc = pair(-sums.c, -sums.c);
-        const typename V::Low low = sums.low();
+          const float mx = max_of<T>(q);
+          gm = fmaxf(gm, mx);
+          if (--left == 0 || ch + 1 == cut.chunks) {
+            if (top) hand.gmax[group][tid] = ord32(gm + 0.f);
+            m = fmaxf(m, gm);
+            gm = -INFINITY;
+            ++group;
+            left = cut.group;
+          }
+          sums.reach(mx);
+          // (while everything is masked the reference is kNone and what is added 0)
+          const uint64_t cc = pair(-sums.c, -sums.c);
+          const typename V::Low low = sums.low();
+          uint64_t s, u;
+          V::template sums<true>(q[0], low, cc, s, u);
 #pragma unroll
-        for (int j = 0; j < kVpt; ++j) V::template sums<true>(q[j], low, cc, sums.s[j & 1], sums.u[j & 1]);
-        typename V::Count count;
-        if (vt < vc || vt >= vc + kChunkVecs) {   // (the same for all)
-          const typename V::Thr t = vt < vc ? above : from;
+          for (int j = 1; j < kVpt; ++j) V::template sums<false>(q[j], low, cc, s, u);
+          sums.s = add_pair(sums.s, s);
+          sums.u = add_pair(sums.u, u);
+          typename V::Count count;
+          if (vt < vc || vt >= vc + kChunkVecs) {   // (the same for all)
+            const typename V::Thr t = vt < vc ? above : from;
 #pragma unroll
-          for (int j = 0; j < kVpt; ++j)
-            count.add(q[j], t);
-        } else {
+            for (int j = 0; j < kVpt; ++j)
+              count.add(q[j], t);
+          } else {
 #pragma unroll
-          for (int j = 0; j < kVpt; ++j) {
-            const int v = vc + j * kReaders + tid;
-            if (v != vt) {
-              count.add(q[j], v < vt ? from : above);
-            } else {
+            for (int j = 0; j < kVpt; ++j) {
+              const int v = vc + j * kReaders + tid;
+              if (v != vt) {
+                count.add(q[j], v < vt ? from : above);
+              } else {
 #pragma unroll
-              for (int e = 0; e < V::kN; ++e) {
-                const float x = V::at(q[j], e);
-                greater += x > xt || (x == xt && v * V::kN + e - r.off < token);
+                for (int e = 0; e < V::kN; ++e) {
+                  const float x = V::at(q[j], e);
+                  greater += x > xt || (x == xt && v * V::kN + e - r.off < token);
+                }
               }
             }
           }
+          greater += count.total();
         }
-        greater += count.total();
+      };
+      if constexpr (kLong) {
+#pragma unroll 1
+        for (int ch = 0; ch < cut.chunks; ch += kCarry) {
+          if (ch > 0) carry(sh->carried[tid], sums, ch == kCarry);
+          chunks(ch, min(ch + kCarry, cut.chunks));
+        }
+      } else {
+        chunks(0, cut.chunks);
       }
       // ---------------- the warp's part to the selectors
-      const LpPart a = join_lanes(sums.part(m, greater), 32);
+      LpPart a = sums.part(m, greater);
+      if (kLong && cut.chunks > kCarry) {
+        const LpCarried& b = sh->carried[tid];
+        a = join(a, {b.c, b.s, b.u, -INFINITY, 0});
+      }
+      a = join_lanes(a, 32);
       if (lane == 0) hand.warp[warp] = a;
       if (top) {
         hand.tmax[tid] = ord32(m + 0.f);
@@ -1157,11 +1217,11 @@ cudaError_t launch_t(const T* logits, size_t stride, int rows, int vocab, const 
     return go(k_lp_held<T, 16>);
   }
   const size_t smem = 128 + (size_t)kStages * kChunkBytes + sizeof(LpShared);
-  auto k = k_lp_stream<T>;
-  cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem);
-  if (e != cudaSuccess) return e;
   S = 1;
   while (S < kLpMaxSlices && (long long)2 * S * rows <= 2 * sms && 2ll * S * kChunkVecs <= nv) S *= 2;
+  const auto k = vocab > S << 17 ? k_lp_stream<T, true> : k_lp_stream<T, false>;
+  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), (int)smem);
+  if (e != cudaSuccess) return e;
   return launch_cluster(k, dim3(S, S > 1 ? rows : (rows < 2 * sms ? rows : 2 * sms)), kStreamThreads, smem, S, st, logits,
                         stride, rows, vocab, tokens, top, out, err);
 }
