@@ -347,6 +347,7 @@ struct __align__(16) LpSelect {
   uint64_t merged[kLpMaxTop];          // the row's, from several slices'
   LpPart part, whole;                  // the slice's, the row's
   float z, z_lo, m;                    // log S of the row, relative to its maximum m, in two parts
+  float h;                             // the entropy of one that was summed again
   int n_cand, n_hit, n_over;
   float sum[G::kSize / 32][2];
   int equal[G::kSize / 32];
@@ -467,48 +468,6 @@ __device__ __forceinline__ int survivors(LpSelect<G>* sh, const G& g, int k, flo
   return ties && n < k ? equal(tie, n) : n;
 }
 
-// log S and the entropy of a row whose maximum m is finite and large, or +inf
-// (then the +inf tokens share the probability).
-template <typename T, class G>
-__device__ __noinline__ float2 row_again(LpSelect<G>* sh, const G g, const RowAt<T> r, float m) {
-  using V = Vec<T>;
-  float s = 0.f, u = 0.f;
-#pragma unroll 4
-  for (int v = g.at; v < r.nv; v += G::kSize) {
-    uint4 q = __ldg(r.vec + v);
-    if (r.edge(v)) r.edges(q, v);
-#pragma unroll
-    for (int e = 0; e < V::kN; ++e) {
-      const float x = V::at(q, e);
-      if (m == INFINITY) {
-        s += x == INFINITY ? 1.f : 0.f;
-      } else {
-        const float d = x - m, p = expf(d);
-        if (p > 0.f) s += p, u = fmaf(p, d, u);
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o), u += __shfl_xor_sync(0xffffffffu, u, o);
-  g.sync();
-  if ((g.at & 31) == 0) sh->sum[g.at >> 5][0] = s, sh->sum[g.at >> 5][1] = u;
-  g.sync();
-  s = u = 0.f;
-#pragma unroll
-  for (int w = 0; w < G::kSize / 32; ++w) s += sh->sum[w][0], u += sh->sum[w][1];
-  const float z = logf(s);
-  return make_float2(z, z - u / s);
-}
-
-// A row and the token to score in it.
-template <typename T>
-struct LpJob {
-  RowAt<T> r;
-  int row, vocab, token;
-  float xt;   // its logit
-  __device__ bool valid() const { return token >= 0 && token < vocab; }
-};
-
 // a + b exactly, as a rounded sum and its error.
 struct Two {
   float hi, lo;
@@ -522,6 +481,67 @@ __device__ __forceinline__ Two add(const Two& a, float b) {
   const Two s = two_sum(a.hi, b);
   return {s.hi, s.lo + a.lo};
 }
+// log s in two parts: s = 2^e f with f near 1, log s = e ln 2 + log f.
+__device__ __forceinline__ Two log_parts(float s) {
+  const int e = (int)((__float_as_uint(s) + 0x4AFB0Du) >> 23) - 127;
+  const float lf = logf(__uint_as_float(__float_as_uint(s) - ((uint32_t)e << 23))), ef = (float)e;
+  const float el = ef * kLn2;
+  return add(add({el, fmaf(ef, kLn2, -el) + ef * kLn2Lo}, lf), 0.f);
+}
+
+// log S and the entropy of a row whose maximum m is finite and large, or +inf
+// (then the +inf tokens share the probability), left in sh by the first thread.
+// A thread adds up to 2^24 / 96 terms, which among equal logits err to the same
+// side (as in Sums::carry): a vector's at first, these sums then with what is
+// rounded off beside them.
+template <typename T, class G>
+__device__ __noinline__ void row_again(LpSelect<G>* sh, const G g, const RowAt<T> r, float m) {
+  using V = Vec<T>;
+  Two s = {0.f, 0.f}, u = {0.f, 0.f};
+#pragma unroll 4
+  for (int v = g.at; v < r.nv; v += G::kSize) {
+    uint4 q = __ldg(r.vec + v);
+    if (r.edge(v)) r.edges(q, v);
+    float sv = 0.f, uv = 0.f;
+#pragma unroll
+    for (int e = 0; e < V::kN; ++e) {
+      const float x = V::at(q, e);
+      if (m == INFINITY) {
+        sv += x == INFINITY ? 1.f : 0.f;
+      } else {
+        const float d = x - m, p = expf(d);
+        if (p > 0.f) sv += p, uv = fmaf(p, d, uv);
+      }
+    }
+    s = add(s, sv);
+    u = add(u, uv);
+  }
+  float a = s.hi + s.lo, b = u.hi + u.lo;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o), b += __shfl_xor_sync(0xffffffffu, b, o);
+  g.sync();
+  if ((g.at & 31) == 0) sh->sum[g.at >> 5][0] = a, sh->sum[g.at >> 5][1] = b;
+  g.sync();
+  a = b = 0.f;
+#pragma unroll
+  for (int w = 0; w < G::kSize / 32; ++w) a += sh->sum[w][0], b += sh->sum[w][1];
+  if (g.at == 0) {
+    const Two z = log_parts(a);
+    sh->z = z.hi;
+    sh->z_lo = z.lo;
+    sh->h = z.hi - (b / a - z.lo);
+  }
+}
+
+// A row and the token to score in it.
+template <typename T>
+struct LpJob {
+  RowAt<T> r;
+  int row, vocab, token;
+  float xt;   // its logit
+  __device__ bool valid() const { return token >= 0 && token < vocab; }
+};
+
 // x - m - z, rounded once but for the errors' errors.
 __device__ __forceinline__ float minus_z(float x, float m, float z, float z_lo) {
   const Two d = two_sum(x, -m);
@@ -531,19 +551,17 @@ __device__ __forceinline__ float minus_z(float x, float m, float z, float z_lo) 
 }
 
 // What the given token and the entropy get from the whole row's part b (one
-// thread); `again`: log S and the entropy of an odd row.  In pairs of f32
-// values: a double's operations take this one thread longer than the rest of a
-// short row's.
+// thread; an odd row's log S and entropy are in sh).  In pairs of f32 values: a
+// double's operations take this one thread longer than the rest of a short
+// row's.
 template <typename T, class G>
-__device__ __forceinline__ void finish(LpSelect<G>* sh, const LpJob<T>& job, const LpPart& b, float2 again,
-                                       const LpOut& out, bool scored, int* err) {
-  float z = again.x, z_lo = 0.f, h = again.y;
-  if (!is_odd(b.m) && b.m > -INFINITY) {
-    // S = 2^e f with f near 1: log S = e ln 2 + log f
-    const int e = (int)((__float_as_uint(b.s) + 0x4AFB0Du) >> 23) - 127;
-    const float lf = logf(__uint_as_float(__float_as_uint(b.s) - ((uint32_t)e << 23))), ef = (float)e;
-    const float el = ef * kLn2;
-    const Two ln = add(add({el, fmaf(ef, kLn2, -el) + ef * kLn2Lo}, lf), 0.f);
+__device__ __forceinline__ void finish(LpSelect<G>* sh, const LpJob<T>& job, const LpPart& b, const LpOut& out,
+                                       bool scored, int* err) {
+  float z = 0.f, z_lo = 0.f, h = 0.f;
+  if (is_odd(b.m)) {
+    z = sh->z, z_lo = sh->z_lo, h = sh->h;
+  } else if (b.m > -INFINITY) {
+    const Two ln = log_parts(b.s);
     // z = log S + (c ln 2 - m) + m (log2 e - L) ln 2
     const float rest = b.m * (float)(kLRest * 0.693147180559945309), cl = b.c * kLn2;
     const Two dc = two_sum(cl, -b.m);
@@ -560,7 +578,6 @@ __device__ __forceinline__ void finish(LpSelect<G>* sh, const LpJob<T>& job, con
   sh->z = z;
   sh->z_lo = z_lo;
   sh->m = b.m;
-  if (!(b.m > -INFINITY)) h = 0.f;
   if (out.entropy) out.entropy[job.row] = fmaxf(h, 0.f);
   if (!scored) return;
   float lp = 0.f;
@@ -622,7 +639,7 @@ __device__ __forceinline__ void row_results(LpSelect<G>* sh, const G& g, const L
       const LpPart b = join_lanes(mine, S);
       if (g.at == G::kSize - 32) {
         sh->whole = b;
-        if (!is_odd(b.m)) finish(sh, job, b, make_float2(0.f, 0.f), out, scored, err);
+        if (!is_odd(b.m)) finish(sh, job, b, out, scored, err);
       }
       __syncwarp();
     }
@@ -631,8 +648,8 @@ __device__ __forceinline__ void row_results(LpSelect<G>* sh, const G& g, const L
   }
   const LpPart b = S > 1 ? sh->whole : sh->part;
   if (is_odd(b.m)) {   // (the same for all)
-    const float2 again = row_again<T, G>(sh, g, job.r, b.m);
-    if (g.at == 0) finish(sh, job, b, again, out, scored, err);
+    row_again<T, G>(sh, g, job.r, b.m);
+    if (g.at == 0) finish(sh, job, b, out, scored, err);
     g.sync();
   }
   for (int i = g.at; i < top; i += G::kSize) {
@@ -811,7 +828,7 @@ __global__ void __launch_bounds__(kHeldThreads, VPT == 16 ? 2 : VPT == 8 ? 3 : 5
         }
       }
       if (first && S == 1 && tid == 32 * (kHeldWarps - 1) && !is_odd(sel.part.m))   // (beside the others' search)
-        finish(&sel, job, sel.part, make_float2(0.f, 0.f), out, tokens != nullptr, err);
+        finish(&sel, job, sel.part, out, tokens != nullptr, err);
       first = false;
       __syncthreads();
       return max(sel.n_cand, sel.n_hit);
@@ -828,7 +845,7 @@ __global__ void __launch_bounds__(kHeldThreads, VPT == 16 ? 2 : VPT == 8 ? 3 : 5
   } else {
     __syncthreads();
     if (S == 1 && tid == 0 && !is_odd(sel.part.m))
-      finish(&sel, job, sel.part, make_float2(0.f, 0.f), out, tokens != nullptr, err);
+      finish(&sel, job, sel.part, out, tokens != nullptr, err);
   }
   if (S > 1) {
     cluster_sync();
@@ -1086,7 +1103,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         const LpPart b = join_lanes(lane < kReadWarps ? hand.warp[lane] : LpPart{kNone, 0.f, 0.f, -INFINITY, 0}, 16);
         if (lane == 0) {
           sel->part = b;
-          if (S == 1 && !is_odd(b.m)) finish(sel, job, b, make_float2(0.f, 0.f), out, tokens != nullptr, err);
+          if (S == 1 && !is_odd(b.m)) finish(sel, job, b, out, tokens != nullptr, err);
         }
         __syncwarp();
       }

@@ -13,9 +13,12 @@ entropy, ranks and alternatives have closed forms.  Bound of log S in units of
  - lanes, warps and slices are joined in at most 5 + 3 + 3 levels (11);
  - what a reference in base 2 leaves out of a spread of d <= 17 (4), the
    logarithm and its parts (2).
-50 together.  The entropy is log S less the mean of x - m: with a share w of the
-weight d away from the rest, d w (1 - w) <= 17 / 4 times the bound more: 250
-units, 300 here.  Results are rounded to f32 once."""
+50 together.  Logits beyond +-2^16 are summed as x - m, which is exact (they are
+multiples of 2^-8 at least, and close): an exponential within an ulp (2), 8 terms
+of a vector (5), lanes and warps (5 + 8): less.  The entropy is log S less the
+mean of x - m: with a share w of the weight d away from the rest, d w (1 - w) <=
+17 / 4 times the bound more: 250 units, 300 here.  Results are rounded to f32
+once."""
 import numpy as np
 import pytest
 import torch
@@ -85,3 +88,11 @@ def test_one_likely_token_among_equal_ones(rows, v, dtype):
     base = (r + 1) * 0.125 - 9.9375 if dtype == F32 else (r % 31 + 1) * 0.0625
     d = (r % 17) + 0.5 if dtype == F32 else np.where(r % 2, 1.0, 2.0) - base + np.where(r % 3, 2.0, 12.0)
     check_rows(base, d, v, dtype, (r * 7919 % v).astype(np.int64))
+
+
+@pytest.mark.parametrize("around", [70000.0, -70000.0, 1000000.0])
+@pytest.mark.parametrize("rows,v", [(3, 131071), (3, 60000), (200, 131072), (160, 1 << 20), (2, 1 << 23), (1, 1 << 24)])
+def test_large_logits(rows, v, around):
+    r = np.arange(rows, dtype=np.float64)
+    d = (r * 5 % 150 + 2) / 16
+    check_rows(around + r - d, d, v, F32, (r * 7919 % v).astype(np.int64))
