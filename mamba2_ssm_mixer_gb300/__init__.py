@@ -1004,7 +1004,7 @@ def mxfp4_linear_bf16(x: torch.Tensor, w: Mxfp4, y: torch.Tensor | None = None, 
 
     def call(handle):
         o = torch.empty((M, N), dtype=dtype, device=x.device) if y is None else y
-        ws, nbytes = _scratch(workspace, mxfp4_linear_bf16_workspace_size(M, N, K), x.device)
+        ws, nbytes = _scratch(workspace, _mx_workspace_size(x.get_device(), M, N, K), x.device)
         _check(_lib.mxfp4_linear_bf16(x.data_ptr(), stride, w.codes.data_ptr(), w.scales.data_ptr(), o.data_ptr(), out_dtype,
                                       M, N, K, _ptr(ws), nbytes, handle))
         return o
