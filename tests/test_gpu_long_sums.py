@@ -96,3 +96,50 @@ def test_large_logits(rows, v, around):
     r = np.arange(rows, dtype=np.float64)
     d = (r * 5 % 150 + 2) / 16
     check_rows(around + r - d, d, v, F32, (r * 7919 % v).astype(np.int64))
+
+
+def patterns(v, dtype):
+    """Rows of v tokens: random, masked in front, behind and nearly everywhere (by
+    -inf, NaN, finite values), in order, of +inf, of nothing."""
+    g = torch.Generator(device="cuda").manual_seed(v)
+    lowest = torch.finfo(dtype).min
+
+    def random():
+        return torch.randn(v, generator=g, device="cuda") * 2.5
+
+    rows = [random() for _ in range(10)]
+    rows[1][:v * 9 // 10] = float("-inf")
+    rows[2][v // 10:] = float("nan")
+    rows[3] = torch.linspace(-60000, 60000, v, device="cuda")
+    rows[4] = torch.linspace(60000, -60000, v, device="cuda")
+    few = torch.tensor([v // 7, v // 2, v - 2], device="cuda")
+    rows[5][:] = float("-inf")
+    rows[5][few] = torch.tensor([1.0, 3.0, 2.0], device="cuda")
+    rows[6][:] = lowest
+    rows[6][few] = torch.tensor([-1.0, 0.5, 0.25], device="cuda")
+    rows[7][:] = float("-inf")
+    rows[8][few] = float("inf")
+    rows[9][:] = lowest
+    return torch.stack(rows).to(dtype)
+
+
+# (slices of 2^17 tokens and more; whole rows)
+@pytest.mark.parametrize("rows,v,dtype", [(10, 4000003, F32), (10, 4000003, BF), (160, 600001, F32), (160, 600001, BF)])
+def test_masks_and_order_in_long_rows(rows, v, dtype):
+    """Against 64 bits, where terms differ and any of n additions may err by half a
+    step of the whole sum: 40 units for 21 in the bound above, 70 together; the
+    entropy's mean is of |x - m| up to 17 under the weights, half of it apart."""
+    from test_gpu_token_logprobs import close, reference
+    some = patterns(v, dtype)
+    logits = some.repeat(rows // 10, 1)
+    tokens = torch.tensor([v // 2, v - 2, 5, v - 1, 0, v // 7, v - 2, 3, v // 2, v // 3], dtype=torch.int32, device="cuda")
+    o = m2.m2_token_logprobs(logits, tokens.repeat(rows // 10), 20)
+    torch.cuda.synchronize()
+    m2.check_standalone()
+    lp, rk, h, tt, tl = reference(some.float().cpu().numpy().astype(np.float64), tokens.cpu().numpy(), 20)
+    for at in (slice(0, 10), slice(rows - 10, rows)):
+        close(o.logprobs[at], lp, 70 * UNIT)
+        close(o.entropy[at], h, 70 * 9.5 * UNIT)
+        close(o.top_logprobs[at], tl, 70 * UNIT)
+        assert np.array_equal(o.ranks[at].cpu().numpy(), rk)
+        assert np.array_equal(o.top_tokens[at].cpu().numpy(), tt)
