@@ -21,7 +21,7 @@
 // k_lp_held (few rows, or short ones): a CTA, or each of a cluster's, holds its
 // slice of one row in registers; the first CTA joins the slices' parts through
 // distributed shared memory.  A row's latency is what counts: 1 x 131072 bf16
-// takes 8.9 us of which 0.04 are its bytes', 64 x 65536 f32 9.3 (2.5).
+// takes 8.3 us of which 0.04 are its bytes', 64 x 65536 f32 8.9 (2.5).
 // k_lp_stream (many long rows): two persistent CTAs per SM.  One warp copies
 // chunks into a ring, from row to row without a pause; eight warps (the readers)
 // sum; three warps (the selectors) find a row's largest tokens and write its
@@ -29,7 +29,7 @@
 // tokens: 172 us (0.93 of the copy rate); 4096 x 131072 bf16: 201 (0.80), where
 // the readers' latency counts (as many elements for half the bytes).  Shorter
 // rows are bound by the selection of one, 12000 clocks beside the readers: 4096
-// x 32000 bf16 takes 65 us without tokens to select, with 20 107.
+// x 32000 bf16 takes 65 us without tokens to select, with 20 108.
 #include <cuda_bf16.h>
 
 #include "launch_util.h"
@@ -444,8 +444,8 @@ __device__ __noinline__ int first_equal(LpSelect<G>* sh, const G g, const RowAt<
 // the sample shows nothing but the bound itself, only what is greater is
 // gathered and equal(x, n) adds the first tokens that equal it, in order, until
 // there are k.  (512 rows of 131072 bf16 logits, 10 of them above a finite
-// mask, 20 asked for: 78 us; another pass over the row
-// against a running k-th best 594.)
+// mask, 20 asked for: 79 us; another pass over the row against a running k-th
+// best 594.)
 template <typename T, class G, class Gather, class Equal>
 __device__ __forceinline__ int survivors(LpSelect<G>* sh, const G& g, int k, float lo, Gather gather, Equal equal) {
   using V = Vec<T>;
