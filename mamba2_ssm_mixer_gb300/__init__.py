@@ -855,6 +855,9 @@ class Mxfp4(typing.NamedTuple):
         return self.codes.shape[0], 2 * self.codes.shape[1]
 
 
+_LIMIT = 1 << 24   # of rows, columns and alternatives (ctypes cuts what 32 bits do not hold)
+
+
 def _scales_shape(rows: int, K: int):
     return (rows + 127) // 128, (K + 127) // 128, 512
 
@@ -872,6 +875,8 @@ def _need_mx(q: Mxfp4, name: str, rows=None, K=None):
         raise ValueError(f"{name} must be [{'any' if rows is None else rows}, {'any' if K is None else K}], got [{r}, {k}]")
     if k < 32 or k % 32:
         raise ValueError(f"{name}: K must be a multiple of 32, got {k}")
+    if r > _LIMIT or k > _LIMIT:
+        raise ValueError(f"{name} may have up to 2^24 rows and values of K, got [{r}, {k}]")
     tiles = _scales_shape(r, k)
     if not (codes.dtype == scales.dtype == torch.uint8 and scales.shape == tiles and codes.is_cuda and scales.is_cuda and
             codes.is_contiguous() and scales.is_contiguous()):
@@ -890,6 +895,8 @@ def _need_rows(x: torch.Tensor, name: str, dtypes, multiple: int = 1) -> int:
     if x.dim() != 2 or not x.shape[1]:
         raise ValueError(f"{name} must be a matrix with columns, got {tuple(x.shape)}")
     rows, cols = x.shape
+    if rows > _LIMIT or cols > _LIMIT:
+        raise ValueError(f"{name} may have up to 2^24 rows and columns, got {tuple(x.shape)}")
     if cols > 1 and x.stride(1) != 1:
         raise ValueError(f"{name} rows must be contiguous")
     if rows <= 1:
@@ -915,6 +922,8 @@ def mxfp4_pack(codes: torch.Tensor, scales: torch.Tensor, stream=None) -> Mxfp4:
     _need(codes, "codes", torch.uint8)
     if K < 32 or K % 32:
         raise ValueError(f"K must be a multiple of 32, got {K}")
+    if rows > _LIMIT or K > _LIMIT:
+        raise ValueError(f"codes may have up to 2^24 rows and values of K, got [{rows}, {K}]")
     _need(scales, "scales", torch.uint8, (rows, K // 32))
 
     def call(handle):
@@ -980,6 +989,8 @@ def mxfp4_linear(a: Mxfp4, w: Mxfp4, y: torch.Tensor | None = None, dtype=torch.
 
 @functools.lru_cache(maxsize=1024)
 def _mx_workspace_size(device: int, M: int, N: int, K: int) -> int:   # (device: the current one)
+    if max(M, N, K) > _LIMIT:
+        raise ValueError(f"M, N and K may be up to 2^24, got {M}, {N}, {K}")
     n = _sz()
     _check(_lib.mxfp4_linear_bf16_workspace_size(M, N, K, ctypes.byref(n)))
     return n.value
@@ -1031,8 +1042,8 @@ def m2_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
     masked.  out: a TokenLogprobs of tensors to write."""
     stride = _need_rows(logits, "logits", (torch.bfloat16, torch.float32))
     rows, vocab = logits.shape
-    if top < 0:
-        raise ValueError(f"top must not be negative, got {top}")
+    if not 0 <= top <= _LIMIT:   # (the library refuses more than 64)
+        raise ValueError(f"top must be in [0, 64], got {top}")
     if tokens is not None:
         _need(tokens, "tokens", torch.int32, (rows,))
     if out is not None:
